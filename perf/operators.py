@@ -379,7 +379,7 @@ def _plain_plan(s):
     block = torch.gather(table, 1, (pos // page).clamp(0, wide - 1))
     slots = torch.where(live & (block >= 0), block * page + pos % page, -1)
     out = {"block_table": table, "slots": slots,
-           "taken": torch.where(given, upto, 0).amax(0, keepdim=True),
+           "taken": torch.where(given & (need > 0), upto, 0).amax(0, keepdim=True),
            "status": torch.where(fine, torch.where(given, 0, 10), 11)}
     if T <= 64:
         if s["parents"] is not None:
