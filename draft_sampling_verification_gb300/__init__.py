@@ -2,7 +2,9 @@
 
 Thin Python binding of the C ABI in ``include/dspark.h``: the functions named
 like the C calls (``dspark_q_build``, ``dspark_draft_sample``,
-``dspark_verify_greedy``, ``dspark_verify_ratio``, ``dspark_target_probs``)
+``dspark_verify_greedy``, ``dspark_verify_ratio``, ``dspark_target_probs``,
+``dspark_cache_plan``, ``dspark_kv_write``, ``dspark_tree_attention``,
+``dspark_logits_process``)
 take torch CUDA tensors, pass their device pointers, sizes and the current
 stream to libdspark.so, and raise on a nonzero return.  Every step of the
 path runs in the library's CUDA kernels; torch only provides device memory
@@ -18,10 +20,11 @@ import torch
 from . import _lib
 
 M = 1 << 24
-F32, BF16 = 0, 1
+F32, BF16, F16 = 0, 1, 2
 ST_OK, ST_NONFINITE, ST_ZERO_MASS, ST_ALLOC_INCONSISTENT = 0, 1, 2, 3
 ST_BAD_TEMPERATURE, ST_BAD_Q, ST_BAD_DRAFT, ST_TIMEOUT, ST_INTERNAL = 4, 5, 6, 7, 8
-ST_BAD_CHECKSUM = 9
+ST_BAD_CHECKSUM, ST_NO_BLOCKS, ST_BAD_LENGTH, ST_BAD_TREE, ST_BAD_PENALTY = 9, 10, 11, 12, 13
+MAX_NODES = 64
 FLAG_AMBIG_ACCEPT, FLAG_NEAR_BOUNDARY, FLAG_DEGENERATE = 1, 2, 4
 SCHEDULE_AUTO, SCHEDULE_ONE_LAUNCH, SCHEDULE_SEPARATE = 0, 1, 2
 PURPOSE_PROPOSAL, PURPOSE_ACCEPT, PURPOSE_RESIDUAL, PURPOSE_BONUS, PURPOSE_MATCH = 0, 1, 2, 3, 4
@@ -35,7 +38,9 @@ __all__ = ["dspark_q_build", "dspark_q_build_sample", "dspark_draft_sample", "ds
            "q_build_sample_sharded", "dspark_spec_step_host",
            "dspark_spec_step_host_staging_bytes", "q_build",
            "draft_sample", "verify_greedy", "verify_ratio", "target_probs", "q_build_sample",
-           "spec_step", "version"]
+           "spec_step", "version", "dspark_cache_plan", "cache_plan", "dspark_kv_write", "kv_write",
+           "dspark_tree_attention", "dspark_tree_attention_workspace_bytes", "tree_attention",
+           "dspark_logits_process", "logits_process"]
 
 
 def version() -> str:
@@ -314,6 +319,163 @@ def dspark_spec_step(draft_logits, target_logits, B, depth, temperature, seed, r
           _i32(r[1]), _i32(r[2]), _i32(r[3]), _i32(workspace), int(schedule), _stream(stream))
 
 
+def _arg(name, t, dtype, shape):
+    """The pointer of an optional contiguous CUDA tensor of this dtype and shape."""
+    if t is None:
+        return None
+    if t.dtype is not dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous tensor of shape %s" % (name, tuple(shape)))
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    return t.data_ptr()
+
+
+_HALF = {torch.bfloat16: BF16, torch.float16: F16}
+
+
+def _cache_args(k_cache, v_cache):
+    """(dtype code, k pointer, v pointer, block / token / head strides) of the two caches
+    [n_blocks, page_size, n_heads, head_dim]: any strides, the same for both, the last one 1."""
+    if k_cache.dtype not in _HALF or v_cache.dtype is not k_cache.dtype:
+        raise TypeError("the caches must both be bfloat16 or float16")
+    st = k_cache.stride()
+    if (k_cache.dim() != 4 or v_cache.shape != k_cache.shape or v_cache.stride() != st
+            or st[3] != 1):
+        raise ValueError("the caches must be [n_blocks, page_size, n_heads, head_dim] of the same "
+                         "shape and strides, contiguous in head_dim")
+    if not (k_cache.is_cuda and v_cache.is_cuda):
+        raise ValueError("expected a CUDA tensor")
+    return _HALF[k_cache.dtype], k_cache.data_ptr(), v_cache.data_ptr(), st[0], st[1], st[2]
+
+
+def dspark_cache_plan(ctx_len, new_len, max_new, page_size, block_table, free_blocks, n_free,
+                      parents, slots, positions, tree_mask, taken, req_status, stream=None):
+    """ctx_len / new_len / req_status int32 [B]; block_table int32 [B, max_blocks] (rows may be
+    strided), updated in place; free_blocks int32 [max_free]; n_free int32 [1] or None; parents
+    int32 [B, max_new] or None; slots int32 [B, max_new]; positions the same or None; tree_mask
+    int64 [B, max_new] (holding the uint64 masks) or None; taken int32 [1]."""
+    i32, B = torch.int32, ctx_len.shape[0]
+    if (block_table.dtype is not i32 or block_table.dim() != 2 or block_table.shape[0] != B
+            or block_table.stride(1) != 1 or not block_table.is_cuda):
+        raise ValueError("block_table must be an int32 CUDA tensor [B, max_blocks]")
+    cells = (B, max_new)
+    _call("dspark_cache_plan", _arg("ctx_len", ctx_len, i32, (B,)),
+          _arg("new_len", new_len, i32, (B,)), B, max_new, page_size, block_table.data_ptr(),
+          block_table.stride(0) if B > 1 else block_table.shape[1], block_table.shape[1],
+          _arg("free_blocks", free_blocks, i32, free_blocks.shape[:1]), free_blocks.shape[0],
+          _arg("n_free", n_free, i32, (1,)), _arg("parents", parents, i32, cells),
+          _arg("slots", slots, i32, cells), _arg("positions", positions, i32, cells),
+          _arg("tree_mask", tree_mask, torch.int64, cells), _arg("taken", taken, i32, (1,)),
+          _arg("req_status", req_status, i32, (B,)), _stream(stream))
+
+
+def dspark_kv_write(k, v, k_cache, v_cache, slots, rows=None, stream=None):
+    """k, v [.., n_heads, head_dim] (leading dimensions uniformly strided; the same shape and
+    strides), float32 or the caches' type; k_cache, v_cache [n_blocks, page_size, n_heads,
+    head_dim]; slots int32 of n_tokens; rows int32 of n_tokens or None (then n_tokens is the
+    number of source tokens)."""
+    code, kp, vp, sb, st, sh = _cache_args(k_cache, v_cache)
+    if k.dim() < 3 or v.shape != k.shape or v.stride() != k.stride() or k.stride(-1) != 1:
+        raise ValueError("k and v must have the same shape [.., n_heads, head_dim] and strides, "
+                         "contiguous in head_dim")
+    if k.shape[-2:] != k_cache.shape[-2:]:
+        raise ValueError("k and v must have the caches' heads and head_dim")
+    if v.dtype is not k.dtype or (k.dtype is not torch.float32 and k.dtype is not k_cache.dtype):
+        raise TypeError("k and v must be float32 or of the caches' type")
+    n, step = 1, k.stride(-3)
+    for i in range(k.dim() - 3, -1, -1):
+        if k.shape[i] > 1 and k.stride(i) != step * n:
+            raise ValueError("the tokens of k and v must be uniformly strided")
+        n *= k.shape[i]
+    if not (k.is_cuda and v.is_cuda):
+        raise ValueError("expected a CUDA tensor")
+    if rows is None and slots.numel() != n:
+        raise ValueError("slots must hold one slot for each token")
+    _call("dspark_kv_write", k.data_ptr(), v.data_ptr(),
+          F32 if k.dtype is torch.float32 else code, step if n > 1 else 0, k.stride(-2), n,
+          k.shape[-2], k.shape[-1], kp, vp, code, sb, st, sh, k_cache.shape[0], k_cache.shape[1],
+          _arg("slots", slots, torch.int32, slots.shape),
+          _arg("rows", rows, torch.int32, slots.shape), slots.numel(), _stream(stream))
+
+
+def dspark_tree_attention_workspace_bytes(B, nodes, n_heads, n_kv_heads, head_dim):
+    return int(_lib.load().dspark_tree_attention_workspace_bytes(B, nodes, n_heads, n_kv_heads,
+                                                                 head_dim))
+
+
+def dspark_tree_attention(q, k_cache, v_cache, block_table, ctx_len, n_nodes, tree_mask, scale,
+                          out, lse, req_status, workspace, stream=None):
+    """q [B, nodes, n_heads, head_dim] (strided, contiguous in head_dim) of the caches' type;
+    block_table int32 [B, max_blocks] (rows may be strided); ctx_len / n_nodes / req_status int32
+    [B]; tree_mask int64 [B, nodes] (holding the uint64 masks) or None; out like q, contiguous;
+    lse float32 [B, nodes, n_heads] or None; workspace: uint8, at least
+    dspark_tree_attention_workspace_bytes bytes."""
+    code, kp, vp, sb, st, sh = _cache_args(k_cache, v_cache)
+    i32 = torch.int32
+    if q.dim() != 4 or q.dtype is not k_cache.dtype or q.stride(3) != 1 or not q.is_cuda:
+        raise ValueError("q must be a CUDA tensor [B, nodes, n_heads, head_dim] of the caches' "
+                         "type, contiguous in head_dim")
+    B, nodes, heads, dim = q.shape
+    if k_cache.shape[3] != dim:
+        raise ValueError("q and the caches must have the same head_dim")
+    if (block_table.dtype is not i32 or block_table.dim() != 2 or block_table.shape[0] != B
+            or block_table.stride(1) != 1 or not block_table.is_cuda):
+        raise ValueError("block_table must be an int32 CUDA tensor [B, max_blocks]")
+    if (workspace.numel() * workspace.element_size()
+            < dspark_tree_attention_workspace_bytes(B, nodes, heads, k_cache.shape[2], dim)):
+        raise ValueError("the workspace is too small")
+    _call("dspark_tree_attention", q.data_ptr(), code, q.stride(0), q.stride(1), q.stride(2), B,
+          nodes, heads, k_cache.shape[2], dim, kp, vp, sb, st, sh, k_cache.shape[0],
+          k_cache.shape[1], block_table.data_ptr(),
+          block_table.stride(0) if B > 1 else block_table.shape[1], block_table.shape[1],
+          _arg("ctx_len", ctx_len, i32, (B,)), _arg("n_nodes", n_nodes, i32, (B,)),
+          _arg("tree_mask", tree_mask, torch.int64, (B, nodes)), scale,
+          _arg("out", out, q.dtype, q.shape),
+          _arg("lse", lse, torch.float32, (B, nodes, heads)),
+          _arg("req_status", req_status, i32, (B,)), _ptr(workspace), _stream(stream))
+
+
+def dspark_logits_process(logits, history, prompt_len, history_len, draft_tokens, row_mask,
+                          repetition, frequency, presence, bias_ids, bias_values, n_bias,
+                          mask_words, mask_rows, out, req_status, stream=None):
+    """logits [B, rows, V] float32 or bfloat16, rows uniformly strided; out the same (or logits
+    itself).  Optional (None): history int32 [B, history_ld] with history_len (and prompt_len)
+    int32 [B]; draft_tokens int32 [B, n_drafts]; row_mask int64 [B, rows] (holding the uint64
+    masks); repetition / frequency / presence float32 [B]; bias_ids int32 and bias_values float32
+    [B, max_bias] with n_bias int32 [B]; mask_words int32 [n_masks, words] (rows may be strided)
+    with mask_rows int32 [B, rows].  req_status int32 [B]."""
+    if logits.dim() != 3 or out.shape != logits.shape or out.dtype is not logits.dtype:
+        raise ValueError("logits must be [B, rows, V], and out of the same shape and type")
+    n, V, ld = _rows(logits)
+    ld_out = _rows(out)[2]
+    B, rows = logits.shape[:2]
+    i32, f32, one, per = torch.int32, torch.float32, (B,), (B, rows)
+    wide = 0 if history is None else history.shape[-1]
+    drafts = 0 if draft_tokens is None else draft_tokens.shape[-1]
+    biases = 0 if bias_ids is None else bias_ids.shape[-1]
+    if mask_words is None:
+        wp, wld, n_masks = None, 0, 0
+    else:
+        n_masks, words = mask_words.shape
+        if (mask_words.dtype not in (i32, torch.uint32) or mask_words.stride(1) != 1
+                or not mask_words.is_cuda or words < (V + 31) // 32):
+            raise ValueError("mask_words must be an int32 CUDA tensor [n_masks, ceil(V / 32)]")
+        wp, wld = mask_words.data_ptr(), mask_words.stride(0) if n_masks > 1 else words
+    _call("dspark_logits_process", _ptr(logits), _dtype_code(logits), ld if n > 1 else V, B, rows,
+          V, _arg("history", history, i32, (B, wide)), wide,
+          _arg("prompt_len", prompt_len, i32, one), _arg("history_len", history_len, i32, one),
+          _arg("draft_tokens", draft_tokens, i32, (B, drafts)), drafts,
+          _arg("row_mask", row_mask, torch.int64, per), _arg("repetition", repetition, f32, one),
+          _arg("frequency", frequency, f32, one), _arg("presence", presence, f32, one),
+          _arg("bias_ids", bias_ids, i32, (B, biases)),
+          _arg("bias_values", bias_values, f32, (B, biases)), biases,
+          _arg("n_bias", n_bias, i32, one), wp, wld, n_masks,
+          _arg("mask_rows", mask_rows, i32, per), _ptr(out), ld_out if n > 1 else V,
+          _arg("req_status", req_status, i32, one), _stream(stream))
+
+
 # --------------------------------------------------- allocating helpers
 def _empty(shape, dtype, device):
     return torch.empty(shape, dtype=dtype, device=device)
@@ -493,3 +655,62 @@ def target_probs(target_logits, want_p=True, stream=None):
     st = _empty((rows,), torch.int32, dev)
     dspark_target_probs(target_logits, p, am, st, stream)
     return p, am, st
+
+
+def cache_plan(ctx_len, new_len, max_new, page_size, block_table, free_blocks, n_free=None,
+               parents=None, stream=None):
+    """Grants the step's blocks and maps its new tokens; returns dict(block_table (the caller's,
+    updated), slots, positions [B, max_new], taken [1], status [B]) and, for max_new <= 64,
+    tree_mask int64 [B, max_new]."""
+    B, dev, i32 = ctx_len.shape[0], ctx_len.device, torch.int32
+    out = {"block_table": block_table, "slots": _empty((B, max_new), i32, dev),
+           "positions": _empty((B, max_new), i32, dev), "taken": _empty((1,), i32, dev),
+           "status": _empty((B,), i32, dev)}
+    if max_new <= MAX_NODES:
+        out["tree_mask"] = _empty((B, max_new), torch.int64, dev)
+    dspark_cache_plan(ctx_len, new_len, max_new, page_size, block_table, free_blocks, n_free,
+                      parents, out["slots"], out["positions"], out.get("tree_mask"), out["taken"],
+                      out["status"], stream)
+    return out
+
+
+def kv_write(k, v, k_cache, v_cache, slots, rows=None, stream=None):
+    """Writes tokens' keys and values into their slots; returns the two caches."""
+    dspark_kv_write(k, v, k_cache, v_cache, slots, rows, stream)
+    return k_cache, v_cache
+
+
+def tree_attention(q, k_cache, v_cache, block_table, ctx_len, n_nodes, tree_mask=None, scale=None,
+                   stream=None):
+    """Attention of the nodes over the cache (scale 1 / sqrt(head_dim) when None); returns (out
+    like q, lse [B, nodes, n_heads], status [B]).  Outputs and workspace are allocated on
+    `stream`."""
+    if stream is not None:  # the workspace is given back when this returns
+        with torch.cuda.stream(stream):
+            return tree_attention(q, k_cache, v_cache, block_table, ctx_len, n_nodes, tree_mask,
+                                  scale)
+    B, nodes, heads, dim = q.shape
+    dev = q.device
+    out = _empty(q.shape, q.dtype, dev)
+    lse = _empty((B, nodes, heads), torch.float32, dev)
+    st = _empty((B,), torch.int32, dev)
+    ws = _empty((dspark_tree_attention_workspace_bytes(B, nodes, heads, k_cache.shape[2], dim),),
+                torch.uint8, dev)
+    dspark_tree_attention(q, k_cache, v_cache, block_table, ctx_len, n_nodes, tree_mask,
+                          dim ** -0.5 if scale is None else scale, out, lse, st, ws, stream)
+    return out, lse, st
+
+
+def logits_process(logits, history=None, prompt_len=None, history_len=None, draft_tokens=None,
+                   row_mask=None, repetition=None, frequency=None, presence=None, bias_ids=None,
+                   bias_values=None, n_bias=None, mask_words=None, mask_rows=None, out=None,
+                   stream=None):
+    """Penalties, biases and grammar masks on logits [B, rows, V]; returns (out (a new tensor when
+    None; logits itself for in place), status [B])."""
+    if out is None:
+        out = _empty(logits.shape, logits.dtype, logits.device)
+    st = _empty((logits.shape[0],), torch.int32, logits.device)
+    dspark_logits_process(logits, history, prompt_len, history_len, draft_tokens, row_mask,
+                          repetition, frequency, presence, bias_ids, bias_values, n_bias,
+                          mask_words, mask_rows, out, st, stream)
+    return out, st

@@ -68,7 +68,39 @@ cudaError_t launch_verify_stats(const uint32_t* flags, int B, uint32_t* stats,
 cudaError_t launch_target_probs(const void* z, int dtype, int64_t ld, int n_rows, int V,
                                 float* p_out, int32_t* argmax, int32_t* status,
                                 cudaStream_t stream);
+cudaError_t launch_cache_plan(const int32_t* ctx, const int32_t* added, int B, int max_new,
+                              int page, int32_t* table, int64_t table_ld, int max_blocks,
+                              const int32_t* free_blocks, int max_free, const int32_t* n_free,
+                              const int32_t* parents, int32_t* slots, int32_t* positions,
+                              uint64_t* mask, int32_t* taken, int32_t* status,
+                              cudaStream_t stream);
+cudaError_t launch_kv_write(const void* k, const void* v, int src_dtype, int64_t src_token,
+                            int64_t src_head, int n_src, int n_heads, int head_dim, void* k_cache,
+                            void* v_cache, int cache_dtype, int64_t block_stride,
+                            int64_t token_stride, int64_t head_stride, int n_blocks, int page,
+                            const int32_t* slots, const int32_t* rows, int n_tokens,
+                            cudaStream_t stream);
+int64_t tree_attention_workspace_bytes(int B, int nodes, int heads, int kv_heads, int head_dim);
+cudaError_t launch_tree_attention(const void* q, int dtype, int64_t q_req, int64_t q_node,
+                                  int64_t q_head, int B, int nodes, int heads, int kv_heads,
+                                  int head_dim, const void* k, const void* v,
+                                  int64_t block_stride, int64_t token_stride, int64_t head_stride,
+                                  int n_blocks, int page, const int32_t* table, int64_t table_ld,
+                                  int max_blocks, const int32_t* ctx, const int32_t* n_nodes,
+                                  const uint64_t* mask, float scale, void* out, float* lse,
+                                  int32_t* status, void* workspace, cudaStream_t stream);
+cudaError_t launch_logits_process(
+    const void* x, int dtype, int64_t ld, int B, int rows, int V, const int32_t* history,
+    int64_t history_ld, const int32_t* prompt_len, const int32_t* history_len,
+    const int32_t* drafts, int n_drafts, const uint64_t* row_mask, const float* repetition,
+    const float* frequency, const float* presence, const int32_t* bias_ids,
+    const float* bias_values, int max_bias, const int32_t* n_bias, const uint32_t* words,
+    int64_t mask_ld, int n_masks, const int32_t* mask_rows, void* out, int64_t ld_out,
+    int32_t* status, cudaStream_t stream);
 #ifdef DSPARK_CHECKED
+cudaError_t dspark_check_collect_cache(uint32_t* out);
+cudaError_t dspark_check_collect_logits(uint32_t* out);
+cudaError_t dspark_check_collect_tree_attention(uint32_t* out);
 cudaError_t dspark_check_collect_chain(uint32_t* out);
 cudaError_t dspark_check_collect_debug(uint32_t* out);
 cudaError_t dspark_check_collect_q_dense(uint32_t* out);
@@ -125,6 +157,8 @@ int dspark_checked_status(uint32_t* out) {
   out[2] = 1u;
   cudaError_t e = cudaSuccess;
   cudaError_t (*collect[])(uint32_t*) = {
+      dspark::dspark_check_collect_cache, dspark::dspark_check_collect_logits,
+      dspark::dspark_check_collect_tree_attention,
       dspark::dspark_check_collect_chain, dspark::dspark_check_collect_debug,
       dspark::dspark_check_collect_q_dense, dspark::dspark_check_collect_q_topk,
       dspark::dspark_check_collect_q_wire, dspark::dspark_check_collect_sample,
@@ -627,6 +661,162 @@ int dspark_target_probs(const void* target_logits, int32_t dtype, int64_t ld, in
   return launch_result(dspark::launch_target_probs(target_logits, dtype, ld, n_rows, V, p_out,
                                                    argmax, row_status,
                                                    static_cast<cudaStream_t>(stream)));
+}
+
+static bool aligned_or_null(const void* p, uintptr_t a) { return !p || aligned(p, a); }
+
+// every address of a paged cache fits 63 bits and its slots 31
+static int check_cache(int32_t n_blocks, int32_t page_size, int32_t cache_dtype,
+                       int64_t block_stride, int64_t token_stride, int64_t head_stride) {
+  if (cache_dtype != DSPARK_BF16 && cache_dtype != DSPARK_F16) return DSPARK_ERR_DTYPE;
+  if (n_blocks < 1 || page_size < 1 || page_size > DSPARK_MAX_PAGE ||
+      (int64_t)n_blocks * page_size > INT32_MAX)
+    return DSPARK_ERR_SIZE;
+  if (block_stride < 0 || token_stride < 0 || head_stride < 0) return DSPARK_ERR_SIZE;
+  if (block_stride % 8 || token_stride % 8 || head_stride % 8) return DSPARK_ERR_ALIGN;
+  return 0;
+}
+
+int dspark_cache_plan(const int32_t* ctx_len, const int32_t* new_len, int32_t B, int32_t max_new,
+                      int32_t page_size, int32_t* block_table, int64_t table_ld,
+                      int32_t max_blocks, const int32_t* free_blocks, int32_t max_free,
+                      const int32_t* n_free, const int32_t* parents, int32_t* slots,
+                      int32_t* positions, uint64_t* tree_mask, int32_t* taken,
+                      int32_t* req_status, void* stream) {
+  const NvtxRange nvtx_range("dspark_cache_plan");
+  if (B < 0 || max_new < 1 || page_size < 1 || page_size > DSPARK_MAX_PAGE || max_blocks < 1 ||
+      table_ld < max_blocks || max_free < 0 || (int64_t)max_blocks * page_size > INT32_MAX ||
+      max_new > (1 << 24) || (int64_t)B * max_new > INT32_MAX)
+    return DSPARK_ERR_SIZE;
+  if ((parents || tree_mask) && max_new > DSPARK_MAX_NODES) return DSPARK_ERR_SIZE;
+  if (B == 0) return 0;
+  if (!ctx_len || !new_len || !block_table || (max_free > 0 && !free_blocks) || !slots || !taken ||
+      !req_status)
+    return DSPARK_ERR_NULL;
+  if (!aligned(ctx_len, 4) || !aligned(new_len, 4) || !aligned(block_table, 4) ||
+      !aligned_or_null(free_blocks, 4) || !aligned_or_null(n_free, 4) ||
+      !aligned_or_null(parents, 4) || !aligned(slots, 4) || !aligned_or_null(positions, 4) ||
+      !aligned_or_null(tree_mask, 8) || !aligned(taken, 4) || !aligned(req_status, 4))
+    return DSPARK_ERR_ALIGN;
+  return launch_result(dspark::launch_cache_plan(
+      ctx_len, new_len, B, max_new, page_size, block_table, table_ld, max_blocks, free_blocks,
+      max_free, n_free, parents, slots, positions, tree_mask, taken, req_status,
+      static_cast<cudaStream_t>(stream)));
+}
+
+int dspark_kv_write(const void* k, const void* v, int32_t src_dtype, int64_t src_token_stride,
+                    int64_t src_head_stride, int32_t n_src, int32_t n_heads, int32_t head_dim,
+                    void* k_cache, void* v_cache, int32_t cache_dtype, int64_t block_stride,
+                    int64_t token_stride, int64_t head_stride, int32_t n_blocks,
+                    int32_t page_size, const int32_t* slots, const int32_t* rows,
+                    int32_t n_tokens, void* stream) {
+  const NvtxRange nvtx_range("dspark_kv_write");
+  if (int e = check_cache(n_blocks, page_size, cache_dtype, block_stride, token_stride,
+                          head_stride))
+    return e;
+  if (src_dtype != DSPARK_F32 && src_dtype != cache_dtype) return DSPARK_ERR_DTYPE;
+  if (n_src < 0 || n_tokens < 0 || n_heads < 1 || n_heads > 65535 || head_dim < 8 ||
+      head_dim > 1024 || head_dim % 8 || src_token_stride < 0 || src_head_stride < 0)
+    return DSPARK_ERR_SIZE;
+  if (n_tokens == 0 || n_src == 0) return 0;
+  if (!k || !v || !k_cache || !v_cache || !slots) return DSPARK_ERR_NULL;
+  const int unit = src_dtype == DSPARK_F32 ? 4 : 8;
+  if (src_token_stride % unit || src_head_stride % unit || !aligned(k, 16) || !aligned(v, 16) ||
+      !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(slots, 4) ||
+      !aligned_or_null(rows, 4))
+    return DSPARK_ERR_ALIGN;
+  return launch_result(dspark::launch_kv_write(
+      k, v, src_dtype, src_token_stride, src_head_stride, n_src, n_heads, head_dim, k_cache,
+      v_cache, cache_dtype, block_stride, token_stride, head_stride, n_blocks, page_size, slots,
+      rows, n_tokens, static_cast<cudaStream_t>(stream)));
+}
+
+static int check_heads(int32_t B, int32_t nodes, int32_t n_heads, int32_t n_kv_heads,
+                       int32_t head_dim) {
+  if (B < 0 || B > 65535 || nodes < 1 || nodes > DSPARK_MAX_NODES || n_kv_heads < 1 ||
+      n_kv_heads > 1024 || n_heads < n_kv_heads || n_heads % n_kv_heads ||
+      n_heads / n_kv_heads > 64 || (head_dim != 64 && head_dim != 128 && head_dim != 256))
+    return DSPARK_ERR_SIZE;
+  return 0;
+}
+
+int64_t dspark_tree_attention_workspace_bytes(int32_t B, int32_t nodes, int32_t n_heads,
+                                              int32_t n_kv_heads, int32_t head_dim) {
+  if (check_heads(B, nodes, n_heads, n_kv_heads, head_dim)) return 0;
+  return dspark::tree_attention_workspace_bytes(B, nodes, n_heads, n_kv_heads, head_dim);
+}
+
+int dspark_tree_attention(const void* q, int32_t dtype, int64_t q_req_stride,
+                          int64_t q_node_stride, int64_t q_head_stride, int32_t B, int32_t nodes,
+                          int32_t n_heads, int32_t n_kv_heads, int32_t head_dim,
+                          const void* k_cache, const void* v_cache, int64_t block_stride,
+                          int64_t token_stride, int64_t head_stride, int32_t n_blocks,
+                          int32_t page_size, const int32_t* block_table, int64_t table_ld,
+                          int32_t max_blocks, const int32_t* ctx_len, const int32_t* n_nodes,
+                          const uint64_t* tree_mask, float scale, void* out, float* lse,
+                          int32_t* req_status, void* workspace, void* stream) {
+  const NvtxRange nvtx_range("dspark_tree_attention");
+  if (int e = check_cache(n_blocks, page_size, dtype, block_stride, token_stride, head_stride))
+    return e;
+  if (int e = check_heads(B, nodes, n_heads, n_kv_heads, head_dim)) return e;
+  if (max_blocks < 1 || table_ld < max_blocks || (int64_t)max_blocks * page_size > INT32_MAX ||
+      q_req_stride < 0 || q_node_stride < 0 || q_head_stride < 0)
+    return DSPARK_ERR_SIZE;
+  if (!(scale > -3.0e38f && scale < 3.0e38f)) return DSPARK_ERR_ARG;
+  if (B == 0) return 0;
+  if (!q || !k_cache || !v_cache || !block_table || !ctx_len || !n_nodes || !out || !req_status ||
+      !workspace)
+    return DSPARK_ERR_NULL;
+  if (q_req_stride % 8 || q_node_stride % 8 || q_head_stride % 8 || !aligned(q, 16) ||
+      !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16) ||
+      !aligned(workspace, 16) || !aligned(block_table, 4) || !aligned(ctx_len, 4) ||
+      !aligned(n_nodes, 4) || !aligned_or_null(tree_mask, 8) || !aligned_or_null(lse, 4) ||
+      !aligned(req_status, 4))
+    return DSPARK_ERR_ALIGN;
+  return launch_result(dspark::launch_tree_attention(
+      q, dtype, q_req_stride, q_node_stride, q_head_stride, B, nodes, n_heads, n_kv_heads,
+      head_dim, k_cache, v_cache, block_stride, token_stride, head_stride, n_blocks, page_size,
+      block_table, table_ld, max_blocks, ctx_len, n_nodes, tree_mask, scale, out, lse, req_status,
+      workspace, static_cast<cudaStream_t>(stream)));
+}
+
+int dspark_logits_process(const void* logits, int32_t dtype, int64_t ld, int32_t B, int32_t rows,
+                          int32_t V, const int32_t* history, int64_t history_ld,
+                          const int32_t* prompt_len, const int32_t* history_len,
+                          const int32_t* draft_tokens, int32_t n_drafts,
+                          const uint64_t* row_mask, const float* repetition,
+                          const float* frequency, const float* presence,
+                          const int32_t* bias_ids, const float* bias_values, int32_t max_bias,
+                          const int32_t* n_bias, const uint32_t* mask_words, int64_t mask_ld,
+                          int32_t n_masks, const int32_t* mask_rows, void* out, int64_t ld_out,
+                          int32_t* req_status, void* stream) {
+  const NvtxRange nvtx_range("dspark_logits_process");
+  if (int e = check_common(dtype, V, ld)) return e;
+  if (B < 0 || B > 65535 || rows < 1 || rows > DSPARK_MAX_NODES || ld_out < V || n_drafts < 0 ||
+      n_drafts > DSPARK_MAX_NODES || max_bias < 0 || max_bias > 65535 || history_ld < 0 ||
+      history_ld >= (1 << 24))
+    return DSPARK_ERR_SIZE;
+  if (mask_words && (mask_ld < (V + 31) / 32 || n_masks < 1)) return DSPARK_ERR_SIZE;
+  if (B == 0) return 0;
+  if (!logits || !out || !req_status || (history && !history_len) ||
+      (n_drafts > 0 && !draft_tokens) || (max_bias > 0 && (!bias_ids || !bias_values)))
+    return DSPARK_ERR_NULL;
+  if (out == logits && ld_out != ld) return DSPARK_ERR_ARG;
+  const int es = esize(dtype);
+  if (!aligned(logits, es) || !aligned(out, es) || !aligned_or_null(history, 4) ||
+      !aligned_or_null(prompt_len, 4) || !aligned_or_null(history_len, 4) ||
+      !aligned_or_null(draft_tokens, 4) || !aligned_or_null(row_mask, 8) ||
+      !aligned_or_null(repetition, 4) || !aligned_or_null(frequency, 4) ||
+      !aligned_or_null(presence, 4) || !aligned_or_null(bias_ids, 4) ||
+      !aligned_or_null(bias_values, 4) || !aligned_or_null(n_bias, 4) ||
+      !aligned_or_null(mask_words, 4) || !aligned_or_null(mask_rows, 4) ||
+      !aligned(req_status, 4))
+    return DSPARK_ERR_ALIGN;
+  return launch_result(dspark::launch_logits_process(
+      logits, dtype, ld, B, rows, V, history, history_ld, prompt_len, history_len, draft_tokens,
+      n_drafts, row_mask, repetition, frequency, presence, bias_ids, bias_values, max_bias, n_bias,
+      mask_words, mask_ld, n_masks, mask_rows, out, ld_out, req_status,
+      static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -63,6 +63,8 @@ extern "C" {
 /* logit element types */
 #define DSPARK_F32 0
 #define DSPARK_BF16 1
+/* element type of caches and attention tensors only (not of logits) */
+#define DSPARK_F16 2
 
 /* Philox purposes (word 2 of the counter), fixed in the ABI */
 #define DSPARK_PURPOSE_PROPOSAL 0u
@@ -91,6 +93,10 @@ extern "C" {
 #define DSPARK_ST_TIMEOUT 7          /* a bounded wait inside a kernel expired */
 #define DSPARK_ST_INTERNAL 8         /* an internal capacity was exceeded    */
 #define DSPARK_ST_BAD_CHECKSUM 9     /* a received q row's checksum differs  */
+#define DSPARK_ST_NO_BLOCKS 10       /* the free list ran out before it      */
+#define DSPARK_ST_BAD_LENGTH 11      /* a length negative or out of range    */
+#define DSPARK_ST_BAD_TREE 12        /* a parent not before its node         */
+#define DSPARK_ST_BAD_PENALTY 13     /* a penalty not finite, repetition <= 0 */
 
 /* verification flags (per request, ratio verification) */
 #define DSPARK_FLAG_AMBIG_ACCEPT 1u  /* |u*q - p| <= 1e-6 * q at a tested row */
@@ -517,6 +523,173 @@ int dspark_q_validate(const float* q, const int32_t* sparse_ids, const int32_t* 
                       int32_t top_k, int32_t n_rows, int32_t V, const int32_t* tokens,
                       const uint64_t* expect, uint32_t* counts_out, int32_t* row_status,
                       void* stream);
+
+/* ------------------------------------------------------------------------
+ * The target pass around a speculative step: a paged key/value cache planned
+ * and written on the GPU, attention of the drafted nodes over it, and the
+ * processing of the target logits that verification reads.  Request b's
+ * nodes are the anchor (node 0, the last committed token) and its drafts:
+ * a chain (node i follows node i-1) or a tree (node i follows parents[i]).
+ *
+ * The cache: n_blocks blocks of page_size token rows each; a token row holds
+ * head_dim elements for each cached head.  Element (block, row, head, d) is
+ * at block*block_stride + row*token_stride + head*head_stride + d, in
+ * elements, the same for the key and the value cache, so a block may be
+ * stored by token or by head and both caches may be views of one tensor.
+ * Slot s is row s % page_size of block s / page_size.  Position i of request
+ * b is in block block_table[b*table_ld + i / page_size].
+ */
+#define DSPARK_MAX_NODES 64          /* nodes of a request's tree            */
+#define DSPARK_MAX_PAGE 1024         /* token rows of a block                */
+
+/*
+ * dspark_cache_plan -- grants blocks to the requests of a step and maps their
+ * new tokens to slots, from the lengths on the device.
+ *
+ * Request b holds ctx_len[b] cached tokens in its first ceil(ctx/page) table
+ * entries and adds new_len[b] <= max_new.  need[b] = the further blocks for
+ * ctx + new tokens; off[b] = the sum of need over the requests before b.
+ * Request b is granted when need[b] == 0 or off[b] + need[b] <= n_free: then
+ * its next need[b] table entries become free_blocks[off[b] ...].  A refused
+ * request (NO_BLOCKS) gets nothing, and so does every later one that needs
+ * a block.  A request with a length out of range (ctx < 0, new outside
+ * [0, max_new], or more blocks than max_blocks) is refused with BAD_LENGTH
+ * and needs none.  taken[0]: the blocks granted, from the front of the list.
+ * The lengths and the list stay the caller's: a second call with the same
+ * arguments gives the same outputs.
+ *
+ * slots[B][max_new]: the slot of new token t of request b (position ctx + t),
+ * -1 from new_len on, for a refused request, and where the table entry is
+ * negative or the slot would pass 2^31 - 1.
+ * positions[B][max_new] (may be NULL): the token's place in the text: ctx
+ * plus its number of ancestors; -1 where there is no token.
+ * parents[B][max_new] (NULL: chains): parents[t] < t, or -1 for a node that
+ * hangs below the cached text alone.  tree_mask[B][max_new] (may be NULL):
+ * bit j set when node j is node t or an ancestor, 0 where there is no node.
+ * Both need max_new <= DSPARK_MAX_NODES (DSPARK_ERR_SIZE otherwise).  A
+ * request with a parent out of range keeps its blocks and slots and gets
+ * BAD_TREE, masks 0 and positions -1.
+ * n_free: device int32, read as at most max_free, the list's length (NULL:
+ * max_free).  Limits: 1 <= page_size <= DSPARK_MAX_PAGE, max_new in [1, 2^24],
+ * max_blocks >= 1, table_ld >= max_blocks, max_blocks*page_size < 2^31,
+ * B*max_new < 2^31, max_free >= 0.
+ */
+int dspark_cache_plan(const int32_t* ctx_len, const int32_t* new_len, int32_t B, int32_t max_new,
+                      int32_t page_size, int32_t* block_table, int64_t table_ld,
+                      int32_t max_blocks, const int32_t* free_blocks, int32_t max_free,
+                      const int32_t* n_free, const int32_t* parents, int32_t* slots,
+                      int32_t* positions, uint64_t* tree_mask, int32_t* taken,
+                      int32_t* req_status, void* stream);
+
+/*
+ * dspark_kv_write -- writes the keys and values of n_tokens tokens into the
+ * cache: slot slots[i] gets source token rows[i] (i when rows is NULL).  A
+ * slot outside [0, n_blocks*page_size) or a source token outside
+ * [0, n_src) is skipped, so -1 marks a token that is not stored.  Two tokens
+ * with one slot leave either one's values there.
+ *
+ * Source element (token, head, d) is at token*src_token_stride +
+ * head*src_head_stride + d, the same for k and v.  cache_dtype DSPARK_BF16
+ * or DSPARK_F16; src_dtype the same, or DSPARK_F32, rounded to the nearest
+ * (ties to even) as it is written.  With rows and slots a committed path's
+ * nodes can be written again to the positions that follow the text.
+ * head_dim a multiple of 8 in [8, 1024]; all four pointers 16-byte aligned,
+ * source and cache strides multiples of 16 bytes (DSPARK_ERR_ALIGN);
+ * n_blocks*page_size < 2^31.
+ */
+int dspark_kv_write(const void* k, const void* v, int32_t src_dtype, int64_t src_token_stride,
+                    int64_t src_head_stride, int32_t n_src, int32_t n_heads, int32_t head_dim,
+                    void* k_cache, void* v_cache, int32_t cache_dtype, int64_t block_stride,
+                    int64_t token_stride, int64_t head_stride, int32_t n_blocks,
+                    int32_t page_size, const int32_t* slots, const int32_t* rows,
+                    int32_t n_tokens, void* stream);
+
+/*
+ * dspark_tree_attention -- attention of each request's nodes over its cached
+ * text and over the nodes that its tree shows.
+ *
+ * Node t of request b sees the positions i < ctx_len[b] and the position
+ * ctx_len[b] + j of every node j < n_nodes[b] whose bit j is set in
+ * tree_mask[b*nodes + t] (NULL: j <= t).  Positions whose table entry is
+ * outside [0, n_blocks) hold no key and are not seen.  Query head h reads
+ * cached head h / (n_heads / n_kv_heads).  With s_i = scale * q . k_i over
+ * the seen positions: out = sum_i exp(s_i - lse) v_i, lse = log sum exp s_i
+ * (natural logarithm).  A row that sees nothing, and every row t >=
+ * n_nodes[b], gets out 0 and lse -infinity.  Keys and values that a row does
+ * not see do not reach it, whatever they hold.
+ * Products take the 16-bit inputs; scores, maxima, sums and accumulators are
+ * fp32; the softmax weights are rounded to the inputs' type for the second
+ * product (the sum is taken before that), and out is rounded once.
+ *
+ * q: element (request, node, head, d) at request*q_req_stride +
+ * node*q_node_stride + head*q_head_stride + d.  out [B][nodes][n_heads]
+ * [head_dim] contiguous, of q's dtype; lse [B][nodes][n_heads] fp32 (may be
+ * NULL).  dtype: DSPARK_BF16 or DSPARK_F16, for q, both caches and out.
+ * req_status[B]: BAD_LENGTH for ctx < 0, n_nodes outside [0, nodes] or more
+ * tokens than max_blocks*page_size (every row of the request gets out 0).
+ * Limits: head_dim 64, 128 or 256; 1 <= nodes <= DSPARK_MAX_NODES; n_heads a
+ * multiple of n_kv_heads, at most 64 times it; q, out, caches and workspace
+ * 16-byte aligned and their strides multiples of 8 elements.  scale finite.
+ * workspace: dspark_tree_attention_workspace_bytes(...) bytes of device
+ * memory owned by the caller, with no content to keep; calls that may
+ * overlap need separate ones.  The result does not depend on the batch's
+ * other requests beyond the order of fp32 sums, and is the same from run to
+ * run.
+ */
+int64_t dspark_tree_attention_workspace_bytes(int32_t B, int32_t nodes, int32_t n_heads,
+                                              int32_t n_kv_heads, int32_t head_dim);
+int dspark_tree_attention(const void* q, int32_t dtype, int64_t q_req_stride,
+                          int64_t q_node_stride, int64_t q_head_stride, int32_t B, int32_t nodes,
+                          int32_t n_heads, int32_t n_kv_heads, int32_t head_dim,
+                          const void* k_cache, const void* v_cache, int64_t block_stride,
+                          int64_t token_stride, int64_t head_stride, int32_t n_blocks,
+                          int32_t page_size, const int32_t* block_table, int64_t table_ld,
+                          int32_t max_blocks, const int32_t* ctx_len, const int32_t* n_nodes,
+                          const uint64_t* tree_mask, float scale, void* out, float* lse,
+                          int32_t* req_status, void* workspace, void* stream);
+
+/*
+ * dspark_logits_process -- penalties for repeated tokens, biases and grammar
+ * masks on the logits of B requests, `rows` rows each: the processors whose
+ * result dspark_q_build and the verifiers take as their logits.
+ *
+ * Row (b, r) at logits + (b*rows + r)*ld, written to out + (b*rows + r)*
+ * ld_out with the same dtype; out may be logits itself (with ld_out == ld),
+ * and must not overlap it otherwise.  Its text is history[b][0 ..
+ * history_len[b]) -- the first prompt_len[b] tokens the prompt, the rest
+ * generated -- and the drafts that come before the row: draft j when bit j of
+ * row_mask[b*rows + r] is set (NULL: j < r, the drafts that target row r
+ * follows).  Ids outside [0, V) count as nothing.
+ * For token v with c occurrences in the generated text and those drafts:
+ *   y = x;
+ *   if v is in the text or those drafts:  y = x > 0 ? x / R : x * R;
+ *   y -= F*c;  y -= P if c > 0;
+ *   y += every bias of b whose id is v, in list order;
+ *   y = -infinity if the row's mask has v's bit 0 (whatever x held).
+ * Each step is one fp32 rounding; the result is rounded once to the dtype.
+ * R, F, P: repetition[b], frequency[b], presence[b] (NULL: 1, 0, 0).  A
+ * request whose R is not finite or not > 0, or whose F or P is not finite,
+ * is refused: BAD_PENALTY, and all its rows become -infinity.
+ * bias_ids / bias_values [B][max_bias], the first n_bias[b] of them (NULL:
+ * max_bias; max_bias 0: none).  mask_words [n_masks][mask_ld] uint32, bit v % 32 of
+ * word v / 32 for token v; mask_rows[B*rows] picks each row's mask, an index
+ * outside [0, n_masks) (such as -1): no mask; NULL: mask b*rows + r.
+ * mask_words NULL: no masks.  history, history_len NULL: no text;
+ * prompt_len NULL: all of it generated.  Lengths are read as at least 0 and
+ * at most history_ld, max_bias; prompt_len as at most history_len.
+ * req_status[B].  Limits: rows in [1, DSPARK_MAX_NODES], n_drafts in
+ * [0, DSPARK_MAX_NODES], 0 <= history_ld < 2^24, 0 <= max_bias <= 65535.
+ */
+int dspark_logits_process(const void* logits, int32_t dtype, int64_t ld, int32_t B, int32_t rows,
+                          int32_t V, const int32_t* history, int64_t history_ld,
+                          const int32_t* prompt_len, const int32_t* history_len,
+                          const int32_t* draft_tokens, int32_t n_drafts,
+                          const uint64_t* row_mask, const float* repetition,
+                          const float* frequency, const float* presence,
+                          const int32_t* bias_ids, const float* bias_values, int32_t max_bias,
+                          const int32_t* n_bias, const uint32_t* mask_words, int64_t mask_ld,
+                          int32_t n_masks, const int32_t* mask_rows, void* out, int64_t ld_out,
+                          int32_t* req_status, void* stream);
 
 /* Library build identifier (static string, host). */
 const char* dspark_version(void);
