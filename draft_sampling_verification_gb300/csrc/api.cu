@@ -100,7 +100,6 @@ cudaError_t launch_logits_process(
 #ifdef DSPARK_CHECKED
 cudaError_t dspark_check_collect_cache(uint32_t* out);
 cudaError_t dspark_check_collect_logits(uint32_t* out);
-cudaError_t dspark_check_collect_tree_attention(uint32_t* out);
 cudaError_t dspark_check_collect_chain(uint32_t* out);
 cudaError_t dspark_check_collect_debug(uint32_t* out);
 cudaError_t dspark_check_collect_q_dense(uint32_t* out);
@@ -158,7 +157,6 @@ int dspark_checked_status(uint32_t* out) {
   cudaError_t e = cudaSuccess;
   cudaError_t (*collect[])(uint32_t*) = {
       dspark::dspark_check_collect_cache, dspark::dspark_check_collect_logits,
-      dspark::dspark_check_collect_tree_attention,
       dspark::dspark_check_collect_chain, dspark::dspark_check_collect_debug,
       dspark::dspark_check_collect_q_dense, dspark::dspark_check_collect_q_topk,
       dspark::dspark_check_collect_q_wire, dspark::dspark_check_collect_sample,
@@ -685,7 +683,8 @@ int dspark_cache_plan(const int32_t* ctx_len, const int32_t* new_len, int32_t B,
                       int32_t* req_status, void* stream) {
   const NvtxRange nvtx_range("dspark_cache_plan");
   if (B < 0 || max_new < 1 || page_size < 1 || page_size > DSPARK_MAX_PAGE || max_blocks < 1 ||
-      table_ld < max_blocks || max_free < 0 || (int64_t)max_blocks * page_size > INT32_MAX ||
+      table_ld < max_blocks || max_free < 0 ||
+      (int64_t)max_blocks * page_size > DSPARK_MAX_TOKENS ||
       max_new > (1 << 24) || (int64_t)B * max_new > INT32_MAX)
     return DSPARK_ERR_SIZE;
   if ((parents || tree_mask) && max_new > DSPARK_MAX_NODES) return DSPARK_ERR_SIZE;
@@ -759,7 +758,8 @@ int dspark_tree_attention(const void* q, int32_t dtype, int64_t q_req_stride,
   if (int e = check_cache(n_blocks, page_size, dtype, block_stride, token_stride, head_stride))
     return e;
   if (int e = check_heads(B, nodes, n_heads, n_kv_heads, head_dim)) return e;
-  if (max_blocks < 1 || table_ld < max_blocks || (int64_t)max_blocks * page_size > INT32_MAX ||
+  if (max_blocks < 1 || table_ld < max_blocks ||
+      (int64_t)max_blocks * page_size > DSPARK_MAX_TOKENS ||
       q_req_stride < 0 || q_node_stride < 0 || q_head_stride < 0)
     return DSPARK_ERR_SIZE;
   if (!(scale > -3.0e38f && scale < 3.0e38f)) return DSPARK_ERR_ARG;

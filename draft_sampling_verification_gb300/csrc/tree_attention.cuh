@@ -1,0 +1,724 @@
+// tree_attention.cuh -- the kernels of dspark_tree_attention, shared by the
+// translation units that instantiate them (one per head_dim).
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+
+namespace dspark {
+namespace attn {
+
+struct Params {
+  const void* q;
+  int64_t q_req, q_node, q_head;  // elements, as all strides
+  int B, nodes, heads, kv_heads, group;  // group: query heads per cached head
+  const void* k;
+  const void* v;
+  int64_t block_stride, token_stride, head_stride;
+  int n_blocks, page;
+  const int32_t* table;
+  int64_t table_ld;
+  int max_blocks;
+  const int32_t* ctx;
+  const int32_t* n_nodes;
+  const uint64_t* mask;
+  float scale2;  // scale * log2(e): scores are kept in units of log2
+  void* out;
+  float* lse;
+  int32_t* status;
+  char* workspace;
+  int row_tiles;  // items of one (request, cached head): ceil(nodes * group / rows per CTA)
+};
+
+// ------------------------------------------------------------ PTX wrappers
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(on ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int kLeft>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+// the 8 x 8 matrix of 16-bit elements that a warp holds, transposed
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+template <typename T>
+struct Half;
+template <>
+struct Half<__nv_bfloat16> {
+  static constexpr uint32_t kExponent = 0x7F80u;
+  static __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                             uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, "
+        "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  }
+  static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  static __device__ __forceinline__ float widen(uint32_t h) { return __uint_as_float(h << 16); }
+};
+template <>
+struct Half<__half> {
+  static constexpr uint32_t kExponent = 0x7C00u;
+  static __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                             uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
+        "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  }
+  static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  static __device__ __forceinline__ float widen(uint32_t h) {
+    return __half2float(__ushort_as_half((unsigned short)h));
+  }
+};
+
+// whether either 16-bit half is an infinity or a NaN
+template <typename T>
+__device__ __forceinline__ bool any_special(uint32_t w) {
+  constexpr uint32_t e = Half<T>::kExponent;
+  return (w & e) == e || ((w >> 16) & e) == e;
+}
+// the halves that are neither; 0 in place of the others
+template <typename T>
+__device__ __forceinline__ uint32_t without_special(uint32_t w) {
+  constexpr uint32_t e = Half<T>::kExponent;
+  if ((w & e) == e) w &= 0xFFFF0000u;
+  if (((w >> 16) & e) == e) w &= 0x0000FFFFu;
+  return w;
+}
+
+// --------------------------------------------------------- division of work
+// Positions are taken in tiles.  The tiles of all (request, cached head, row
+// tile) items in a row form one axis, cut into equal ranges, one per CTA, so
+// that every SM reads the same number of bytes whatever the lengths.  An item
+// that lies inside one range is finished by its CTA; the others leave partial
+// rows in the workspace for the joining kernel.  Each item has at least one
+// tile (a request without tokens still writes its zero rows).
+constexpr int kMaxCtas = 320;
+
+struct Start {  // where a CTA's range begins
+  int b, item, tile, tiles;
+};
+
+struct Workspace {
+  int64_t* total;
+  Start* start;   // [kMaxCtas]
+  float2* stats;  // [2 * kMaxCtas][rows]: the reference of the exponents, the sum
+  float* rows;    // [2 * kMaxCtas][rows][dim]
+};
+
+__host__ __device__ inline int64_t workspace_bytes(int rows, int dim) {
+  return 16 + (int64_t)kMaxCtas * sizeof(Start) +
+         2ll * kMaxCtas * rows * (sizeof(float2) + (int64_t)dim * sizeof(float));
+}
+
+__device__ __forceinline__ Workspace carve(char* w, int rows) {
+  Workspace s;
+  s.total = reinterpret_cast<int64_t*>(w);
+  s.start = reinterpret_cast<Start*>(w + 16);
+  s.stats = reinterpret_cast<float2*>(w + 16 + kMaxCtas * sizeof(Start));
+  s.rows = reinterpret_cast<float*>(s.stats + 2 * kMaxCtas * rows);
+  return s;
+}
+
+// a request's tokens: the cached text, and all with its nodes (0 when refused)
+struct Lengths {
+  int ctx, len, nodes;
+  bool bad;
+};
+
+__device__ __forceinline__ Lengths request_lengths(const Params& p, int b) {
+  Lengths r;
+  r.ctx = p.ctx[b];
+  r.nodes = p.n_nodes[b];
+  r.bad = r.ctx < 0 || r.nodes < 0 || r.nodes > p.nodes ||
+          (int64_t)r.ctx + r.nodes > (int64_t)p.max_blocks * p.page;
+  if (r.bad) r.ctx = r.nodes = 0;
+  r.len = r.nodes > 0 ? r.ctx + r.nodes : 0;  // no row: nothing to read
+  return r;
+}
+
+__device__ __forceinline__ int request_tiles(const Params& p, int b, int tile) {
+  const int len = request_lengths(p, b).len;
+  return len > 0 ? (len - 1) / tile + 1 : 1;
+}
+
+// the CTA whose range holds tile x of `total`, and the first tile of CTA c
+__device__ __forceinline__ int owner_of(int64_t x, int64_t total, int ctas) {
+  return (int)(((x + 1) * ctas - 1) / total);
+}
+__device__ __forceinline__ int64_t first_of(int c, int64_t total, int ctas) {
+  return (int64_t)c * total / ctas;
+}
+
+// ------------------------------------------------------ the streaming kernel
+// For up to 64 rows of an item.  A row is one query head of one node; all
+// rows of an item read the same keys, so they stand side by side.
+//
+// Products: the transposed forms S^T = K Q^T and O^T = V^T P^T on m16n8k16
+// (16 keys or 16 dims by 8 rows), so the rows are padded to eights only, K
+// and V are the first operand straight from shared memory (ldmatrix; V
+// through its transposing form), Q stays in registers as the second, and the
+// weights go from the accumulators of S^T to the second operand of the next
+// product by one 8 x 8 transpose in registers.
+//
+// Softmax: each row keeps a reference r (of which the exponents are taken
+// off), a sum and the accumulators.  A step whose scores all stay below
+// r + 8 leaves r alone, so most steps need no maximum across the warp and no
+// rescaling: the weights stay below 2^8 and the sums far inside fp32.
+//
+// Warps: KW groups of MW warps.  A group takes every KW-th step of 16 keys,
+// with its own ring of asynchronous copies and its own softmax state: no
+// barrier in the loop but the pair's own.  The MW warps of a group share its
+// keys and split the rows.  Groups are joined in shared memory at the end of
+// an item.
+//
+// Bound by HBM: 16 steps of 8 KB are in flight per SM at head_dim 128.
+constexpr int kThreads = 128;
+constexpr int kWarps = kThreads / 32;
+constexpr int kKeys = 16;
+constexpr float kSlack = 8.0f;
+
+template <int D, int N8, int MW>
+struct Shape {
+  static constexpr int kGroups = kWarps / MW;
+  static constexpr int kTile = kKeys * kGroups;       // positions a CTA takes at once
+  static constexpr int kRows = 8 * N8 * MW;
+  static constexpr int kRowBytes = D * 2;
+  static constexpr int kStageBytes = 2 * kKeys * kRowBytes;
+  static constexpr int kSmem = D == 256 ? 196608 : 98304;  // one or two CTAs per SM
+  static constexpr int kStages = kSmem / (kGroups * kStageBytes);
+  static constexpr int kPitch = D + 4;                // floats of a joined row: no bank twice
+  static_assert(kGroups * kRows * kPitch * 4 <= kSmem, "the joined rows fit the copies' memory");
+};
+
+template <typename T, int D, int N8, int MW>
+__global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2)
+    tree_attention_kernel(const __grid_constant__ Params p) {
+  using S = Shape<D, N8, MW>;
+  using H = Half<T>;
+  constexpr int KW = S::kGroups, kStages = S::kStages, kRows = S::kRows;
+  constexpr int kChunks = D / 8;  // 16-byte pieces of a row
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ uint64_t s_scan[32];
+  __shared__ Start s_start;
+  __shared__ uint32_t s_valid[KW][kStages];
+  __shared__ float2 s_stat[KW][kRows];
+  __shared__ uint64_t s_mask[kRows];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int mw = warp % MW, kw = warp / MW;
+  const int items = p.kv_heads * p.row_tiles;
+
+  // this CTA's range
+  const int per = (p.B + kThreads - 1) / kThreads;
+  const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
+  uint64_t sum = 0, total_u;
+  for (int b = b0; b < b1; ++b) sum += (uint64_t)request_tiles(p, b, S::kTile) * items;
+  const uint64_t upto = block_inclusive_scan_u64(sum, s_scan, &total_u);
+  const int64_t total = (int64_t)total_u;
+  const int ctas = (int)min((int64_t)gridDim.x, total);
+  if ((int)blockIdx.x >= ctas) return;
+  const int64_t x0 = first_of(blockIdx.x, total, ctas), x1 = first_of(blockIdx.x + 1, total, ctas);
+  {
+    int64_t at = (int64_t)(upto - sum);
+    if (x0 >= at && x0 < (int64_t)upto) {
+      for (int b = b0; b < b1; ++b) {
+        const int tiles = request_tiles(p, b, S::kTile);
+        const int64_t end = at + (int64_t)tiles * items;
+        if (x0 < end) {
+          s_start = {b, (int)((x0 - at) / tiles), (int)((x0 - at) % tiles), tiles};
+          break;
+        }
+        at = end;
+      }
+    }
+  }
+  __syncthreads();
+  Start cur = s_start;
+  const Workspace ws = carve(p.workspace, kRows);
+  if (tid == 0) {
+    ws.start[blockIdx.x] = cur;
+    if (blockIdx.x == 0) *ws.total = total;
+  }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  const T* kc = static_cast<const T*>(p.k);
+  const T* vc = static_cast<const T*>(p.v);
+  const bool whole = p.page % kKeys == 0;  // a step lies in one block
+  const uint32_t ring = smem_u32(smem) + kw * kStages * S::kStageBytes;
+  int64_t left = x1 - x0;
+
+  while (left > 0) {
+    const int tiles = (int)min(left, (int64_t)(cur.tiles - cur.tile));
+    const Lengths len = request_lengths(p, cur.b);
+    const int kvh = cur.item / p.row_tiles, r0 = (cur.item % p.row_tiles) * kRows;
+    const int32_t* table = p.table + cur.b * p.table_ld;
+    const int live = len.nodes * p.group;  // rows below this one have a node
+
+    if (tid == 0 && cur.item == 0 && cur.tile == 0)
+      p.status[cur.b] = len.bad ? DSPARK_ST_BAD_LENGTH : DSPARK_ST_OK;
+
+    // ---- copies: 16 positions of this group into a stage of its ring
+    const int first = cur.tile * S::kTile + kw * kKeys;  // this group's first position
+    const int64_t head_off = kvh * p.head_stride;
+    auto entry_of = [&](int step) -> int {  // the block of this lane's position in a step
+      const int pos = first + step * S::kTile + (whole ? 0 : (lane & 15));
+      return step < tiles && pos < len.len ? __ldg(table + pos / p.page) : -1;
+    };
+    auto issue = [&](int step, int block) {
+      const int pos = first + step * S::kTile;
+      const int mine = pos + (whole ? 0 : (lane & 15));
+      const bool held = block >= 0 && block < p.n_blocks && mine < len.len;
+      const int64_t off = held ? block * p.block_stride +
+                                     (int64_t)(mine - mine / p.page * p.page) * p.token_stride
+                               : 0;
+      uint32_t valid = __ballot_sync(0xffffffffu, held) & 0xFFFFu;
+      if (whole) valid = held ? (len.len - pos >= 16 ? 0xFFFFu : (1u << (len.len - pos)) - 1u) : 0u;
+      const int stage = step % kStages;
+      if (lane == 0 && mw == 0) s_valid[kw][stage] = valid;
+      const uint32_t to = ring + stage * S::kStageBytes;
+#pragma unroll
+      for (int i = 0; i < kKeys * kChunks / (32 * MW); ++i) {
+        const int at = (i * MW + mw) * 32 + lane;
+        const int row = at / kChunks, chunk = at % kChunks;
+        const bool on = (valid >> row) & 1u;
+        const int64_t row_off = whole ? off + row * p.token_stride
+                                      : __shfl_sync(0xffffffffu, (long long)off, row);
+        const int64_t from = on ? row_off + head_off + chunk * 8 : 0;
+        const uint32_t d = to + row * S::kRowBytes + ((chunk ^ (row & 7)) << 4);
+        cp_async16(d, kc + from, on);
+        cp_async16(d + kKeys * S::kRowBytes, vc + from, on);
+      }
+    };
+    int ahead = entry_of(0);
+#pragma unroll
+    for (int s = 0; s < kStages - 1; ++s) {
+      const int block = ahead;
+      ahead = entry_of(s + 1);
+      if (s < tiles) issue(s, block);
+      cp_async_commit();
+    }
+
+    // ---- the rows: masks, and Q as the second operand's fragments
+    for (int r = tid; r < kRows; r += kThreads) {
+      const int row = r0 + r, node = row / p.group;
+      uint64_t m = 0;
+      if (row < live) {
+        m = p.mask ? p.mask[(int64_t)cur.b * p.nodes + node] : ~0ull >> (63 - node);
+      }
+      s_mask[r] = m;
+    }
+    uint32_t q[D / 16][N8][2];
+#pragma unroll
+    for (int n = 0; n < N8; ++n) {
+      const int row = r0 + (mw * N8 + n) * 8 + (lane >> 2);
+      const int node = row / p.group, h = kvh * p.group + row - node * p.group;
+      const T* from = static_cast<const T*>(p.q) + cur.b * p.q_req + node * p.q_node +
+                      h * p.q_head + (lane & 3) * 2;
+#pragma unroll
+      for (int kt = 0; kt < D / 16; ++kt) {
+        q[kt][n][0] = row < live ? __ldg(reinterpret_cast<const uint32_t*>(from + kt * 16)) : 0u;
+        q[kt][n][1] = row < live ? __ldg(reinterpret_cast<const uint32_t*>(from + kt * 16 + 8)) : 0u;
+      }
+    }
+    float o[D / 16][N8][4];
+    float ref[N8][2], l[N8][2];
+#pragma unroll
+    for (int n = 0; n < N8; ++n) {
+      ref[n][0] = ref[n][1] = -INFINITY;
+      l[n][0] = l[n][1] = 0.0f;
+#pragma unroll
+      for (int mt = 0; mt < D / 16; ++mt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[mt][n][e] = 0.0f;
+    }
+    __syncthreads();
+
+    for (int step = 0; step < tiles; ++step) {
+      cp_async_wait<kStages - 2>();
+      if constexpr (MW == 1)
+        __syncwarp();
+      else
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + kw), "n"(32 * MW) : "memory");
+      if (step + kStages - 1 < tiles) {
+        const int block = ahead;
+        ahead = entry_of(step + kStages);
+        issue(step + kStages - 1, block);
+      }
+      cp_async_commit();
+      const int stage = step % kStages;
+      const uint32_t valid = s_valid[kw][stage];
+      if (valid == 0u) continue;
+      const uint32_t kbase = ring + stage * S::kStageBytes;
+      const uint32_t vbase = kbase + kKeys * S::kRowBytes;
+      const int pos = first + step * S::kTile;
+
+      float s[N8][4];
+#pragma unroll
+      for (int n = 0; n < N8; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.0f;
+      const int krow = (lane & 7) + ((lane >> 3) & 1) * 8;
+#pragma unroll
+      for (int kt = 0; kt < D / 16; ++kt) {
+        uint32_t a[4];
+        const int chunk = 2 * kt + (lane >> 4);
+        ldmatrix4(a, kbase + krow * S::kRowBytes + ((chunk ^ (krow & 7)) << 4));
+#pragma unroll
+        for (int n = 0; n < N8; ++n) H::mma(s[n], a, q[kt][n][0], q[kt][n][1]);
+      }
+
+      // element e of s[n]: key lane / 4 + 8 (e / 2), row 8 n + 2 (lane % 4) + e % 2
+      const bool nodes_here = pos + kKeys > len.ctx;
+      bool special = false;
+      if (nodes_here || valid != 0xFFFFu) {
+#pragma unroll
+        for (int n = 0; n < N8; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int key = (lane >> 2) + (e >> 1) * 8;
+            bool on = (valid >> key) & 1u;
+            const int node = pos + key - len.ctx;
+            if (on && node >= 0)
+              on = (s_mask[(mw * N8 + n) * 8 + (lane & 3) * 2 + (e & 1)] >> node) & 1ull;
+            s[n][e] = on ? s[n][e] * p.scale2 : -INFINITY;
+          }
+        if (nodes_here) {  // values that some rows see and others do not: any not finite?
+          for (int i = lane; i < kKeys * kChunks; i += 32) {
+            uint32_t w[4];
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                         : "r"(vbase + i * 16));
+            special |= any_special<T>(w[0]) || any_special<T>(w[1]) || any_special<T>(w[2]) ||
+                       any_special<T>(w[3]);
+          }
+          special = __any_sync(0xffffffffu, special);
+        }
+      } else {
+#pragma unroll
+        for (int n = 0; n < N8; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[n][e] *= p.scale2;
+      }
+
+      bool over = false;
+#pragma unroll
+      for (int n = 0; n < N8; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) over |= s[n][e] > ref[n][e & 1] + kSlack;
+      if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+        for (int n = 0; n < N8; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float top = fmaxf(s[n][e], s[n][e + 2]);
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+            top = fmaxf(top, ref[n][e]);
+            const float scale = top == -INFINITY ? 1.0f : exp2_approx(ref[n][e] - top);
+            ref[n][e] = top;
+            l[n][e] *= scale;
+#pragma unroll
+            for (int mt = 0; mt < D / 16; ++mt) {
+              o[mt][n][e] *= scale;
+              o[mt][n][e + 2] *= scale;
+            }
+          }
+      }
+
+      uint32_t w[N8][2];
+      float pr[N8][4];
+#pragma unroll
+      for (int n = 0; n < N8; ++n) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float r = ref[n][e & 1];
+          pr[n][e] = exp2_approx(s[n][e] - (r == -INFINITY ? 0.0f : r));
+          l[n][e & 1] += pr[n][e];
+        }
+        w[n][0] = transpose8x8(H::pack(pr[n][0], pr[n][1]));
+        w[n][1] = transpose8x8(H::pack(pr[n][2], pr[n][3]));
+      }
+
+      const int vrow = (lane & 7) + (lane >> 4) * 8;
+#pragma unroll
+      for (int mt = 0; mt < D / 16; ++mt) {
+        uint32_t a[4];
+        const int chunk = 2 * mt + ((lane >> 3) & 1);
+        ldmatrix4_trans(a, vbase + vrow * S::kRowBytes + ((chunk ^ (vrow & 7)) << 4));
+        if (special) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) a[i] = without_special<T>(a[i]);
+        }
+#pragma unroll
+        for (int n = 0; n < N8; ++n) H::mma(o[mt][n], a, w[n][0], w[n][1]);
+      }
+      if (special) {
+        // infinities and NaN, left out above, reach the rows that see their key only
+#pragma unroll 1
+        for (int key = 0; key < kKeys; ++key) {
+          const int from = (key & 7) * 4 + (lane & 3);
+#pragma unroll
+          for (int n = 0; n < N8; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float score = __shfl_sync(0xffffffffu, key < 8 ? s[n][e] : s[n][e + 2], from);
+              const float weight =
+                  __shfl_sync(0xffffffffu, key < 8 ? pr[n][e] : pr[n][e + 2], from);
+#pragma unroll
+              for (int mt = 0; mt < D / 16; ++mt)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  const int d = mt * 16 + h * 8 + (lane >> 2);
+                  unsigned short bits;
+                  asm volatile("ld.shared.u16 %0, [%1];"
+                               : "=h"(bits)
+                               : "r"(vbase + key * S::kRowBytes +
+                                     (((d >> 3) ^ (key & 7)) << 4) + (d & 7) * 2));
+                  if ((bits & H::kExponent) == H::kExponent && score != -INFINITY)
+                    o[mt][n][e + 2 * h] += weight * H::widen(bits);
+                }
+            }
+        }
+      }
+    }
+
+    // ---- join the groups
+    cp_async_wait<0>();
+    __syncthreads();
+    float* joined = reinterpret_cast<float*>(smem);  // [KW][kRows][kPitch]
+#pragma unroll
+    for (int n = 0; n < N8; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float sum_l = l[n][e];
+        sum_l += __shfl_xor_sync(0xffffffffu, sum_l, 4);
+        sum_l += __shfl_xor_sync(0xffffffffu, sum_l, 8);
+        sum_l += __shfl_xor_sync(0xffffffffu, sum_l, 16);
+        const int r = (mw * N8 + n) * 8 + (lane & 3) * 2 + e;
+        if (lane < 4) s_stat[kw][r] = make_float2(ref[n][e], sum_l);
+        float* row = joined + (kw * kRows + r) * S::kPitch + (lane >> 2);
+#pragma unroll
+        for (int mt = 0; mt < D / 16; ++mt) {
+          row[mt * 16] = o[mt][n][e];
+          row[mt * 16 + 8] = o[mt][n][e + 2];
+        }
+      }
+    __syncthreads();
+    const bool full = tiles == cur.tiles;
+    const int64_t slot = 2ll * blockIdx.x + (cur.tile == 0 ? 1 : 0);
+    for (int i = tid; i < kRows * (D / 4); i += kThreads) {
+      const int r = i / (D / 4), d = (i % (D / 4)) * 4;
+      const int row = r0 + r;
+      if (row >= p.nodes * p.group) break;
+      float top = -INFINITY;
+#pragma unroll
+      for (int g = 0; g < KW; ++g) top = fmaxf(top, s_stat[g][r].x);
+      const float safe = top == -INFINITY ? 0.0f : top;
+      float all = 0.0f;
+      float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+      for (int g = 0; g < KW; ++g) {
+        const float2 st = s_stat[g][r];
+        const float f = exp2_approx(st.x - safe);
+        const float4 v = *reinterpret_cast<const float4*>(joined + (g * kRows + r) * S::kPitch + d);
+        all += st.y * f;
+        a.x += v.x * f;
+        a.y += v.y * f;
+        a.z += v.z * f;
+        a.w += v.w * f;
+      }
+      if (row >= live) {  // a row of no node: its zero query saw the text all the same
+        top = -INFINITY;
+        all = a.x = a.y = a.z = a.w = 0.0f;
+      }
+      if (full) {
+        const int node = row / p.group, h = kvh * p.group + row - node * p.group;
+        const int64_t to = ((int64_t)cur.b * p.nodes + node) * p.heads + h;
+        const float inv = all == 0.0f ? 0.0f : 1.0f / all;
+        uint2 w;
+        w.x = H::pack(a.x * inv, a.y * inv);
+        w.y = H::pack(a.z * inv, a.w * inv);
+        *reinterpret_cast<uint2*>(static_cast<T*>(p.out) + to * D + d) = w;
+        if (d == 0 && p.lse)
+          p.lse[to] = all == 0.0f ? -INFINITY : (top + log2f(all)) * 0.6931471805599453f;
+      } else {
+        *reinterpret_cast<float4*>(ws.rows + (slot * kRows + r) * D + d) = a;
+        if (d == 0) ws.stats[slot * kRows + r] = make_float2(top, all);
+      }
+    }
+    __syncthreads();
+
+    left -= tiles;
+    cur.tile = 0;
+    if (++cur.item == items) {
+      cur.item = 0;
+      ++cur.b;
+    }
+    if (left > 0) cur.tiles = request_tiles(p, cur.b, S::kTile);
+  }
+}
+
+// ------------------------------------------------------- the joining kernel
+// CTA (i, y): if the boundary before CTA i's range is the first one inside
+// its item, the item's partial rows [8 y, 8 y + 8) are joined, a warp per
+// row, in the order of the ranges.
+constexpr int kJoinThreads = 256;
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kJoinThreads)
+    tree_attention_join_kernel(const __grid_constant__ Params p, int rows, int grid) {
+  using H = Half<T>;
+  constexpr int kPer = D / 32;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const Workspace ws = carve(p.workspace, rows);
+  const int i = blockIdx.x + 1;
+  const int64_t total = *ws.total;
+  const int ctas = (int)min((int64_t)grid, total);
+  if (i >= ctas) return;
+  const Start at = ws.start[i];
+  if (at.tile == 0) return;
+  const int64_t begin = first_of(i, total, ctas) - at.tile;
+  const int c0 = owner_of(begin, total, ctas);
+  if (c0 != i - 1) return;
+  const int c1 = owner_of(begin + at.tiles - 1, total, ctas);
+  const int lane = threadIdx.x & 31;
+  const int r = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5);
+  const int kvh = at.item / p.row_tiles, row = (at.item % p.row_tiles) * rows + r;
+  if (r >= rows || row >= p.nodes * p.group) return;
+
+  float top = -INFINITY;
+  for (int c = c0 + lane; c <= c1; c += 32)
+    top = fmaxf(top, ws.stats[(int64_t)(c == c0 ? 2 * c + 1 : 2 * c) * rows + r].x);
+  top = warp_reduce(top, OpMaxF());
+  const float safe = top == -INFINITY ? 0.0f : top;
+  float all = 0.0f, a[kPer];
+#pragma unroll
+  for (int d = 0; d < kPer; ++d) a[d] = 0.0f;
+#pragma unroll 4
+  for (int c = c0; c <= c1; ++c) {
+    const int64_t slot = c == c0 ? 2 * c + 1 : 2 * c;
+    const float2 st = ws.stats[slot * rows + r];
+    const float f = exp2_approx(st.x - safe);
+    const float* v = ws.rows + (slot * rows + r) * D + lane * kPer;
+    float x[kPer];
+    if constexpr (kPer == 2) {
+      *reinterpret_cast<float2*>(x) = *reinterpret_cast<const float2*>(v);
+    } else {
+#pragma unroll
+      for (int d = 0; d < kPer; d += 4)
+        *reinterpret_cast<float4*>(x + d) = *reinterpret_cast<const float4*>(v + d);
+    }
+    all += st.y * f;
+#pragma unroll
+    for (int d = 0; d < kPer; ++d) a[d] += x[d] * f;
+  }
+  const int node = row / p.group, h = kvh * p.group + row - node * p.group;
+  const int64_t to = ((int64_t)at.b * p.nodes + node) * p.heads + h;
+  const float inv = all == 0.0f ? 0.0f : 1.0f / all;
+  uint32_t w[kPer / 2];
+#pragma unroll
+  for (int d = 0; d < kPer; d += 2) w[d / 2] = H::pack(a[d] * inv, a[d + 1] * inv);
+  uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<T*>(p.out) + to * D) + lane * (kPer / 2);
+  if constexpr (kPer == 2)
+    *out = w[0];
+  else if constexpr (kPer == 4)
+    *reinterpret_cast<uint2*>(out) = make_uint2(w[0], w[1]);
+  else
+    *reinterpret_cast<uint4*>(out) = make_uint4(w[0], w[1], w[2], w[3]);
+  if (lane == 0 && p.lse)
+    p.lse[to] = all == 0.0f ? -INFINITY : (top + log2f(all)) * 0.6931471805599453f;
+}
+
+// ---------------------------------------------------------------- launches
+template <typename T, int D, int N8, int MW>
+cudaError_t launch_shape(Params p, int sms, cudaStream_t stream) {
+  using S = Shape<D, N8, MW>;
+  const int rows = p.nodes * p.group;
+  p.row_tiles = (rows + S::kRows - 1) / S::kRows;
+  auto* kernel = tree_attention_kernel<T, D, N8, MW>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       S::kSmem);
+  if (e != cudaSuccess) return e;
+  const int grid = min(kMaxCtas, sms * (D == 256 ? 1 : 2));
+  kernel<<<grid, kThreads, S::kSmem, stream>>>(p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || grid == 1) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid - 1, (S::kRows + kJoinThreads / 32 - 1) / (kJoinThreads / 32));
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, tree_attention_join_kernel<T, D>, p, (int)S::kRows,
+                            grid);
+}
+
+// rows of a CTA for `rows` rows of an item: the smallest shape that holds
+// them all, else tiles of 64
+inline int shape_rows(int rows, int dim) {
+  const int eights = (rows + 7) / 8;
+  if (eights <= 2) return 8 * eights;
+  if (eights <= 4) return dim == 256 ? 32 : 8 * eights;
+  return eights <= 6 && dim != 256 ? 48 : 64;
+}
+
+template <typename T, int D>
+cudaError_t launch_dim(const Params& p, int sms, cudaStream_t stream) {
+  const int rows = shape_rows(p.nodes * p.group, D);
+  if (rows == 8) return launch_shape<T, D, 1, 1>(p, sms, stream);
+  if (rows == 16) return launch_shape<T, D, 2, 1>(p, sms, stream);
+  if constexpr (D == 256) {
+    if (rows == 32) return launch_shape<T, D, 2, 2>(p, sms, stream);
+    return launch_shape<T, D, 2, 4>(p, sms, stream);
+  } else {
+    if (rows == 24) return launch_shape<T, D, 3, 1>(p, sms, stream);
+    if (rows == 32) return launch_shape<T, D, 4, 1>(p, sms, stream);
+    if (rows == 48) return launch_shape<T, D, 3, 2>(p, sms, stream);
+    return launch_shape<T, D, 4, 2>(p, sms, stream);
+  }
+}
+
+cudaError_t launch_64(const Params& p, int dtype, int sms, cudaStream_t stream);
+cudaError_t launch_128(const Params& p, int dtype, int sms, cudaStream_t stream);
+cudaError_t launch_256(const Params& p, int dtype, int sms, cudaStream_t stream);
+
+}  // namespace attn
+}  // namespace dspark

@@ -541,6 +541,7 @@ int dspark_q_validate(const float* q, const int32_t* sparse_ids, const int32_t* 
  */
 #define DSPARK_MAX_NODES 64          /* nodes of a request's tree            */
 #define DSPARK_MAX_PAGE 1024         /* token rows of a block                */
+#define DSPARK_MAX_TOKENS 1073741824 /* positions of a request's table, 2^30 */
 
 /*
  * dspark_cache_plan -- grants blocks to the requests of a step and maps their
@@ -571,7 +572,7 @@ int dspark_q_validate(const float* q, const int32_t* sparse_ids, const int32_t* 
  * BAD_TREE, masks 0 and positions -1.
  * n_free: device int32, read as at most max_free, the list's length (NULL:
  * max_free).  Limits: 1 <= page_size <= DSPARK_MAX_PAGE, max_new in [1, 2^24],
- * max_blocks >= 1, table_ld >= max_blocks, max_blocks*page_size < 2^31,
+ * max_blocks >= 1, table_ld >= max_blocks, max_blocks*page_size <= 2^30,
  * B*max_new < 2^31, max_free >= 0.
  */
 int dspark_cache_plan(const int32_t* ctx_len, const int32_t* new_len, int32_t B, int32_t max_new,
@@ -629,7 +630,8 @@ int dspark_kv_write(const void* k, const void* v, int32_t src_dtype, int64_t src
  * tokens than max_blocks*page_size (every row of the request gets out 0).
  * Limits: head_dim 64, 128 or 256; 1 <= nodes <= DSPARK_MAX_NODES; n_heads a
  * multiple of n_kv_heads, at most 64 times it; q, out, caches and workspace
- * 16-byte aligned and their strides multiples of 8 elements.  scale finite.
+ * 16-byte aligned and their strides multiples of 8 elements; max_blocks*
+ * page_size <= 2^30.  scale finite.
  * workspace: dspark_tree_attention_workspace_bytes(...) bytes of device
  * memory owned by the caller, with no content to keep; calls that may
  * overlap need separate ones.  The result does not depend on the batch's
