@@ -29,7 +29,7 @@ struct Params {
   float* lse;
   int32_t* status;
   char* workspace;
-  int row_tiles;  // items of one (request, cached head): ceil(nodes * group / rows per CTA)
+  int row_tiles;  // tiles of an item's rows: ceil(nodes * group / rows per CTA)
 };
 
 // ------------------------------------------------------------ PTX wrappers
@@ -123,16 +123,18 @@ __device__ __forceinline__ uint32_t without_special(uint32_t w) {
 }
 
 // --------------------------------------------------------- division of work
-// Positions are taken in tiles.  The tiles of all (request, cached head, row
-// tile) items in a row form one axis, cut into equal ranges, one per CTA, so
-// that every SM reads the same number of bytes whatever the lengths.  An item
-// that lies inside one range is finished by its CTA; the others leave partial
-// rows in the workspace for the joining kernel.  Each item has at least one
-// tile (a request without tokens still writes its zero rows).
+// Positions are taken in tiles.  The tiles of all (request, cached head)
+// items in a row form one axis, cut into equal ranges, one per team of CTAs,
+// so that every SM reads the same number of bytes whatever the lengths.  The
+// CTAs of a team take one tile of the item's rows each and go over the same
+// keys at the same time, so that all but the first find them in L2.  An item
+// that lies inside one range is finished by its team; the others leave
+// partial rows in the workspace for the joining kernel.  Each item has at
+// least one tile (a request without tokens still writes its zero rows).
 constexpr int kMaxCtas = 320;
 
-struct Start {  // where a CTA's range begins
-  int b, item, tile, tiles;
+struct Start {  // where a team's range begins
+  int b, head, tile, tiles;
 };
 
 struct Workspace {
@@ -178,12 +180,46 @@ __device__ __forceinline__ int request_tiles(const Params& p, int b, int tile) {
   return len > 0 ? (len - 1) / tile + 1 : 1;
 }
 
-// the CTA whose range holds tile x of `total`, and the first tile of CTA c
-__device__ __forceinline__ int owner_of(int64_t x, int64_t total, int ctas) {
-  return (int)(((x + 1) * ctas - 1) / total);
+// the team whose range holds tile x of `total`, and the first tile of team c
+__device__ __forceinline__ int owner_of(int64_t x, int64_t total, int teams) {
+  return (int)(((x + 1) * teams - 1) / total);
 }
-__device__ __forceinline__ int64_t first_of(int c, int64_t total, int ctas) {
-  return (int64_t)c * total / ctas;
+__device__ __forceinline__ int64_t first_of(int c, int64_t total, int teams) {
+  return (int64_t)c * total / teams;
+}
+
+// This CTA's range of the tile axis: its length, and where it begins (shared
+// memory, valid after the call); 0 for a CTA without work.  All threads call.
+template <int kBlock>
+__device__ __forceinline__ int64_t find_range(const Params& p, int tile, const Workspace& ws,
+                                              uint64_t* scan, Start* start) {
+  const int tid = threadIdx.x;
+  const int per = (p.B + kBlock - 1) / kBlock;
+  const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
+  uint64_t sum = 0, total_u;
+  for (int b = b0; b < b1; ++b) sum += (uint64_t)request_tiles(p, b, tile) * p.kv_heads;
+  const uint64_t upto = block_inclusive_scan_u64(sum, scan, &total_u);
+  const int64_t total = (int64_t)total_u;
+  const int teams = (int)min((int64_t)(gridDim.x / p.row_tiles), total);
+  const int team = blockIdx.x / p.row_tiles;
+  if (team >= teams) return 0;
+  const int64_t x0 = first_of(team, total, teams);
+  int64_t at = (int64_t)(upto - sum);
+  if (x0 >= at && x0 < (int64_t)upto) {
+    for (int b = b0; b < b1; ++b) {
+      const int tiles = request_tiles(p, b, tile);
+      const int64_t end = at + (int64_t)tiles * p.kv_heads;
+      if (x0 < end) {
+        *start = {b, (int)((x0 - at) / tiles), (int)((x0 - at) % tiles), tiles};
+        if (blockIdx.x % p.row_tiles == 0) ws.start[team] = *start;
+        break;
+      }
+      at = end;
+    }
+  }
+  if (blockIdx.x == 0 && tid == 0) *ws.total = total;
+  __syncthreads();
+  return first_of(team + 1, total, teams) - x0;
 }
 
 // ------------------------------------------------------ the streaming kernel
@@ -242,55 +278,25 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2)
   __shared__ uint64_t s_mask[kRows];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int mw = warp % MW, kw = warp / MW;
-  const int items = p.kv_heads * p.row_tiles;
-
-  // this CTA's range
-  const int per = (p.B + kThreads - 1) / kThreads;
-  const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
-  uint64_t sum = 0, total_u;
-  for (int b = b0; b < b1; ++b) sum += (uint64_t)request_tiles(p, b, S::kTile) * items;
-  const uint64_t upto = block_inclusive_scan_u64(sum, s_scan, &total_u);
-  const int64_t total = (int64_t)total_u;
-  const int ctas = (int)min((int64_t)gridDim.x, total);
-  if ((int)blockIdx.x >= ctas) return;
-  const int64_t x0 = first_of(blockIdx.x, total, ctas), x1 = first_of(blockIdx.x + 1, total, ctas);
-  {
-    int64_t at = (int64_t)(upto - sum);
-    if (x0 >= at && x0 < (int64_t)upto) {
-      for (int b = b0; b < b1; ++b) {
-        const int tiles = request_tiles(p, b, S::kTile);
-        const int64_t end = at + (int64_t)tiles * items;
-        if (x0 < end) {
-          s_start = {b, (int)((x0 - at) / tiles), (int)((x0 - at) % tiles), tiles};
-          break;
-        }
-        at = end;
-      }
-    }
-  }
-  __syncthreads();
-  Start cur = s_start;
   const Workspace ws = carve(p.workspace, kRows);
-  if (tid == 0) {
-    ws.start[blockIdx.x] = cur;
-    if (blockIdx.x == 0) *ws.total = total;
-  }
+  int64_t left = find_range<kThreads>(p, S::kTile, ws, s_scan, &s_start);
+  Start cur = s_start;
+  const int r0 = (blockIdx.x % p.row_tiles) * kRows;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   const T* kc = static_cast<const T*>(p.k);
   const T* vc = static_cast<const T*>(p.v);
   const bool whole = p.page % kKeys == 0;  // a step lies in one block
   const uint32_t ring = smem_u32(smem) + kw * kStages * S::kStageBytes;
-  int64_t left = x1 - x0;
 
   while (left > 0) {
     const int tiles = (int)min(left, (int64_t)(cur.tiles - cur.tile));
     const Lengths len = request_lengths(p, cur.b);
-    const int kvh = cur.item / p.row_tiles, r0 = (cur.item % p.row_tiles) * kRows;
+    const int kvh = cur.head;
     const int32_t* table = p.table + cur.b * p.table_ld;
     const int live = len.nodes * p.group;  // rows below this one have a node
 
-    if (tid == 0 && cur.item == 0 && cur.tile == 0)
+    if (tid == 0 && r0 == 0 && kvh == 0 && cur.tile == 0)
       p.status[cur.b] = len.bad ? DSPARK_ST_BAD_LENGTH : DSPARK_ST_OK;
 
     // ---- copies: 16 positions of this group into a stage of its ring
@@ -585,8 +591,8 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2)
 
     left -= tiles;
     cur.tile = 0;
-    if (++cur.item == items) {
-      cur.item = 0;
+    if (++cur.head == p.kv_heads) {
+      cur.head = 0;
       ++cur.b;
     }
     if (left > 0) cur.tiles = request_tiles(p, cur.b, S::kTile);
@@ -594,9 +600,9 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2)
 }
 
 // ------------------------------------------------------- the joining kernel
-// CTA (i, y): if the boundary before CTA i's range is the first one inside
-// its item, the item's partial rows [8 y, 8 y + 8) are joined, a warp per
-// row, in the order of the ranges.
+// CTA (x, y, z): if the boundary before the range of team x + 1 is the first
+// one inside its item, rows [8 y, 8 y + 8) of the item's row tile z are
+// joined from the teams' partial rows, a warp per row, in the teams' order.
 constexpr int kJoinThreads = 256;
 
 template <typename T, int D>
@@ -608,22 +614,26 @@ __global__ void __launch_bounds__(kJoinThreads)
   const Workspace ws = carve(p.workspace, rows);
   const int i = blockIdx.x + 1;
   const int64_t total = *ws.total;
-  const int ctas = (int)min((int64_t)grid, total);
-  if (i >= ctas) return;
+  const int teams = (int)min((int64_t)(grid / p.row_tiles), total);
+  if (i >= teams) return;
   const Start at = ws.start[i];
   if (at.tile == 0) return;
-  const int64_t begin = first_of(i, total, ctas) - at.tile;
-  const int c0 = owner_of(begin, total, ctas);
+  const int64_t begin = first_of(i, total, teams) - at.tile;
+  const int c0 = owner_of(begin, total, teams);
   if (c0 != i - 1) return;
-  const int c1 = owner_of(begin + at.tiles - 1, total, ctas);
+  const int c1 = owner_of(begin + at.tiles - 1, total, teams);
   const int lane = threadIdx.x & 31;
   const int r = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5);
-  const int kvh = at.item / p.row_tiles, row = (at.item % p.row_tiles) * rows + r;
+  const int row = blockIdx.z * rows + r;
   if (r >= rows || row >= p.nodes * p.group) return;
+  // the partial rows of team c: its first range's in slot 0, its last's in slot 1
+  auto slot_of = [&](int c) -> int64_t {
+    return 2ll * (c * p.row_tiles + blockIdx.z) + (c == c0 ? 1 : 0);
+  };
 
   float top = -INFINITY;
   for (int c = c0 + lane; c <= c1; c += 32)
-    top = fmaxf(top, ws.stats[(int64_t)(c == c0 ? 2 * c + 1 : 2 * c) * rows + r].x);
+    top = fmaxf(top, ws.stats[slot_of(c) * rows + r].x);
   top = warp_reduce(top, OpMaxF());
   const float safe = top == -INFINITY ? 0.0f : top;
   float all = 0.0f, a[kPer];
@@ -631,7 +641,7 @@ __global__ void __launch_bounds__(kJoinThreads)
   for (int d = 0; d < kPer; ++d) a[d] = 0.0f;
 #pragma unroll 4
   for (int c = c0; c <= c1; ++c) {
-    const int64_t slot = c == c0 ? 2 * c + 1 : 2 * c;
+    const int64_t slot = slot_of(c);
     const float2 st = ws.stats[slot * rows + r];
     const float f = exp2_approx(st.x - safe);
     const float* v = ws.rows + (slot * rows + r) * D + lane * kPer;
@@ -647,7 +657,7 @@ __global__ void __launch_bounds__(kJoinThreads)
 #pragma unroll
     for (int d = 0; d < kPer; ++d) a[d] += x[d] * f;
   }
-  const int node = row / p.group, h = kvh * p.group + row - node * p.group;
+  const int node = row / p.group, h = at.head * p.group + row - node * p.group;
   const int64_t to = ((int64_t)at.b * p.nodes + node) * p.heads + h;
   const float inv = all == 0.0f ? 0.0f : 1.0f / all;
   uint32_t w[kPer / 2];
@@ -665,21 +675,14 @@ __global__ void __launch_bounds__(kJoinThreads)
 }
 
 // ---------------------------------------------------------------- launches
-template <typename T, int D, int N8, int MW>
-cudaError_t launch_shape(Params p, int sms, cudaStream_t stream) {
-  using S = Shape<D, N8, MW>;
-  const int rows = p.nodes * p.group;
-  p.row_tiles = (rows + S::kRows - 1) / S::kRows;
-  auto* kernel = tree_attention_kernel<T, D, N8, MW>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       S::kSmem);
-  if (e != cudaSuccess) return e;
-  const int grid = min(kMaxCtas, sms * (D == 256 ? 1 : 2));
-  kernel<<<grid, kThreads, S::kSmem, stream>>>(p);
-  e = cudaGetLastError();
-  if (e != cudaSuccess || grid == 1) return e;
+// the joining kernel after a streaming kernel of `grid` CTAs; it is launched
+// while that one runs and waits on the device for its end
+template <typename T, int D>
+cudaError_t launch_join(const Params& p, int rows, int grid, cudaStream_t stream) {
+  const int teams = grid / p.row_tiles;
+  if (teams == 1) return cudaSuccess;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid - 1, (S::kRows + kJoinThreads / 32 - 1) / (kJoinThreads / 32));
+  cfg.gridDim = dim3(teams - 1, (rows + kJoinThreads / 32 - 1) / (kJoinThreads / 32), p.row_tiles);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -687,33 +690,31 @@ cudaError_t launch_shape(Params p, int sms, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, tree_attention_join_kernel<T, D>, p, (int)S::kRows,
-                            grid);
+  return cudaLaunchKernelEx(&cfg, tree_attention_join_kernel<T, D>, p, rows, grid);
+}
+
+template <typename T, int D, int N8, int MW>
+cudaError_t launch_shape(Params p, int sms, cudaStream_t stream) {
+  using S = Shape<D, N8, MW>;
+  p.row_tiles = (p.nodes * p.group + S::kRows - 1) / S::kRows;
+  auto* kernel = tree_attention_kernel<T, D, N8, MW>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       S::kSmem);
+  if (e != cudaSuccess) return e;
+  const int grid = min(kMaxCtas, max(sms * (D == 256 ? 1 : 2), p.row_tiles));
+  kernel<<<grid, kThreads, S::kSmem, stream>>>(p);
+  e = cudaGetLastError();
+  return e != cudaSuccess ? e : launch_join<T, D>(p, S::kRows, grid, stream);
 }
 
 // rows of a CTA for `rows` rows of an item: the smallest shape that holds
-// them all, else tiles of 64
+// them all; beyond 64 the wide kernel's 256, or tiles of 64 for head_dim 256
 inline int shape_rows(int rows, int dim) {
   const int eights = (rows + 7) / 8;
+  if (eights > 8 && dim != 256) return 256;
   if (eights <= 2) return 8 * eights;
   if (eights <= 4) return dim == 256 ? 32 : 8 * eights;
   return eights <= 6 && dim != 256 ? 48 : 64;
-}
-
-template <typename T, int D>
-cudaError_t launch_dim(const Params& p, int sms, cudaStream_t stream) {
-  const int rows = shape_rows(p.nodes * p.group, D);
-  if (rows == 8) return launch_shape<T, D, 1, 1>(p, sms, stream);
-  if (rows == 16) return launch_shape<T, D, 2, 1>(p, sms, stream);
-  if constexpr (D == 256) {
-    if (rows == 32) return launch_shape<T, D, 2, 2>(p, sms, stream);
-    return launch_shape<T, D, 2, 4>(p, sms, stream);
-  } else {
-    if (rows == 24) return launch_shape<T, D, 3, 1>(p, sms, stream);
-    if (rows == 32) return launch_shape<T, D, 4, 1>(p, sms, stream);
-    if (rows == 48) return launch_shape<T, D, 3, 2>(p, sms, stream);
-    return launch_shape<T, D, 4, 2>(p, sms, stream);
-  }
 }
 
 cudaError_t launch_64(const Params& p, int dtype, int sms, cudaStream_t stream);

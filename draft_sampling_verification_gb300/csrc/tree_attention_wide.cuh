@@ -1,0 +1,607 @@
+// tree_attention_wide.cuh -- the attention kernel for items of more than 64
+// rows (wide trees, many query heads to a cached head), on the fifth
+// generation's tensor instructions.  Included by the translation units of
+// tree_attention.cuh.
+#pragma once
+
+#include "tree_attention.cuh"
+
+namespace dspark {
+namespace attn {
+
+// ------------------------------------------------- tcgen05 and its barriers
+// Shared-memory operand descriptor: start address, leading and stride byte
+// offsets (each / 16), version 1, 128-byte swizzle.
+__device__ __forceinline__ uint64_t operand_desc(uint32_t addr, uint32_t lead, uint32_t stride) {
+  return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(lead >> 4) << 16) |
+         ((uint64_t)(stride >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+// d[tmem] (+)= a b with a and b in shared memory
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                       bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      : "memory");
+}
+// the same with a in tensor memory
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                       bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      : "memory");
+}
+// arrives on `bar` once every product issued before it is done
+__device__ __forceinline__ void mma_commit(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+          smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void fence_async_shared() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+__device__ __forceinline__ void tc_before_sync() {
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tc_after_sync() {
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+// 32 columns of this warp's 32 lanes
+__device__ __forceinline__ void tmem_load32(float (&v)[32], uint32_t addr) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
+        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15, %16};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_store32(uint32_t addr, const float (&v)[32]) {
+  uint32_t r[16];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(v[h * 16 + i]);
+    tmem_store16(addr + h * 16, r);
+  }
+}
+__device__ __forceinline__ void tmem_wait_load() {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_wait_store() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// ------------------------------------------------------------ the kernel
+// Up to 256 rows of an item, as two tiles of 128, over tiles of 128
+// positions: S = Q K^T into tensor memory, softmax by the warpgroup that owns
+// the row tile (a thread per row, so no exchange between threads), the
+// weights back into tensor memory over the scores, O += P V.  The two row
+// tiles alternate: the tensor cores work for one while the other is in its
+// softmax.  Bound by the products (2 * 2 * 128 * 128 * D operations per row
+// tile and step) and, beside them, the exponentials.
+//
+// The products run in the order they are issued, so the barrier of a tile's
+// scores also says that its accumulators hold every earlier step: the
+// softmax warpgroup may then rescale them.  It does so only when a score
+// passes the row's reference by more than 8, as in the streaming kernel.
+//
+// Warps 0-3 and 4-7: softmax, Q and the results of row tile 0 and 1.  Warps
+// 8-11: copies of keys and values into two stages each.  Warp 12: issues the
+// products.  K and Q lie in rows of 64 dims (128 bytes, swizzled in groups of
+// eight rows); V the same, read with dims as its major axis.
+constexpr int kWideThreads = 416;
+constexpr int kWideRows = 256;
+constexpr int kWideTile = 128;
+
+template <int D>
+struct Wide {
+  static constexpr int kHalves = D / 64;
+  static constexpr int kOperand = 128 * D * 2;  // 128 rows of Q, K or V
+  static constexpr int kSmem = 6 * kOperand + 1024;
+};
+
+struct WideShared {
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
+  uint64_t q_full[2], s_full[2], p_full[2], o_full[2], drained;
+  uint64_t scan[32];
+  Start start;
+  int64_t offset[2][kWideTile];  // of a tile's rows in the caches; -1: no key
+  uint32_t valid[4][4];          // the same as bits, by tile number modulo 4
+  uint32_t special[4];           // a value of a tile's nodes is an infinity or a NaN
+  uint32_t tmem;
+  uint32_t failed;               // a wait expired
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kWideThreads, 1)
+    tree_attention_wide_kernel(const __grid_constant__ Params p) {
+  using H = Half<T>;
+  using W = Wide<D>;
+  constexpr int kChunks = D / 8;
+  extern __shared__ unsigned char smem_raw[];
+  __shared__ WideShared sh;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  const uint32_t q_at = base, k_at = base + 2 * W::kOperand, v_at = base + 4 * W::kOperand;
+
+  const Workspace ws = carve(p.workspace, kWideRows);
+  int64_t left = find_range<kWideThreads>(p, kWideTile, ws, sh.scan, &sh.start);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (left <= 0) return;
+  Start cur = sh.start;
+  const Start begin = cur;
+  const int64_t all_tiles = left;
+  const int r0 = (blockIdx.x % p.row_tiles) * kWideRows;
+  const int n_tiles = p.nodes * p.group - r0 > 128 ? 2 : 1;
+
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.k_full[i], 128);
+      mbar_init(&sh.k_empty[i], 1);
+      mbar_init(&sh.v_full[i], 128);
+      mbar_init(&sh.v_empty[i], 1);
+      mbar_init(&sh.q_full[i], 128);
+      mbar_init(&sh.s_full[i], 1);
+      mbar_init(&sh.p_full[i], 128);
+      mbar_init(&sh.o_full[i], 1);
+    }
+    mbar_init(&sh.drained, 1);
+    sh.failed = 0u;
+    mbar_init_fence();
+  }
+  if (warp == 12) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                     smem_u32(&sh.tmem))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_before_sync();
+  __syncthreads();
+  tc_after_sync();
+  // columns: the scores of row tile m (the weights over their first half), then its accumulators
+  const uint32_t tmem = sh.tmem;
+  auto s_col = [&](int m) -> uint32_t { return tmem + 128u * m; };
+  auto o_col = [&](int m) -> uint32_t { return tmem + 256u + 128u * m; };
+
+  // a bounded wait; once one expires, every later one of the CTA gives up at once
+  auto wait = [&](uint64_t* bar, uint32_t phase) -> bool {
+    if (mbar_try_wait(bar, phase)) return true;
+    if (*(volatile uint32_t*)&sh.failed) return false;
+    if (mbar_wait_bounded(bar, phase)) return true;
+    *(volatile uint32_t*)&sh.failed = 1u;
+    return false;
+  };
+  auto segment = [&]() -> int { return (int)min(left, (int64_t)(cur.tiles - cur.tile)); };
+  auto next = [&](int tiles) {
+    left -= tiles;
+    cur.tile = 0;
+    if (++cur.head == p.kv_heads) {
+      cur.head = 0;
+      ++cur.b;
+    }
+    if (left > 0) cur.tiles = request_tiles(p, cur.b, kWideTile);
+  };
+
+  if (warp < 8) {
+    // -------------------------------------------------- softmax and results
+    const int m = warp >> 2;
+    const int t = tid & 127;  // this thread's row of the tile and lane of tensor memory
+    const uint32_t sc = s_col(m) + ((uint32_t)(t & ~31) << 16);
+    const uint32_t oc = o_col(m) + ((uint32_t)(t & ~31) << 16);
+    // a negative scale goes into Q's sign, so that the largest score stays the largest; 0 would
+    // make NaN of a hidden score
+    const uint32_t flip = p.scale2 < 0.0f ? 0x80008000u : 0u;
+    const float scale = fmaxf(fabsf(p.scale2), 1.17549435e-38f);
+    uint32_t tile_no = 0, segments = 0;
+    bool ok = m < n_tiles;
+    while (ok && left > 0) {
+      const int tiles = segment();
+      const Lengths len = request_lengths(p, cur.b);
+      const int live = len.nodes * p.group;
+      if (tid == 0 && r0 == 0 && cur.head == 0 && cur.tile == 0)
+        p.status[cur.b] = len.bad ? DSPARK_ST_BAD_LENGTH : DSPARK_ST_OK;
+
+      // Q, 16 bytes at a time
+#pragma unroll 4
+      for (int i = t; i < 128 * kChunks; i += 128) {
+        const int r = i / kChunks, c = i % kChunks;
+        const int row = r0 + m * 128 + r, node = row / p.group;
+        uint4 w = make_uint4(0u, 0u, 0u, 0u);
+        if (row < live) {
+          const int h = cur.head * p.group + row - node * p.group;
+          w = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + cur.b * p.q_req +
+                                                   node * p.q_node + h * p.q_head) +
+                    c);
+          w.x ^= flip;
+          w.y ^= flip;
+          w.z ^= flip;
+          w.w ^= flip;
+        }
+        const uint32_t to = q_at + m * W::kOperand + (c >> 3) * 16384 + r * 128 +
+                            (((c & 7) ^ (r & 7)) << 4);
+        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(w.x), "r"(w.y),
+                     "r"(w.z), "r"(w.w)
+                     : "memory");
+      }
+      fence_async_shared();
+      mbar_arrive(&sh.q_full[m]);
+
+      const int row = r0 + m * 128 + t, node = row / p.group;
+      uint64_t mask = 0;
+      if (row < live)
+        mask = p.mask ? p.mask[(int64_t)cur.b * p.nodes + node] : ~0ull >> (63 - node);
+      float ref = -INFINITY;
+      float2 sum2 = make_float2(0.0f, 0.0f);
+      bool special = false;
+      for (int i = 0; i < tiles; ++i, ++tile_no) {
+        ok = __all_sync(0xffffffffu, wait(&sh.s_full[m], tile_no & 1u));
+        if (!ok) break;
+        tc_after_sync();
+        if (i > 0) special |= sh.special[(tile_no - 1u) & 3u] != 0u;
+        const int pos = (cur.tile + i) * kWideTile;
+        const uint32_t* words = sh.valid[tile_no & 3u];
+        const bool plain = pos + kWideTile <= len.ctx &&
+                           (words[0] & words[1] & words[2] & words[3]) == 0xFFFFFFFFu;
+        // scores of chunk c: positions pos + 32 c ..; -infinity where the row does not see them
+        float v[32];
+        auto load_scores = [&](int c) {
+          tmem_load32(v, sc + c * 32);
+          tmem_wait_load();
+          if (plain) return;
+          uint32_t w = words[c];
+          const int node0 = pos + c * 32 - len.ctx;  // the node of the chunk's first position
+          if (node0 >= 0)
+            w &= node0 < 64 ? (uint32_t)(mask >> node0) : 0u;
+          else if (node0 > -32)
+            w &= (uint32_t)(mask << -node0) | ((1u << -node0) - 1u);
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            if (!((w >> j) & 1u)) v[j] = -INFINITY;
+        };
+        float top = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          load_scores(c);
+          float a = v[0], z = v[1];
+#pragma unroll
+          for (int j = 2; j < 32; j += 2) {
+            a = fmaxf(a, v[j]);
+            z = fmaxf(z, v[j + 1]);
+          }
+          top = fmaxf(top, fmaxf(a, z));
+        }
+        top *= scale;
+        if (__any_sync(0xffffffffu, top > ref + kSlack)) {
+          top = fmaxf(top, ref);
+          const float f = top == -INFINITY ? 1.0f : exp2_approx(ref - top);
+          ref = top;
+          sum2.x *= f;
+          sum2.y *= f;
+          if (i > 0) {
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+              tmem_load32(v, oc + c * 32);
+              tmem_wait_load();
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[j] *= f;
+              tmem_store32(oc + c * 32, v);
+            }
+          }
+        }
+        const float2 off = f2(ref == -INFINITY ? 0.0f : -ref), by = f2(scale);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          load_scores(c);
+          uint32_t w[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            float2 x = fma2_rn(make_float2(v[2 * j], v[2 * j + 1]), by, off);
+            x.x = exp2_approx(x.x);
+            x.y = exp2_approx(x.y);
+            sum2 = add2_rn(sum2, x);
+            w[j] = H::pack(x.x, x.y);
+          }
+          tmem_store16(sc + c * 16, w);
+        }
+        tmem_wait_store();
+        tc_before_sync();
+        mbar_arrive(&sh.p_full[m]);
+      }
+      if (ok) ok = __all_sync(0xffffffffu, wait(&sh.o_full[m], segments & 1u));
+      ++segments;
+      if (!ok) break;
+      tc_after_sync();
+      special |= sh.special[(tile_no - 1u) & 3u] != 0u;
+
+      float sum = sum2.x + sum2.y;
+      if (row >= live) {  // a row of no node: its zero query saw the text all the same
+        ref = -INFINITY;
+        sum = 0.0f;
+      }
+      const bool full = tiles == cur.tiles;
+      const int h = cur.head * p.group + row - node * p.group;
+      const int64_t to = ((int64_t)cur.b * p.nodes + node) * p.heads + h;
+      const int64_t slot = 2ll * blockIdx.x + (cur.tile == 0 ? 1 : 0);
+      const bool mine = row < p.nodes * p.group;
+      const float inv = sum == 0.0f ? 0.0f : full ? 1.0f / sum : 1.0f;
+#pragma unroll 1
+      for (int c = 0; c < D / 32; ++c) {
+        float v[32];
+        tmem_load32(v, oc + c * 32);
+        tmem_wait_load();
+        if (row >= live) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = 0.0f;
+        }
+        if (special) {
+          // infinities and NaN, left out of the product, reach the rows that see their key
+#pragma unroll 1
+          for (int k = 0; k < len.nodes; ++k) {
+            const int at = len.ctx + k, tile = at / kWideTile;
+            if (!((mask >> k) & 1ull) || tile < cur.tile || tile >= cur.tile + tiles) continue;
+            const int block = p.table[cur.b * p.table_ld + at / p.page];
+            if (block < 0 || block >= p.n_blocks) continue;
+            const T* from = static_cast<const T*>(p.v) + block * p.block_stride +
+                            (int64_t)(at % p.page) * p.token_stride + cur.head * p.head_stride +
+                            c * 32;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              const uint32_t bits = __ldg(reinterpret_cast<const unsigned short*>(from) + j);
+              if (any_special<T>(bits)) v[j] += H::widen(bits);
+            }
+          }
+        }
+        if (mine && full) {
+          uint4* out = reinterpret_cast<uint4*>(static_cast<T*>(p.out) + to * D + c * 32);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            out[j] = make_uint4(H::pack(v[8 * j] * inv, v[8 * j + 1] * inv),
+                                H::pack(v[8 * j + 2] * inv, v[8 * j + 3] * inv),
+                                H::pack(v[8 * j + 4] * inv, v[8 * j + 5] * inv),
+                                H::pack(v[8 * j + 6] * inv, v[8 * j + 7] * inv));
+        } else if (mine) {
+          float4* out =
+              reinterpret_cast<float4*>(ws.rows + (slot * kWideRows + m * 128 + t) * D + c * 32);
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            out[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+        }
+        __syncwarp();
+      }
+      if (mine) {
+        if (!full)
+          ws.stats[slot * kWideRows + m * 128 + t] = make_float2(ref, sum);
+        else if (p.lse)
+          p.lse[to] = sum == 0.0f ? -INFINITY : (ref + log2f(sum)) * 0.6931471805599453f;
+      }
+      tc_before_sync();  // the accumulators are read: the next item may take them
+      next(tiles);
+    }
+  } else if (warp < 12) {
+    // ------------------------------------------------------ keys and values
+    const int t = tid - 256;
+    const T* kc = static_cast<const T*>(p.k);
+    const T* vc = static_cast<const T*>(p.v);
+    uint32_t g = 0;
+    bool ok = true;             // this thread's waits
+    bool go = true;             // everybody's, agreed on at each tile
+    int node_row = kWideTile;   // of the tile before: its first row that holds a node
+    auto copy = [&](const T* cache, uint32_t to) {
+      const int64_t* offset = sh.offset[g & 1u];
+#pragma unroll
+      for (int i = 0; i < kChunks; ++i) {
+        const int r = (i * 128 + t) / kChunks, c = (i * 128 + t) % kChunks;
+        const int64_t off = offset[r];
+        cp_async16(to + (c >> 3) * 16384 + r * 128 + (((c & 7) ^ (r & 7)) << 4),
+                   cache + (off >= 0 ? off + c * 8 : 0), off >= 0);
+      }
+      cp_async_commit();
+    };
+    // this thread's pieces of the values of tile n are there: those of nodes
+    // are cleared of infinities and NaN, which would reach rows that do not
+    // see them (0 times infinity)
+    auto values_landed = [&](uint32_t n) {
+      if (node_row < kWideTile) {
+        const uint32_t at = v_at + (n & 1u) * W::kOperand;
+#pragma unroll 1
+        for (int i = 0; i < kChunks; ++i) {
+          const int r = (i * 128 + t) / kChunks, c = (i * 128 + t) % kChunks;
+          if (r < node_row) continue;
+          const uint32_t addr = at + (c >> 3) * 16384 + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+          uint32_t w[4];
+          asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                       : "r"(addr)
+                       : "memory");
+          if (any_special<T>(w[0]) || any_special<T>(w[1]) || any_special<T>(w[2]) ||
+              any_special<T>(w[3])) {
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr),
+                         "r"(without_special<T>(w[0])), "r"(without_special<T>(w[1])),
+                         "r"(without_special<T>(w[2])), "r"(without_special<T>(w[3]))
+                         : "memory");
+            *(volatile uint32_t*)&sh.special[n & 3u] = 1u;
+          }
+        }
+      }
+      fence_async_shared();
+      mbar_arrive(&sh.v_full[n & 1u]);
+    };
+    while (go && left > 0) {
+      const int tiles = segment();
+      const Lengths len = request_lengths(p, cur.b);
+      const int32_t* table = p.table + cur.b * p.table_ld;
+      const int64_t head_off = cur.head * p.head_stride;
+      auto entry_of = [&](int i) -> int {
+        const int pos = (cur.tile + i) * kWideTile + t;
+        return i < tiles && pos < len.len ? __ldg(table + pos / p.page) : -1;
+      };
+      int ahead = entry_of(0);
+      for (int i = 0; i < tiles; ++i, ++g) {
+        const int pos = (cur.tile + i) * kWideTile + t, block = ahead;
+        ahead = entry_of(i + 1);
+        const bool held = block >= 0 && block < p.n_blocks;
+        sh.offset[g & 1u][t] =
+            held ? block * p.block_stride + (int64_t)(pos % p.page) * p.token_stride + head_off
+                 : -1;
+        const uint32_t bits = __ballot_sync(0xffffffffu, held);
+        if (t == 0) sh.special[g & 3u] = 0u;
+        ok = ok && wait(&sh.k_empty[g & 1u], ((g >> 1) & 1u) ^ 1u);
+        {  // the offsets are written, and all or none go on
+          uint32_t all_ok;
+          asm volatile(
+              "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
+              "barrier.red.and.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+              : "=r"(all_ok)
+              : "r"((uint32_t)ok)
+              : "memory");
+          go = all_ok != 0u;
+        }
+        if (!go) break;
+        if (lane == 0) sh.valid[g & 3u][t >> 5] = bits;
+        copy(kc, k_at + (g & 1u) * W::kOperand);
+        if (g > 0) {
+          cp_async_wait<1>();
+          values_landed(g - 1u);
+        }
+        ok = wait(&sh.v_empty[g & 1u], ((g >> 1) & 1u) ^ 1u);
+        copy(vc, v_at + (g & 1u) * W::kOperand);
+        node_row = max(0, min(kWideTile, len.ctx - (pos - t)));
+        cp_async_wait<1>();
+        fence_async_shared();
+        mbar_arrive(&sh.k_full[g & 1u]);
+      }
+      if (go) next(tiles);
+    }
+    cp_async_wait<0>();
+    if (go) values_landed(g - 1u);
+  } else if (lane == 0) {
+    // ------------------------------------------------------------- products
+    constexpr uint32_t kFormat = sizeof(T) == 2 && H::kExponent == 0x7F80u ? 1u : 0u;
+    // fp32 accumulators, both operands of T, 128 rows; for P V the second has its dims outermost
+    constexpr uint32_t kCommon = (1u << 4) | (kFormat << 7) | (kFormat << 10) | (8u << 24);
+    constexpr uint32_t kScores = kCommon | ((kWideTile / 8u) << 17);
+    constexpr uint32_t kValues = kCommon | (1u << 16) | (((uint32_t)D / 8u) << 17);
+    auto scores = [&](int m, uint32_t g) {
+#pragma unroll
+      for (int kt = 0; kt < D / 16; ++kt) {
+        const uint32_t at = (kt >> 2) * 16384 + (kt & 3) * 32;
+        mma_ss(s_col(m), operand_desc(q_at + m * W::kOperand + at, 16, 1024),
+               operand_desc(k_at + (g & 1u) * W::kOperand + at, 16, 1024), kScores, kt > 0);
+      }
+      mma_commit(&sh.s_full[m]);
+    };
+    auto values = [&](int m, uint32_t g, bool add) {
+#pragma unroll
+      for (int kt = 0; kt < kWideTile / 16; ++kt)
+        mma_ts(o_col(m), s_col(m) + kt * 8,
+               operand_desc(v_at + (g & 1u) * W::kOperand + kt * 2048, 16384, 1024), kValues,
+               add || kt > 0);
+    };
+    uint32_t g = 0, segments = 0;
+    bool ok = true;
+    while (ok && left > 0) {
+      const int tiles = segment();
+      for (int m = 0; m < n_tiles; ++m) ok = ok && wait(&sh.q_full[m], segments & 1u);
+      ok = ok && wait(&sh.k_full[g & 1u], (g >> 1) & 1u);
+      if (!ok) break;
+      tc_after_sync();
+      for (int m = 0; m < n_tiles; ++m) scores(m, g);
+      mma_commit(&sh.k_empty[g & 1u]);
+      for (int i = 0; i < tiles && ok; ++i, ++g) {
+        const bool more = i + 1 < tiles;
+        for (int m = 0; m < n_tiles; ++m) {
+          ok = ok && wait(&sh.p_full[m], g & 1u);
+          if (m == 0) ok = ok && wait(&sh.v_full[g & 1u], (g >> 1) & 1u);
+          if (!ok) break;
+          tc_after_sync();
+          values(m, g, i > 0);
+          if (m == n_tiles - 1) mma_commit(&sh.v_empty[g & 1u]);
+          if (more) {
+            if (m == 0) ok = wait(&sh.k_full[(g + 1u) & 1u], ((g + 1u) >> 1) & 1u);
+            if (!ok) break;
+            scores(m, g + 1u);
+          } else {
+            mma_commit(&sh.o_full[m]);
+          }
+        }
+        if (ok && more) mma_commit(&sh.k_empty[(g + 1u) & 1u]);
+      }
+      ++segments;
+      if (ok) next(tiles);
+    }
+    // nothing of this CTA's is in flight when its memory is given back
+    mma_commit(&sh.drained);
+    mbar_wait_bounded(&sh.drained, 0);
+  }
+  __syncwarp();
+  tc_before_sync();
+  __syncthreads();
+  if (warp == 12) {
+    tc_after_sync();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  }
+  if (sh.failed && tid == 0) {  // the requests of this range are refused
+    left = all_tiles;
+    cur = begin;
+    while (left > 0) {
+      p.status[cur.b] = DSPARK_ST_TIMEOUT;
+      next(segment());
+    }
+  }
+}
+
+template <typename T, int D>
+cudaError_t launch_wide(Params p, int sms, cudaStream_t stream) {
+  p.row_tiles = (p.nodes * p.group + kWideRows - 1) / kWideRows;
+  auto* kernel = tree_attention_wide_kernel<T, D>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       Wide<D>::kSmem);
+  if (e != cudaSuccess) return e;
+  const int grid = min(kMaxCtas, max(sms, p.row_tiles));
+  kernel<<<grid, kWideThreads, Wide<D>::kSmem, stream>>>(p);
+  e = cudaGetLastError();
+  return e != cudaSuccess ? e : launch_join<T, D>(p, kWideRows, grid, stream);
+}
+
+template <typename T, int D>
+cudaError_t launch_dim(const Params& p, int sms, cudaStream_t stream) {
+  const int rows = shape_rows(p.nodes * p.group, D);
+  if (rows == 8) return launch_shape<T, D, 1, 1>(p, sms, stream);
+  if (rows == 16) return launch_shape<T, D, 2, 1>(p, sms, stream);
+  if constexpr (D == 256) {
+    if (rows == 32) return launch_shape<T, D, 2, 2>(p, sms, stream);
+    return launch_shape<T, D, 2, 4>(p, sms, stream);
+  } else {
+    if (rows == 24) return launch_shape<T, D, 3, 1>(p, sms, stream);
+    if (rows == 32) return launch_shape<T, D, 4, 1>(p, sms, stream);
+    if (rows == 48) return launch_shape<T, D, 3, 2>(p, sms, stream);
+    if (rows == 256) return launch_wide<T, D>(p, sms, stream);
+    return launch_shape<T, D, 4, 2>(p, sms, stream);
+  }
+}
+
+}  // namespace attn
+}  // namespace dspark
