@@ -14,6 +14,7 @@ with torch and call the same entry points.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
@@ -48,15 +49,15 @@ def version() -> str:
 
 
 def _call(name, *args):
-    rc = getattr(_lib.load(), name)(*args)
+    rc = getattr(_lib._lib or _lib.load(), name)(*args)
     if rc != 0:
         raise RuntimeError("%s failed with code %d" % (name, rc))
 
 
 def _stream(stream):
     if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream
 
 
 def _ptr(t):
@@ -323,13 +324,11 @@ def _arg(name, t, dtype, shape):
     """The pointer of an optional contiguous CUDA tensor of this dtype and shape."""
     if t is None:
         return None
+    if t.dtype is dtype and t.is_cuda and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
     if t.dtype is not dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if t.shape != shape or not t.is_contiguous():
-        raise ValueError("%s must be a contiguous tensor of shape %s" % (name, tuple(shape)))
-    if not t.is_cuda:
-        raise ValueError("%s must be a CUDA tensor" % name)
-    return t.data_ptr()
+    raise ValueError("%s must be a contiguous CUDA tensor of shape %s" % (name, tuple(shape)))
 
 
 _HALF = {torch.bfloat16: BF16, torch.float16: F16}
@@ -400,6 +399,7 @@ def dspark_kv_write(k, v, k_cache, v_cache, slots, rows=None, stream=None):
           _arg("rows", rows, torch.int32, slots.shape), slots.numel(), _stream(stream))
 
 
+@functools.lru_cache(maxsize=256)
 def dspark_tree_attention_workspace_bytes(B, nodes, n_heads, n_kv_heads, head_dim):
     return int(_lib.load().dspark_tree_attention_workspace_bytes(B, nodes, n_heads, n_kv_heads,
                                                                  head_dim))
@@ -662,12 +662,11 @@ def cache_plan(ctx_len, new_len, max_new, page_size, block_table, free_blocks, n
     """Grants the step's blocks and maps its new tokens; returns dict(block_table (the caller's,
     updated), slots, positions [B, max_new], taken [1], status [B]) and, for max_new <= 64,
     tree_mask int64 [B, max_new]."""
-    B, dev, i32 = ctx_len.shape[0], ctx_len.device, torch.int32
-    out = {"block_table": block_table, "slots": _empty((B, max_new), i32, dev),
-           "positions": _empty((B, max_new), i32, dev), "taken": _empty((1,), i32, dev),
-           "status": _empty((B,), i32, dev)}
+    B, new = ctx_len.shape[0], ctx_len.new_empty  # int32, checked by the call
+    out = {"block_table": block_table, "slots": new((B, max_new)),
+           "positions": new((B, max_new)), "taken": new((1,)), "status": new((B,))}
     if max_new <= MAX_NODES:
-        out["tree_mask"] = _empty((B, max_new), torch.int64, dev)
+        out["tree_mask"] = new((B, max_new), dtype=torch.int64)
     dspark_cache_plan(ctx_len, new_len, max_new, page_size, block_table, free_blocks, n_free,
                       parents, out["slots"], out["positions"], out.get("tree_mask"), out["taken"],
                       out["status"], stream)
@@ -690,12 +689,11 @@ def tree_attention(q, k_cache, v_cache, block_table, ctx_len, n_nodes, tree_mask
             return tree_attention(q, k_cache, v_cache, block_table, ctx_len, n_nodes, tree_mask,
                                   scale)
     B, nodes, heads, dim = q.shape
-    dev = q.device
-    out = _empty(q.shape, q.dtype, dev)
-    lse = _empty((B, nodes, heads), torch.float32, dev)
-    st = _empty((B,), torch.int32, dev)
-    ws = _empty((dspark_tree_attention_workspace_bytes(B, nodes, heads, k_cache.shape[2], dim),),
-                torch.uint8, dev)
+    out = q.new_empty(q.shape)
+    lse = q.new_empty((B, nodes, heads), dtype=torch.float32)
+    st = ctx_len.new_empty((B,))  # int32, checked by the call
+    ws = q.new_empty((dspark_tree_attention_workspace_bytes(B, nodes, heads, k_cache.shape[2],
+                                                            dim),), dtype=torch.uint8)
     dspark_tree_attention(q, k_cache, v_cache, block_table, ctx_len, n_nodes, tree_mask,
                           dim ** -0.5 if scale is None else scale, out, lse, st, ws, stream)
     return out, lse, st
@@ -708,8 +706,8 @@ def logits_process(logits, history=None, prompt_len=None, history_len=None, draf
     """Penalties, biases and grammar masks on logits [B, rows, V]; returns (out (a new tensor when
     None; logits itself for in place), status [B])."""
     if out is None:
-        out = _empty(logits.shape, logits.dtype, logits.device)
-    st = _empty((logits.shape[0],), torch.int32, logits.device)
+        out = logits.new_empty(logits.shape)
+    st = logits.new_empty((logits.shape[0],), dtype=torch.int32)
     dspark_logits_process(logits, history, prompt_len, history_len, draft_tokens, row_mask,
                           repetition, frequency, presence, bias_ids, bias_values, n_bias,
                           mask_words, mask_rows, out, st, stream)

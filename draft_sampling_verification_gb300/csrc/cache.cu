@@ -18,7 +18,7 @@ namespace dspark {
 namespace {
 
 constexpr int kPlanThreads = 256;
-constexpr int kPlanCells = 1024;   // (request, token) pairs a CTA plans at once
+constexpr int kPlanCells = 1024;   // most (request, token) pairs of a CTA
 constexpr int kPlanMaxGroup = kPlanThreads;  // one thread takes one request's need
 
 struct PlanParams {
@@ -37,7 +37,7 @@ struct PlanParams {
   uint64_t* mask;
   int32_t* taken;
   int32_t* status;
-  int group, span;  // requests per CTA; tokens of each per CTA
+  int group, span;  // requests per CTA (at most kPlanMaxGroup); tokens of each per CTA
 };
 
 struct Need {
@@ -190,17 +190,23 @@ cudaError_t launch_cache_plan(const int32_t* ctx, const int32_t* added, int B, i
   p.mask = mask;
   p.taken = taken;
   p.status = status;
-  p.group = max_new >= kPlanCells ? 1 : kPlanCells / max_new;
+  // one pair a thread while that makes no more CTAs than the GPU holds at
+  // once, else four: a CTA's time is its chain of loads, not its pairs
+  const int cells = (int64_t)B * max_new <= 1024 * kPlanThreads ? kPlanThreads : kPlanCells;
+  p.group = max_new >= cells ? 1 : cells / max_new;
   if (p.group > kPlanMaxGroup) p.group = kPlanMaxGroup;
-  p.span = max_new < kPlanCells ? max_new : kPlanCells;
+  p.span = max_new < cells ? max_new : cells;
   const dim3 grid((B + p.group - 1) / p.group, (max_new + p.span - 1) / p.span);
   cache_plan_kernel<<<grid, kPlanThreads, 0, stream>>>(p);
   return cudaGetLastError();
 }
 
 // ------------------------------------------------------------ cache write
-// A thread moves 8 elements of one token and head, of the keys or of the
-// values (blockIdx.y): 16 bytes written; 16 read, or 32 from fp32.
+// A piece is 8 elements of one token and head, of the keys or of the values
+// (blockIdx.y): 16 bytes written; 16 read, or 32 from fp32.  A thread moves
+// kUnroll pieces, whose sources it reads before it knows their slots: one
+// where the pieces do not fill the GPU, four to keep more reads in flight
+// where they do.
 namespace {
 
 constexpr int kWriteThreads = 256;
@@ -214,7 +220,7 @@ struct WriteParams {
   int n_blocks, page;
   const int32_t* slots;
   const int32_t* rows;
-  int64_t pieces;                           // n_tokens * n_heads * vecs
+  int n_tokens;
 };
 
 template <typename T>
@@ -232,33 +238,51 @@ __device__ __forceinline__ uint32_t round_pair<__half>(float a, float b) {
 
 }  // namespace
 
-template <typename T, bool kFromF32>
+template <typename T, bool kFromF32, int kUnroll>
 __global__ void __launch_bounds__(kWriteThreads) kv_write_kernel(const WriteParams p) {
   const void* src = p.src[blockIdx.y];
   T* cache = static_cast<T*>(p.cache[blockIdx.y]);
-  for (int64_t i = (int64_t)blockIdx.x * kWriteThreads + threadIdx.x; i < p.pieces;
-       i += (int64_t)gridDim.x * kWriteThreads) {
-    const int per = p.n_heads * p.vecs;
-    const int token = (int)(i / per);
-    const int rest = (int)(i - (int64_t)token * per);
-    const int head = rest / p.vecs, vec = rest - head * p.vecs;
-    const int slot = p.slots[token];
+  const uint32_t per = (uint32_t)(p.n_heads * p.vecs), vecs = (uint32_t)p.vecs;
+  // the CTA's pieces begin inside one token: from there 32-bit divisions do
+  const int64_t first = (int64_t)blockIdx.x * (kWriteThreads * kUnroll);
+  const int token0 = (int)(first / per);
+  const uint32_t rest0 = (uint32_t)(first - (int64_t)token0 * per);
+  uint4 w[kUnroll];
+  float4 f[kUnroll][2];
+  int slot[kUnroll];
+  uint32_t at[kUnroll];  // the piece within its token
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u) {
+    const uint32_t i = rest0 + u * kWriteThreads + threadIdx.x;
+    const int token = token0 + (int)(i / per);
+    at[u] = i % per;
+    slot[u] = -1;
+    if (token >= p.n_tokens) continue;
     const int row = p.rows ? p.rows[token] : token;
-    if (slot < 0 || slot >= p.n_blocks * p.page || row < 0 || row >= p.n_src) continue;
-    const int block = slot / p.page;
-    const int64_t from = row * p.src_token + head * p.src_head + vec * 8;
-    const int64_t to = block * p.block_stride + (int64_t)(slot - block * p.page) * p.token_stride +
-                       head * p.head_stride + vec * 8;
-    uint4 w;
+    if (row < 0 || row >= p.n_src) continue;
+    slot[u] = p.slots[token];
+    const uint32_t head = at[u] / vecs;
+    const int64_t from = row * p.src_token + head * p.src_head + (at[u] - head * vecs) * 8;
     if constexpr (kFromF32) {
-      const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(src) + from);
-      const float4 a = __ldcs(f), b = __ldcs(f + 1);
-      w = make_uint4(round_pair<T>(a.x, a.y), round_pair<T>(a.z, a.w), round_pair<T>(b.x, b.y),
-                     round_pair<T>(b.z, b.w));
+      const float4* x = reinterpret_cast<const float4*>(static_cast<const float*>(src) + from);
+      f[u][0] = __ldcs(x);
+      f[u][1] = __ldcs(x + 1);
     } else {
-      w = __ldcs(reinterpret_cast<const uint4*>(static_cast<const T*>(src) + from));
+      w[u] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const T*>(src) + from));
     }
-    *reinterpret_cast<uint4*>(cache + to) = w;
+  }
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u) {
+    if (slot[u] < 0 || slot[u] >= p.n_blocks * p.page) continue;
+    const int block = slot[u] / p.page;
+    const uint32_t head = at[u] / vecs;
+    const int64_t to = block * p.block_stride +
+                       (int64_t)(slot[u] - block * p.page) * p.token_stride +
+                       head * p.head_stride + (at[u] - head * vecs) * 8;
+    if constexpr (kFromF32)
+      w[u] = make_uint4(round_pair<T>(f[u][0].x, f[u][0].y), round_pair<T>(f[u][0].z, f[u][0].w),
+                        round_pair<T>(f[u][1].x, f[u][1].y), round_pair<T>(f[u][1].z, f[u][1].w));
+    *reinterpret_cast<uint4*>(cache + to) = w[u];
   }
 }
 
@@ -285,21 +309,23 @@ cudaError_t launch_kv_write(const void* k, const void* v, int src_dtype, int64_t
   p.page = page;
   p.slots = slots;
   p.rows = rows;
-  p.pieces = (int64_t)n_tokens * n_heads * p.vecs;
-  const int64_t want = (p.pieces + kWriteThreads - 1) / kWriteThreads;
-  const dim3 grid((unsigned)(want < (1 << 20) ? want : (1 << 20)), 2);
-  if (cache_dtype == DSPARK_BF16) {
-    if (src_dtype == DSPARK_F32)
-      kv_write_kernel<__nv_bfloat16, true><<<grid, kWriteThreads, 0, stream>>>(p);
-    else
-      kv_write_kernel<__nv_bfloat16, false><<<grid, kWriteThreads, 0, stream>>>(p);
-  } else {
-    if (src_dtype == DSPARK_F32)
-      kv_write_kernel<__half, true><<<grid, kWriteThreads, 0, stream>>>(p);
-    else
-      kv_write_kernel<__half, false><<<grid, kWriteThreads, 0, stream>>>(p);
-  }
-  return cudaGetLastError();
+  p.n_tokens = n_tokens;
+  const int64_t pieces = (int64_t)n_tokens * n_heads * p.vecs;
+  const bool few = pieces <= 1024 * kWriteThreads;
+  const int64_t per_cta = kWriteThreads * (few ? 1 : 4);
+  const dim3 grid((unsigned)((pieces + per_cta - 1) / per_cta), 2);
+  auto launch = [&](auto* one, auto* four) {
+    (few ? one : four)<<<grid, kWriteThreads, 0, stream>>>(p);
+    return cudaGetLastError();
+  };
+  using B16 = __nv_bfloat16;
+  if (cache_dtype == DSPARK_BF16)
+    return src_dtype == DSPARK_F32
+               ? launch(kv_write_kernel<B16, true, 1>, kv_write_kernel<B16, true, 4>)
+               : launch(kv_write_kernel<B16, false, 1>, kv_write_kernel<B16, false, 4>);
+  return src_dtype == DSPARK_F32
+             ? launch(kv_write_kernel<__half, true, 1>, kv_write_kernel<__half, true, 4>)
+             : launch(kv_write_kernel<__half, false, 1>, kv_write_kernel<__half, false, 4>);
 }
 
 DSPARK_CHECK_COLLECTOR(cache)

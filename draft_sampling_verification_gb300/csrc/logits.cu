@@ -50,7 +50,7 @@ struct LParams {
   int64_t ld_out;
   int32_t* status;
   int slice;       // vocabulary ids per CTA (a multiple of 256)
-  int row_step;    // CTAs over a request's rows (gridDim.z)
+  int row_step;    // rows per CTA
   int bias_cap;    // entries of the shared bias array
 };
 
@@ -89,38 +89,64 @@ __device__ __forceinline__ T minus_inf() {
   return narrow<T>(-INFINITY);
 }
 
-// elements [0, n) of a row's slice, of which element i is token v0 + i:
-// copied, or -infinity where the mask has a 0.  Sixteen bytes at a time where
-// source and destination share their alignment, else one element at a time.
+// A row's part in the CTA's slice, for the copy.
 template <typename T>
-__device__ void masked_copy(const T* x, T* out, int v0, int n, const uint32_t* words,
-                            int n_words) {
+struct RowPart {
+  const T* x;             // element 0 is token v0
+  T* out;
+  const uint32_t* words;  // the row's mask, or NULL
+  int head, vecs;         // 16-byte pieces [head, head + vecs * kVec); the rest one by one
+  bool copied;            // false: in place and without a mask, nothing to do
+};
+
+// Copies the slice's n elements of `rows` rows, with -infinity where a row's
+// mask has a 0.  Sixteen bytes at a time where a row's source and destination
+// share their alignment, else one element at a time.  The pieces of all rows
+// stand in one line, so that every thread has kUnroll loads in flight
+// whatever the rows' and the slice's sizes.
+template <typename T>
+__device__ __forceinline__ void masked_copy(const RowPart<T>* parts, int rows, int slice, int v0,
+                                            int n, int n_words) {
   constexpr int kVec = 16 / sizeof(T);
-  const uintptr_t ax = reinterpret_cast<uintptr_t>(x) & 15, ao = reinterpret_cast<uintptr_t>(out) & 15;
-  int head = n, vecs = 0;
-  if (ax == ao) {
-    head = min(n, (int)(((16 - ax) & 15) / sizeof(T)));
-    vecs = (n - head) / kVec;
-  }
-  const int tail = head + vecs * kVec;
-  for (int i = threadIdx.x; i < head + (n - tail); i += kLThreads) {
-    const int e = i < head ? i : tail + (i - head);
-    const bool on = !words || (mask_bits(words, v0 + e, 1, n_words) & 1u);
-    out[e] = on ? x[e] : minus_inf<T>();
-  }
-  if (!words && x == out) return;
-  const uint4* xv = reinterpret_cast<const uint4*>(x + head);
-  uint4* ov = reinterpret_cast<uint4*>(out + head);
-  for (int i = threadIdx.x; i < vecs; i += kLThreads) {
-    uint4 q = __ldcs(xv + i);
-    if (words) {
-      const uint32_t bits = mask_bits(words, v0 + head + i * kVec, kVec, n_words);
-      T* e = reinterpret_cast<T*>(&q);
+  constexpr int kUnroll = 6;
+  const int per = slice / kVec;  // places of a row in the line
+  const int all = rows * per;
+  for (int i0 = threadIdx.x; i0 < all; i0 += kUnroll * kLThreads) {
+    uint4 q[kUnroll];
+    uint32_t bits[kUnroll];
+    T* to[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int i = i0 + u * kLThreads;
+      const int r = i / per, at = i - r * per;
+      to[u] = nullptr;
+      if (i >= all) continue;
+      const RowPart<T> part = parts[r];
+      if (at >= part.vecs) continue;
+      const int e = part.head + at * kVec;
+      q[u] = __ldcs(reinterpret_cast<const uint4*>(part.x + e));
+      bits[u] = part.words ? mask_bits(part.words, v0 + e, kVec, n_words) : ~0u;
+      to[u] = part.out + e;
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      if (!to[u]) continue;
+      T* e = reinterpret_cast<T*>(&q[u]);
 #pragma unroll
       for (int j = 0; j < kVec; ++j)
-        if (!((bits >> j) & 1u)) e[j] = minus_inf<T>();
+        if (!((bits[u] >> j) & 1u)) e[j] = minus_inf<T>();
+      __stcs(reinterpret_cast<uint4*>(to[u]), q[u]);
     }
-    __stcs(ov + i, q);
+  }
+  for (int r = 0; r < rows; ++r) {
+    const RowPart<T> part = parts[r];
+    if (!part.copied) continue;
+    const int tail = part.head + part.vecs * kVec;
+    for (int i = threadIdx.x; i < part.head + (n - tail); i += kLThreads) {
+      const int e = i < part.head ? i : tail + (i - part.head);
+      const bool on = !part.words || (mask_bits(part.words, v0 + e, 1, n_words) & 1u);
+      part.out[e] = on ? part.x[e] : minus_inf<T>();
+    }
   }
 }
 
@@ -134,6 +160,8 @@ __global__ void __launch_bounds__(kLThreads) logits_process_kernel(const LParams
   uint16_t* list = reinterpret_cast<uint16_t*>(bias + p.bias_cap);  // [slice] touched tokens
   __shared__ int32_t s_draft[DSPARK_MAX_NODES];
   __shared__ uint32_t s_count, s_twice;
+  __shared__ RowPart<T> s_part[DSPARK_MAX_NODES];
+  __shared__ uint64_t s_seen[DSPARK_MAX_NODES];  // the drafts before each row
   const int tid = threadIdx.x;
   const int b = blockIdx.y;
   const int v0 = blockIdx.x * p.slice;
@@ -149,12 +177,45 @@ __global__ void __launch_bounds__(kLThreads) logits_process_kernel(const LParams
   if (tid == 0 && blockIdx.x == 0 && blockIdx.z == 0)
     p.status[b] = bad ? DSPARK_ST_BAD_PENALTY : DSPARK_ST_OK;
   if (bad) {
-    for (int r = blockIdx.z; r < p.rows; r += p.row_step) {
+    for (int r = blockIdx.z * p.row_step; r < min(p.rows, (int)(blockIdx.z + 1) * p.row_step);
+         ++r) {
       T* row = out + ((int64_t)b * p.rows + r) * p.ld_out + v0;
       for (int i = tid; i < n; i += kLThreads) row[i] = minus_inf<T>();
     }
     return;
   }
+
+  // this CTA's rows: r0, r0 + 1, ...
+  const int r0 = blockIdx.z * p.row_step, rows = min(p.row_step, p.rows - r0);
+  if (tid < rows) {
+    constexpr int kVec = 16 / sizeof(T);
+    const int64_t row = (int64_t)b * p.rows + r0 + tid;
+    RowPart<T> part;
+    part.x = x + row * p.ld + v0;
+    part.out = out + row * p.ld_out + v0;
+    part.words = nullptr;
+    if (p.words) {
+      const int64_t m = p.mask_rows ? (int64_t)p.mask_rows[row] : row;
+      if (m >= 0 && m < p.n_masks) part.words = p.words + m * p.mask_ld;
+    }
+    part.copied = part.words || (const void*)part.x != (const void*)part.out;
+    const uintptr_t ax = reinterpret_cast<uintptr_t>(part.x) & 15;
+    part.head = n;
+    part.vecs = 0;
+    if (!part.copied) {
+      part.head = 0;
+    } else if (ax == (reinterpret_cast<uintptr_t>(part.out) & 15)) {
+      part.head = min(n, (int)(((16 - ax) & 15) / sizeof(T)));
+      part.vecs = (n - part.head) / kVec;
+    }
+    s_part[tid] = part;
+    s_seen[tid] = p.row_mask ? p.row_mask[row] : (1ull << (r0 + tid)) - 1ull;
+  }
+  __syncthreads();
+  // the rows go through first: the copies are in flight while the text is
+  // counted.  In place, a row without a mask is left as it is; a token that
+  // its mask lets through still holds its input below.
+  masked_copy(s_part, rows, p.slice, v0, n, n_words);
 
   for (int i = tid; i < n; i += kLThreads) table[i] = 0u;
   if (tid == 0) s_count = s_twice = 0u;
@@ -222,34 +283,23 @@ __global__ void __launch_bounds__(kLThreads) logits_process_kernel(const LParams
   __syncthreads();
   const int touched = (int)s_count;
 
-  for (int r = blockIdx.z; r < p.rows; r += p.row_step) {
-    const int64_t row = (int64_t)b * p.rows + r;
-    const T* xr = x + row * p.ld + v0;
-    T* yr = out + row * p.ld_out + v0;
-    const uint32_t* words = nullptr;
-    if (p.words) {
-      const int64_t m = p.mask_rows ? (int64_t)p.mask_rows[row] : row;
-      if (m >= 0 && m < p.n_masks) words = p.words + m * p.mask_ld;
-    }
-    const uint64_t seen = p.row_mask ? p.row_mask[row] : (r < 64 ? (1ull << r) - 1ull : ~0ull);
-    // in place, an unmasked token still holds its input when it is computed
-    if (words || (const void*)xr != (const void*)yr) masked_copy(xr, yr, v0, n, words, n_words);
-    __syncthreads();
-    for (int i = tid; i < touched; i += kLThreads) {
-      const int t = list[i];
-      if (words && !(mask_bits(words, v0 + t, 1, n_words) & 1u)) continue;
-      const uint32_t w = table[t];
-      uint32_t c = w & kCountBits;
-      if (w & kDrafted)
-        for (int j = 0; j < p.n_drafts; ++j)
-          if (((seen >> j) & 1ull) && s_draft[j] == v0 + t) ++c;
-      float y = widen(xr[t]);
-      if (c > 0u || (w & kPrompt)) y = y > 0.0f ? __fdiv_rn(y, R) : __fmul_rn(y, R);
-      y = __fsub_rn(y, __fmul_rn(F, (float)c));
-      if (c > 0u) y = __fsub_rn(y, P);
-      if (i < n_biased) y = __fadd_rn(y, bias[i]);
-      yr[t] = narrow<T>(y);
-    }
+  // each touched token of each row, from its input
+  for (int k = tid; k < touched * rows; k += kLThreads) {
+    const int r = k / touched, i = k - r * touched;
+    const RowPart<T> part = s_part[r];
+    const int t = list[i];
+    if (part.words && !(mask_bits(part.words, v0 + t, 1, n_words) & 1u)) continue;
+    const uint32_t w = table[t];
+    uint32_t c = w & kCountBits;
+    if (w & kDrafted)
+      for (int j = 0; j < p.n_drafts; ++j)
+        if (((s_seen[r] >> j) & 1ull) && s_draft[j] == v0 + t) ++c;
+    float y = widen(part.x[t]);
+    if (c > 0u || (w & kPrompt)) y = y > 0.0f ? __fdiv_rn(y, R) : __fmul_rn(y, R);
+    y = __fsub_rn(y, __fmul_rn(F, (float)c));
+    if (c > 0u) y = __fsub_rn(y, P);
+    if (i < n_biased) y = __fadd_rn(y, bias[i]);
+    part.out[t] = narrow<T>(y);
   }
 }
 
@@ -289,10 +339,15 @@ cudaError_t launch_logits_process(
   p.ld_out = ld_out;
   p.status = status;
   p.slice = 4096;
-  p.row_step = 1;
+  const int slices = (V + p.slice - 1) / p.slice;
+  // a CTA takes all rows of its request, as the text is counted once for
+  // them, unless that leaves SMs without work
+  const int64_t ctas = (int64_t)slices * B, wanted = 1024;
+  const int parts = (int)(ctas >= wanted ? 1 : (wanted + ctas - 1) / ctas);
+  p.row_step = parts >= rows ? 1 : (rows + parts - 1) / parts;
   p.bias_cap = max_bias < p.slice ? max_bias : p.slice;
   const size_t smem = (size_t)p.slice * 6 + (size_t)p.bias_cap * 4;
-  const dim3 grid((V + p.slice - 1) / p.slice, B, p.row_step);
+  const dim3 grid(slices, B, (rows + p.row_step - 1) / p.row_step);
   if (dtype == DSPARK_F32)
     logits_process_kernel<float><<<grid, kLThreads, smem, stream>>>(p);
   else

@@ -130,11 +130,15 @@ __device__ __forceinline__ uint32_t without_special(uint32_t w) {
 // keys at the same time, so that all but the first find them in L2.  An item
 // that lies inside one range is finished by its team; the others leave
 // partial rows in the workspace for the joining kernel.  Each item has at
-// least one tile (a request without tokens still writes its zero rows).
+// least one tile (a request without tokens still writes its zero rows), and
+// counts for kItemCost tiles more, ahead of its first: the time that its
+// queries, its first copies and its results take, without which the teams
+// that get many short items end last.
 constexpr int kMaxCtas = 320;
+constexpr int kItemCost = 5;
 
-struct Start {  // where a team's range begins
-  int b, head, tile, tiles;
+struct Start {  // where a team's range begins: `at` into the item, of kItemCost + tiles
+  int b, head, at, tiles;
 };
 
 struct Workspace {
@@ -180,12 +184,51 @@ __device__ __forceinline__ int request_tiles(const Params& p, int b, int tile) {
   return len > 0 ? (len - 1) / tile + 1 : 1;
 }
 
-// the team whose range holds tile x of `total`, and the first tile of team c
+// the team whose range holds point x of the axis, and the first point of team c
 __device__ __forceinline__ int owner_of(int64_t x, int64_t total, int teams) {
   return (int)(((x + 1) * teams - 1) / total);
 }
 __device__ __forceinline__ int64_t first_of(int c, int64_t total, int teams) {
   return (int64_t)c * total / teams;
+}
+
+// A CTA's way along its range.
+struct Walk {
+  int64_t left;  // of the range
+  int b, head, tiles;
+  int at;             // into the item
+  int first, count;   // the tiles of the item that are this CTA's
+  // the part of the range in the current item; false at the range's end
+  __device__ __forceinline__ bool part() {
+    if (left <= 0) return false;
+    const int take = (int)min(left, (int64_t)(kItemCost + tiles - at));
+    first = max(0, at - kItemCost);
+    count = max(0, at + take - kItemCost) - first;
+    left -= take;
+    return true;
+  }
+  __device__ __forceinline__ void next(const Params& p, int tile) {
+    at = 0;
+    if (++head == p.kv_heads) {
+      head = 0;
+      ++b;
+    }
+    if (left > 0) tiles = request_tiles(p, b, tile);
+  }
+  __device__ __forceinline__ bool whole() const { return count == tiles; }
+  __device__ __forceinline__ int64_t slot() const {  // of the partial rows
+    return 2ll * blockIdx.x + (first == 0 ? 1 : 0);
+  }
+};
+__device__ __forceinline__ Walk walk_from(const Start& s, int64_t left) {
+  Walk w;
+  w.left = left;
+  w.b = s.b;
+  w.head = s.head;
+  w.tiles = s.tiles;
+  w.at = s.at;
+  w.first = w.count = 0;
+  return w;
 }
 
 // This CTA's range of the tile axis: its length, and where it begins (shared
@@ -197,7 +240,7 @@ __device__ __forceinline__ int64_t find_range(const Params& p, int tile, const W
   const int per = (p.B + kBlock - 1) / kBlock;
   const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
   uint64_t sum = 0, total_u;
-  for (int b = b0; b < b1; ++b) sum += (uint64_t)request_tiles(p, b, tile) * p.kv_heads;
+  for (int b = b0; b < b1; ++b) sum += (uint64_t)(request_tiles(p, b, tile) + kItemCost) * p.kv_heads;
   const uint64_t upto = block_inclusive_scan_u64(sum, scan, &total_u);
   const int64_t total = (int64_t)total_u;
   const int teams = (int)min((int64_t)(gridDim.x / p.row_tiles), total);
@@ -208,9 +251,10 @@ __device__ __forceinline__ int64_t find_range(const Params& p, int tile, const W
   if (x0 >= at && x0 < (int64_t)upto) {
     for (int b = b0; b < b1; ++b) {
       const int tiles = request_tiles(p, b, tile);
-      const int64_t end = at + (int64_t)tiles * p.kv_heads;
+      const int item = tiles + kItemCost;
+      const int64_t end = at + (int64_t)item * p.kv_heads;
       if (x0 < end) {
-        *start = {b, (int)((x0 - at) / tiles), (int)((x0 - at) % tiles), tiles};
+        *start = {b, (int)((x0 - at) / item), (int)((x0 - at) % item), tiles};
         if (blockIdx.x % p.row_tiles == 0) ws.start[team] = *start;
         break;
       }
@@ -279,8 +323,8 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int mw = warp % MW, kw = warp / MW;
   const Workspace ws = carve(p.workspace, kRows);
-  int64_t left = find_range<kThreads>(p, S::kTile, ws, s_scan, &s_start);
-  Start cur = s_start;
+  const int64_t range = find_range<kThreads>(p, S::kTile, ws, s_scan, &s_start);
+  Walk cur = walk_from(s_start, range);
   const int r0 = (blockIdx.x % p.row_tiles) * kRows;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
@@ -289,18 +333,19 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2)
   const bool whole = p.page % kKeys == 0;  // a step lies in one block
   const uint32_t ring = smem_u32(smem) + kw * kStages * S::kStageBytes;
 
-  while (left > 0) {
-    const int tiles = (int)min(left, (int64_t)(cur.tiles - cur.tile));
+  for (; cur.part(); cur.next(p, S::kTile)) {
+    const int tiles = cur.count;
+    if (tiles == 0) continue;
     const Lengths len = request_lengths(p, cur.b);
     const int kvh = cur.head;
     const int32_t* table = p.table + cur.b * p.table_ld;
     const int live = len.nodes * p.group;  // rows below this one have a node
 
-    if (tid == 0 && r0 == 0 && kvh == 0 && cur.tile == 0)
+    if (tid == 0 && r0 == 0 && kvh == 0 && cur.first == 0)
       p.status[cur.b] = len.bad ? DSPARK_ST_BAD_LENGTH : DSPARK_ST_OK;
 
     // ---- copies: 16 positions of this group into a stage of its ring
-    const int first = cur.tile * S::kTile + kw * kKeys;  // this group's first position
+    const int first = cur.first * S::kTile + kw * kKeys;  // this group's first position
     const int64_t head_off = kvh * p.head_stride;
     auto entry_of = [&](int step) -> int {  // the block of this lane's position in a step
       const int pos = first + step * S::kTile + (whole ? 0 : (lane & 15));
@@ -545,8 +590,8 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2)
         }
       }
     __syncthreads();
-    const bool full = tiles == cur.tiles;
-    const int64_t slot = 2ll * blockIdx.x + (cur.tile == 0 ? 1 : 0);
+    const bool full = cur.whole();
+    const int64_t slot = cur.slot();
     for (int i = tid; i < kRows * (D / 4); i += kThreads) {
       const int r = i / (D / 4), d = (i % (D / 4)) * 4;
       const int row = r0 + r;
@@ -588,14 +633,6 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2)
       }
     }
     __syncthreads();
-
-    left -= tiles;
-    cur.tile = 0;
-    if (++cur.head == p.kv_heads) {
-      cur.head = 0;
-      ++cur.b;
-    }
-    if (left > 0) cur.tiles = request_tiles(p, cur.b, S::kTile);
   }
 }
 
@@ -617,8 +654,8 @@ __global__ void __launch_bounds__(kJoinThreads)
   const int teams = (int)min((int64_t)(grid / p.row_tiles), total);
   if (i >= teams) return;
   const Start at = ws.start[i];
-  if (at.tile == 0) return;
-  const int64_t begin = first_of(i, total, teams) - at.tile;
+  if (at.at <= kItemCost) return;  // before the item's second tile: not split here
+  const int64_t begin = first_of(i, total, teams) - at.at + kItemCost;
   const int c0 = owner_of(begin, total, teams);
   if (c0 != i - 1) return;
   const int c1 = owner_of(begin + at.tiles - 1, total, teams);

@@ -16,33 +16,49 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t addr, uint32_t lead, u
   return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(lead >> 4) << 16) |
          ((uint64_t)(stride >> 4) << 32) | (1ull << 46) | (2ull << 61);
 }
-// d[tmem] (+)= a b with a and b in shared memory
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                       bool add) {
+// One lane of a converged warp: the products' operands are warp-uniform, and
+// stay in uniform registers when only the instruction itself is predicated.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(p));
+  return p != 0u;
+}
+// d[tmem] (+)= a b with a and b in shared memory, by the lane with `on`
+__device__ __forceinline__ void mma_ss(bool on, uint32_t d, uint64_t a, uint64_t b,
+                                       uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add), "r"((uint32_t)on)
       : "memory");
 }
 // the same with a in tensor memory
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
-                                       bool add) {
+__device__ __forceinline__ void mma_ts(bool on, uint32_t d, uint32_t a, uint64_t b,
+                                       uint32_t idesc, bool add) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add), "r"((uint32_t)on)
       : "memory");
 }
 // arrives on `bar` once every product issued before it is done
-__device__ __forceinline__ void mma_commit(uint64_t* bar) {
+__device__ __forceinline__ void mma_commit(bool on, uint64_t* bar) {
   asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-          smem_u32(bar))
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+          smem_u32(bar)),
+      "r"((uint32_t)on)
       : "memory");
 }
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+// arrives on `bar` once every cp.async that this thread has issued is done
+__device__ __forceinline__ void mbar_arrive_copied(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar))
+               : "memory");
 }
 __device__ __forceinline__ void fence_async_shared() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -54,7 +70,7 @@ __device__ __forceinline__ void tc_after_sync() {
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
 // 32 columns of this warp's 32 lanes
-__device__ __forceinline__ void tmem_load32(float (&v)[32], uint32_t addr) {
+__device__ __forceinline__ void tmem_load32(float* v, uint32_t addr) {
   uint32_t r[32];
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
@@ -78,14 +94,24 @@ __device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t (&r)[
       "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
-__device__ __forceinline__ void tmem_store32(uint32_t addr, const float (&v)[32]) {
-  uint32_t r[16];
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(v[h * 16 + i]);
-    tmem_store16(addr + h * 16, r);
-  }
+__device__ __forceinline__ void tmem_load16(uint32_t (&r)[16], uint32_t addr) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(addr)
+      : "memory");
+}
+// registers of a warpgroup's threads beside the launch's 128
+template <int kRegs>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
 }
 __device__ __forceinline__ void tmem_wait_load() {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
@@ -110,9 +136,10 @@ __device__ __forceinline__ void tmem_wait_store() {
 //
 // Warps 0-3 and 4-7: softmax, Q and the results of row tile 0 and 1.  Warps
 // 8-11: copies of keys and values into two stages each.  Warp 12: issues the
-// products.  K and Q lie in rows of 64 dims (128 bytes, swizzled in groups of
+// products (its warpgroup is whole because registers are shared out by
+// warpgroup: 2 * 192 + 72 + 56 a thread of the launch's 4 * 128).  K and Q lie in rows of 64 dims (128 bytes, swizzled in groups of
 // eight rows); V the same, read with dims as its major axis.
-constexpr int kWideThreads = 416;
+constexpr int kWideThreads = 512;
 constexpr int kWideRows = 256;
 constexpr int kWideTile = 128;
 
@@ -148,12 +175,10 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   const uint32_t q_at = base, k_at = base + 2 * W::kOperand, v_at = base + 4 * W::kOperand;
 
   const Workspace ws = carve(p.workspace, kWideRows);
-  int64_t left = find_range<kWideThreads>(p, kWideTile, ws, sh.scan, &sh.start);
+  const int64_t range = find_range<kWideThreads>(p, kWideTile, ws, sh.scan, &sh.start);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (left <= 0) return;
-  Start cur = sh.start;
-  const Start begin = cur;
-  const int64_t all_tiles = left;
+  if (range <= 0) return;
+  Walk cur = walk_from(sh.start, range);
   const int r0 = (blockIdx.x % p.row_tiles) * kWideRows;
   const int n_tiles = p.nodes * p.group - r0 > 128 ? 2 : 1;
 
@@ -194,18 +219,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     *(volatile uint32_t*)&sh.failed = 1u;
     return false;
   };
-  auto segment = [&]() -> int { return (int)min(left, (int64_t)(cur.tiles - cur.tile)); };
-  auto next = [&](int tiles) {
-    left -= tiles;
-    cur.tile = 0;
-    if (++cur.head == p.kv_heads) {
-      cur.head = 0;
-      ++cur.b;
-    }
-    if (left > 0) cur.tiles = request_tiles(p, cur.b, kWideTile);
-  };
-
   if (warp < 8) {
+    more_registers<192>();
     // -------------------------------------------------- softmax and results
     const int m = warp >> 2;
     const int t = tid & 127;  // this thread's row of the tile and lane of tensor memory
@@ -217,11 +232,12 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     const float scale = fmaxf(fabsf(p.scale2), 1.17549435e-38f);
     uint32_t tile_no = 0, segments = 0;
     bool ok = m < n_tiles;
-    while (ok && left > 0) {
-      const int tiles = segment();
+    for (; ok && cur.part(); cur.next(p, kWideTile)) {
+      const int tiles = cur.count;
+      if (tiles == 0) continue;
       const Lengths len = request_lengths(p, cur.b);
       const int live = len.nodes * p.group;
-      if (tid == 0 && r0 == 0 && cur.head == 0 && cur.tile == 0)
+      if (tid == 0 && r0 == 0 && cur.head == 0 && cur.first == 0)
         p.status[cur.b] = len.bad ? DSPARK_ST_BAD_LENGTH : DSPARK_ST_OK;
 
       // Q, 16 bytes at a time
@@ -261,39 +277,37 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         if (!ok) break;
         tc_after_sync();
         if (i > 0) special |= sh.special[(tile_no - 1u) & 3u] != 0u;
-        const int pos = (cur.tile + i) * kWideTile;
+        const int pos = (cur.first + i) * kWideTile;
         const uint32_t* words = sh.valid[tile_no & 3u];
         const bool plain = pos + kWideTile <= len.ctx &&
                            (words[0] & words[1] & words[2] & words[3]) == 0xFFFFFFFFu;
-        // scores of chunk c: positions pos + 32 c ..; -infinity where the row does not see them
-        float v[32];
-        auto load_scores = [&](int c) {
-          tmem_load32(v, sc + c * 32);
-          tmem_wait_load();
-          if (plain) return;
-          uint32_t w = words[c];
-          const int node0 = pos + c * 32 - len.ctx;  // the node of the chunk's first position
-          if (node0 >= 0)
-            w &= node0 < 64 ? (uint32_t)(mask >> node0) : 0u;
-          else if (node0 > -32)
-            w &= (uint32_t)(mask << -node0) | ((1u << -node0) - 1u);
+        float v[128];
 #pragma unroll
-          for (int j = 0; j < 32; ++j)
-            if (!((w >> j) & 1u)) v[j] = -INFINITY;
-        };
-        float top = -INFINITY;
+        for (int c = 0; c < 4; ++c) tmem_load32(v + c * 32, sc + c * 32);
+        tmem_wait_load();
+        if (!plain) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          load_scores(c);
-          float a = v[0], z = v[1];
+          for (int c = 0; c < 4; ++c) {
+            uint32_t w = words[c];
+            const int node0 = pos + c * 32 - len.ctx;  // the node of the chunk's first position
+            if (node0 >= 0)
+              w &= node0 < 64 ? (uint32_t)(mask >> node0) : 0u;
+            else if (node0 > -32)
+              w &= (uint32_t)(mask << -node0) | ((1u << -node0) - 1u);
 #pragma unroll
-          for (int j = 2; j < 32; j += 2) {
-            a = fmaxf(a, v[j]);
-            z = fmaxf(z, v[j + 1]);
+            for (int j = 0; j < 32; ++j)
+              if (!((w >> j) & 1u)) v[c * 32 + j] = -INFINITY;
           }
-          top = fmaxf(top, fmaxf(a, z));
         }
-        top *= scale;
+        float m4[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+        for (int j = 4; j < 124; j += 8) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) m4[k] = fmaxf(fmaxf(m4[k], v[j + k]), v[j + 4 + k]);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) m4[k] = fmaxf(m4[k], v[124 + k]);
+        float top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * scale;
         if (__any_sync(0xffffffffu, top > ref + kSlack)) {
           top = fmaxf(top, ref);
           const float f = top == -INFINITY ? 1.0f : exp2_approx(ref - top);
@@ -302,30 +316,35 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           sum2.y *= f;
           if (i > 0) {
 #pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-              tmem_load32(v, oc + c * 32);
+            for (int c = 0; c < D / 16; ++c) {
+              uint32_t a[16];
+              tmem_load16(a, oc + c * 16);
               tmem_wait_load();
 #pragma unroll
-              for (int j = 0; j < 32; ++j) v[j] *= f;
-              tmem_store32(oc + c * 32, v);
+              for (int j = 0; j < 16; ++j) a[j] = __float_as_uint(__uint_as_float(a[j]) * f);
+              tmem_store16(oc + c * 16, a);
             }
           }
         }
         const float2 off = f2(ref == -INFINITY ? 0.0f : -ref), by = f2(scale);
+        float2 part2 = make_float2(0.0f, 0.0f);
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          load_scores(c);
           uint32_t w[16];
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
-            float2 x = fma2_rn(make_float2(v[2 * j], v[2 * j + 1]), by, off);
+            float2 x = fma2_rn(make_float2(v[c * 32 + 2 * j], v[c * 32 + 2 * j + 1]), by, off);
             x.x = exp2_approx(x.x);
             x.y = exp2_approx(x.y);
-            sum2 = add2_rn(sum2, x);
+            if (j & 1)
+              part2 = add2_rn(part2, x);
+            else
+              sum2 = add2_rn(sum2, x);
             w[j] = H::pack(x.x, x.y);
           }
           tmem_store16(sc + c * 16, w);
         }
+        sum2 = add2_rn(sum2, part2);
         tmem_wait_store();
         tc_before_sync();
         mbar_arrive(&sh.p_full[m]);
@@ -341,10 +360,10 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         ref = -INFINITY;
         sum = 0.0f;
       }
-      const bool full = tiles == cur.tiles;
+      const bool full = cur.whole();
       const int h = cur.head * p.group + row - node * p.group;
       const int64_t to = ((int64_t)cur.b * p.nodes + node) * p.heads + h;
-      const int64_t slot = 2ll * blockIdx.x + (cur.tile == 0 ? 1 : 0);
+      const int64_t slot = cur.slot();
       const bool mine = row < p.nodes * p.group;
       const float inv = sum == 0.0f ? 0.0f : full ? 1.0f / sum : 1.0f;
 #pragma unroll 1
@@ -361,7 +380,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
 #pragma unroll 1
           for (int k = 0; k < len.nodes; ++k) {
             const int at = len.ctx + k, tile = at / kWideTile;
-            if (!((mask >> k) & 1ull) || tile < cur.tile || tile >= cur.tile + tiles) continue;
+            if (!((mask >> k) & 1ull) || tile < cur.first || tile >= cur.first + tiles) continue;
             const int block = p.table[cur.b * p.table_ld + at / p.page];
             if (block < 0 || block >= p.n_blocks) continue;
             const T* from = static_cast<const T*>(p.v) + block * p.block_stride +
@@ -398,9 +417,9 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           p.lse[to] = sum == 0.0f ? -INFINITY : (ref + log2f(sum)) * 0.6931471805599453f;
       }
       tc_before_sync();  // the accumulators are read: the next item may take them
-      next(tiles);
     }
   } else if (warp < 12) {
+    fewer_registers<72>();
     // ------------------------------------------------------ keys and values
     const int t = tid - 256;
     const T* kc = static_cast<const T*>(p.k);
@@ -408,7 +427,6 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     uint32_t g = 0;
     bool ok = true;             // this thread's waits
     bool go = true;             // everybody's, agreed on at each tile
-    int node_row = kWideTile;   // of the tile before: its first row that holds a node
     auto copy = [&](const T* cache, uint32_t to) {
       const int64_t* offset = sh.offset[g & 1u];
 #pragma unroll
@@ -418,49 +436,45 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         cp_async16(to + (c >> 3) * 16384 + r * 128 + (((c & 7) ^ (r & 7)) << 4),
                    cache + (off >= 0 ? off + c * 8 : 0), off >= 0);
       }
-      cp_async_commit();
     };
-    // this thread's pieces of the values of tile n are there: those of nodes
-    // are cleared of infinities and NaN, which would reach rows that do not
-    // see them (0 times infinity)
-    auto values_landed = [&](uint32_t n) {
-      if (node_row < kWideTile) {
-        const uint32_t at = v_at + (n & 1u) * W::kOperand;
+    // a tile that holds nodes, from row node_row on: its values are cleared of
+    // infinities and NaN, which would reach rows that do not see them (0 times
+    // infinity), before the products may read them
+    auto clear_values = [&](int node_row) {
+      const uint32_t at = v_at + (g & 1u) * W::kOperand;
+      asm volatile("cp.async.wait_all;" ::: "memory");
 #pragma unroll 1
-        for (int i = 0; i < kChunks; ++i) {
-          const int r = (i * 128 + t) / kChunks, c = (i * 128 + t) % kChunks;
-          if (r < node_row) continue;
-          const uint32_t addr = at + (c >> 3) * 16384 + r * 128 + (((c & 7) ^ (r & 7)) << 4);
-          uint32_t w[4];
-          asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                       : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                       : "r"(addr)
+      for (int i = 0; i < kChunks; ++i) {  // the pieces that this thread copied
+        const int r = (i * 128 + t) / kChunks, c = (i * 128 + t) % kChunks;
+        if (r < node_row) continue;
+        const uint32_t addr = at + (c >> 3) * 16384 + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+        uint32_t w[4];
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                     : "r"(addr)
+                     : "memory");
+        if (any_special<T>(w[0]) || any_special<T>(w[1]) || any_special<T>(w[2]) ||
+            any_special<T>(w[3])) {
+          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr),
+                       "r"(without_special<T>(w[0])), "r"(without_special<T>(w[1])),
+                       "r"(without_special<T>(w[2])), "r"(without_special<T>(w[3]))
                        : "memory");
-          if (any_special<T>(w[0]) || any_special<T>(w[1]) || any_special<T>(w[2]) ||
-              any_special<T>(w[3])) {
-            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr),
-                         "r"(without_special<T>(w[0])), "r"(without_special<T>(w[1])),
-                         "r"(without_special<T>(w[2])), "r"(without_special<T>(w[3]))
-                         : "memory");
-            *(volatile uint32_t*)&sh.special[n & 3u] = 1u;
-          }
+          *(volatile uint32_t*)&sh.special[g & 3u] = 1u;
         }
       }
-      fence_async_shared();
-      mbar_arrive(&sh.v_full[n & 1u]);
     };
-    while (go && left > 0) {
-      const int tiles = segment();
+    for (; go && cur.part(); cur.next(p, kWideTile)) {
+      const int tiles = cur.count;
       const Lengths len = request_lengths(p, cur.b);
       const int32_t* table = p.table + cur.b * p.table_ld;
       const int64_t head_off = cur.head * p.head_stride;
       auto entry_of = [&](int i) -> int {
-        const int pos = (cur.tile + i) * kWideTile + t;
+        const int pos = (cur.first + i) * kWideTile + t;
         return i < tiles && pos < len.len ? __ldg(table + pos / p.page) : -1;
       };
       int ahead = entry_of(0);
       for (int i = 0; i < tiles; ++i, ++g) {
-        const int pos = (cur.tile + i) * kWideTile + t, block = ahead;
+        const int pos = (cur.first + i) * kWideTile + t, block = ahead;
         ahead = entry_of(i + 1);
         const bool held = block >= 0 && block < p.n_blocks;
         sh.offset[g & 1u][t] =
@@ -482,78 +496,95 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         if (!go) break;
         if (lane == 0) sh.valid[g & 3u][t >> 5] = bits;
         copy(kc, k_at + (g & 1u) * W::kOperand);
-        if (g > 0) {
-          cp_async_wait<1>();
-          values_landed(g - 1u);
-        }
+        mbar_arrive_copied(&sh.k_full[g & 1u]);
         ok = wait(&sh.v_empty[g & 1u], ((g >> 1) & 1u) ^ 1u);
         copy(vc, v_at + (g & 1u) * W::kOperand);
-        node_row = max(0, min(kWideTile, len.ctx - (pos - t)));
-        cp_async_wait<1>();
-        fence_async_shared();
-        mbar_arrive(&sh.k_full[g & 1u]);
+        const int node_row = len.ctx - (pos - t);
+        if (node_row < kWideTile) {
+          clear_values(node_row);
+          fence_async_shared();
+          mbar_arrive(&sh.v_full[g & 1u]);
+        } else {
+          mbar_arrive_copied(&sh.v_full[g & 1u]);
+        }
       }
-      if (go) next(tiles);
     }
-    cp_async_wait<0>();
-    if (go) values_landed(g - 1u);
-  } else if (lane == 0) {
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  } else {
+    fewer_registers<56>();
+  }
+  if (warp == 12) {
     // ------------------------------------------------------------- products
-    constexpr uint32_t kFormat = sizeof(T) == 2 && H::kExponent == 0x7F80u ? 1u : 0u;
+    // The warp goes through the loop together; one lane issues.
+    constexpr uint32_t kFormat = H::kExponent == 0x7F80u ? 1u : 0u;  // bf16 or f16
     // fp32 accumulators, both operands of T, 128 rows; for P V the second has its dims outermost
     constexpr uint32_t kCommon = (1u << 4) | (kFormat << 7) | (kFormat << 10) | (8u << 24);
     constexpr uint32_t kScores = kCommon | ((kWideTile / 8u) << 17);
     constexpr uint32_t kValues = kCommon | (1u << 16) | (((uint32_t)D / 8u) << 17);
+    const bool on = elect_one();
+    // descriptors of Q's tiles, and of the stages of keys and values; an
+    // operand further on adds its distance / 16
+    const uint64_t q_desc = operand_desc(q_at, 16, 1024), k_desc = operand_desc(k_at, 16, 1024);
+    const uint64_t v_desc = operand_desc(v_at, 16384, 1024);
     auto scores = [&](int m, uint32_t g) {
+      const uint64_t a = q_desc + (uint32_t)m * (W::kOperand / 16);
+      const uint64_t b = k_desc + (g & 1u) * (W::kOperand / 16);
 #pragma unroll
       for (int kt = 0; kt < D / 16; ++kt) {
-        const uint32_t at = (kt >> 2) * 16384 + (kt & 3) * 32;
-        mma_ss(s_col(m), operand_desc(q_at + m * W::kOperand + at, 16, 1024),
-               operand_desc(k_at + (g & 1u) * W::kOperand + at, 16, 1024), kScores, kt > 0);
+        constexpr int kHalf = 16384 / 16, kStep = 32 / 16;
+        const uint32_t at = (kt >> 2) * kHalf + (kt & 3) * kStep;
+        mma_ss(on, s_col(m), a + at, b + at, kScores, kt > 0);
       }
-      mma_commit(&sh.s_full[m]);
+      mma_commit(on, &sh.s_full[m]);
     };
     auto values = [&](int m, uint32_t g, bool add) {
+      const uint64_t b = v_desc + (g & 1u) * (W::kOperand / 16);
 #pragma unroll
       for (int kt = 0; kt < kWideTile / 16; ++kt)
-        mma_ts(o_col(m), s_col(m) + kt * 8,
-               operand_desc(v_at + (g & 1u) * W::kOperand + kt * 2048, 16384, 1024), kValues,
-               add || kt > 0);
+        mma_ts(on, o_col(m), s_col(m) + kt * 8, b + kt * (2048 / 16), kValues, add || kt > 0);
+    };
+    auto wait_all = [&](uint64_t* bar, uint32_t phase) -> bool {
+      return __all_sync(0xffffffffu, wait(bar, phase));
     };
     uint32_t g = 0, segments = 0;
     bool ok = true;
-    while (ok && left > 0) {
-      const int tiles = segment();
-      for (int m = 0; m < n_tiles; ++m) ok = ok && wait(&sh.q_full[m], segments & 1u);
-      ok = ok && wait(&sh.k_full[g & 1u], (g >> 1) & 1u);
+    for (; ok && cur.part(); cur.next(p, kWideTile)) {
+      const int tiles = cur.count;
+      if (tiles == 0) continue;
+      for (int m = 0; m < n_tiles; ++m) ok = ok && wait_all(&sh.q_full[m], segments & 1u);
+      ok = ok && wait_all(&sh.k_full[g & 1u], (g >> 1) & 1u);
       if (!ok) break;
       tc_after_sync();
+      fence_async_shared();  // the copies, seen through their barrier, for the products' reads
       for (int m = 0; m < n_tiles; ++m) scores(m, g);
-      mma_commit(&sh.k_empty[g & 1u]);
+      mma_commit(on, &sh.k_empty[g & 1u]);
       for (int i = 0; i < tiles && ok; ++i, ++g) {
         const bool more = i + 1 < tiles;
         for (int m = 0; m < n_tiles; ++m) {
-          ok = ok && wait(&sh.p_full[m], g & 1u);
-          if (m == 0) ok = ok && wait(&sh.v_full[g & 1u], (g >> 1) & 1u);
+          ok = wait_all(&sh.p_full[m], g & 1u);
+          if (m == 0) ok = ok && wait_all(&sh.v_full[g & 1u], (g >> 1) & 1u);
           if (!ok) break;
           tc_after_sync();
+          if (m == 0) fence_async_shared();
           values(m, g, i > 0);
-          if (m == n_tiles - 1) mma_commit(&sh.v_empty[g & 1u]);
+          if (m == n_tiles - 1) mma_commit(on, &sh.v_empty[g & 1u]);
           if (more) {
-            if (m == 0) ok = wait(&sh.k_full[(g + 1u) & 1u], ((g + 1u) >> 1) & 1u);
+            if (m == 0) {
+              ok = wait_all(&sh.k_full[(g + 1u) & 1u], ((g + 1u) >> 1) & 1u);
+              fence_async_shared();
+            }
             if (!ok) break;
             scores(m, g + 1u);
           } else {
-            mma_commit(&sh.o_full[m]);
+            mma_commit(on, &sh.o_full[m]);
           }
         }
-        if (ok && more) mma_commit(&sh.k_empty[(g + 1u) & 1u]);
+        if (ok && more) mma_commit(on, &sh.k_empty[(g + 1u) & 1u]);
       }
       ++segments;
-      if (ok) next(tiles);
     }
     // nothing of this CTA's is in flight when its memory is given back
-    mma_commit(&sh.drained);
+    mma_commit(on, &sh.drained);
     mbar_wait_bounded(&sh.drained, 0);
   }
   __syncwarp();
@@ -564,12 +595,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
   }
   if (sh.failed && tid == 0) {  // the requests of this range are refused
-    left = all_tiles;
-    cur = begin;
-    while (left > 0) {
+    for (cur = walk_from(sh.start, range); cur.part(); cur.next(p, kWideTile))
       p.status[cur.b] = DSPARK_ST_TIMEOUT;
-      next(segment());
-    }
   }
 }
 
