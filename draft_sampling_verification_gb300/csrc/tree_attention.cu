@@ -6,7 +6,10 @@
 namespace dspark {
 
 int64_t tree_attention_workspace_bytes(int B, int nodes, int heads, int kv_heads, int head_dim) {
-  return attn::workspace_bytes(attn::shape_rows(nodes * (heads / kv_heads), head_dim), head_dim);
+  const int rows = nodes * (heads / kv_heads);
+  return attn::workspace_bytes(rows > 64 && head_dim != 256 ? attn::kWideRows
+                                                            : attn::shape_rows(rows, head_dim),
+                               head_dim);
 }
 
 cudaError_t launch_tree_attention(const void* q, int dtype, int64_t q_req, int64_t q_node,

@@ -135,6 +135,7 @@ __device__ __forceinline__ uint32_t without_special(uint32_t w) {
 // queries, its first copies and its results take, without which the teams
 // that get many short items end last.
 constexpr int kMaxCtas = 320;
+constexpr int kWideRows = 256;  // rows of a CTA of the wide kernel
 constexpr int kItemCost = 5;
 
 struct Start {  // where a team's range begins: `at` into the item, of kItemCost + tiles
@@ -744,11 +745,10 @@ cudaError_t launch_shape(Params p, int sms, cudaStream_t stream) {
   return e != cudaSuccess ? e : launch_join<T, D>(p, S::kRows, grid, stream);
 }
 
-// rows of a CTA for `rows` rows of an item: the smallest shape that holds
-// them all; beyond 64 the wide kernel's 256, or tiles of 64 for head_dim 256
+// rows of a streaming CTA for `rows` rows of an item: the smallest shape that
+// holds them all, else tiles of 64
 inline int shape_rows(int rows, int dim) {
   const int eights = (rows + 7) / 8;
-  if (eights > 8 && dim != 256) return 256;
   if (eights <= 2) return 8 * eights;
   if (eights <= 4) return dim == 256 ? 32 : 8 * eights;
   return eights <= 6 && dim != 256 ? 48 : 64;

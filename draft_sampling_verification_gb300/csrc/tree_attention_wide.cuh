@@ -4,6 +4,8 @@
 // tree_attention.cuh.
 #pragma once
 
+#include <cuda.h>
+
 #include "tree_attention.cuh"
 
 namespace dspark {
@@ -55,10 +57,15 @@ __device__ __forceinline__ void mma_commit(bool on, uint64_t* bar) {
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
-// arrives on `bar` once every cp.async that this thread has issued is done
-__device__ __forceinline__ void mbar_arrive_copied(uint64_t* bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar))
-               : "memory");
+// one box of a cache, from (dim x, row r of head h of block b), completing on `bar`; a block
+// beyond the cache gives zeros
+__device__ __forceinline__ void tma_load_box(uint32_t dst, const CUtensorMap* map, int x, int r,
+                                             int h, int b, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(r), "r"(h), "r"(b), "r"(smem_u32(bar))
+      : "memory");
 }
 __device__ __forceinline__ void fence_async_shared() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -134,45 +141,51 @@ __device__ __forceinline__ void tmem_wait_store() {
 // softmax warpgroup may then rescale them.  It does so only when a score
 // passes the row's reference by more than 8, as in the streaming kernel.
 //
-// Warps 0-3 and 4-7: softmax, Q and the results of row tile 0 and 1.  Warps
-// 8-11: copies of keys and values into two stages each.  Warp 12: issues the
-// products (its warpgroup is whole because registers are shared out by
+// Warps 0-3 and 4-7: softmax, Q and the results of row tile 0 and 1.  Warp 8:
+// tensor copies of keys and values, box by box of a block's rows, into a ring
+// of stages each.  Warps 9-11: where a tile holds nodes, clear its values of
+// infinities and NaN.  Warp 12: issues the products (its warpgroup is whole because registers are shared out by
 // warpgroup: 2 * 192 + 72 + 56 a thread of the launch's 4 * 128).  K and Q lie in rows of 64 dims (128 bytes, swizzled in groups of
 // eight rows); V the same, read with dims as its major axis.
 constexpr int kWideThreads = 512;
-constexpr int kWideRows = 256;
 constexpr int kWideTile = 128;
 
 template <int D>
 struct Wide {
   static constexpr int kHalves = D / 64;
-  static constexpr int kOperand = 128 * D * 2;  // 128 rows of Q, K or V
-  static constexpr int kSmem = 6 * kOperand + 1024;
+  static constexpr int kOperand = 128 * D * 2;  // bytes of 128 rows of Q, K or V
+  static constexpr int kStages = D == 64 ? 4 : 2;
+  static constexpr int kSmem = (2 + 2 * kStages) * kOperand + 1024;
 };
+constexpr int kWideMaxStages = 4;
+constexpr int kClearThreads = 96;
 
 struct WideShared {
-  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
+  uint64_t k_full[kWideMaxStages], k_empty[kWideMaxStages];
+  uint64_t v_full[kWideMaxStages], v_empty[kWideMaxStages];
+  uint64_t v_nodes[kWideMaxStages], v_clear[kWideMaxStages];
   uint64_t q_full[2], s_full[2], p_full[2], o_full[2], drained;
   uint64_t scan[32];
   Start start;
-  int64_t offset[2][kWideTile];  // of a tile's rows in the caches; -1: no key
-  uint32_t valid[4][4];          // the same as bits, by tile number modulo 4
-  uint32_t special[4];           // a value of a tile's nodes is an infinity or a NaN
+  uint32_t valid[8][4];  // a tile's positions that hold a key, by tile number modulo 8
+  uint32_t special[8];   // a value of a tile's nodes is an infinity or a NaN
   uint32_t tmem;
-  uint32_t failed;               // a wait expired
+  uint32_t failed;       // a wait expired
 };
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kWideThreads, 1)
-    tree_attention_wide_kernel(const __grid_constant__ Params p) {
+    tree_attention_wide_kernel(const __grid_constant__ Params p,
+                               const __grid_constant__ CUtensorMap k_map,
+                               const __grid_constant__ CUtensorMap v_map, int box_rows) {
   using H = Half<T>;
   using W = Wide<D>;
-  constexpr int kChunks = D / 8;
+  constexpr int kChunks = D / 8, kStages = W::kStages;
   extern __shared__ unsigned char smem_raw[];
   __shared__ WideShared sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  const uint32_t q_at = base, k_at = base + 2 * W::kOperand, v_at = base + 4 * W::kOperand;
+  const uint32_t q_at = base, k_at = base + 2 * W::kOperand, v_at = k_at + kStages * W::kOperand;
 
   const Workspace ws = carve(p.workspace, kWideRows);
   const int64_t range = find_range<kWideThreads>(p, kWideTile, ws, sh.scan, &sh.start);
@@ -183,11 +196,15 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   const int n_tiles = p.nodes * p.group - r0 > 128 ? 2 : 1;
 
   if (tid == 0) {
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&sh.k_full[i], 128);
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&sh.k_full[i], 1);
       mbar_init(&sh.k_empty[i], 1);
-      mbar_init(&sh.v_full[i], 128);
+      mbar_init(&sh.v_full[i], 1);
       mbar_init(&sh.v_empty[i], 1);
+      mbar_init(&sh.v_nodes[i], 1);
+      mbar_init(&sh.v_clear[i], kClearThreads);
+    }
+    for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.q_full[i], 128);
       mbar_init(&sh.s_full[i], 1);
       mbar_init(&sh.p_full[i], 128);
@@ -276,9 +293,9 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         ok = __all_sync(0xffffffffu, wait(&sh.s_full[m], tile_no & 1u));
         if (!ok) break;
         tc_after_sync();
-        if (i > 0) special |= sh.special[(tile_no - 1u) & 3u] != 0u;
+        if (i > 0) special |= sh.special[(tile_no - 1u) & 7u] != 0u;
         const int pos = (cur.first + i) * kWideTile;
-        const uint32_t* words = sh.valid[tile_no & 3u];
+        const uint32_t* words = sh.valid[tile_no & 7u];
         const bool plain = pos + kWideTile <= len.ctx &&
                            (words[0] & words[1] & words[2] & words[3]) == 0xFFFFFFFFu;
         float v[128];
@@ -353,7 +370,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       ++segments;
       if (!ok) break;
       tc_after_sync();
-      special |= sh.special[(tile_no - 1u) & 3u] != 0u;
+      special |= sh.special[(tile_no - 1u) & 7u] != 0u;
 
       float sum = sum2.x + sum2.y;
       if (row >= live) {  // a row of no node: its zero query saw the text all the same
@@ -421,95 +438,96 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   } else if (warp < 12) {
     fewer_registers<72>();
     // ------------------------------------------------------ keys and values
-    const int t = tid - 256;
-    const T* kc = static_cast<const T*>(p.k);
-    const T* vc = static_cast<const T*>(p.v);
-    uint32_t g = 0;
-    bool ok = true;             // this thread's waits
-    bool go = true;             // everybody's, agreed on at each tile
-    auto copy = [&](const T* cache, uint32_t to) {
-      const int64_t* offset = sh.offset[g & 1u];
-#pragma unroll
-      for (int i = 0; i < kChunks; ++i) {
-        const int r = (i * 128 + t) / kChunks, c = (i * 128 + t) % kChunks;
-        const int64_t off = offset[r];
-        cp_async16(to + (c >> 3) * 16384 + r * 128 + (((c & 7) ^ (r & 7)) << 4),
-                   cache + (off >= 0 ? off + c * 8 : 0), off >= 0);
-      }
-    };
-    // a tile that holds nodes, from row node_row on: its values are cleared of
-    // infinities and NaN, which would reach rows that do not see them (0 times
-    // infinity), before the products may read them
-    auto clear_values = [&](int node_row) {
-      const uint32_t at = v_at + (g & 1u) * W::kOperand;
-      asm volatile("cp.async.wait_all;" ::: "memory");
-#pragma unroll 1
-      for (int i = 0; i < kChunks; ++i) {  // the pieces that this thread copied
-        const int r = (i * 128 + t) / kChunks, c = (i * 128 + t) % kChunks;
-        if (r < node_row) continue;
-        const uint32_t addr = at + (c >> 3) * 16384 + r * 128 + (((c & 7) ^ (r & 7)) << 4);
-        uint32_t w[4];
-        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                     : "r"(addr)
-                     : "memory");
-        if (any_special<T>(w[0]) || any_special<T>(w[1]) || any_special<T>(w[2]) ||
-            any_special<T>(w[3])) {
-          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr),
-                       "r"(without_special<T>(w[0])), "r"(without_special<T>(w[1])),
-                       "r"(without_special<T>(w[2])), "r"(without_special<T>(w[3]))
-                       : "memory");
-          *(volatile uint32_t*)&sh.special[g & 3u] = 1u;
-        }
-      }
-    };
-    for (; go && cur.part(); cur.next(p, kWideTile)) {
+    // Lane i copies the tile's box i, box_rows positions of one block.
+    const int boxes = kWideTile / box_rows;  // at most 16
+    uint32_t g = 0, turns = 0;  // turns: each stage's phase of the tiles with nodes
+    bool ok = true;
+    for (; ok && cur.part(); cur.next(p, kWideTile)) {
       const int tiles = cur.count;
       const Lengths len = request_lengths(p, cur.b);
-      const int32_t* table = p.table + cur.b * p.table_ld;
-      const int64_t head_off = cur.head * p.head_stride;
-      auto entry_of = [&](int i) -> int {
-        const int pos = (cur.first + i) * kWideTile + t;
-        return i < tiles && pos < len.len ? __ldg(table + pos / p.page) : -1;
-      };
-      int ahead = entry_of(0);
-      for (int i = 0; i < tiles; ++i, ++g) {
-        const int pos = (cur.first + i) * kWideTile + t, block = ahead;
-        ahead = entry_of(i + 1);
-        const bool held = block >= 0 && block < p.n_blocks;
-        sh.offset[g & 1u][t] =
-            held ? block * p.block_stride + (int64_t)(pos % p.page) * p.token_stride + head_off
-                 : -1;
-        const uint32_t bits = __ballot_sync(0xffffffffu, held);
-        if (t == 0) sh.special[g & 3u] = 0u;
-        ok = ok && wait(&sh.k_empty[g & 1u], ((g >> 1) & 1u) ^ 1u);
-        {  // the offsets are written, and all or none go on
-          uint32_t all_ok;
-          asm volatile(
-              "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
-              "barrier.red.and.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-              : "=r"(all_ok)
-              : "r"((uint32_t)ok)
-              : "memory");
-          go = all_ok != 0u;
+      const int first = cur.first * kWideTile;
+      if (warp == 8) {
+        const int32_t* table = p.table + cur.b * p.table_ld;
+        auto entry_of = [&](int i) -> int {
+          const int pos = first + i * kWideTile + lane * box_rows;
+          return i < tiles && lane < boxes && pos < len.len ? __ldg(table + pos / p.page) : -1;
+        };
+        int ahead = entry_of(0);
+        for (int i = 0; i < tiles; ++i, ++g) {
+          const int pos0 = first + i * kWideTile, pos = pos0 + lane * box_rows, block = ahead;
+          ahead = entry_of(i + 1);
+          const bool held = block >= 0 && block < p.n_blocks;
+          const int from = held ? block : p.n_blocks, row = held ? pos % p.page : 0;
+          const uint32_t held_boxes = __ballot_sync(0xffffffffu, held);
+          const uint32_t stage = g % kStages, phase = (g / kStages) & 1u;
+          ok = __all_sync(0xffffffffu, wait(&sh.k_empty[stage], phase ^ 1u));
+          if (!ok) break;
+          if (lane < 4) {
+            uint32_t word = 0u;  // positions 32 lane .. of the tile
+            if (box_rows >= 32) {
+              word = (held_boxes >> (lane * 32 / box_rows)) & 1u ? ~0u : 0u;
+            } else {
+              for (int j = 0; j < 32 / box_rows; ++j)
+                if ((held_boxes >> (lane * 32 / box_rows + j)) & 1u)
+                  word |= ((1u << box_rows) - 1u) << (j * box_rows);
+            }
+            const int past = len.len - (pos0 + lane * 32);  // positions before the end
+            sh.valid[g & 7u][lane] = past >= 32 ? word : past > 0 ? word & ((1u << past) - 1u) : 0u;
+            sh.special[g & 7u] = 0u;
+          }
+          auto copy = [&](const CUtensorMap* map, uint32_t at, uint64_t* full) {
+            if (lane == 0) mbar_arrive_expect_tx(full, W::kOperand);
+            __syncwarp();
+            if (lane < boxes) {
+#pragma unroll
+              for (int h = 0; h < W::kHalves; ++h)
+                tma_load_box(at + stage * W::kOperand + h * 16384 + lane * box_rows * 128, map,
+                             h * 64, row, cur.head, from, full);
+            }
+          };
+          copy(&k_map, k_at, &sh.k_full[stage]);
+          ok = __all_sync(0xffffffffu, wait(&sh.v_empty[stage], phase ^ 1u));
+          if (!ok) break;
+          // values that are to be cleared first land on a barrier of their own
+          const bool nodes_here = pos0 + kWideTile > len.ctx;
+          copy(&v_map, v_at, nodes_here ? &sh.v_nodes[stage] : &sh.v_full[stage]);
+          if (nodes_here && lane == 0) mbar_arrive(&sh.v_full[stage]);
         }
-        if (!go) break;
-        if (lane == 0) sh.valid[g & 3u][t >> 5] = bits;
-        copy(kc, k_at + (g & 1u) * W::kOperand);
-        mbar_arrive_copied(&sh.k_full[g & 1u]);
-        ok = wait(&sh.v_empty[g & 1u], ((g >> 1) & 1u) ^ 1u);
-        copy(vc, v_at + (g & 1u) * W::kOperand);
-        const int node_row = len.ctx - (pos - t);
-        if (node_row < kWideTile) {
-          clear_values(node_row);
+      } else {
+        // Rows from the first node on: nodes, which some rows see and others
+        // do not, and what lies behind the end.  0 times an infinity or a NaN
+        // would reach rows that do not see it.
+        for (int i = 0; i < tiles; ++i, ++g) {
+          const int pos0 = first + i * kWideTile;
+          if (pos0 + kWideTile <= len.ctx) continue;
+          const uint32_t stage = g % kStages;
+          ok = __all_sync(0xffffffffu, wait(&sh.v_nodes[stage], (turns >> stage) & 1u));
+          if (!ok) break;
+          turns ^= 1u << stage;
+          const int from = max(0, len.ctx - pos0);
+          for (int j = tid - 288; j < (kWideTile - from) * kChunks; j += kClearThreads) {
+            const int r = from + j / kChunks, c = j % kChunks;
+            const uint32_t addr = v_at + stage * W::kOperand + (c >> 3) * 16384 + r * 128 +
+                                  (((c & 7) ^ (r & 7)) << 4);
+            uint32_t w[4];
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                         : "r"(addr)
+                         : "memory");
+            if (any_special<T>(w[0]) || any_special<T>(w[1]) || any_special<T>(w[2]) ||
+                any_special<T>(w[3])) {
+              asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr),
+                           "r"(without_special<T>(w[0])), "r"(without_special<T>(w[1])),
+                           "r"(without_special<T>(w[2])), "r"(without_special<T>(w[3]))
+                           : "memory");
+              if (pos0 + r < len.len) *(volatile uint32_t*)&sh.special[g & 7u] = 1u;
+            }
+          }
           fence_async_shared();
-          mbar_arrive(&sh.v_full[g & 1u]);
-        } else {
-          mbar_arrive_copied(&sh.v_full[g & 1u]);
+          mbar_arrive(&sh.v_clear[stage]);
         }
       }
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
   } else {
     fewer_registers<56>();
   }
@@ -528,7 +546,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     const uint64_t v_desc = operand_desc(v_at, 16384, 1024);
     auto scores = [&](int m, uint32_t g) {
       const uint64_t a = q_desc + (uint32_t)m * (W::kOperand / 16);
-      const uint64_t b = k_desc + (g & 1u) * (W::kOperand / 16);
+      const uint64_t b = k_desc + (g % kStages) * (W::kOperand / 16);
 #pragma unroll
       for (int kt = 0; kt < D / 16; ++kt) {
         constexpr int kHalf = 16384 / 16, kStep = 32 / 16;
@@ -538,7 +556,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       mma_commit(on, &sh.s_full[m]);
     };
     auto values = [&](int m, uint32_t g, bool add) {
-      const uint64_t b = v_desc + (g & 1u) * (W::kOperand / 16);
+      const uint64_t b = v_desc + (g % kStages) * (W::kOperand / 16);
 #pragma unroll
       for (int kt = 0; kt < kWideTile / 16; ++kt)
         mma_ts(on, o_col(m), s_col(m) + kt * 8, b + kt * (2048 / 16), kValues, add || kt > 0);
@@ -546,40 +564,43 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     auto wait_all = [&](uint64_t* bar, uint32_t phase) -> bool {
       return __all_sync(0xffffffffu, wait(bar, phase));
     };
-    uint32_t g = 0, segments = 0;
+    auto phase_of = [](uint32_t g) -> uint32_t { return (g / kStages) & 1u; };
+    uint32_t g = 0, segments = 0, turns = 0;
     bool ok = true;
     for (; ok && cur.part(); cur.next(p, kWideTile)) {
       const int tiles = cur.count;
       if (tiles == 0) continue;
+      const Lengths len = request_lengths(p, cur.b);
       for (int m = 0; m < n_tiles; ++m) ok = ok && wait_all(&sh.q_full[m], segments & 1u);
-      ok = ok && wait_all(&sh.k_full[g & 1u], (g >> 1) & 1u);
+      ok = ok && wait_all(&sh.k_full[g % kStages], phase_of(g));
       if (!ok) break;
       tc_after_sync();
-      fence_async_shared();  // the copies, seen through their barrier, for the products' reads
       for (int m = 0; m < n_tiles; ++m) scores(m, g);
-      mma_commit(on, &sh.k_empty[g & 1u]);
+      mma_commit(on, &sh.k_empty[g % kStages]);
       for (int i = 0; i < tiles && ok; ++i, ++g) {
         const bool more = i + 1 < tiles;
         for (int m = 0; m < n_tiles; ++m) {
           ok = wait_all(&sh.p_full[m], g & 1u);
-          if (m == 0) ok = ok && wait_all(&sh.v_full[g & 1u], (g >> 1) & 1u);
+          if (m == 0) {
+            ok = ok && wait_all(&sh.v_full[g % kStages], phase_of(g));
+            if ((cur.first + i + 1) * kWideTile > len.ctx) {
+              ok = ok && wait_all(&sh.v_clear[g % kStages], (turns >> (g % kStages)) & 1u);
+              turns ^= 1u << (g % kStages);
+            }
+          }
           if (!ok) break;
           tc_after_sync();
-          if (m == 0) fence_async_shared();
           values(m, g, i > 0);
-          if (m == n_tiles - 1) mma_commit(on, &sh.v_empty[g & 1u]);
+          if (m == n_tiles - 1) mma_commit(on, &sh.v_empty[g % kStages]);
           if (more) {
-            if (m == 0) {
-              ok = wait_all(&sh.k_full[(g + 1u) & 1u], ((g + 1u) >> 1) & 1u);
-              fence_async_shared();
-            }
+            if (m == 0) ok = wait_all(&sh.k_full[(g + 1u) % kStages], phase_of(g + 1u));
             if (!ok) break;
             scores(m, g + 1u);
           } else {
             mma_commit(on, &sh.o_full[m]);
           }
         }
-        if (ok && more) mma_commit(on, &sh.k_empty[(g + 1u) & 1u]);
+        if (ok && more) mma_commit(on, &sh.k_empty[(g + 1u) % kStages]);
       }
       ++segments;
     }
@@ -600,17 +621,60 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   }
 }
 
+// rows of a tensor copy: the most that divide a block and a tile; the swizzle
+// wants whole groups of eight
+inline int wide_box_rows(int page) {
+  int rows = kWideTile;
+  while (page % rows) rows /= 2;
+  return rows;
+}
+
+// the map of one cache: dims, rows of a block, heads, blocks
+template <typename T>
+bool map_cache(CUtensorMap* map, const Params& p, const void* cache, int dim, int box_rows) {
+  using Encode = decltype(&cuTensorMapEncodeTiled);
+  static const Encode encode = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
+                                         &found) != cudaSuccess ||
+        found != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return reinterpret_cast<Encode>(f);
+  }();
+  if (!encode) return false;
+  const cuuint64_t sizes[4] = {(cuuint64_t)dim, (cuuint64_t)p.page, (cuuint64_t)p.kv_heads,
+                               (cuuint64_t)p.n_blocks};
+  const cuuint64_t strides[3] = {(cuuint64_t)p.token_stride * 2, (cuuint64_t)p.head_stride * 2,
+                                 (cuuint64_t)p.block_stride * 2};
+  const cuuint32_t box[4] = {64, (cuuint32_t)box_rows, 1, 1}, steps[4] = {1, 1, 1, 1};
+  return encode(map,
+                Half<T>::kExponent == 0x7F80u ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                              : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                4, const_cast<void*>(cache), sizes, strides, box, steps,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// false: the cache's shape has no map, or blocks too short for one
 template <typename T, int D>
-cudaError_t launch_wide(Params p, int sms, cudaStream_t stream) {
+bool launch_wide(Params p, int sms, cudaStream_t stream, cudaError_t* error) {
+  const int box_rows = wide_box_rows(p.page);
+  CUtensorMap k_map, v_map;
+  if (box_rows < 8 || !map_cache<T>(&k_map, p, p.k, D, box_rows) ||
+      !map_cache<T>(&v_map, p, p.v, D, box_rows))
+    return false;
   p.row_tiles = (p.nodes * p.group + kWideRows - 1) / kWideRows;
   auto* kernel = tree_attention_wide_kernel<T, D>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       Wide<D>::kSmem);
-  if (e != cudaSuccess) return e;
+  *error = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                Wide<D>::kSmem);
+  if (*error != cudaSuccess) return true;
   const int grid = min(kMaxCtas, max(sms, p.row_tiles));
-  kernel<<<grid, kWideThreads, Wide<D>::kSmem, stream>>>(p);
-  e = cudaGetLastError();
-  return e != cudaSuccess ? e : launch_join<T, D>(p, kWideRows, grid, stream);
+  kernel<<<grid, kWideThreads, Wide<D>::kSmem, stream>>>(p, k_map, v_map, box_rows);
+  *error = cudaGetLastError();
+  if (*error == cudaSuccess) *error = launch_join<T, D>(p, kWideRows, grid, stream);
+  return true;
 }
 
 template <typename T, int D>
@@ -625,7 +689,8 @@ cudaError_t launch_dim(const Params& p, int sms, cudaStream_t stream) {
     if (rows == 24) return launch_shape<T, D, 3, 1>(p, sms, stream);
     if (rows == 32) return launch_shape<T, D, 4, 1>(p, sms, stream);
     if (rows == 48) return launch_shape<T, D, 3, 2>(p, sms, stream);
-    if (rows == 256) return launch_wide<T, D>(p, sms, stream);
+    cudaError_t e;
+    if (p.nodes * p.group > 64 && launch_wide<T, D>(p, sms, stream, &e)) return e;
     return launch_shape<T, D, 4, 2>(p, sms, stream);
   }
 }
