@@ -150,15 +150,16 @@ struct Workspace {
 };
 
 __host__ __device__ inline int64_t workspace_bytes(int rows, int dim) {
-  return 16 + (int64_t)kMaxCtas * sizeof(Start) +
+  return 64 + (int64_t)kMaxCtas * sizeof(Start) +
          2ll * kMaxCtas * rows * (sizeof(float2) + (int64_t)dim * sizeof(float));
 }
 
 __device__ __forceinline__ Workspace carve(char* w, int rows) {
-  Workspace s;
+  Workspace s;  // every part 32-byte aligned
+  w = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(w) + 31) & ~(uintptr_t)31);
   s.total = reinterpret_cast<int64_t*>(w);
-  s.start = reinterpret_cast<Start*>(w + 16);
-  s.stats = reinterpret_cast<float2*>(w + 16 + kMaxCtas * sizeof(Start));
+  s.start = reinterpret_cast<Start*>(w + 32);
+  s.stats = reinterpret_cast<float2*>(w + 32 + kMaxCtas * sizeof(Start));
   s.rows = reinterpret_cast<float*>(s.stats + 2 * kMaxCtas * rows);
   return s;
 }
@@ -193,28 +194,30 @@ __device__ __forceinline__ int64_t first_of(int c, int64_t total, int teams) {
   return (int64_t)c * total / teams;
 }
 
-// A CTA's way along its range.
+// A CTA's way along its range, item by item.
 struct Walk {
-  int64_t left;  // of the range
+  int64_t left;       // of the range
   int b, head, tiles;
   int at;             // into the item
   int first, count;   // the tiles of the item that are this CTA's
-  // the part of the range in the current item; false at the range's end
-  __device__ __forceinline__ bool part() {
-    if (left <= 0) return false;
-    const int take = (int)min(left, (int64_t)(kItemCost + tiles - at));
-    first = max(0, at - kItemCost);
-    count = max(0, at + take - kItemCost) - first;
-    left -= take;
-    return true;
-  }
-  __device__ __forceinline__ void next(const Params& p, int tile) {
-    at = 0;
-    if (++head == p.kv_heads) {
-      head = 0;
-      ++b;
+  // on to the next item of which a tile is this CTA's; false at the end
+  __device__ __forceinline__ bool advance(const Params& p, int tile) {
+    count = 0;
+    while (left > 0 && count == 0) {
+      if (at < 0) {  // the item before is done
+        at = 0;
+        if (++head == p.kv_heads) {
+          head = 0;
+          tiles = request_tiles(p, ++b, tile);
+        }
+      }
+      const int take = (int)min(left, (int64_t)(kItemCost + tiles - at));
+      first = max(0, at - kItemCost);
+      count = max(0, at + take - kItemCost) - first;
+      left -= take;
+      at = -1;
     }
-    if (left > 0) tiles = request_tiles(p, b, tile);
+    return count > 0;
   }
   __device__ __forceinline__ bool whole() const { return count == tiles; }
   __device__ __forceinline__ int64_t slot() const {  // of the partial rows
@@ -334,9 +337,8 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2)
   const bool whole = p.page % kKeys == 0;  // a step lies in one block
   const uint32_t ring = smem_u32(smem) + kw * kStages * S::kStageBytes;
 
-  for (; cur.part(); cur.next(p, S::kTile)) {
+  while (cur.advance(p, S::kTile)) {
     const int tiles = cur.count;
-    if (tiles == 0) continue;
     const Lengths len = request_lengths(p, cur.b);
     const int kvh = cur.head;
     const int32_t* table = p.table + cur.b * p.table_ld;
@@ -639,88 +641,113 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2)
 
 // ------------------------------------------------------- the joining kernel
 // CTA (x, y, z): if the boundary before the range of team x + 1 is the first
-// one inside its item, rows [8 y, 8 y + 8) of the item's row tile z are
-// joined from the teams' partial rows, a warp per row, in the teams' order.
+// one inside its item, a block of rows of the item's row tile z is joined
+// from the teams' partial rows, in the teams' order.  A warp takes kRowsAtOnce
+// rows, and kAhead teams' parts of them are in flight together: one row and
+// many parts for the streaming kernel's few rows, cut among many teams; four
+// rows for the wide kernel's.
 constexpr int kJoinThreads = 256;
 
-template <typename T, int D>
+template <typename T, int D, int kRowsAtOnce>
 __global__ void __launch_bounds__(kJoinThreads)
     tree_attention_join_kernel(const __grid_constant__ Params p, int rows, int grid) {
   using H = Half<T>;
-  constexpr int kPer = D / 32;
+  constexpr int kPer = D / 32, kJoinUnroll = kRowsAtOnce;
+  constexpr int kJoinRows = kJoinThreads / 32 * kRowsAtOnce, kAhead = 8 / kRowsAtOnce;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Workspace ws = carve(p.workspace, rows);
   const int i = blockIdx.x + 1;
   const int64_t total = *ws.total;
+  const Start at = ws.start[i];  // of a team without work: not looked at
   const int teams = (int)min((int64_t)(grid / p.row_tiles), total);
   if (i >= teams) return;
-  const Start at = ws.start[i];
   if (at.at <= kItemCost) return;  // before the item's second tile: not split here
   const int64_t begin = first_of(i, total, teams) - at.at + kItemCost;
   const int c0 = owner_of(begin, total, teams);
   if (c0 != i - 1) return;
   const int c1 = owner_of(begin + at.tiles - 1, total, teams);
   const int lane = threadIdx.x & 31;
-  const int r = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5);
-  const int row = blockIdx.z * rows + r;
-  if (r >= rows || row >= p.nodes * p.group) return;
+  const int r0 = blockIdx.y * kJoinRows + (threadIdx.x >> 5);
+  const int item_rows = p.nodes * p.group - blockIdx.z * rows;  // of this row tile, and more
+  const int n_rows = min(rows, item_rows);
   // the partial rows of team c: its first range's in slot 0, its last's in slot 1
   auto slot_of = [&](int c) -> int64_t {
-    return 2ll * (c * p.row_tiles + blockIdx.z) + (c == c0 ? 1 : 0);
+    return (2ll * (c * p.row_tiles + blockIdx.z) + (c == c0 ? 1 : 0)) * rows;
   };
 
-  float top = -INFINITY;
-  for (int c = c0 + lane; c <= c1; c += 32)
-    top = fmaxf(top, ws.stats[slot_of(c) * rows + r].x);
-  top = warp_reduce(top, OpMaxF());
-  const float safe = top == -INFINITY ? 0.0f : top;
-  float all = 0.0f, a[kPer];
+  float top[kJoinUnroll], all[kJoinUnroll], a[kJoinUnroll][kPer];
 #pragma unroll
-  for (int d = 0; d < kPer; ++d) a[d] = 0.0f;
-#pragma unroll 4
-  for (int c = c0; c <= c1; ++c) {
-    const int64_t slot = slot_of(c);
-    const float2 st = ws.stats[slot * rows + r];
-    const float f = exp2_approx(st.x - safe);
-    const float* v = ws.rows + (slot * rows + r) * D + lane * kPer;
-    float x[kPer];
-    if constexpr (kPer == 2) {
-      *reinterpret_cast<float2*>(x) = *reinterpret_cast<const float2*>(v);
-    } else {
+  for (int u = 0; u < kJoinUnroll; ++u) {
+    const int r = min(r0 + u * (kJoinThreads / 32), n_rows - 1);
+    top[u] = -INFINITY;
+    for (int c = c0 + lane; c <= c1; c += 32) top[u] = fmaxf(top[u], ws.stats[slot_of(c) + r].x);
+    all[u] = 0.0f;
 #pragma unroll
-      for (int d = 0; d < kPer; d += 4)
-        *reinterpret_cast<float4*>(x + d) = *reinterpret_cast<const float4*>(v + d);
-    }
-    all += st.y * f;
-#pragma unroll
-    for (int d = 0; d < kPer; ++d) a[d] += x[d] * f;
+    for (int d = 0; d < kPer; ++d) a[u][d] = 0.0f;
   }
-  const int node = row / p.group, h = at.head * p.group + row - node * p.group;
-  const int64_t to = ((int64_t)at.b * p.nodes + node) * p.heads + h;
-  const float inv = all == 0.0f ? 0.0f : 1.0f / all;
-  uint32_t w[kPer / 2];
 #pragma unroll
-  for (int d = 0; d < kPer; d += 2) w[d / 2] = H::pack(a[d] * inv, a[d + 1] * inv);
-  uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<T*>(p.out) + to * D) + lane * (kPer / 2);
-  if constexpr (kPer == 2)
-    *out = w[0];
-  else if constexpr (kPer == 4)
-    *reinterpret_cast<uint2*>(out) = make_uint2(w[0], w[1]);
-  else
-    *reinterpret_cast<uint4*>(out) = make_uint4(w[0], w[1], w[2], w[3]);
-  if (lane == 0 && p.lse)
-    p.lse[to] = all == 0.0f ? -INFINITY : (top + log2f(all)) * 0.6931471805599453f;
+  for (int u = 0; u < kJoinUnroll; ++u) {
+    top[u] = warp_reduce(top[u], OpMaxF());
+  }
+#pragma unroll kAhead
+  for (int c = c0; c <= c1; ++c) {
+    float2 st[kJoinUnroll];
+    float x[kJoinUnroll][kPer];
+#pragma unroll
+    for (int u = 0; u < kJoinUnroll; ++u) {
+      const int r = min(r0 + u * (kJoinThreads / 32), n_rows - 1);
+      st[u] = ws.stats[slot_of(c) + r];
+      const float* v = ws.rows + (slot_of(c) + r) * D + lane * kPer;
+      if constexpr (kPer == 2) {
+        *reinterpret_cast<float2*>(x[u]) = *reinterpret_cast<const float2*>(v);
+      } else {
+#pragma unroll
+        for (int d = 0; d < kPer; d += 4)
+          *reinterpret_cast<float4*>(x[u] + d) = *reinterpret_cast<const float4*>(v + d);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kJoinUnroll; ++u) {
+      const float f = exp2_approx(st[u].x - (top[u] == -INFINITY ? 0.0f : top[u]));
+      all[u] += st[u].y * f;
+#pragma unroll
+      for (int d = 0; d < kPer; ++d) a[u][d] += x[u][d] * f;
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < kJoinUnroll; ++u) {
+    const int r = r0 + u * (kJoinThreads / 32);
+    if (r >= n_rows) break;
+    const int row = blockIdx.z * rows + r;
+    const int node = row / p.group, h = at.head * p.group + row - node * p.group;
+    const int64_t to = ((int64_t)at.b * p.nodes + node) * p.heads + h;
+    const float inv = all[u] == 0.0f ? 0.0f : 1.0f / all[u];
+    uint32_t w[kPer / 2];
+#pragma unroll
+    for (int d = 0; d < kPer; d += 2) w[d / 2] = H::pack(a[u][d] * inv, a[u][d + 1] * inv);
+    uint32_t* out =
+        reinterpret_cast<uint32_t*>(static_cast<T*>(p.out) + to * D) + lane * (kPer / 2);
+    if constexpr (kPer == 2)
+      *out = w[0];
+    else if constexpr (kPer == 4)
+      *reinterpret_cast<uint2*>(out) = make_uint2(w[0], w[1]);
+    else
+      *reinterpret_cast<uint4*>(out) = make_uint4(w[0], w[1], w[2], w[3]);
+    if (lane == 0 && p.lse)
+      p.lse[to] = all[u] == 0.0f ? -INFINITY : (top[u] + log2f(all[u])) * 0.6931471805599453f;
+  }
 }
 
 // ---------------------------------------------------------------- launches
 // the joining kernel after a streaming kernel of `grid` CTAs; it is launched
 // while that one runs and waits on the device for its end
-template <typename T, int D>
+template <typename T, int D, int kRowsAtOnce>
 cudaError_t launch_join(const Params& p, int rows, int grid, cudaStream_t stream) {
   const int teams = grid / p.row_tiles;
   if (teams == 1) return cudaSuccess;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(teams - 1, (rows + kJoinThreads / 32 - 1) / (kJoinThreads / 32), p.row_tiles);
+  const int at_once = kJoinThreads / 32 * kRowsAtOnce;
+  cfg.gridDim = dim3(teams - 1, (rows + at_once - 1) / at_once, p.row_tiles);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -728,7 +755,7 @@ cudaError_t launch_join(const Params& p, int rows, int grid, cudaStream_t stream
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, tree_attention_join_kernel<T, D>, p, rows, grid);
+  return cudaLaunchKernelEx(&cfg, tree_attention_join_kernel<T, D, kRowsAtOnce>, p, rows, grid);
 }
 
 template <typename T, int D, int N8, int MW>
@@ -742,7 +769,7 @@ cudaError_t launch_shape(Params p, int sms, cudaStream_t stream) {
   const int grid = min(kMaxCtas, max(sms * (D == 256 ? 1 : 2), p.row_tiles));
   kernel<<<grid, kThreads, S::kSmem, stream>>>(p);
   e = cudaGetLastError();
-  return e != cudaSuccess ? e : launch_join<T, D>(p, S::kRows, grid, stream);
+  return e != cudaSuccess ? e : launch_join<T, D, 1>(p, S::kRows, grid, stream);
 }
 
 // rows of a streaming CTA for `rows` rows of an item: the smallest shape that

@@ -111,15 +111,6 @@ __device__ __forceinline__ void tmem_load16(uint32_t (&r)[16], uint32_t addr) {
       : "r"(addr)
       : "memory");
 }
-// registers of a warpgroup's threads beside the launch's 128
-template <int kRegs>
-__device__ __forceinline__ void more_registers() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
-}
-template <int kRegs>
-__device__ __forceinline__ void fewer_registers() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
-}
 __device__ __forceinline__ void tmem_wait_load() {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
@@ -143,11 +134,11 @@ __device__ __forceinline__ void tmem_wait_store() {
 //
 // Warps 0-3 and 4-7: softmax, Q and the results of row tile 0 and 1.  Warp 8:
 // tensor copies of keys and values, box by box of a block's rows, into a ring
-// of stages each.  Warps 9-11: where a tile holds nodes, clear its values of
-// infinities and NaN.  Warp 12: issues the products (its warpgroup is whole because registers are shared out by
-// warpgroup: 2 * 192 + 72 + 56 a thread of the launch's 4 * 128).  K and Q lie in rows of 64 dims (128 bytes, swizzled in groups of
-// eight rows); V the same, read with dims as its major axis.
-constexpr int kWideThreads = 512;
+// of stages each.  Warp 9: issues the products.  Warps 10-11: where a tile
+// holds nodes, clear its values of infinities and NaN.  K and Q lie in rows
+// of 64 dims (128 bytes, swizzled in groups of eight rows); V the same, read
+// with dims as its major axis.
+constexpr int kWideThreads = 384;  // 168 registers a thread: a row's 128 scores and more
 constexpr int kWideTile = 128;
 
 template <int D>
@@ -158,7 +149,7 @@ struct Wide {
   static constexpr int kSmem = (2 + 2 * kStages) * kOperand + 1024;
 };
 constexpr int kWideMaxStages = 4;
-constexpr int kClearThreads = 96;
+constexpr int kClearThreads = 64;
 
 struct WideShared {
   uint64_t k_full[kWideMaxStages], k_empty[kWideMaxStages];
@@ -214,7 +205,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     sh.failed = 0u;
     mbar_init_fence();
   }
-  if (warp == 12) {
+  if (warp == 9) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
                      smem_u32(&sh.tmem))
                  : "memory");
@@ -237,7 +228,6 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     return false;
   };
   if (warp < 8) {
-    more_registers<192>();
     // -------------------------------------------------- softmax and results
     const int m = warp >> 2;
     const int t = tid & 127;  // this thread's row of the tile and lane of tensor memory
@@ -249,38 +239,49 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     const float scale = fmaxf(fabsf(p.scale2), 1.17549435e-38f);
     uint32_t tile_no = 0, segments = 0;
     bool ok = m < n_tiles;
-    for (; ok && cur.part(); cur.next(p, kWideTile)) {
-      const int tiles = cur.count;
-      if (tiles == 0) continue;
-      const Lengths len = request_lengths(p, cur.b);
-      const int live = len.nodes * p.group;
-      if (tid == 0 && r0 == 0 && cur.head == 0 && cur.first == 0)
-        p.status[cur.b] = len.bad ? DSPARK_ST_BAD_LENGTH : DSPARK_ST_OK;
-
-      // Q, 16 bytes at a time
-#pragma unroll 4
-      for (int i = t; i < 128 * kChunks; i += 128) {
-        const int r = i / kChunks, c = i % kChunks;
-        const int row = r0 + m * 128 + r, node = row / p.group;
-        uint4 w = make_uint4(0u, 0u, 0u, 0u);
-        if (row < live) {
-          const int h = cur.head * p.group + row - node * p.group;
-          w = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + cur.b * p.q_req +
-                                                   node * p.q_node + h * p.q_head) +
-                    c);
-          w.x ^= flip;
-          w.y ^= flip;
-          w.z ^= flip;
-          w.w ^= flip;
-        }
+    // the item's Q: 16-byte pieces of this thread's column, every kStep-th row
+    constexpr int kStep = 128 / kChunks;
+    uint4 q[kChunks];
+    auto load_q = [&](const Walk& w) {
+      const int live = request_lengths(p, w.b).nodes * p.group;
+      const T* from = static_cast<const T*>(p.q) + w.b * p.q_req + (t % kChunks) * 8;
+#pragma unroll
+      for (int i = 0; i < kChunks; ++i) {
+        const int row = r0 + m * 128 + i * kStep + t / kChunks;
+        const int at = row < live ? row : 0, node = at / p.group;  // no branch: all loads at once
+        const int h = w.head * p.group + at - node * p.group;
+        const T* piece = from + node * p.q_node + h * p.q_head;
+        q[i] = live > 0 ? __ldg(reinterpret_cast<const uint4*>(piece)) : make_uint4(0u, 0u, 0u, 0u);
+        const uint32_t keep = row < live ? ~0u : 0u;
+        q[i] = make_uint4((q[i].x ^ flip) & keep, (q[i].y ^ flip) & keep, (q[i].z ^ flip) & keep,
+                          (q[i].w ^ flip) & keep);
+      }
+    };
+    auto store_q = [&] {
+      const int c = t % kChunks;
+#pragma unroll
+      for (int i = 0; i < kChunks; ++i) {
+        const int r = i * kStep + t / kChunks;
         const uint32_t to = q_at + m * W::kOperand + (c >> 3) * 16384 + r * 128 +
                             (((c & 7) ^ (r & 7)) << 4);
-        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(w.x), "r"(w.y),
-                     "r"(w.z), "r"(w.w)
+        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(q[i].x),
+                     "r"(q[i].y), "r"(q[i].z), "r"(q[i].w)
                      : "memory");
       }
       fence_async_shared();
       mbar_arrive(&sh.q_full[m]);
+    };
+    bool more = ok && cur.advance(p, kWideTile);
+    if (more) {
+      load_q(cur);
+      store_q();
+    }
+    while (ok && more) {
+      const int tiles = cur.count;
+      const Lengths len = request_lengths(p, cur.b);
+      const int live = len.nodes * p.group;
+      if (tid == 0 && r0 == 0 && cur.head == 0 && cur.first == 0)
+        p.status[cur.b] = len.bad ? DSPARK_ST_BAD_LENGTH : DSPARK_ST_OK;
 
       const int row = r0 + m * 128 + t, node = row / p.group;
       uint64_t mask = 0;
@@ -366,10 +367,16 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         tc_before_sync();
         mbar_arrive(&sh.p_full[m]);
       }
+      // the next item's Q is on its way while this one's last products run, and
+      // its first scores are computed while this one's results are written
+      Walk ahead = cur;
+      more = ok && ahead.advance(p, kWideTile);
+      if (more) load_q(ahead);
       if (ok) ok = __all_sync(0xffffffffu, wait(&sh.o_full[m], segments & 1u));
       ++segments;
       if (!ok) break;
       tc_after_sync();
+      if (more) store_q();
       special |= sh.special[(tile_no - 1u) & 7u] != 0u;
 
       float sum = sum2.x + sum2.y;
@@ -419,11 +426,14 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                                 H::pack(v[8 * j + 4] * inv, v[8 * j + 5] * inv),
                                 H::pack(v[8 * j + 6] * inv, v[8 * j + 7] * inv));
         } else if (mine) {
-          float4* out =
-              reinterpret_cast<float4*>(ws.rows + (slot * kWideRows + m * 128 + t) * D + c * 32);
+          // whole 32-byte sectors: a warp's rows lie far apart
+          float* out = ws.rows + (slot * kWideRows + m * 128 + t) * D + c * 32;
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            out[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+          for (int j = 0; j < 32; j += 8)
+            asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(out + j),
+                         "f"(v[j]), "f"(v[j + 1]), "f"(v[j + 2]), "f"(v[j + 3]), "f"(v[j + 4]),
+                         "f"(v[j + 5]), "f"(v[j + 6]), "f"(v[j + 7])
+                         : "memory");
         }
         __syncwarp();
       }
@@ -434,15 +444,15 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           p.lse[to] = sum == 0.0f ? -INFINITY : (ref + log2f(sum)) * 0.6931471805599453f;
       }
       tc_before_sync();  // the accumulators are read: the next item may take them
+      cur = ahead;
     }
-  } else if (warp < 12) {
-    fewer_registers<72>();
+  } else if (warp != 9) {
     // ------------------------------------------------------ keys and values
     // Lane i copies the tile's box i, box_rows positions of one block.
     const int boxes = kWideTile / box_rows;  // at most 16
     uint32_t g = 0, turns = 0;  // turns: each stage's phase of the tiles with nodes
     bool ok = true;
-    for (; ok && cur.part(); cur.next(p, kWideTile)) {
+    while (ok && cur.advance(p, kWideTile)) {
       const int tiles = cur.count;
       const Lengths len = request_lengths(p, cur.b);
       const int first = cur.first * kWideTile;
@@ -505,7 +515,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           if (!ok) break;
           turns ^= 1u << stage;
           const int from = max(0, len.ctx - pos0);
-          for (int j = tid - 288; j < (kWideTile - from) * kChunks; j += kClearThreads) {
+          for (int j = tid - 320; j < (kWideTile - from) * kChunks; j += kClearThreads) {
             const int r = from + j / kChunks, c = j % kChunks;
             const uint32_t addr = v_at + stage * W::kOperand + (c >> 3) * 16384 + r * 128 +
                                   (((c & 7) ^ (r & 7)) << 4);
@@ -529,9 +539,6 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       }
     }
   } else {
-    fewer_registers<56>();
-  }
-  if (warp == 12) {
     // ------------------------------------------------------------- products
     // The warp goes through the loop together; one lane issues.
     constexpr uint32_t kFormat = H::kExponent == 0x7F80u ? 1u : 0u;  // bf16 or f16
@@ -567,9 +574,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     auto phase_of = [](uint32_t g) -> uint32_t { return (g / kStages) & 1u; };
     uint32_t g = 0, segments = 0, turns = 0;
     bool ok = true;
-    for (; ok && cur.part(); cur.next(p, kWideTile)) {
+    while (ok && cur.advance(p, kWideTile)) {
       const int tiles = cur.count;
-      if (tiles == 0) continue;
       const Lengths len = request_lengths(p, cur.b);
       for (int m = 0; m < n_tiles; ++m) ok = ok && wait_all(&sh.q_full[m], segments & 1u);
       ok = ok && wait_all(&sh.k_full[g % kStages], phase_of(g));
@@ -611,12 +617,12 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   __syncwarp();
   tc_before_sync();
   __syncthreads();
-  if (warp == 12) {
+  if (warp == 9) {
     tc_after_sync();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
   }
   if (sh.failed && tid == 0) {  // the requests of this range are refused
-    for (cur = walk_from(sh.start, range); cur.part(); cur.next(p, kWideTile))
+    for (cur = walk_from(sh.start, range); cur.advance(p, kWideTile);)
       p.status[cur.b] = DSPARK_ST_TIMEOUT;
   }
 }
@@ -673,7 +679,7 @@ bool launch_wide(Params p, int sms, cudaStream_t stream, cudaError_t* error) {
   const int grid = min(kMaxCtas, max(sms, p.row_tiles));
   kernel<<<grid, kWideThreads, Wide<D>::kSmem, stream>>>(p, k_map, v_map, box_rows);
   *error = cudaGetLastError();
-  if (*error == cudaSuccess) *error = launch_join<T, D>(p, kWideRows, grid, stream);
+  if (*error == cudaSuccess) *error = launch_join<T, D, 4>(p, kWideRows, grid, stream);
   return true;
 }
 
