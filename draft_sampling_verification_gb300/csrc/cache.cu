@@ -4,6 +4,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #define DSPARK_TU 10  // this file's number in the checked build's site codes
 #include "common.cuh"
 
@@ -202,25 +204,26 @@ cudaError_t launch_cache_plan(const int32_t* ctx, const int32_t* added, int B, i
 }
 
 // ------------------------------------------------------------ cache write
-// A piece is 8 elements of one token and head, of the keys or of the values
-// (blockIdx.y): 16 bytes written; 16 read, or 32 from fp32.  A thread moves
-// kUnroll pieces, whose sources it reads before it knows their slots: one
-// where the pieces do not fill the GPU, four to keep more reads in flight
-// where they do.
+// A piece is 8 elements of one token and head: 16 bytes written; 16 read, or
+// 32 from fp32.  2^lane_bits lanes take one token, its keys and its values,
+// so that the token's slot is worked out once for all its pieces, and each
+// keeps kUnroll pieces of both in flight.  Bound by HBM.
 namespace {
 
 constexpr int kWriteThreads = 256;
 
 struct WriteParams {
-  const void* src[2];
-  void* cache[2];
+  const void* k;
+  const void* v;
+  void* k_cache;
+  void* v_cache;
   int64_t src_token, src_head;              // elements
   int64_t block_stride, token_stride, head_stride;
-  int n_src, n_heads, vecs;                 // vecs: 8-element pieces of a head's row
-  int n_blocks, page;
+  int n_src, n_tokens;
+  int vecs, per;                            // pieces of a head's row, of a token
+  int n_blocks, page, lane_bits;
   const int32_t* slots;
   const int32_t* rows;
-  int n_tokens;
 };
 
 template <typename T>
@@ -238,51 +241,56 @@ __device__ __forceinline__ uint32_t round_pair<__half>(float a, float b) {
 
 }  // namespace
 
-template <typename T, bool kFromF32, int kUnroll>
+// one piece as it is stored
+template <typename T>
+__device__ __forceinline__ uint4 stored(const float4 (&f)[2]) {
+  return make_uint4(round_pair<T>(f[0].x, f[0].y), round_pair<T>(f[0].z, f[0].w),
+                    round_pair<T>(f[1].x, f[1].y), round_pair<T>(f[1].z, f[1].w));
+}
+template <typename T>
+__device__ __forceinline__ uint4 stored(const uint4 (&w)[1]) {
+  return w[0];
+}
+
+template <typename T, bool kFromF32>
 __global__ void __launch_bounds__(kWriteThreads) kv_write_kernel(const WriteParams p) {
-  const void* src = p.src[blockIdx.y];
-  T* cache = static_cast<T*>(p.cache[blockIdx.y]);
-  const uint32_t per = (uint32_t)(p.n_heads * p.vecs), vecs = (uint32_t)p.vecs;
-  // the CTA's pieces begin inside one token: from there 32-bit divisions do
-  const int64_t first = (int64_t)blockIdx.x * (kWriteThreads * kUnroll);
-  const int token0 = (int)(first / per);
-  const uint32_t rest0 = (uint32_t)(first - (int64_t)token0 * per);
-  uint4 w[kUnroll];
-  float4 f[kUnroll][2];
-  int slot[kUnroll];
-  uint32_t at[kUnroll];  // the piece within its token
+  using Src = std::conditional_t<kFromF32, float, T>;
+  using Load = std::conditional_t<kFromF32, float4, uint4>;
+  constexpr int kLoads = kFromF32 ? 2 : 1;
+  constexpr int kUnroll = kFromF32 ? 2 : 4;
+  const int lanes = 1 << p.lane_bits;
+  const int64_t thread = (int64_t)blockIdx.x * kWriteThreads + threadIdx.x;
+  const int64_t token = thread >> p.lane_bits;
+  if (token >= p.n_tokens) return;
+  const int slot = p.slots[token];
+  const int64_t row = p.rows ? p.rows[token] : token;
+  if (slot < 0 || slot >= p.n_blocks * p.page || row < 0 || row >= p.n_src) return;
+  const int block = slot / p.page;
+  const int64_t to = block * p.block_stride + (int64_t)(slot - block * p.page) * p.token_stride;
+  const Src* k = static_cast<const Src*>(p.k) + row * p.src_token;
+  const Src* v = static_cast<const Src*>(p.v) + row * p.src_token;
+  for (int j0 = (int)threadIdx.x & (lanes - 1); j0 < p.per; j0 += kUnroll * lanes) {
+    Load a[kUnroll][kLoads], c[kUnroll][kLoads];
+    int64_t at[kUnroll];
 #pragma unroll
-  for (int u = 0; u < kUnroll; ++u) {
-    const uint32_t i = rest0 + u * kWriteThreads + threadIdx.x;
-    const int token = token0 + (int)(i / per);
-    at[u] = i % per;
-    slot[u] = -1;
-    if (token >= p.n_tokens) continue;
-    const int row = p.rows ? p.rows[token] : token;
-    if (row < 0 || row >= p.n_src) continue;
-    slot[u] = p.slots[token];
-    const uint32_t head = at[u] / vecs;
-    const int64_t from = row * p.src_token + head * p.src_head + (at[u] - head * vecs) * 8;
-    if constexpr (kFromF32) {
-      const float4* x = reinterpret_cast<const float4*>(static_cast<const float*>(src) + from);
-      f[u][0] = __ldcs(x);
-      f[u][1] = __ldcs(x + 1);
-    } else {
-      w[u] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const T*>(src) + from));
+    for (int u = 0; u < kUnroll; ++u) {
+      const int j = j0 + u * lanes;
+      if (j >= p.per) continue;
+      const int head = j / p.vecs, d = (j - head * p.vecs) * 8;
+      const int64_t from = head * p.src_head + d;
+      at[u] = to + head * p.head_stride + d;
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        a[u][i] = __ldcs(reinterpret_cast<const Load*>(k + from) + i);
+        c[u][i] = __ldcs(reinterpret_cast<const Load*>(v + from) + i);
+      }
     }
-  }
 #pragma unroll
-  for (int u = 0; u < kUnroll; ++u) {
-    if (slot[u] < 0 || slot[u] >= p.n_blocks * p.page) continue;
-    const int block = slot[u] / p.page;
-    const uint32_t head = at[u] / vecs;
-    const int64_t to = block * p.block_stride +
-                       (int64_t)(slot[u] - block * p.page) * p.token_stride +
-                       head * p.head_stride + (at[u] - head * vecs) * 8;
-    if constexpr (kFromF32)
-      w[u] = make_uint4(round_pair<T>(f[u][0].x, f[u][0].y), round_pair<T>(f[u][0].z, f[u][0].w),
-                        round_pair<T>(f[u][1].x, f[u][1].y), round_pair<T>(f[u][1].z, f[u][1].w));
-    *reinterpret_cast<uint4*>(cache + to) = w[u];
+    for (int u = 0; u < kUnroll; ++u) {
+      if (j0 + u * lanes >= p.per) continue;
+      *reinterpret_cast<uint4*>(static_cast<T*>(p.k_cache) + at[u]) = stored<T>(a[u]);
+      *reinterpret_cast<uint4*>(static_cast<T*>(p.v_cache) + at[u]) = stored<T>(c[u]);
+    }
   }
 }
 
@@ -293,39 +301,38 @@ cudaError_t launch_kv_write(const void* k, const void* v, int src_dtype, int64_t
                             const int32_t* slots, const int32_t* rows, int n_tokens,
                             cudaStream_t stream) {
   WriteParams p;
-  p.src[0] = k;
-  p.src[1] = v;
-  p.cache[0] = k_cache;
-  p.cache[1] = v_cache;
+  p.k = k;
+  p.v = v;
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
   p.src_token = src_token;
   p.src_head = src_head;
   p.block_stride = block_stride;
   p.token_stride = token_stride;
   p.head_stride = head_stride;
   p.n_src = n_src;
-  p.n_heads = n_heads;
+  p.n_tokens = n_tokens;
   p.vecs = head_dim / 8;
+  p.per = n_heads * p.vecs;
   p.n_blocks = n_blocks;
   p.page = page;
   p.slots = slots;
   p.rows = rows;
-  p.n_tokens = n_tokens;
-  const int64_t pieces = (int64_t)n_tokens * n_heads * p.vecs;
-  const bool few = pieces <= 1024 * kWriteThreads;
-  const int64_t per_cta = kWriteThreads * (few ? 1 : 4);
-  const dim3 grid((unsigned)((pieces + per_cta - 1) / per_cta), 2);
-  auto launch = [&](auto* one, auto* four) {
-    (few ? one : four)<<<grid, kWriteThreads, 0, stream>>>(p);
-    return cudaGetLastError();
-  };
+  p.lane_bits = 0;  // as many lanes as the token has pieces, at most a warp
+  while (p.lane_bits < 5 && (2 << p.lane_bits) <= p.per) ++p.lane_bits;
+  const int64_t threads = (int64_t)n_tokens << p.lane_bits;
+  const unsigned grid = (unsigned)((threads + kWriteThreads - 1) / kWriteThreads);
+  const bool wide = src_dtype == DSPARK_F32;
   using B16 = __nv_bfloat16;
-  if (cache_dtype == DSPARK_BF16)
-    return src_dtype == DSPARK_F32
-               ? launch(kv_write_kernel<B16, true, 1>, kv_write_kernel<B16, true, 4>)
-               : launch(kv_write_kernel<B16, false, 1>, kv_write_kernel<B16, false, 4>);
-  return src_dtype == DSPARK_F32
-             ? launch(kv_write_kernel<__half, true, 1>, kv_write_kernel<__half, true, 4>)
-             : launch(kv_write_kernel<__half, false, 1>, kv_write_kernel<__half, false, 4>);
+  if (cache_dtype == DSPARK_BF16 && wide)
+    kv_write_kernel<B16, true><<<grid, kWriteThreads, 0, stream>>>(p);
+  else if (cache_dtype == DSPARK_BF16)
+    kv_write_kernel<B16, false><<<grid, kWriteThreads, 0, stream>>>(p);
+  else if (wide)
+    kv_write_kernel<__half, true><<<grid, kWriteThreads, 0, stream>>>(p);
+  else
+    kv_write_kernel<__half, false><<<grid, kWriteThreads, 0, stream>>>(p);
+  return cudaGetLastError();
 }
 
 DSPARK_CHECK_COLLECTOR(cache)
