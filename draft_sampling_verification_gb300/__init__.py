@@ -78,6 +78,9 @@ def _dtype_code(t):
 
 def _rows(t):
     """(rows, V, ld) of a logit tensor whose rows are uniformly strided."""
+    if t.dim() >= 2 and t.is_contiguous() and t.shape[-1] > 0:
+        V = t.shape[-1]
+        return t.numel() // V, V, V
     if t.dim() < 2 or t.stride(-1) != 1:
         raise ValueError("logit rows must be contiguous in their last dimension")
     V = t.shape[-1]
@@ -355,19 +358,34 @@ def dspark_cache_plan(ctx_len, new_len, max_new, page_size, block_table, free_bl
     strided), updated in place; free_blocks int32 [max_free]; n_free int32 [1] or None; parents
     int32 [B, max_new] or None; slots int32 [B, max_new]; positions the same or None; tree_mask
     int64 [B, max_new] (holding the uint64 masks) or None; taken int32 [1]."""
-    i32, B = torch.int32, ctx_len.shape[0]
-    if (block_table.dtype is not i32 or block_table.dim() != 2 or block_table.shape[0] != B
-            or block_table.stride(1) != 1 or not block_table.is_cuda):
+    i32, cells = torch.int32, (ctx_len.shape[0], max_new)
+    _cache_plan(ctx_len, new_len, max_new, page_size, block_table, free_blocks, n_free, parents,
+                _arg("slots", slots, i32, cells), _arg("positions", positions, i32, cells),
+                _arg("tree_mask", tree_mask, torch.int64, cells), _arg("taken", taken, i32, (1,)),
+                _arg("req_status", req_status, i32, cells[:1]), stream)
+
+
+def _table_args(block_table, B):
+    """(pointer, row stride, max_blocks) of a block table int32 [B, max_blocks]."""
+    if (block_table.dtype is not torch.int32 or block_table.dim() != 2
+            or block_table.shape[0] != B or block_table.stride(1) != 1
+            or not block_table.is_cuda):
         raise ValueError("block_table must be an int32 CUDA tensor [B, max_blocks]")
-    cells = (B, max_new)
+    wide = block_table.shape[1]
+    return block_table.data_ptr(), block_table.stride(0) if B > 1 else wide, wide
+
+
+def _cache_plan(ctx_len, new_len, max_new, page_size, block_table, free_blocks, n_free, parents,
+                slots, positions, tree_mask, taken, req_status, stream):
+    """The call, with the outputs as pointers."""
+    i32, B = torch.int32, ctx_len.shape[0]
+    table, ld, wide = _table_args(block_table, B)
+    n = free_blocks.shape[0]
     _call("dspark_cache_plan", _arg("ctx_len", ctx_len, i32, (B,)),
-          _arg("new_len", new_len, i32, (B,)), B, max_new, page_size, block_table.data_ptr(),
-          block_table.stride(0) if B > 1 else block_table.shape[1], block_table.shape[1],
-          _arg("free_blocks", free_blocks, i32, free_blocks.shape[:1]), free_blocks.shape[0],
-          _arg("n_free", n_free, i32, (1,)), _arg("parents", parents, i32, cells),
-          _arg("slots", slots, i32, cells), _arg("positions", positions, i32, cells),
-          _arg("tree_mask", tree_mask, torch.int64, cells), _arg("taken", taken, i32, (1,)),
-          _arg("req_status", req_status, i32, (B,)), _stream(stream))
+          _arg("new_len", new_len, i32, (B,)), B, max_new, page_size, table, ld, wide,
+          _arg("free_blocks", free_blocks, i32, (n,)), n, _arg("n_free", n_free, i32, (1,)),
+          _arg("parents", parents, i32, (B, max_new)), slots, positions, tree_mask, taken,
+          req_status, _stream(stream))
 
 
 def dspark_kv_write(k, v, k_cache, v_cache, slots, rows=None, stream=None):
@@ -412,29 +430,34 @@ def dspark_tree_attention(q, k_cache, v_cache, block_table, ctx_len, n_nodes, tr
     [B]; tree_mask int64 [B, nodes] (holding the uint64 masks) or None; out like q, contiguous;
     lse float32 [B, nodes, n_heads] or None; workspace: uint8, at least
     dspark_tree_attention_workspace_bytes bytes."""
+    B, nodes, heads = q.shape[:3]
+    need = dspark_tree_attention_workspace_bytes(B, nodes, heads, k_cache.shape[2], q.shape[3])
+    if workspace.numel() * workspace.element_size() < need:
+        raise ValueError("the workspace is too small")
+    _tree_attention(q, k_cache, v_cache, block_table, ctx_len, n_nodes, tree_mask, scale,
+                    _arg("out", out, q.dtype, q.shape),
+                    _arg("lse", lse, torch.float32, (B, nodes, heads)),
+                    _arg("req_status", req_status, torch.int32, (B,)), _ptr(workspace), stream)
+
+
+def _tree_attention(q, k_cache, v_cache, block_table, ctx_len, n_nodes, tree_mask, scale, out,
+                    lse, req_status, workspace, stream):
+    """The call, with outputs and workspace as pointers."""
     code, kp, vp, sb, st, sh = _cache_args(k_cache, v_cache)
-    i32 = torch.int32
-    if q.dim() != 4 or q.dtype is not k_cache.dtype or q.stride(3) != 1 or not q.is_cuda:
+    i32, strides = torch.int32, q.stride()
+    if q.dim() != 4 or q.dtype is not k_cache.dtype or strides[3] != 1 or not q.is_cuda:
         raise ValueError("q must be a CUDA tensor [B, nodes, n_heads, head_dim] of the caches' "
                          "type, contiguous in head_dim")
     B, nodes, heads, dim = q.shape
-    if k_cache.shape[3] != dim:
+    n_blocks, page, kv_heads, kv_dim = k_cache.shape
+    if kv_dim != dim:
         raise ValueError("q and the caches must have the same head_dim")
-    if (block_table.dtype is not i32 or block_table.dim() != 2 or block_table.shape[0] != B
-            or block_table.stride(1) != 1 or not block_table.is_cuda):
-        raise ValueError("block_table must be an int32 CUDA tensor [B, max_blocks]")
-    if (workspace.numel() * workspace.element_size()
-            < dspark_tree_attention_workspace_bytes(B, nodes, heads, k_cache.shape[2], dim)):
-        raise ValueError("the workspace is too small")
-    _call("dspark_tree_attention", q.data_ptr(), code, q.stride(0), q.stride(1), q.stride(2), B,
-          nodes, heads, k_cache.shape[2], dim, kp, vp, sb, st, sh, k_cache.shape[0],
-          k_cache.shape[1], block_table.data_ptr(),
-          block_table.stride(0) if B > 1 else block_table.shape[1], block_table.shape[1],
+    table, ld, wide = _table_args(block_table, B)
+    _call("dspark_tree_attention", q.data_ptr(), code, strides[0], strides[1], strides[2], B,
+          nodes, heads, kv_heads, dim, kp, vp, sb, st, sh, n_blocks, page, table, ld, wide,
           _arg("ctx_len", ctx_len, i32, (B,)), _arg("n_nodes", n_nodes, i32, (B,)),
-          _arg("tree_mask", tree_mask, torch.int64, (B, nodes)), scale,
-          _arg("out", out, q.dtype, q.shape),
-          _arg("lse", lse, torch.float32, (B, nodes, heads)),
-          _arg("req_status", req_status, i32, (B,)), _ptr(workspace), _stream(stream))
+          _arg("tree_mask", tree_mask, torch.int64, (B, nodes)), scale, out, lse, req_status,
+          workspace, _stream(stream))
 
 
 def dspark_logits_process(logits, history, prompt_len, history_len, draft_tokens, row_mask,
@@ -449,7 +472,7 @@ def dspark_logits_process(logits, history, prompt_len, history_len, draft_tokens
     if logits.dim() != 3 or out.shape != logits.shape or out.dtype is not logits.dtype:
         raise ValueError("logits must be [B, rows, V], and out of the same shape and type")
     n, V, ld = _rows(logits)
-    ld_out = _rows(out)[2]
+    ld_out = ld if out is logits else _rows(out)[2]
     B, rows = logits.shape[:2]
     i32, f32, one, per = torch.int32, torch.float32, (B,), (B, rows)
     wide = 0 if history is None else history.shape[-1]
@@ -662,14 +685,18 @@ def cache_plan(ctx_len, new_len, max_new, page_size, block_table, free_blocks, n
     """Grants the step's blocks and maps its new tokens; returns dict(block_table (the caller's,
     updated), slots, positions [B, max_new], taken [1], status [B]) and, for max_new <= 64,
     tree_mask int64 [B, max_new]."""
-    B, new = ctx_len.shape[0], ctx_len.new_empty  # int32, checked by the call
-    out = {"block_table": block_table, "slots": new((B, max_new)),
-           "positions": new((B, max_new)), "taken": new((1,)), "status": new((B,))}
-    if max_new <= MAX_NODES:
-        out["tree_mask"] = new((B, max_new), dtype=torch.int64)
-    dspark_cache_plan(ctx_len, new_len, max_new, page_size, block_table, free_blocks, n_free,
-                      parents, out["slots"], out["positions"], out.get("tree_mask"), out["taken"],
-                      out["status"], stream)
+    B, dev, i32 = ctx_len.shape[0], ctx_len.device, torch.int32
+    slots, taken, status = (_empty((B, max_new), i32, dev), _empty((1,), i32, dev),
+                            _empty((B,), i32, dev))
+    positions = torch.empty_like(slots)
+    mask = _empty((B, max_new), torch.int64, dev) if max_new <= MAX_NODES else None
+    _cache_plan(ctx_len, new_len, max_new, page_size, block_table, free_blocks, n_free, parents,
+                slots.data_ptr(), positions.data_ptr(), None if mask is None else mask.data_ptr(),
+                taken.data_ptr(), status.data_ptr(), stream)
+    out = {"block_table": block_table, "slots": slots, "positions": positions, "taken": taken,
+           "status": status}
+    if mask is not None:
+        out["tree_mask"] = mask
     return out
 
 
@@ -689,13 +716,15 @@ def tree_attention(q, k_cache, v_cache, block_table, ctx_len, n_nodes, tree_mask
             return tree_attention(q, k_cache, v_cache, block_table, ctx_len, n_nodes, tree_mask,
                                   scale)
     B, nodes, heads, dim = q.shape
-    out = q.new_empty(q.shape)
-    lse = q.new_empty((B, nodes, heads), dtype=torch.float32)
-    st = ctx_len.new_empty((B,))  # int32, checked by the call
-    ws = q.new_empty((dspark_tree_attention_workspace_bytes(B, nodes, heads, k_cache.shape[2],
-                                                            dim),), dtype=torch.uint8)
-    dspark_tree_attention(q, k_cache, v_cache, block_table, ctx_len, n_nodes, tree_mask,
-                          dim ** -0.5 if scale is None else scale, out, lse, st, ws, stream)
+    dev = q.device
+    out = _empty((B, nodes, heads, dim), q.dtype, dev)
+    lse = _empty((B, nodes, heads), torch.float32, dev)
+    st = _empty((B,), torch.int32, dev)
+    ws = _empty((dspark_tree_attention_workspace_bytes(B, nodes, heads, k_cache.shape[2], dim),),
+                torch.uint8, dev)
+    _tree_attention(q, k_cache, v_cache, block_table, ctx_len, n_nodes, tree_mask,
+                    dim ** -0.5 if scale is None else scale, out.data_ptr(), lse.data_ptr(),
+                    st.data_ptr(), ws.data_ptr(), None)
     return out, lse, st
 
 
@@ -706,8 +735,8 @@ def logits_process(logits, history=None, prompt_len=None, history_len=None, draf
     """Penalties, biases and grammar masks on logits [B, rows, V]; returns (out (a new tensor when
     None; logits itself for in place), status [B])."""
     if out is None:
-        out = logits.new_empty(logits.shape)
-    st = logits.new_empty((logits.shape[0],), dtype=torch.int32)
+        out = _empty(logits.shape, logits.dtype, logits.device)
+    st = _empty((logits.shape[0],), torch.int32, logits.device)
     dspark_logits_process(logits, history, prompt_len, history_len, draft_tokens, row_mask,
                           repetition, frequency, presence, bias_ids, bias_values, n_bias,
                           mask_words, mask_rows, out, st, stream)
