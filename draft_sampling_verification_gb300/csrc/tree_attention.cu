@@ -6,10 +6,14 @@
 namespace dspark {
 
 int64_t tree_attention_workspace_bytes(int B, int nodes, int heads, int kv_heads, int head_dim) {
+  // the more of what the two kernels want: the blocks' size decides between them
   const int rows = nodes * (heads / kv_heads);
-  return attn::workspace_bytes(rows > 64 && head_dim != 256 ? attn::kWideRows
-                                                            : attn::shape_rows(rows, head_dim),
-                               head_dim);
+  const int64_t streaming =
+      attn::workspace_bytes(attn::stream_rows(rows, head_dim), head_dim, attn::kStreamCtas);
+  const bool pair = head_dim != 256 && rows <= 128;
+  const int64_t wide = attn::workspace_bytes(head_dim == 256 || pair ? 128 : 256, head_dim,
+                                             attn::wide_ctas(pair));
+  return streaming > wide ? streaming : wide;
 }
 
 cudaError_t launch_tree_attention(const void* q, int dtype, int64_t q_req, int64_t q_node,
@@ -49,6 +53,7 @@ cudaError_t launch_tree_attention(const void* q, int dtype, int64_t q_req, int64
   p.status = status;
   p.workspace = static_cast<char*>(workspace);
   p.row_tiles = 1;
+  p.max_ctas = p.item_cost = 0;
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);

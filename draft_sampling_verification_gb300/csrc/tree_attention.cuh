@@ -29,6 +29,8 @@ struct Params {
   float* lse;
   int32_t* status;
   char* workspace;
+  int max_ctas;   // ranges that the workspace has room for
+  int item_cost;  // an item's start and end, in tiles
   int row_tiles;  // tiles of an item's rows: ceil(nodes * group / rows per CTA)
 };
 
@@ -131,36 +133,35 @@ __device__ __forceinline__ uint32_t without_special(uint32_t w) {
 // that lies inside one range is finished by its team; the others leave
 // partial rows in the workspace for the joining kernel.  Each item has at
 // least one tile (a request without tokens still writes its zero rows), and
-// counts for kItemCost tiles more, ahead of its first: the time that its
+// counts for item_cost tiles more, ahead of its first: the time that its
 // queries, its first copies and its results take, without which the teams
-// that get many short items end last.
-constexpr int kMaxCtas = 320;
-constexpr int kWideRows = 256;  // rows of a CTA of the wide kernel
-constexpr int kItemCost = 5;
+// that get many short items end last.  (A pair of ranges in one CTA counts as
+// two CTAs here.)
+constexpr int kStreamCost = 5, kPairCost = 2, kWideCost = 3;
 
-struct Start {  // where a team's range begins: `at` into the item, of kItemCost + tiles
+struct Start {  // where a team's range begins: `at` into the item, of item_cost + tiles
   int b, head, at, tiles;
 };
 
 struct Workspace {
   int64_t* total;
-  Start* start;   // [kMaxCtas]
-  float2* stats;  // [2 * kMaxCtas][rows]: the reference of the exponents, the sum
-  float* rows;    // [2 * kMaxCtas][rows][dim]
+  Start* start;   // [ctas]
+  float2* stats;  // [2 * ctas][rows]: the reference of the exponents, the sum
+  float* rows;    // [2 * ctas][rows][dim]
 };
 
-__host__ __device__ inline int64_t workspace_bytes(int rows, int dim) {
-  return 64 + (int64_t)kMaxCtas * sizeof(Start) +
-         2ll * kMaxCtas * rows * (sizeof(float2) + (int64_t)dim * sizeof(float));
+__host__ __device__ inline int64_t workspace_bytes(int rows, int dim, int ctas) {
+  return 64 + (int64_t)ctas * sizeof(Start) +
+         2ll * ctas * rows * (sizeof(float2) + (int64_t)dim * sizeof(float));
 }
 
-__device__ __forceinline__ Workspace carve(char* w, int rows) {
+__device__ __forceinline__ Workspace carve(char* w, int rows, int ctas) {
   Workspace s;  // every part 32-byte aligned
   w = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(w) + 31) & ~(uintptr_t)31);
   s.total = reinterpret_cast<int64_t*>(w);
   s.start = reinterpret_cast<Start*>(w + 32);
-  s.stats = reinterpret_cast<float2*>(w + 32 + kMaxCtas * sizeof(Start));
-  s.rows = reinterpret_cast<float*>(s.stats + 2 * kMaxCtas * rows);
+  s.stats = reinterpret_cast<float2*>(w + 32 + ctas * sizeof(Start));
+  s.rows = reinterpret_cast<float*>(s.stats + 2 * ctas * rows);
   return s;
 }
 
@@ -181,9 +182,9 @@ __device__ __forceinline__ Lengths request_lengths(const Params& p, int b) {
   return r;
 }
 
-__device__ __forceinline__ int request_tiles(const Params& p, int b, int tile) {
-  const int len = request_lengths(p, b).len;
-  return len > 0 ? (len - 1) / tile + 1 : 1;
+// an item's tiles of `tile` positions
+__device__ __forceinline__ int tiles_of(const Lengths& r, int tile) {
+  return r.len > 0 ? (r.len - 1) / tile + 1 : 1;
 }
 
 // the team whose range holds point x of the axis, and the first point of team c
@@ -199,7 +200,9 @@ struct Walk {
   int64_t left;       // of the range
   int b, head, tiles;
   int at;             // into the item
+  int cost;           // an item's, ahead of its tiles
   int first, count;   // the tiles of the item that are this CTA's
+  Lengths len;        // of request b
   // on to the next item of which a tile is this CTA's; false at the end
   __device__ __forceinline__ bool advance(const Params& p, int tile) {
     count = 0;
@@ -208,58 +211,69 @@ struct Walk {
         at = 0;
         if (++head == p.kv_heads) {
           head = 0;
-          tiles = request_tiles(p, ++b, tile);
+          len = request_lengths(p, ++b);
+          tiles = tiles_of(len, tile);
         }
       }
-      const int take = (int)min(left, (int64_t)(kItemCost + tiles - at));
-      first = max(0, at - kItemCost);
-      count = max(0, at + take - kItemCost) - first;
+      const int take = (int)min(left, (int64_t)(cost + tiles - at));
+      first = max(0, at - cost);
+      count = max(0, at + take - cost) - first;
       left -= take;
       at = -1;
     }
     return count > 0;
   }
   __device__ __forceinline__ bool whole() const { return count == tiles; }
-  __device__ __forceinline__ int64_t slot() const {  // of the partial rows
-    return 2ll * blockIdx.x + (first == 0 ? 1 : 0);
+  __device__ __forceinline__ int64_t slot(int cta) const {  // of the partial rows
+    return 2ll * cta + (first == 0 ? 1 : 0);
   }
 };
-__device__ __forceinline__ Walk walk_from(const Start& s, int64_t left) {
+__device__ __forceinline__ Walk walk_from(const Params& p, const Start& s, int64_t left,
+                                           int cost) {
   Walk w;
   w.left = left;
+  w.cost = cost;
   w.b = s.b;
   w.head = s.head;
   w.tiles = s.tiles;
   w.at = s.at;
   w.first = w.count = 0;
+  w.len = {0, 0, 0, false};
+  if (left > 0) w.len = request_lengths(p, s.b);
   return w;
 }
 
-// This CTA's range of the tile axis: its length, and where it begins (shared
-// memory, valid after the call); 0 for a CTA without work.  All threads call.
-template <int kBlock>
-__device__ __forceinline__ int64_t find_range(const Params& p, int tile, const Workspace& ws,
-                                              uint64_t* scan, Start* start) {
+// This CTA's ranges of the tile axis, kStreams of them side by side: their
+// lengths (0: no work), and where they begin (shared memory, valid after the
+// call).  All threads call.
+template <int kBlock, int kStreams>
+__device__ __forceinline__ void find_range(const Params& p, int tile, const Workspace& ws,
+                                           uint64_t* scan, Start* start, int64_t* range) {
   const int tid = threadIdx.x;
   const int per = (p.B + kBlock - 1) / kBlock;
   const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
   uint64_t sum = 0, total_u;
-  for (int b = b0; b < b1; ++b) sum += (uint64_t)(request_tiles(p, b, tile) + kItemCost) * p.kv_heads;
+  for (int b = b0; b < b1; ++b)
+    sum += (uint64_t)(tiles_of(request_lengths(p, b), tile) + p.item_cost) * p.kv_heads;
   const uint64_t upto = block_inclusive_scan_u64(sum, scan, &total_u);
   const int64_t total = (int64_t)total_u;
-  const int teams = (int)min((int64_t)(gridDim.x / p.row_tiles), total);
-  const int team = blockIdx.x / p.row_tiles;
-  if (team >= teams) return 0;
-  const int64_t x0 = first_of(team, total, teams);
-  int64_t at = (int64_t)(upto - sum);
-  if (x0 >= at && x0 < (int64_t)upto) {
+  const int teams = (int)min((int64_t)(gridDim.x * kStreams / p.row_tiles), total);
+#pragma unroll
+  for (int x = 0; x < kStreams; ++x) {
+    const int team = blockIdx.x / p.row_tiles * kStreams + x;
+    range[x] = 0;
+    if (team >= teams) continue;
+    const int64_t x0 = first_of(team, total, teams);
+    range[x] = first_of(team + 1, total, teams) - x0;
+    int64_t at = (int64_t)(upto - sum);
+    if (x0 < at || x0 >= (int64_t)upto) continue;
     for (int b = b0; b < b1; ++b) {
-      const int tiles = request_tiles(p, b, tile);
-      const int item = tiles + kItemCost;
+      const int tiles = tiles_of(request_lengths(p, b), tile);
+      const int item = tiles + p.item_cost;
       const int64_t end = at + (int64_t)item * p.kv_heads;
       if (x0 < end) {
-        *start = {b, (int)((x0 - at) / item), (int)((x0 - at) % item), tiles};
-        if (blockIdx.x % p.row_tiles == 0) ws.start[team] = *start;
+        start[x] = {b, (int)((x0 - at) / item), (int)((x0 - at) % item), tiles};
+        if (blockIdx.x % p.row_tiles == 0) ws.start[team] = start[x];
         break;
       }
       at = end;
@@ -267,7 +281,6 @@ __device__ __forceinline__ int64_t find_range(const Params& p, int tile, const W
   }
   if (blockIdx.x == 0 && tid == 0) *ws.total = total;
   __syncthreads();
-  return first_of(team + 1, total, teams) - x0;
 }
 
 // ------------------------------------------------------ the streaming kernel
@@ -326,9 +339,10 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2)
   __shared__ uint64_t s_mask[kRows];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int mw = warp % MW, kw = warp / MW;
-  const Workspace ws = carve(p.workspace, kRows);
-  const int64_t range = find_range<kThreads>(p, S::kTile, ws, s_scan, &s_start);
-  Walk cur = walk_from(s_start, range);
+  const Workspace ws = carve(p.workspace, kRows, p.max_ctas);
+  int64_t range;
+  find_range<kThreads, 1>(p, S::kTile, ws, s_scan, &s_start, &range);
+  Walk cur = walk_from(p, s_start, range, p.item_cost);
   const int r0 = (blockIdx.x % p.row_tiles) * kRows;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
@@ -339,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2)
 
   while (cur.advance(p, S::kTile)) {
     const int tiles = cur.count;
-    const Lengths len = request_lengths(p, cur.b);
+    const Lengths len = cur.len;
     const int kvh = cur.head;
     const int32_t* table = p.table + cur.b * p.table_ld;
     const int live = len.nodes * p.group;  // rows below this one have a node
@@ -594,7 +608,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2)
       }
     __syncthreads();
     const bool full = cur.whole();
-    const int64_t slot = cur.slot();
+    const int64_t slot = cur.slot(blockIdx.x);
     for (int i = tid; i < kRows * (D / 4); i += kThreads) {
       const int r = i / (D / 4), d = (i % (D / 4)) * 4;
       const int row = r0 + r;
@@ -655,14 +669,14 @@ __global__ void __launch_bounds__(kJoinThreads)
   constexpr int kPer = D / 32, kJoinUnroll = kRowsAtOnce;
   constexpr int kJoinRows = kJoinThreads / 32 * kRowsAtOnce, kAhead = 8 / kRowsAtOnce;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const Workspace ws = carve(p.workspace, rows);
+  const Workspace ws = carve(p.workspace, rows, p.max_ctas);
   const int i = blockIdx.x + 1;
   const int64_t total = *ws.total;
   const Start at = ws.start[i];  // of a team without work: not looked at
   const int teams = (int)min((int64_t)(grid / p.row_tiles), total);
   if (i >= teams) return;
-  if (at.at <= kItemCost) return;  // before the item's second tile: not split here
-  const int64_t begin = first_of(i, total, teams) - at.at + kItemCost;
+  if (at.at <= p.item_cost) return;  // before the item's second tile: not split here
+  const int64_t begin = first_of(i, total, teams) - at.at + p.item_cost;
   const int c0 = owner_of(begin, total, teams);
   if (c0 != i - 1) return;
   const int c1 = owner_of(begin + at.tiles - 1, total, teams);
@@ -739,7 +753,7 @@ __global__ void __launch_bounds__(kJoinThreads)
 }
 
 // ---------------------------------------------------------------- launches
-// the joining kernel after a streaming kernel of `grid` CTAs; it is launched
+// the joining kernel after a kernel of `grid` ranges; it is launched
 // while that one runs and waits on the device for its end
 template <typename T, int D, int kRowsAtOnce>
 cudaError_t launch_join(const Params& p, int rows, int grid, cudaStream_t stream) {
@@ -747,7 +761,8 @@ cudaError_t launch_join(const Params& p, int rows, int grid, cudaStream_t stream
   if (teams == 1) return cudaSuccess;
   cudaLaunchConfig_t cfg = {};
   const int at_once = kJoinThreads / 32 * kRowsAtOnce;
-  cfg.gridDim = dim3(teams - 1, (rows + at_once - 1) / at_once, p.row_tiles);
+  const int used = min(rows, p.nodes * p.group);
+  cfg.gridDim = dim3(teams - 1, (used + at_once - 1) / at_once, p.row_tiles);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -758,6 +773,15 @@ cudaError_t launch_join(const Params& p, int rows, int grid, cudaStream_t stream
   return cudaLaunchKernelEx(&cfg, tree_attention_join_kernel<T, D, kRowsAtOnce>, p, rows, grid);
 }
 
+// rows of a streaming CTA for `rows` rows of an item
+inline int stream_rows(int rows, int dim) {
+  if (dim == 256) return rows <= 16 ? 16 : 64;
+  return rows <= 8 ? 8 : rows <= 32 ? 32 : 64;
+}
+// the workspace's ranges, by kernel
+constexpr int kStreamCtas = 320;
+inline int wide_ctas(bool pair) { return pair ? 320 : 160; }
+
 template <typename T, int D, int N8, int MW>
 cudaError_t launch_shape(Params p, int sms, cudaStream_t stream) {
   using S = Shape<D, N8, MW>;
@@ -766,19 +790,12 @@ cudaError_t launch_shape(Params p, int sms, cudaStream_t stream) {
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        S::kSmem);
   if (e != cudaSuccess) return e;
-  const int grid = min(kMaxCtas, max(sms * (D == 256 ? 1 : 2), p.row_tiles));
+  p.max_ctas = kStreamCtas;
+  p.item_cost = kStreamCost;
+  const int grid = min(kStreamCtas, max(sms * (D == 256 ? 1 : 2), p.row_tiles));
   kernel<<<grid, kThreads, S::kSmem, stream>>>(p);
   e = cudaGetLastError();
   return e != cudaSuccess ? e : launch_join<T, D, 1>(p, S::kRows, grid, stream);
-}
-
-// rows of a streaming CTA for `rows` rows of an item: the smallest shape that
-// holds them all, else tiles of 64
-inline int shape_rows(int rows, int dim) {
-  const int eights = (rows + 7) / 8;
-  if (eights <= 2) return 8 * eights;
-  if (eights <= 4) return dim == 256 ? 32 : 8 * eights;
-  return eights <= 6 && dim != 256 ? 48 : 64;
 }
 
 cudaError_t launch_64(const Params& p, int dtype, int sms, cudaStream_t stream);

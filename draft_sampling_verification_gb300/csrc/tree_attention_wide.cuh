@@ -1,6 +1,6 @@
-// tree_attention_wide.cuh -- the attention kernel for items of more than 64
-// rows (wide trees, many query heads to a cached head), on the fifth
-// generation's tensor instructions.  Included by the translation units of
+// tree_attention_wide.cuh -- the attention kernel on the fifth generation's
+// tensor instructions and tensor copies, for caches whose blocks are made of
+// groups of eight rows.  Included by the translation units of
 // tree_attention.cuh.
 #pragma once
 
@@ -57,14 +57,14 @@ __device__ __forceinline__ void mma_commit(bool on, uint64_t* bar) {
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
-// one box of a cache, from (dim x, row r of head h of block b), completing on `bar`; a block
-// beyond the cache gives zeros
-__device__ __forceinline__ void tma_load_box(uint32_t dst, const CUtensorMap* map, int x, int r,
+// one box of a cache, from row r of block b of head h, dims 64 x .., completing on `bar`; a
+// block beyond the cache gives zeros
+__device__ __forceinline__ void tma_load_box(uint32_t dst, const CUtensorMap* map, int r, int x,
                                              int h, int b, uint64_t* bar) {
   asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-      "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
-      "l"(map), "r"(x), "r"(r), "r"(h), "r"(b), "r"(smem_u32(bar))
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+      "l"(map), "r"(0), "r"(r), "r"(x), "r"(h), "r"(b), "r"(smem_u32(bar))
       : "memory");
 }
 __device__ __forceinline__ void fence_async_shared() {
@@ -119,93 +119,118 @@ __device__ __forceinline__ void tmem_wait_store() {
 }
 
 // ------------------------------------------------------------ the kernel
-// Up to 256 rows of an item, as two tiles of 128, over tiles of 128
-// positions: S = Q K^T into tensor memory, softmax by the warpgroup that owns
-// the row tile (a thread per row, so no exchange between threads), the
-// weights back into tensor memory over the scores, O += P V.  The two row
-// tiles alternate: the tensor cores work for one while the other is in its
-// softmax.  Bound by the products (2 * 2 * 128 * 128 * D operations per row
-// tile and step) and, beside them, the exponentials.
+// S = Q K^T into tensor memory for a tile of 128 rows and kKeys positions,
+// softmax by the warpgroup that owns the row tile (a thread per row, so no
+// exchange between threads), the weights back into tensor memory over the
+// scores, O += P V.  Two warpgroups take turns at the tensor cores: while one
+// is in its softmax the products of the other run.
+//
+// kPair: items of up to 128 rows.  The warpgroups go along two ranges of the
+//   tile axis, each with its own queries and its own copies of keys and
+//   values: two CTAs in one, of which one's starts and results are hidden
+//   behind the other's products.  Bound by HBM.
+// kBoth: items of more rows.  The warpgroups take two row tiles of one item
+//   and share its keys and values.  Bound by the products (2 * 2 * 128 * 128 *
+//   D operations a row tile and tile of positions).
+// kOne: head_dim 256, whose accumulators fill half the tensor memory: one
+//   warpgroup, one row tile, 64 positions at a time.
 //
 // The products run in the order they are issued, so the barrier of a tile's
 // scores also says that its accumulators hold every earlier step: the
 // softmax warpgroup may then rescale them.  It does so only when a score
 // passes the row's reference by more than 8, as in the streaming kernel.
 //
-// Warps 0-3 and 4-7: softmax, Q and the results of row tile 0 and 1.  Warp 8:
-// tensor copies of keys and values, box by box of a block's rows, into a ring
-// of stages each.  Warp 9: issues the products.  Warps 10-11: where a tile
-// holds nodes, clear its values of infinities and NaN.  K and Q lie in rows
-// of 64 dims (128 bytes, swizzled in groups of eight rows); V the same, read
-// with dims as its major axis.
-constexpr int kWideThreads = 384;  // 168 registers a thread: a row's 128 scores and more
-constexpr int kWideTile = 128;
+// Warps 0-3 and 4-7: softmax, queries and results.  Warps 8 and 9: tensor
+// copies of keys and values, box by box of a block's rows, into a ring of
+// stages.  Warps 10 and 11: issue the products.  (The second of each pair has
+// work under kPair only.)  Q lies in rows of 64 dims (128 bytes, swizzled in
+// groups of eight rows), one block of 64 dims after the other; keys the same;
+// values too, read with their dims as the major axis.
+enum WideMode { kPair, kBoth, kOne };
 
-template <int D>
+constexpr int kWideThreads = 384;  // 168 registers a thread: a row's 128 scores and more
+
+template <int D, WideMode kMode>
 struct Wide {
+  static constexpr int kStreams = kMode == kPair ? 2 : 1;   // ranges of the tile axis
+  static constexpr int kRowTiles = kMode == kOne ? 1 : 2;   // of 128 rows, over all streams
+  static constexpr int kRows = kMode == kBoth ? 256 : 128;  // of an item, per CTA
+  static constexpr int kKeys = D == 256 ? 64 : 128;
   static constexpr int kHalves = D / 64;
-  static constexpr int kOperand = 128 * D * 2;  // bytes of 128 rows of Q, K or V
-  static constexpr int kStages = D == 64 ? 4 : 2;
-  static constexpr int kSmem = (2 + 2 * kStages) * kOperand + 1024;
+  static constexpr int kQBytes = 128 * D * 2, kTileBytes = kKeys * D * 2;
+  static constexpr int kStages = D == 64 ? (kMode == kPair ? 2 : 4) : (kMode == kPair ? 1 : 2);
+  static constexpr int kRing = 2 * kStages * kTileBytes;    // keys, then values
+  static constexpr int kSmem = kRowTiles * kQBytes + kStreams * kRing + 1024;
 };
 constexpr int kWideMaxStages = 4;
-constexpr int kClearThreads = 64;
 
-struct WideShared {
+struct WideStream {
   uint64_t k_full[kWideMaxStages], k_empty[kWideMaxStages];
   uint64_t v_full[kWideMaxStages], v_empty[kWideMaxStages];
-  uint64_t v_nodes[kWideMaxStages], v_clear[kWideMaxStages];
-  uint64_t q_full[2], s_full[2], p_full[2], o_full[2], drained;
-  uint64_t scan[32];
-  Start start;
   uint32_t valid[8][4];  // a tile's positions that hold a key, by tile number modulo 8
   uint32_t special[8];   // a value of a tile's nodes is an infinity or a NaN
+};
+struct WideShared {
+  WideStream stream[2];
+  uint64_t q_full[2], s_full[2], p_full[2], o_full[2], drained[2];
+  uint64_t scan[32];
+  int64_t q_row[256];  // where each row of the CTA begins in Q, from its request and cached head on
+  Start start[2];
   uint32_t tmem;
-  uint32_t failed;       // a wait expired
+  uint32_t failed;  // a wait expired
 };
 
-template <typename T, int D>
+template <typename T, int D, WideMode kMode>
 __global__ void __launch_bounds__(kWideThreads, 1)
     tree_attention_wide_kernel(const __grid_constant__ Params p,
                                const __grid_constant__ CUtensorMap k_map,
                                const __grid_constant__ CUtensorMap v_map, int box_rows) {
   using H = Half<T>;
-  using W = Wide<D>;
-  constexpr int kChunks = D / 8, kStages = W::kStages;
+  using W = Wide<D, kMode>;
+  constexpr int kChunks = D / 8, kStages = W::kStages, kKeys = W::kKeys, kHalves = W::kHalves;
+  constexpr bool kPaired = kMode == kPair;
   extern __shared__ unsigned char smem_raw[];
   __shared__ WideShared sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  const uint32_t q_at = base, k_at = base + 2 * W::kOperand, v_at = k_at + kStages * W::kOperand;
+  const uint32_t ring = base + W::kRowTiles * W::kQBytes;
+  // a tile of keys or values: bytes between its groups of eight rows, and between its blocks of
+  // 64 dims.  A box of eight rows brings all blocks, one after the other.
+  const uint32_t group_bytes = box_rows == 8 ? kHalves * 1024u : 1024u;
+  const uint32_t half_bytes = box_rows == 8 ? 1024u : kKeys * 128u;
 
-  const Workspace ws = carve(p.workspace, kWideRows);
-  const int64_t range = find_range<kWideThreads>(p, kWideTile, ws, sh.scan, &sh.start);
+  const Workspace ws = carve(p.workspace, W::kRows, p.max_ctas);
+  int64_t ranges[W::kStreams];
+  find_range<kWideThreads, W::kStreams>(p, kKeys, ws, sh.scan, sh.start, ranges);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (range <= 0) return;
-  Walk cur = walk_from(sh.start, range);
-  const int r0 = (blockIdx.x % p.row_tiles) * kWideRows;
-  const int n_tiles = p.nodes * p.group - r0 > 128 ? 2 : 1;
+  if (ranges[0] <= 0) return;  // the second stream's range comes behind the first's
+  const int r0 = (blockIdx.x % p.row_tiles) * W::kRows;
+  // row tiles of one stream
+  const int n_tiles = kMode == kBoth && p.nodes * p.group - r0 > 128 ? 2 : 1;
 
+  for (int r = tid; r < W::kRows; r += kWideThreads) {
+    const int row = min(r0 + r, p.nodes * p.group - 1), node = row / p.group;  // past the end: the last
+    sh.q_row[r] = node * p.q_node + (row - node * p.group) * p.q_head;
+  }
   if (tid == 0) {
-    for (int i = 0; i < kStages; ++i) {
-      mbar_init(&sh.k_full[i], 1);
-      mbar_init(&sh.k_empty[i], 1);
-      mbar_init(&sh.v_full[i], 1);
-      mbar_init(&sh.v_empty[i], 1);
-      mbar_init(&sh.v_nodes[i], 1);
-      mbar_init(&sh.v_clear[i], kClearThreads);
-    }
+    for (int x = 0; x < W::kStreams; ++x)
+      for (int i = 0; i < kStages; ++i) {
+        mbar_init(&sh.stream[x].k_full[i], 1);
+        mbar_init(&sh.stream[x].k_empty[i], 1);
+        mbar_init(&sh.stream[x].v_full[i], 1);
+        mbar_init(&sh.stream[x].v_empty[i], 1);
+      }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.q_full[i], 128);
       mbar_init(&sh.s_full[i], 1);
       mbar_init(&sh.p_full[i], 128);
       mbar_init(&sh.o_full[i], 1);
+      mbar_init(&sh.drained[i], 1);
     }
-    mbar_init(&sh.drained, 1);
     sh.failed = 0u;
     mbar_init_fence();
   }
-  if (warp == 9) {
+  if (warp == 10) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
                      smem_u32(&sh.tmem))
                  : "memory");
@@ -227,63 +252,82 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     *(volatile uint32_t*)&sh.failed = 1u;
     return false;
   };
+  auto wait_all = [&](uint64_t* bar, uint32_t phase) -> bool {
+    return __all_sync(0xffffffffu, wait(bar, phase));
+  };
+  auto phase_of = [](uint32_t g) -> uint32_t { return (g / kStages) & 1u; };
+
   if (warp < 8) {
     // -------------------------------------------------- softmax and results
-    const int m = warp >> 2;
+    const int m = warp >> 2;               // the row tile
+    const int x = kPaired ? m : 0;         // the stream
+    const int m_rows = r0 + (kPaired ? 0 : m * 128);  // the tile's first row of the item
+    WideStream& stream = sh.stream[x];
     const int t = tid & 127;  // this thread's row of the tile and lane of tensor memory
     const uint32_t sc = s_col(m) + ((uint32_t)(t & ~31) << 16);
     const uint32_t oc = o_col(m) + ((uint32_t)(t & ~31) << 16);
+    const uint32_t q_at = base + m * W::kQBytes;
     // a negative scale goes into Q's sign, so that the largest score stays the largest; 0 would
     // make NaN of a hidden score
     const uint32_t flip = p.scale2 < 0.0f ? 0x80008000u : 0u;
     const float scale = fmaxf(fabsf(p.scale2), 1.17549435e-38f);
     uint32_t tile_no = 0, segments = 0;
-    bool ok = m < n_tiles;
-    // the item's Q: 16-byte pieces of this thread's column, every kStep-th row
+    bool ok = m < (kPaired ? 2 : n_tiles) && m < W::kRowTiles;
+    Walk cur = walk_from(p, sh.start[x], ok ? ranges[x] : 0, p.item_cost);
+    // the item's Q: 16-byte pieces of this thread's column, every kStep-th row, in parts of kPart
     constexpr int kStep = 128 / kChunks;
-    uint4 q[kChunks];
-    auto load_q = [&](const Walk& w) {
-      const int live = request_lengths(p, w.b).nodes * p.group;
-      const T* from = static_cast<const T*>(p.q) + w.b * p.q_req + (t % kChunks) * 8;
-#pragma unroll
-      for (int i = 0; i < kChunks; ++i) {
-        const int row = r0 + m * 128 + i * kStep + t / kChunks;
-        const int at = row < live ? row : 0, node = at / p.group;  // no branch: all loads at once
-        const int h = w.head * p.group + at - node * p.group;
-        const T* piece = from + node * p.q_node + h * p.q_head;
-        q[i] = live > 0 ? __ldg(reinterpret_cast<const uint4*>(piece)) : make_uint4(0u, 0u, 0u, 0u);
-        const uint32_t keep = row < live ? ~0u : 0u;
-        q[i] = make_uint4((q[i].x ^ flip) & keep, (q[i].y ^ flip) & keep, (q[i].z ^ flip) & keep,
-                          (q[i].w ^ flip) & keep);
-      }
+    constexpr int kPart = kChunks > 16 ? 16 : kChunks;
+    const int64_t* q_row = sh.q_row + (m_rows - r0) + t / kChunks;
+    auto q_from = [&](const Walk& w) -> const T* {
+      return static_cast<const T*>(p.q) + w.b * p.q_req + (int64_t)w.head * p.group * p.q_head +
+             (t % kChunks) * 8;
     };
-    auto store_q = [&] {
-      const int c = t % kChunks;
+    auto prefetch_q = [&](const Walk& w) {  // a thread for each 128-byte line
+      if (t % 8 != 0) return;
+      const T* from = q_from(w);
 #pragma unroll
-      for (int i = 0; i < kChunks; ++i) {
-        const int r = i * kStep + t / kChunks;
-        const uint32_t to = q_at + m * W::kOperand + (c >> 3) * 16384 + r * 128 +
-                            (((c & 7) ^ (r & 7)) << 4);
-        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(q[i].x),
-                     "r"(q[i].y), "r"(q[i].z), "r"(q[i].w)
-                     : "memory");
+      for (int i = 0; i < kChunks; ++i)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(from + q_row[i * kStep]));
+    };
+    auto fill_q = [&](const Walk& w) {
+      const int live = w.len.nodes * p.group - m_rows, c = t % kChunks;  // rows of the tile
+      const T* from = q_from(w);
+#pragma unroll
+      for (int part = 0; part < kChunks / kPart; ++part) {
+        uint4 q[kPart];
+#pragma unroll
+        for (int i = 0; i < kPart; ++i)
+          q[i] = __ldg(reinterpret_cast<const uint4*>(from + q_row[(part * kPart + i) * kStep]));
+#pragma unroll
+        for (int i = 0; i < kPart; ++i) {
+          const int r = (part * kPart + i) * kStep + t / kChunks;
+          const uint32_t keep = r < live ? ~0u : 0u;
+          const uint32_t to = q_at + (c >> 3) * 16384 + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to),
+                       "r"((q[i].x ^ flip) & keep), "r"((q[i].y ^ flip) & keep),
+                       "r"((q[i].z ^ flip) & keep), "r"((q[i].w ^ flip) & keep)
+                       : "memory");
+        }
       }
       fence_async_shared();
       mbar_arrive(&sh.q_full[m]);
     };
-    bool more = ok && cur.advance(p, kWideTile);
-    if (more) {
-      load_q(cur);
-      store_q();
-    }
+    bool more = ok && cur.advance(p, kKeys);
+    if (more) fill_q(cur);
+    const int row = m_rows + t, node = row / p.group;
+    const bool mine = row < p.nodes * p.group;
+    const int64_t my_row = (int64_t)node * p.heads + row - node * p.group;  // in an item's results
     while (ok && more) {
       const int tiles = cur.count;
-      const Lengths len = request_lengths(p, cur.b);
+      const Lengths len = cur.len;
       const int live = len.nodes * p.group;
-      if (tid == 0 && r0 == 0 && cur.head == 0 && cur.first == 0)
+      if (t == 0 && m_rows == 0 && cur.head == 0 && cur.first == 0)
         p.status[cur.b] = len.bad ? DSPARK_ST_BAD_LENGTH : DSPARK_ST_OK;
 
-      const int row = r0 + m * 128 + t, node = row / p.group;
+      Walk ahead = cur;
+      more = ahead.advance(p, kKeys);
+      if (more) prefetch_q(ahead);
+      const bool idle = m_rows + (t & ~31) >= live;  // no row of this warp has a node
       uint64_t mask = 0;
       if (row < live)
         mask = p.mask ? p.mask[(int64_t)cur.b * p.nodes + node] : ~0ull >> (63 - node);
@@ -291,93 +335,129 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       float2 sum2 = make_float2(0.0f, 0.0f);
       bool special = false;
       for (int i = 0; i < tiles; ++i, ++tile_no) {
-        ok = __all_sync(0xffffffffu, wait(&sh.s_full[m], tile_no & 1u));
+        ok = wait_all(&sh.s_full[m], tile_no & 1u);
         if (!ok) break;
         tc_after_sync();
-        if (i > 0) special |= sh.special[(tile_no - 1u) & 7u] != 0u;
-        const int pos = (cur.first + i) * kWideTile;
-        const uint32_t* words = sh.valid[tile_no & 7u];
-        const bool plain = pos + kWideTile <= len.ctx &&
-                           (words[0] & words[1] & words[2] & words[3]) == 0xFFFFFFFFu;
-        float v[128];
+        if (i > 0) special |= stream.special[(tile_no - 1u) & 7u] != 0u;
+        const int pos = (cur.first + i) * kKeys;
+        const bool nodes_here = pos + kKeys > len.ctx;
+        if (!idle) {
+          const uint32_t* words = stream.valid[tile_no & 7u];
+          uint32_t all = ~0u;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_load32(v + c * 32, sc + c * 32);
-        tmem_wait_load();
-        if (!plain) {
+          for (int c = 0; c < kKeys / 32; ++c) all &= words[c];
+          float v[kKeys];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t w = words[c];
-            const int node0 = pos + c * 32 - len.ctx;  // the node of the chunk's first position
-            if (node0 >= 0)
-              w &= node0 < 64 ? (uint32_t)(mask >> node0) : 0u;
-            else if (node0 > -32)
-              w &= (uint32_t)(mask << -node0) | ((1u << -node0) - 1u);
+          for (int c = 0; c < kKeys / 32; ++c) tmem_load32(v + c * 32, sc + c * 32);
+          tmem_wait_load();
+          if (nodes_here || all != ~0u) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (!((w >> j) & 1u)) v[c * 32 + j] = -INFINITY;
-          }
-        }
-        float m4[4] = {v[0], v[1], v[2], v[3]};
+            for (int c = 0; c < kKeys / 32; ++c) {
+              uint32_t w = words[c];
+              const int node0 = pos + c * 32 - len.ctx;  // the node of the chunk's first position
+              if (node0 >= 0)
+                w &= node0 < 64 ? (uint32_t)(mask >> node0) : 0u;
+              else if (node0 > -32)
+                w &= (uint32_t)(mask << -node0) | ((1u << -node0) - 1u);
+              if (__all_sync(0xffffffffu, w == ~0u)) continue;
 #pragma unroll
-        for (int j = 4; j < 124; j += 8) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) m4[k] = fmaxf(fmaxf(m4[k], v[j + k]), v[j + 4 + k]);
-        }
-#pragma unroll
-        for (int k = 0; k < 4; ++k) m4[k] = fmaxf(m4[k], v[124 + k]);
-        float top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * scale;
-        if (__any_sync(0xffffffffu, top > ref + kSlack)) {
-          top = fmaxf(top, ref);
-          const float f = top == -INFINITY ? 1.0f : exp2_approx(ref - top);
-          ref = top;
-          sum2.x *= f;
-          sum2.y *= f;
-          if (i > 0) {
-#pragma unroll 1
-            for (int c = 0; c < D / 16; ++c) {
-              uint32_t a[16];
-              tmem_load16(a, oc + c * 16);
-              tmem_wait_load();
-#pragma unroll
-              for (int j = 0; j < 16; ++j) a[j] = __float_as_uint(__uint_as_float(a[j]) * f);
-              tmem_store16(oc + c * 16, a);
+              for (int j = 0; j < 32; ++j)
+                if (!((w >> j) & 1u)) v[c * 32 + j] = -INFINITY;
             }
           }
-        }
-        const float2 off = f2(ref == -INFINITY ? 0.0f : -ref), by = f2(scale);
-        float2 part2 = make_float2(0.0f, 0.0f);
+          float m4[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t w[16];
+          for (int j = 4; j < kKeys - 4; j += 8) {
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            float2 x = fma2_rn(make_float2(v[c * 32 + 2 * j], v[c * 32 + 2 * j + 1]), by, off);
-            x.x = exp2_approx(x.x);
-            x.y = exp2_approx(x.y);
-            if (j & 1)
-              part2 = add2_rn(part2, x);
-            else
-              sum2 = add2_rn(sum2, x);
-            w[j] = H::pack(x.x, x.y);
+            for (int k = 0; k < 4; ++k) m4[k] = fmaxf(fmaxf(m4[k], v[j + k]), v[j + 4 + k]);
           }
-          tmem_store16(sc + c * 16, w);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) m4[k] = fmaxf(m4[k], v[kKeys - 4 + k]);
+          float top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * scale;
+          if (__any_sync(0xffffffffu, top > ref + kSlack)) {
+            top = fmaxf(top, ref);
+            const float f = top == -INFINITY ? 1.0f : exp2_approx(ref - top);
+            ref = top;
+            sum2.x *= f;
+            sum2.y *= f;
+            if (i > 0) {
+#pragma unroll 1
+              for (int c = 0; c < D / 16; ++c) {
+                uint32_t a[16];
+                tmem_load16(a, oc + c * 16);
+                tmem_wait_load();
+#pragma unroll
+                for (int j = 0; j < 16; ++j) a[j] = __float_as_uint(__uint_as_float(a[j]) * f);
+                tmem_store16(oc + c * 16, a);
+              }
+            }
+          }
+          const float2 off = f2(ref == -INFINITY ? 0.0f : -ref), by = f2(scale);
+          float2 part2 = make_float2(0.0f, 0.0f);
+#pragma unroll
+          for (int c = 0; c < kKeys / 32; ++c) {
+            uint32_t w[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              float2 e = fma2_rn(make_float2(v[c * 32 + 2 * j], v[c * 32 + 2 * j + 1]), by, off);
+              e.x = exp2_approx(e.x);
+              e.y = exp2_approx(e.y);
+              if (j & 1)
+                part2 = add2_rn(part2, e);
+              else
+                sum2 = add2_rn(sum2, e);
+              w[j] = H::pack(e.x, e.y);
+            }
+            tmem_store16(sc + c * 16, w);
+          }
+          sum2 = add2_rn(sum2, part2);
+          tmem_wait_store();
         }
-        sum2 = add2_rn(sum2, part2);
-        tmem_wait_store();
+        if (nodes_here && (kMode != kBoth || m == 0)) {
+          // Rows from the first node on: nodes, which some rows see and others
+          // do not, and what lies behind the end.  0 times an infinity or a
+          // NaN would reach rows that do not see it: they are cleared before
+          // the weights are handed over, which lets the product begin (of the
+          // second row tile after that of the first).
+          const uint32_t stage = tile_no % kStages;
+          ok = wait_all(&stream.v_full[stage], phase_of(tile_no));
+          if (!ok) break;
+          const uint32_t v_at = ring + x * W::kRing + (kStages + stage) * W::kTileBytes;
+          const int from = max(0, len.ctx - pos);
+          // blocks' rows that the last copy brought; zeros behind them
+          const int end = min(kKeys, (len.len - pos + box_rows - 1) / box_rows * box_rows);
+          for (int j = t; j < (end - from) * kChunks; j += 128) {
+            const int r = from + j / kChunks, c = j % kChunks;
+            const uint32_t addr = v_at + (r >> 3) * group_bytes + (c >> 3) * half_bytes +
+                                  (r & 7) * 128 + (((c & 7) ^ (r & 7)) << 4);
+            uint32_t w[4];
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                         : "r"(addr)
+                         : "memory");
+            if (any_special<T>(w[0]) || any_special<T>(w[1]) || any_special<T>(w[2]) ||
+                any_special<T>(w[3])) {
+              asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr),
+                           "r"(without_special<T>(w[0])), "r"(without_special<T>(w[1])),
+                           "r"(without_special<T>(w[2])), "r"(without_special<T>(w[3]))
+                           : "memory");
+              if (pos + r < len.len) *(volatile uint32_t*)&stream.special[tile_no & 7u] = 1u;
+            }
+          }
+          __syncwarp();
+          fence_async_shared();
+        }
         tc_before_sync();
         mbar_arrive(&sh.p_full[m]);
       }
-      // the next item's Q is on its way while this one's last products run, and
-      // its first scores are computed while this one's results are written
-      Walk ahead = cur;
-      more = ok && ahead.advance(p, kWideTile);
-      if (more) load_q(ahead);
-      if (ok) ok = __all_sync(0xffffffffu, wait(&sh.o_full[m], segments & 1u));
+      // Q is free, as the last scores are done: the next item's first scores
+      // are computed while this one's results are written
+      if (ok && more) fill_q(ahead);
+      if (ok) ok = wait_all(&sh.o_full[m], segments & 1u);
       ++segments;
       if (!ok) break;
       tc_after_sync();
-      if (more) store_q();
-      special |= sh.special[(tile_no - 1u) & 7u] != 0u;
+      special |= stream.special[(tile_no - 1u) & 7u] != 0u;
 
       float sum = sum2.x + sum2.y;
       if (row >= live) {  // a row of no node: its zero query saw the text all the same
@@ -385,13 +465,13 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         sum = 0.0f;
       }
       const bool full = cur.whole();
-      const int h = cur.head * p.group + row - node * p.group;
-      const int64_t to = ((int64_t)cur.b * p.nodes + node) * p.heads + h;
-      const int64_t slot = cur.slot();
-      const bool mine = row < p.nodes * p.group;
+      const int64_t to = (int64_t)cur.b * p.nodes * p.heads + cur.head * p.group + my_row;
+      const int64_t slot = cur.slot(kPaired ? 2 * blockIdx.x + x : blockIdx.x) * W::kRows +
+                           (kPaired ? 0 : m * 128) + t;
       const float inv = sum == 0.0f ? 0.0f : full ? 1.0f / sum : 1.0f;
+      const int chunks = m_rows + (t & ~31) < p.nodes * p.group ? D / 32 : 0;  // of the warp
 #pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {
+      for (int c = 0; c < chunks; ++c) {
         float v[32];
         tmem_load32(v, oc + c * 32);
         tmem_wait_load();
@@ -403,7 +483,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           // infinities and NaN, left out of the product, reach the rows that see their key
 #pragma unroll 1
           for (int k = 0; k < len.nodes; ++k) {
-            const int at = len.ctx + k, tile = at / kWideTile;
+            const int at = len.ctx + k, tile = at / kKeys;
             if (!((mask >> k) & 1ull) || tile < cur.first || tile >= cur.first + tiles) continue;
             const int block = p.table[cur.b * p.table_ld + at / p.page];
             if (block < 0 || block >= p.n_blocks) continue;
@@ -427,7 +507,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                                 H::pack(v[8 * j + 6] * inv, v[8 * j + 7] * inv));
         } else if (mine) {
           // whole 32-byte sectors: a warp's rows lie far apart
-          float* out = ws.rows + (slot * kWideRows + m * 128 + t) * D + c * 32;
+          float* out = ws.rows + slot * D + c * 32;
 #pragma unroll
           for (int j = 0; j < 32; j += 8)
             asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(out + j),
@@ -439,203 +519,169 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       }
       if (mine) {
         if (!full)
-          ws.stats[slot * kWideRows + m * 128 + t] = make_float2(ref, sum);
+          ws.stats[slot] = make_float2(ref, sum);
         else if (p.lse)
           p.lse[to] = sum == 0.0f ? -INFINITY : (ref + log2f(sum)) * 0.6931471805599453f;
       }
       tc_before_sync();  // the accumulators are read: the next item may take them
       cur = ahead;
     }
-  } else if (warp != 9) {
+  } else if (warp < 8 + W::kStreams) {
     // ------------------------------------------------------ keys and values
     // Lane i copies the tile's box i, box_rows positions of one block.
-    const int boxes = kWideTile / box_rows;  // at most 16
-    uint32_t g = 0, turns = 0;  // turns: each stage's phase of the tiles with nodes
+    const int x = warp - 8;
+    WideStream& stream = sh.stream[x];
+    const uint32_t k_at = ring + x * W::kRing, v_at = k_at + kStages * W::kTileBytes;
+    const int boxes = kKeys / box_rows;  // at most 16
+    uint32_t g = 0;
     bool ok = true;
-    while (ok && cur.advance(p, kWideTile)) {
+    Walk cur = walk_from(p, sh.start[x], ranges[x], p.item_cost);
+    while (ok && cur.advance(p, kKeys)) {
       const int tiles = cur.count;
-      const Lengths len = request_lengths(p, cur.b);
-      const int first = cur.first * kWideTile;
-      if (warp == 8) {
-        const int32_t* table = p.table + cur.b * p.table_ld;
-        auto entry_of = [&](int i) -> int {
-          const int pos = first + i * kWideTile + lane * box_rows;
-          return i < tiles && lane < boxes && pos < len.len ? __ldg(table + pos / p.page) : -1;
-        };
-        int ahead = entry_of(0);
-        for (int i = 0; i < tiles; ++i, ++g) {
-          const int pos0 = first + i * kWideTile, pos = pos0 + lane * box_rows, block = ahead;
-          ahead = entry_of(i + 1);
-          const bool held = block >= 0 && block < p.n_blocks;
-          const int from = held ? block : p.n_blocks, row = held ? pos % p.page : 0;
-          const uint32_t held_boxes = __ballot_sync(0xffffffffu, held);
-          const uint32_t stage = g % kStages, phase = (g / kStages) & 1u;
-          ok = __all_sync(0xffffffffu, wait(&sh.k_empty[stage], phase ^ 1u));
-          if (!ok) break;
-          if (lane < 4) {
-            uint32_t word = 0u;  // positions 32 lane .. of the tile
-            if (box_rows >= 32) {
-              word = (held_boxes >> (lane * 32 / box_rows)) & 1u ? ~0u : 0u;
-            } else {
-              for (int j = 0; j < 32 / box_rows; ++j)
-                if ((held_boxes >> (lane * 32 / box_rows + j)) & 1u)
-                  word |= ((1u << box_rows) - 1u) << (j * box_rows);
-            }
-            const int past = len.len - (pos0 + lane * 32);  // positions before the end
-            sh.valid[g & 7u][lane] = past >= 32 ? word : past > 0 ? word & ((1u << past) - 1u) : 0u;
-            sh.special[g & 7u] = 0u;
+      const Lengths len = cur.len;
+      const int first = cur.first * kKeys;
+      const int32_t* table = p.table + cur.b * p.table_ld;
+      auto entry_of = [&](int i) -> int {
+        const int pos = first + i * kKeys + lane * box_rows;
+        return i < tiles && lane < boxes && pos < len.len ? __ldg(table + pos / p.page) : -1;
+      };
+      int ahead = entry_of(0);
+      for (int i = 0; i < tiles; ++i, ++g) {
+        const int pos0 = first + i * kKeys, pos = pos0 + lane * box_rows, block = ahead;
+        ahead = entry_of(i + 1);
+        const bool held = block >= 0 && block < p.n_blocks;
+        const int from = held ? block : p.n_blocks, row = held ? pos % p.page : 0;
+        const uint32_t held_boxes = __ballot_sync(0xffffffffu, held);
+        const uint32_t stage = g % kStages;
+        ok = wait_all(&stream.k_empty[stage], phase_of(g) ^ 1u);
+        if (!ok) break;
+        if (lane < kKeys / 32) {
+          uint32_t word = 0u;  // positions 32 lane .. of the tile
+          if (box_rows >= 32) {
+            word = (held_boxes >> (lane * 32 / box_rows)) & 1u ? ~0u : 0u;
+          } else {
+            for (int j = 0; j < 32 / box_rows; ++j)
+              if ((held_boxes >> (lane * 32 / box_rows + j)) & 1u)
+                word |= ((1u << box_rows) - 1u) << (j * box_rows);
           }
-          auto copy = [&](const CUtensorMap* map, uint32_t at, uint64_t* full) {
-            if (lane == 0) mbar_arrive_expect_tx(full, W::kOperand);
-            __syncwarp();
-            if (lane < boxes) {
+          const int past = len.len - (pos0 + lane * 32);  // positions before the end
+          stream.valid[g & 7u][lane] =
+              past >= 32 ? word : past > 0 ? word & ((1u << past) - 1u) : 0u;
+        }
+        if (lane == 0) stream.special[g & 7u] = 0u;
+        auto copy = [&](const CUtensorMap* map, uint32_t at, uint64_t* full) {
+          if (lane == 0) mbar_arrive_expect_tx(full, W::kTileBytes);
+          __syncwarp();
+          if (lane >= boxes) return;
+          at += stage * W::kTileBytes;
+          if (box_rows == 8) {
+            tma_load_box(at + lane * group_bytes, map, row, 0, cur.head, from, full);
+          } else {
 #pragma unroll
-              for (int h = 0; h < W::kHalves; ++h)
-                tma_load_box(at + stage * W::kOperand + h * 16384 + lane * box_rows * 128, map,
-                             h * 64, row, cur.head, from, full);
-            }
-          };
-          copy(&k_map, k_at, &sh.k_full[stage]);
-          ok = __all_sync(0xffffffffu, wait(&sh.v_empty[stage], phase ^ 1u));
-          if (!ok) break;
-          // values that are to be cleared first land on a barrier of their own
-          const bool nodes_here = pos0 + kWideTile > len.ctx;
-          copy(&v_map, v_at, nodes_here ? &sh.v_nodes[stage] : &sh.v_full[stage]);
-          if (nodes_here && lane == 0) mbar_arrive(&sh.v_full[stage]);
-        }
-      } else {
-        // Rows from the first node on: nodes, which some rows see and others
-        // do not, and what lies behind the end.  0 times an infinity or a NaN
-        // would reach rows that do not see it.
-        for (int i = 0; i < tiles; ++i, ++g) {
-          const int pos0 = first + i * kWideTile;
-          if (pos0 + kWideTile <= len.ctx) continue;
-          const uint32_t stage = g % kStages;
-          ok = __all_sync(0xffffffffu, wait(&sh.v_nodes[stage], (turns >> stage) & 1u));
-          if (!ok) break;
-          turns ^= 1u << stage;
-          const int from = max(0, len.ctx - pos0);
-          for (int j = tid - 320; j < (kWideTile - from) * kChunks; j += kClearThreads) {
-            const int r = from + j / kChunks, c = j % kChunks;
-            const uint32_t addr = v_at + stage * W::kOperand + (c >> 3) * 16384 + r * 128 +
-                                  (((c & 7) ^ (r & 7)) << 4);
-            uint32_t w[4];
-            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                         : "r"(addr)
-                         : "memory");
-            if (any_special<T>(w[0]) || any_special<T>(w[1]) || any_special<T>(w[2]) ||
-                any_special<T>(w[3])) {
-              asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr),
-                           "r"(without_special<T>(w[0])), "r"(without_special<T>(w[1])),
-                           "r"(without_special<T>(w[2])), "r"(without_special<T>(w[3]))
-                           : "memory");
-              if (pos0 + r < len.len) *(volatile uint32_t*)&sh.special[g & 7u] = 1u;
-            }
+            for (int h = 0; h < kHalves; ++h)
+              tma_load_box(at + h * half_bytes + lane * box_rows * 128, map, row, h, cur.head,
+                           from, full);
           }
-          fence_async_shared();
-          mbar_arrive(&sh.v_clear[stage]);
-        }
+        };
+        copy(&k_map, k_at, &stream.k_full[stage]);
+        __syncwarp();
+        ok = wait_all(&stream.v_empty[stage], phase_of(g) ^ 1u);
+        if (!ok) break;
+        copy(&v_map, v_at, &stream.v_full[stage]);
+        __syncwarp();
       }
     }
-  } else {
+  } else if (warp >= 10 && warp < 10 + W::kStreams) {
     // ------------------------------------------------------------- products
     // The warp goes through the loop together; one lane issues.
+    const int x = warp - 10;
+    WideStream& stream = sh.stream[x];
     constexpr uint32_t kFormat = H::kExponent == 0x7F80u ? 1u : 0u;  // bf16 or f16
     // fp32 accumulators, both operands of T, 128 rows; for P V the second has its dims outermost
     constexpr uint32_t kCommon = (1u << 4) | (kFormat << 7) | (kFormat << 10) | (8u << 24);
-    constexpr uint32_t kScores = kCommon | ((kWideTile / 8u) << 17);
-    constexpr uint32_t kValues = kCommon | (1u << 16) | (((uint32_t)D / 8u) << 17);
+    constexpr uint32_t kScores = kCommon | ((uint32_t)(kKeys / 8) << 17);
+    constexpr uint32_t kValues = kCommon | (1u << 16) | ((uint32_t)(D / 8) << 17);
     const bool on = elect_one();
-    // descriptors of Q's tiles, and of the stages of keys and values; an
+    // descriptors of this stream's first row tile of Q, and of the stages of keys and values; an
     // operand further on adds its distance / 16
-    const uint64_t q_desc = operand_desc(q_at, 16, 1024), k_desc = operand_desc(k_at, 16, 1024);
-    const uint64_t v_desc = operand_desc(v_at, 16384, 1024);
-    auto scores = [&](int m, uint32_t g) {
-      const uint64_t a = q_desc + (uint32_t)m * (W::kOperand / 16);
-      const uint64_t b = k_desc + (g % kStages) * (W::kOperand / 16);
+    const uint64_t q_desc = operand_desc(base + x * W::kQBytes, 16, 1024);
+    const uint64_t k_desc = operand_desc(ring + x * W::kRing, 16, group_bytes);
+    const uint64_t v_desc = operand_desc(ring + x * W::kRing + kStages * W::kTileBytes, half_bytes,
+                                         group_bytes);
+    auto scores = [&](int m, uint32_t g) {  // m: the row tile, of this stream
+      const uint64_t a = q_desc + (uint32_t)m * (W::kQBytes / 16);
+      const uint64_t b = k_desc + (g % kStages) * (W::kTileBytes / 16);
 #pragma unroll
-      for (int kt = 0; kt < D / 16; ++kt) {
-        constexpr int kHalf = 16384 / 16, kStep = 32 / 16;
-        const uint32_t at = (kt >> 2) * kHalf + (kt & 3) * kStep;
-        mma_ss(on, s_col(m), a + at, b + at, kScores, kt > 0);
-      }
-      mma_commit(on, &sh.s_full[m]);
+      for (int kt = 0; kt < D / 16; ++kt)
+        mma_ss(on, s_col(x + m), a + (kt >> 2) * (16384 / 16) + (kt & 3) * 2,
+               b + (kt >> 2) * (half_bytes / 16) + (kt & 3) * 2, kScores, kt > 0);
+      mma_commit(on, &sh.s_full[x + m]);
     };
     auto values = [&](int m, uint32_t g, bool add) {
-      const uint64_t b = v_desc + (g % kStages) * (W::kOperand / 16);
+      const uint64_t b = v_desc + (g % kStages) * (W::kTileBytes / 16);
 #pragma unroll
-      for (int kt = 0; kt < kWideTile / 16; ++kt)
-        mma_ts(on, o_col(m), s_col(m) + kt * 8, b + kt * (2048 / 16), kValues, add || kt > 0);
+      for (int kt = 0; kt < kKeys / 16; ++kt)
+        mma_ts(on, o_col(x + m), s_col(x + m) + kt * 8, b + kt * (2 * group_bytes / 16), kValues,
+               add || kt > 0);
     };
-    auto wait_all = [&](uint64_t* bar, uint32_t phase) -> bool {
-      return __all_sync(0xffffffffu, wait(bar, phase));
-    };
-    auto phase_of = [](uint32_t g) -> uint32_t { return (g / kStages) & 1u; };
-    uint32_t g = 0, segments = 0, turns = 0;
+    uint32_t g = 0, segments = 0;
     bool ok = true;
-    while (ok && cur.advance(p, kWideTile)) {
+    Walk cur = walk_from(p, sh.start[x], ranges[x], p.item_cost);
+    while (ok && cur.advance(p, kKeys)) {
       const int tiles = cur.count;
-      const Lengths len = request_lengths(p, cur.b);
-      for (int m = 0; m < n_tiles; ++m) ok = ok && wait_all(&sh.q_full[m], segments & 1u);
-      ok = ok && wait_all(&sh.k_full[g % kStages], phase_of(g));
+      for (int m = 0; m < n_tiles; ++m) ok = ok && wait_all(&sh.q_full[x + m], segments & 1u);
+      ok = ok && wait_all(&stream.k_full[g % kStages], phase_of(g));
       if (!ok) break;
       tc_after_sync();
       for (int m = 0; m < n_tiles; ++m) scores(m, g);
-      mma_commit(on, &sh.k_empty[g % kStages]);
+      mma_commit(on, &stream.k_empty[g % kStages]);
       for (int i = 0; i < tiles && ok; ++i, ++g) {
         const bool more = i + 1 < tiles;
         for (int m = 0; m < n_tiles; ++m) {
-          ok = wait_all(&sh.p_full[m], g & 1u);
-          if (m == 0) {
-            ok = ok && wait_all(&sh.v_full[g % kStages], phase_of(g));
-            if ((cur.first + i + 1) * kWideTile > len.ctx) {
-              ok = ok && wait_all(&sh.v_clear[g % kStages], (turns >> (g % kStages)) & 1u);
-              turns ^= 1u << (g % kStages);
-            }
-          }
+          ok = wait_all(&sh.p_full[x + m], g & 1u);
+          if (m == 0) ok = ok && wait_all(&stream.v_full[g % kStages], phase_of(g));
           if (!ok) break;
           tc_after_sync();
           values(m, g, i > 0);
-          if (m == n_tiles - 1) mma_commit(on, &sh.v_empty[g % kStages]);
+          if (m == n_tiles - 1) mma_commit(on, &stream.v_empty[g % kStages]);
           if (more) {
-            if (m == 0) ok = wait_all(&sh.k_full[(g + 1u) % kStages], phase_of(g + 1u));
+            if (m == 0) ok = wait_all(&stream.k_full[(g + 1u) % kStages], phase_of(g + 1u));
             if (!ok) break;
             scores(m, g + 1u);
           } else {
-            mma_commit(on, &sh.o_full[m]);
+            mma_commit(on, &sh.o_full[x + m]);
           }
         }
-        if (ok && more) mma_commit(on, &sh.k_empty[(g + 1u) % kStages]);
+        if (ok && more) mma_commit(on, &stream.k_empty[(g + 1u) % kStages]);
       }
       ++segments;
     }
-    // nothing of this CTA's is in flight when its memory is given back
-    mma_commit(on, &sh.drained);
-    mbar_wait_bounded(&sh.drained, 0);
+    // nothing of this stream's is in flight when its memory is given back
+    mma_commit(on, &sh.drained[x]);
+    mbar_wait_bounded(&sh.drained[x], 0);
   }
   __syncwarp();
   tc_before_sync();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == 10) {
     tc_after_sync();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
   }
-  if (sh.failed && tid == 0) {  // the requests of this range are refused
-    for (cur = walk_from(sh.start, range); cur.advance(p, kWideTile);)
+  if (sh.failed && tid < W::kStreams) {  // the requests of this range are refused
+    for (Walk cur = walk_from(p, sh.start[tid], ranges[tid], p.item_cost); cur.advance(p, kKeys);)
       p.status[cur.b] = DSPARK_ST_TIMEOUT;
   }
 }
 
 // rows of a tensor copy: the most that divide a block and a tile; the swizzle
 // wants whole groups of eight
-inline int wide_box_rows(int page) {
-  int rows = kWideTile;
+inline int wide_box_rows(int page, int keys) {
+  int rows = keys;
   while (page % rows) rows /= 2;
   return rows;
 }
 
-// the map of one cache: dims, rows of a block, heads, blocks
+// the map of one cache: 64 dims, rows of a block, blocks of 64 dims, heads, blocks
 template <typename T>
 bool map_cache(CUtensorMap* map, const Params& p, const void* cache, int dim, int box_rows) {
   using Encode = decltype(&cuTensorMapEncodeTiled);
@@ -649,54 +695,64 @@ bool map_cache(CUtensorMap* map, const Params& p, const void* cache, int dim, in
     return reinterpret_cast<Encode>(f);
   }();
   if (!encode) return false;
-  const cuuint64_t sizes[4] = {(cuuint64_t)dim, (cuuint64_t)p.page, (cuuint64_t)p.kv_heads,
-                               (cuuint64_t)p.n_blocks};
-  const cuuint64_t strides[3] = {(cuuint64_t)p.token_stride * 2, (cuuint64_t)p.head_stride * 2,
-                                 (cuuint64_t)p.block_stride * 2};
-  const cuuint32_t box[4] = {64, (cuuint32_t)box_rows, 1, 1}, steps[4] = {1, 1, 1, 1};
+  const cuuint64_t sizes[5] = {64, (cuuint64_t)p.page, (cuuint64_t)dim / 64,
+                               (cuuint64_t)p.kv_heads, (cuuint64_t)p.n_blocks};
+  const cuuint64_t strides[4] = {(cuuint64_t)p.token_stride * 2, 128,
+                                 (cuuint64_t)p.head_stride * 2, (cuuint64_t)p.block_stride * 2};
+  const cuuint32_t box[5] = {64, (cuuint32_t)box_rows,
+                             box_rows == 8 ? (cuuint32_t)dim / 64 : 1u, 1, 1};
+  const cuuint32_t steps[5] = {1, 1, 1, 1, 1};
   return encode(map,
                 Half<T>::kExponent == 0x7F80u ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                               : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
-                4, const_cast<void*>(cache), sizes, strides, box, steps,
+                5, const_cast<void*>(cache), sizes, strides, box, steps,
                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// false: the cache's shape has no map, or blocks too short for one
-template <typename T, int D>
+// false: the cache's shape has no map, or blocks not made of groups of eight
+template <typename T, int D, WideMode kMode>
 bool launch_wide(Params p, int sms, cudaStream_t stream, cudaError_t* error) {
-  const int box_rows = wide_box_rows(p.page);
+  using W = Wide<D, kMode>;
+  const int box_rows = wide_box_rows(p.page, W::kKeys);
   CUtensorMap k_map, v_map;
   if (box_rows < 8 || !map_cache<T>(&k_map, p, p.k, D, box_rows) ||
       !map_cache<T>(&v_map, p, p.v, D, box_rows))
     return false;
-  p.row_tiles = (p.nodes * p.group + kWideRows - 1) / kWideRows;
-  auto* kernel = tree_attention_wide_kernel<T, D>;
-  *error = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                Wide<D>::kSmem);
+  p.row_tiles = (p.nodes * p.group + W::kRows - 1) / W::kRows;
+  p.max_ctas = wide_ctas(kMode == kPair);
+  p.item_cost = kMode == kPair ? kPairCost : kWideCost;
+  auto* kernel = tree_attention_wide_kernel<T, D, kMode>;
+  *error = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, W::kSmem);
   if (*error != cudaSuccess) return true;
-  const int grid = min(kMaxCtas, max(sms, p.row_tiles));
-  kernel<<<grid, kWideThreads, Wide<D>::kSmem, stream>>>(p, k_map, v_map, box_rows);
+  const int grid = min(p.max_ctas / W::kStreams, max(sms, p.row_tiles));
+  kernel<<<grid, kWideThreads, W::kSmem, stream>>>(p, k_map, v_map, box_rows);
   *error = cudaGetLastError();
-  if (*error == cudaSuccess) *error = launch_join<T, D, 4>(p, kWideRows, grid, stream);
+  if (*error == cudaSuccess)
+    *error = launch_join<T, D, kMode == kPair ? 1 : 4>(p, W::kRows, grid * W::kStreams, stream);
   return true;
 }
 
+// The tensor kernel wherever the cache's blocks allow; the streaming kernel
+// for the other block sizes, in the smallest of its shapes that holds the
+// rows.
 template <typename T, int D>
 cudaError_t launch_dim(const Params& p, int sms, cudaStream_t stream) {
-  const int rows = shape_rows(p.nodes * p.group, D);
-  if (rows == 8) return launch_shape<T, D, 1, 1>(p, sms, stream);
-  if (rows == 16) return launch_shape<T, D, 2, 1>(p, sms, stream);
+  const int rows = p.nodes * p.group;
+  cudaError_t e;
   if constexpr (D == 256) {
-    if (rows == 32) return launch_shape<T, D, 2, 2>(p, sms, stream);
+    if (launch_wide<T, D, kOne>(p, sms, stream, &e)) return e;
+    if (stream_rows(rows, D) == 16) return launch_shape<T, D, 2, 1>(p, sms, stream);
     return launch_shape<T, D, 2, 4>(p, sms, stream);
   } else {
-    if (rows == 24) return launch_shape<T, D, 3, 1>(p, sms, stream);
-    if (rows == 32) return launch_shape<T, D, 4, 1>(p, sms, stream);
-    if (rows == 48) return launch_shape<T, D, 3, 2>(p, sms, stream);
-    cudaError_t e;
-    if (p.nodes * p.group > 64 && launch_wide<T, D>(p, sms, stream, &e)) return e;
+    if (rows <= 128) {
+      if (launch_wide<T, D, kPair>(p, sms, stream, &e)) return e;
+    } else {
+      if (launch_wide<T, D, kBoth>(p, sms, stream, &e)) return e;
+    }
+    if (stream_rows(rows, D) == 8) return launch_shape<T, D, 1, 1>(p, sms, stream);
+    if (stream_rows(rows, D) == 32) return launch_shape<T, D, 4, 1>(p, sms, stream);
     return launch_shape<T, D, 4, 2>(p, sms, stream);
   }
 }
