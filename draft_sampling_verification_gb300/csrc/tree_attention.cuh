@@ -137,7 +137,7 @@ __device__ __forceinline__ uint32_t without_special(uint32_t w) {
 // queries, its first copies and its results take, without which the teams
 // that get many short items end last.  (A pair of ranges in one CTA counts as
 // two CTAs here.)
-constexpr int kStreamCost = 5, kPairCost = 2, kWideCost = 3;
+constexpr int kStreamCost = 5, kPairCost = 2, kBothCost = 5, kOneCost = 1;
 
 struct Start {  // where a team's range begins: `at` into the item, of item_cost + tiles
   int b, head, at, tiles;
@@ -318,14 +318,15 @@ struct Shape {
   static constexpr int kRows = 8 * N8 * MW;
   static constexpr int kRowBytes = D * 2;
   static constexpr int kStageBytes = 2 * kKeys * kRowBytes;
-  static constexpr int kSmem = D == 256 ? 196608 : 98304;  // one or two CTAs per SM
+  static constexpr int kCtas = D == 256 ? 1 : D == 64 && N8 <= 2 ? 4 : 2;  // per SM
+  static constexpr int kSmem = 196608 / kCtas;
   static constexpr int kStages = kSmem / (kGroups * kStageBytes);
   static constexpr int kPitch = D + 4;                // floats of a joined row: no bank twice
   static_assert(kGroups * kRows * kPitch * 4 <= kSmem, "the joined rows fit the copies' memory");
 };
 
 template <typename T, int D, int N8, int MW>
-__global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2)
+__global__ void __launch_bounds__(kThreads, Shape<D, N8, MW>::kCtas)
     tree_attention_kernel(const __grid_constant__ Params p) {
   using S = Shape<D, N8, MW>;
   using H = Half<T>;
@@ -336,6 +337,8 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2)
   __shared__ Start s_start;
   __shared__ uint32_t s_valid[KW][kStages];
   __shared__ float2 s_stat[KW][kRows];
+  __shared__ float s_factor[KW][kRows];  // of each group's part of a row
+  __shared__ float2 s_joined[kRows];     // the row's reference and sum
   __shared__ uint64_t s_mask[kRows];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int mw = warp % MW, kw = warp / MW;
@@ -608,45 +611,56 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2)
       }
     __syncthreads();
     const bool full = cur.whole();
-    const int64_t slot = cur.slot(blockIdx.x);
-    for (int i = tid; i < kRows * (D / 4); i += kThreads) {
-      const int r = i / (D / 4), d = (i % (D / 4)) * 4;
+    const int64_t slot = cur.slot(blockIdx.x) * kRows;
+    for (int r = tid; r < kRows; r += kThreads) {
       const int row = r0 + r;
-      if (row >= p.nodes * p.group) break;
       float top = -INFINITY;
 #pragma unroll
       for (int g = 0; g < KW; ++g) top = fmaxf(top, s_stat[g][r].x);
       const float safe = top == -INFINITY ? 0.0f : top;
-      float all = 0.0f;
-      float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      float all = 0.0f, f[KW];
 #pragma unroll
       for (int g = 0; g < KW; ++g) {
-        const float2 st = s_stat[g][r];
-        const float f = exp2_approx(st.x - safe);
-        const float4 v = *reinterpret_cast<const float4*>(joined + (g * kRows + r) * S::kPitch + d);
-        all += st.y * f;
-        a.x += v.x * f;
-        a.y += v.y * f;
-        a.z += v.z * f;
-        a.w += v.w * f;
+        f[g] = exp2_approx(s_stat[g][r].x - safe);
+        all += s_stat[g][r].y * f[g];
       }
-      if (row >= live) {  // a row of no node: its zero query saw the text all the same
-        top = -INFINITY;
-        all = a.x = a.y = a.z = a.w = 0.0f;
+      // a row of no node: its zero query saw the text all the same
+      const float by = row >= live || all == 0.0f ? 0.0f : full ? 1.0f / all : 1.0f;
+#pragma unroll
+      for (int g = 0; g < KW; ++g) s_factor[g][r] = f[g] * by;
+      s_joined[r] = row >= live ? make_float2(-INFINITY, 0.0f) : make_float2(top, all);
+    }
+    __syncthreads();
+    const int rows_here = min(kRows, p.nodes * p.group - r0);
+    for (int i = tid; i < rows_here * (D / 4); i += kThreads) {
+      const int r = i / (D / 4), d = (i % (D / 4)) * 4;
+      float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (r0 + r < live) {
+#pragma unroll
+        for (int g = 0; g < KW; ++g) {
+          const float f = s_factor[g][r];
+          const float4 v = *reinterpret_cast<const float4*>(joined + (g * kRows + r) * S::kPitch + d);
+          a.x += v.x * f;
+          a.y += v.y * f;
+          a.z += v.z * f;
+          a.w += v.w * f;
+        }
       }
       if (full) {
-        const int node = row / p.group, h = kvh * p.group + row - node * p.group;
-        const int64_t to = ((int64_t)cur.b * p.nodes + node) * p.heads + h;
-        const float inv = all == 0.0f ? 0.0f : 1.0f / all;
+        const int row = r0 + r, node = row / p.group;
+        const int64_t to = ((int64_t)cur.b * p.nodes + node) * p.heads + kvh * p.group + row -
+                           node * p.group;
         uint2 w;
-        w.x = H::pack(a.x * inv, a.y * inv);
-        w.y = H::pack(a.z * inv, a.w * inv);
+        w.x = H::pack(a.x, a.y);
+        w.y = H::pack(a.z, a.w);
         *reinterpret_cast<uint2*>(static_cast<T*>(p.out) + to * D + d) = w;
-        if (d == 0 && p.lse)
-          p.lse[to] = all == 0.0f ? -INFINITY : (top + log2f(all)) * 0.6931471805599453f;
+        if (d == 0 && p.lse) {
+          const float2 j = s_joined[r];
+          p.lse[to] = j.y == 0.0f ? -INFINITY : (j.x + log2f(j.y)) * 0.6931471805599453f;
+        }
       } else {
-        *reinterpret_cast<float4*>(ws.rows + (slot * kRows + r) * D + d) = a;
-        if (d == 0) ws.stats[slot * kRows + r] = make_float2(top, all);
+        *reinterpret_cast<float4*>(ws.rows + (slot + r) * D + d) = a;
+        if (d == 0) ws.stats[slot + r] = s_joined[r];
       }
     }
     __syncthreads();
@@ -775,11 +789,13 @@ cudaError_t launch_join(const Params& p, int rows, int grid, cudaStream_t stream
 
 // rows of a streaming CTA for `rows` rows of an item
 inline int stream_rows(int rows, int dim) {
-  if (dim == 256) return rows <= 16 ? 16 : 64;
-  return rows <= 8 ? 8 : rows <= 32 ? 32 : 64;
+  if (dim == 256) return rows <= 8 ? 8 : rows <= 16 ? 16 : 64;
+  return rows <= 24 ? (rows + 7) / 8 * 8 : rows <= 32 ? 32 : 64;
 }
+// rows up to which the streaming kernel is taken, at head_dim 64 and 128, and 256
+constexpr int kFewRows = 16, kFewRows256 = 8;
 // the workspace's ranges, by kernel
-constexpr int kStreamCtas = 320;
+constexpr int kStreamCtas = 640;
 inline int wide_ctas(bool pair) { return pair ? 320 : 160; }
 
 template <typename T, int D, int N8, int MW>
@@ -792,7 +808,7 @@ cudaError_t launch_shape(Params p, int sms, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   p.max_ctas = kStreamCtas;
   p.item_cost = kStreamCost;
-  const int grid = min(kStreamCtas, max(sms * (D == 256 ? 1 : 2), p.row_tiles));
+  const int grid = min(kStreamCtas, max(sms * S::kCtas, p.row_tiles));
   kernel<<<grid, kThreads, S::kSmem, stream>>>(p);
   e = cudaGetLastError();
   return e != cudaSuccess ? e : launch_join<T, D, 1>(p, S::kRows, grid, stream);

@@ -199,6 +199,10 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   const uint32_t group_bytes = box_rows == 8 ? kHalves * 1024u : 1024u;
   const uint32_t half_bytes = box_rows == 8 ? 1024u : kKeys * 128u;
 
+  if (tid == 0) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&k_map) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&v_map) : "memory");
+  }
   const Workspace ws = carve(p.workspace, W::kRows, p.max_ctas);
   int64_t ranges[W::kStreams];
   find_range<kWideThreads, W::kStreams>(p, kKeys, ws, sh.scan, sh.start, ranges);
@@ -722,7 +726,7 @@ bool launch_wide(Params p, int sms, cudaStream_t stream, cudaError_t* error) {
     return false;
   p.row_tiles = (p.nodes * p.group + W::kRows - 1) / W::kRows;
   p.max_ctas = wide_ctas(kMode == kPair);
-  p.item_cost = kMode == kPair ? kPairCost : kWideCost;
+  p.item_cost = kMode == kPair ? kPairCost : kMode == kBoth ? kBothCost : kOneCost;
   auto* kernel = tree_attention_wide_kernel<T, D, kMode>;
   *error = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, W::kSmem);
   if (*error != cudaSuccess) return true;
@@ -734,25 +738,28 @@ bool launch_wide(Params p, int sms, cudaStream_t stream, cudaError_t* error) {
   return true;
 }
 
-// The tensor kernel wherever the cache's blocks allow; the streaming kernel
-// for the other block sizes, in the smallest of its shapes that holds the
-// rows.
+// The streaming kernel for few rows, whose products need no tensor memory and
+// whose two CTAs per SM hide one another's starts, and for blocks that have no
+// tensor copies; else the tensor kernel.
 template <typename T, int D>
 cudaError_t launch_dim(const Params& p, int sms, cudaStream_t stream) {
-  const int rows = p.nodes * p.group;
+  const int rows = p.nodes * p.group, shape = stream_rows(rows, D);
   cudaError_t e;
   if constexpr (D == 256) {
-    if (launch_wide<T, D, kOne>(p, sms, stream, &e)) return e;
-    if (stream_rows(rows, D) == 16) return launch_shape<T, D, 2, 1>(p, sms, stream);
+    if (rows > kFewRows256 && launch_wide<T, D, kOne>(p, sms, stream, &e)) return e;
+    if (shape == 8) return launch_shape<T, D, 1, 1>(p, sms, stream);
+    if (shape == 16) return launch_shape<T, D, 2, 1>(p, sms, stream);
     return launch_shape<T, D, 2, 4>(p, sms, stream);
   } else {
-    if (rows <= 128) {
-      if (launch_wide<T, D, kPair>(p, sms, stream, &e)) return e;
-    } else {
+    if (rows > 128) {
       if (launch_wide<T, D, kBoth>(p, sms, stream, &e)) return e;
+    } else if (rows > kFewRows) {
+      if (launch_wide<T, D, kPair>(p, sms, stream, &e)) return e;
     }
-    if (stream_rows(rows, D) == 8) return launch_shape<T, D, 1, 1>(p, sms, stream);
-    if (stream_rows(rows, D) == 32) return launch_shape<T, D, 4, 1>(p, sms, stream);
+    if (shape == 8) return launch_shape<T, D, 1, 1>(p, sms, stream);
+    if (shape == 16) return launch_shape<T, D, 2, 1>(p, sms, stream);
+    if (shape == 24) return launch_shape<T, D, 3, 1>(p, sms, stream);
+    if (shape == 32) return launch_shape<T, D, 4, 1>(p, sms, stream);
     return launch_shape<T, D, 4, 2>(p, sms, stream);
   }
 }

@@ -123,6 +123,16 @@ def test_pages_end_inside_a_tile(page, layout):
     c.check(c.run())
 
 
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("T,heads", [(2, 4), (13, 8), (20, 16), (64, 16)])
+@pytest.mark.parametrize("page", [8, 24, 32, 12])
+def test_pages_dims_and_row_counts(page, T, heads, dim):
+    """Rows of an item from 4 to 512, on every kernel, with boxes of eight rows, of more, and none."""
+    c = Case([37, 0, 260, 129], [T, max(1, T - 3), T, 1], T, heads=heads, kv_heads=2, dim=dim,
+             page=page, mask="tree", seed=page + T, dtype=torch.float16)
+    c.check(c.run())
+
+
 @pytest.mark.parametrize("ctx", [[0], [1], [0, 0, 0], [8191], [5000, 1, 300, 20000], [40000, 2]])
 @pytest.mark.parametrize("T", [1, 5])
 def test_lengths(ctx, T):
@@ -301,6 +311,15 @@ def test_bad_lengths_are_refused():
     assert (out[1:] == 0).all() and torch.isneginf(lse[1:]).all()
     one = Case([64, 64, 64, 64], [6, 6, 6, 6], 6)
     assert torch.equal(one.run()[0][0], out[0])
+
+
+@pytest.mark.parametrize("dim,T,heads", [(64, 8, 8), (128, 8, 8), (256, 8, 8), (128, 2, 8),
+                                         (128, 40, 16)])
+@pytest.mark.parametrize("scale", [0.0, -0.2])
+def test_zero_and_negative_scales(dim, T, heads, scale):
+    c = Case([100, 3, 300], [T, T, 1], T, heads=heads, dim=dim, mask="tree", seed=2)
+    c.scale = scale
+    c.check(c.run(scale=scale))
 
 
 def test_lse_is_optional():
