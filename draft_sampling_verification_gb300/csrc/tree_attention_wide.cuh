@@ -135,10 +135,16 @@ __device__ __forceinline__ void tmem_wait_store() {
 // kOne: head_dim 256, whose accumulators fill half the tensor memory: one
 //   warpgroup, one row tile, 64 positions at a time.
 //
-// The products run in the order they are issued, so the barrier of a tile's
-// scores also says that its accumulators hold every earlier step: the
-// softmax warpgroup may then rescale them.  It does so only when a score
-// passes the row's reference by more than 8, as in the streaming kernel.
+// kPair and kOne take 64 positions at a time and keep the scores of two tiles
+// in tensor memory, so that the next tile's products run during a softmax
+// (1,024 one-row-tile items of 300 tokens: 86 us, with tiles of 128 and their
+// scores alone 105).  At head_dim 64 a tile of 64 is too little work for its
+// softmax's latency, and under kBoth the other row tile's products run: a tile
+// has 128 positions.
+//
+// A score that passes the row's reference by more than 8 has the accumulators
+// rescaled by the softmax warpgroup, once the products before are done; this
+// is rare after an item's first tile, as in the streaming kernel.
 //
 // Warps 0-3 and 4-7: softmax, queries and results.  Warps 8 and 9: tensor
 // copies of keys and values, box by box of a block's rows, into a ring of
@@ -155,14 +161,24 @@ struct Wide {
   static constexpr int kStreams = kMode == kPair ? 2 : 1;   // ranges of the tile axis
   static constexpr int kRowTiles = kMode == kOne ? 1 : 2;   // of 128 rows, over all streams
   static constexpr int kRows = kMode == kBoth ? 256 : 128;  // of an item, per CTA
-  static constexpr int kKeys = D == 256 ? 64 : 128;
+  // positions of a tile, and the tiles whose scores are held
+  static constexpr int kKeys = kMode == kBoth || D == 64 ? 128 : 64;
+  static constexpr int kScores = kKeys == 128 ? 1 : 2;
   static constexpr int kHalves = D / 64;
   static constexpr int kQBytes = 128 * D * 2, kTileBytes = kKeys * D * 2;
-  static constexpr int kStages = D == 64 ? (kMode == kPair ? 2 : 4) : (kMode == kPair ? 1 : 2);
+  static constexpr int kStages = kMode == kBoth && D == 64 ? 4 : 2;
   static constexpr int kRing = 2 * kStages * kTileBytes;    // keys, then values
   static constexpr int kSmem = kRowTiles * kQBytes + kStreams * kRing + 1024;
 };
 constexpr int kWideMaxStages = 4;
+
+// How a tile comes in boxes of rows of one block.  Keys: boxes of k_rows rows
+// of 64 dims, the tile's rows of each 64 dims together; or (k_whole) boxes of
+// eight rows of all dims, where those are fewer.  Values: boxes of v_rows rows
+// of all dims.
+struct Boxes {
+  int k_rows, k_whole, v_rows;
+};
 
 struct WideStream {
   uint64_t k_full[kWideMaxStages], k_empty[kWideMaxStages];
@@ -172,7 +188,7 @@ struct WideStream {
 };
 struct WideShared {
   WideStream stream[2];
-  uint64_t q_full[2], s_full[2], p_full[2], o_full[2], drained[2];
+  uint64_t q_full[2], s_full[2][2], p_full[2][2], o_full[2][2], drained[2];
   uint64_t scan[32];
   int64_t q_row[256];  // where each row of the CTA begins in Q, from its request and cached head on
   Start start[2];
@@ -184,7 +200,8 @@ template <typename T, int D, WideMode kMode>
 __global__ void __launch_bounds__(kWideThreads, 1)
     tree_attention_wide_kernel(const __grid_constant__ Params p,
                                const __grid_constant__ CUtensorMap k_map,
-                               const __grid_constant__ CUtensorMap v_map, int box_rows) {
+                               const __grid_constant__ CUtensorMap v_map,
+                               const Boxes boxes) {
   using H = Half<T>;
   using W = Wide<D, kMode>;
   constexpr int kChunks = D / 8, kStages = W::kStages, kKeys = W::kKeys, kHalves = W::kHalves;
@@ -194,10 +211,10 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t ring = base + W::kRowTiles * W::kQBytes;
-  // a tile of keys or values: bytes between its groups of eight rows, and between its blocks of
-  // 64 dims.  A box of eight rows brings all blocks, one after the other.
-  const uint32_t group_bytes = box_rows == 8 ? kHalves * 1024u : 1024u;
-  const uint32_t half_bytes = box_rows == 8 ? 1024u : kKeys * 128u;
+  // bytes between the groups of eight rows of a tile, and between its blocks of 64 dims
+  const uint32_t k_group = boxes.k_whole ? kHalves * 1024u : 1024u;
+  const uint32_t k_half = boxes.k_whole ? 1024u : kKeys * 128u;
+  const uint32_t v_half = boxes.v_rows * 128u, v_box = kHalves * v_half;
 
   if (tid == 0) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(&k_map) : "memory");
@@ -226,9 +243,12 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.q_full[i], 128);
-      mbar_init(&sh.s_full[i], 1);
-      mbar_init(&sh.p_full[i], 128);
-      mbar_init(&sh.o_full[i], 1);
+      for (int j = 0; j < W::kScores; ++j) {
+        mbar_init(&sh.s_full[i][j], 1);
+        mbar_init(&sh.p_full[i][j], 128);
+      }
+      mbar_init(&sh.o_full[i][0], 1);
+      mbar_init(&sh.o_full[i][1], 1);
       mbar_init(&sh.drained[i], 1);
     }
     sh.failed = 0u;
@@ -243,9 +263,12 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   tc_before_sync();
   __syncthreads();
   tc_after_sync();
-  // columns: the scores of row tile m (the weights over their first half), then its accumulators
+  // columns: the scores of row tile m and tile g (the weights over their first half), then the
+  // accumulators
   const uint32_t tmem = sh.tmem;
-  auto s_col = [&](int m) -> uint32_t { return tmem + 128u * m; };
+  auto s_col = [&](int m, uint32_t g) -> uint32_t {
+    return tmem + 128u * m + (g % W::kScores) * 64u;
+  };
   auto o_col = [&](int m) -> uint32_t { return tmem + 256u + 128u * m; };
 
   // a bounded wait; once one expires, every later one of the CTA gives up at once
@@ -260,6 +283,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     return __all_sync(0xffffffffu, wait(bar, phase));
   };
   auto phase_of = [](uint32_t g) -> uint32_t { return (g / kStages) & 1u; };
+  auto score_phase = [](uint32_t g) -> uint32_t { return (g / W::kScores) & 1u; };
 
   if (warp < 8) {
     // -------------------------------------------------- softmax and results
@@ -268,14 +292,14 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     const int m_rows = r0 + (kPaired ? 0 : m * 128);  // the tile's first row of the item
     WideStream& stream = sh.stream[x];
     const int t = tid & 127;  // this thread's row of the tile and lane of tensor memory
-    const uint32_t sc = s_col(m) + ((uint32_t)(t & ~31) << 16);
-    const uint32_t oc = o_col(m) + ((uint32_t)(t & ~31) << 16);
+    const uint32_t lanes = (uint32_t)(t & ~31) << 16;
+    const uint32_t oc = o_col(m) + lanes;
     const uint32_t q_at = base + m * W::kQBytes;
     // a negative scale goes into Q's sign, so that the largest score stays the largest; 0 would
     // make NaN of a hidden score
     const uint32_t flip = p.scale2 < 0.0f ? 0x80008000u : 0u;
     const float scale = fmaxf(fabsf(p.scale2), 1.17549435e-38f);
-    uint32_t tile_no = 0, segments = 0;
+    uint32_t tile_no = 0;
     bool ok = m < (kPaired ? 2 : n_tiles) && m < W::kRowTiles;
     Walk cur = walk_from(p, sh.start[x], ok ? ranges[x] : 0, p.item_cost);
     // the item's Q: 16-byte pieces of this thread's column, every kStep-th row, in parts of kPart
@@ -316,6 +340,13 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       fence_async_shared();
       mbar_arrive(&sh.q_full[m]);
     };
+    // tile g's second product is done.  Called for the tile before the one in
+    // hand or for an item's last, whose scores say that every product up to
+    // two tiles before is: two barriers in turn, so that no phase is mistaken
+    // for one two further.
+    auto wait_values = [&](uint32_t g) -> bool {
+      return wait_all(&sh.o_full[m][g & 1u], (g >> 1) & 1u);
+    };
     bool more = ok && cur.advance(p, kKeys);
     if (more) fill_q(cur);
     const int row = m_rows + t, node = row / p.group;
@@ -337,12 +368,11 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         mask = p.mask ? p.mask[(int64_t)cur.b * p.nodes + node] : ~0ull >> (63 - node);
       float ref = -INFINITY;
       float2 sum2 = make_float2(0.0f, 0.0f);
-      bool special = false;
       for (int i = 0; i < tiles; ++i, ++tile_no) {
-        ok = wait_all(&sh.s_full[m], tile_no & 1u);
+        ok = wait_all(&sh.s_full[m][tile_no % W::kScores], score_phase(tile_no));
         if (!ok) break;
         tc_after_sync();
-        if (i > 0) special |= stream.special[(tile_no - 1u) & 7u] != 0u;
+        const uint32_t sc = s_col(m, tile_no) + lanes;
         const int pos = (cur.first + i) * kKeys;
         const bool nodes_here = pos + kKeys > len.ctx;
         if (!idle) {
@@ -385,6 +415,9 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             sum2.x *= f;
             sum2.y *= f;
             if (i > 0) {
+              ok = wait_values(tile_no - 1u);
+              if (!ok) break;
+              tc_after_sync();
 #pragma unroll 1
               for (int c = 0; c < D / 16; ++c) {
                 uint32_t a[16];
@@ -429,11 +462,12 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           const uint32_t v_at = ring + x * W::kRing + (kStages + stage) * W::kTileBytes;
           const int from = max(0, len.ctx - pos);
           // blocks' rows that the last copy brought; zeros behind them
-          const int end = min(kKeys, (len.len - pos + box_rows - 1) / box_rows * box_rows);
+          const int end =
+              min(kKeys, (len.len - pos + boxes.v_rows - 1) / boxes.v_rows * boxes.v_rows);
           for (int j = t; j < (end - from) * kChunks; j += 128) {
             const int r = from + j / kChunks, c = j % kChunks;
-            const uint32_t addr = v_at + (r >> 3) * group_bytes + (c >> 3) * half_bytes +
-                                  (r & 7) * 128 + (((c & 7) ^ (r & 7)) << 4);
+            const uint32_t addr = v_at + r / boxes.v_rows * v_box + (c >> 3) * v_half +
+                                  r % boxes.v_rows * 128 + (((c & 7) ^ (r & 7)) << 4);
             uint32_t w[4];
             asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                          : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
@@ -452,16 +486,18 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           fence_async_shared();
         }
         tc_before_sync();
-        mbar_arrive(&sh.p_full[m]);
+        mbar_arrive(&sh.p_full[m][tile_no % W::kScores]);
       }
       // Q is free, as the last scores are done: the next item's first scores
       // are computed while this one's results are written
       if (ok && more) fill_q(ahead);
-      if (ok) ok = wait_all(&sh.o_full[m], segments & 1u);
-      ++segments;
+      if (ok) ok = wait_values(tile_no - 1u);
       if (!ok) break;
       tc_after_sync();
-      special |= stream.special[(tile_no - 1u) & 7u] != 0u;
+      // nodes lie in the item's last tiles: at most 64 of them, and their last tile's rest
+      bool special = false;
+      for (uint32_t k = 1; k <= min(3, tiles); ++k)
+        special |= stream.special[(tile_no - k) & 7u] != 0u;
 
       float sum = sum2.x + sum2.y;
       if (row >= live) {  // a row of no node: its zero query saw the text all the same
@@ -532,11 +568,13 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     }
   } else if (warp < 8 + W::kStreams) {
     // ------------------------------------------------------ keys and values
-    // Lane i copies the tile's box i, box_rows positions of one block.
+    // Lane i copies the tile's box i of keys and of values, a part of one block.
     const int x = warp - 8;
     WideStream& stream = sh.stream[x];
     const uint32_t k_at = ring + x * W::kRing, v_at = k_at + kStages * W::kTileBytes;
-    const int boxes = kKeys / box_rows;  // at most 16
+    const int k_rows = boxes.k_rows, v_rows = boxes.v_rows;  // v_rows a multiple of k_rows
+    const int k_boxes = kKeys / k_rows, v_boxes = kKeys / v_rows;  // at most 16
+    const int v_lane = lane * v_rows / k_rows & 31;  // the keys' box where this lane's values begin
     uint32_t g = 0;
     bool ok = true;
     Walk cur = walk_from(p, sh.start[x], ranges[x], p.item_cost);
@@ -546,12 +584,12 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       const int first = cur.first * kKeys;
       const int32_t* table = p.table + cur.b * p.table_ld;
       auto entry_of = [&](int i) -> int {
-        const int pos = first + i * kKeys + lane * box_rows;
-        return i < tiles && lane < boxes && pos < len.len ? __ldg(table + pos / p.page) : -1;
+        const int pos = first + i * kKeys + lane * k_rows;
+        return i < tiles && lane < k_boxes && pos < len.len ? __ldg(table + pos / p.page) : -1;
       };
       int ahead = entry_of(0);
       for (int i = 0; i < tiles; ++i, ++g) {
-        const int pos0 = first + i * kKeys, pos = pos0 + lane * box_rows, block = ahead;
+        const int pos0 = first + i * kKeys, pos = pos0 + lane * k_rows, block = ahead;
         ahead = entry_of(i + 1);
         const bool held = block >= 0 && block < p.n_blocks;
         const int from = held ? block : p.n_blocks, row = held ? pos % p.page : 0;
@@ -561,37 +599,44 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         if (!ok) break;
         if (lane < kKeys / 32) {
           uint32_t word = 0u;  // positions 32 lane .. of the tile
-          if (box_rows >= 32) {
-            word = (held_boxes >> (lane * 32 / box_rows)) & 1u ? ~0u : 0u;
+          if (k_rows >= 32) {
+            word = (held_boxes >> (lane * 32 / k_rows)) & 1u ? ~0u : 0u;
           } else {
-            for (int j = 0; j < 32 / box_rows; ++j)
-              if ((held_boxes >> (lane * 32 / box_rows + j)) & 1u)
-                word |= ((1u << box_rows) - 1u) << (j * box_rows);
+            for (int j = 0; j < 32 / k_rows; ++j)
+              if ((held_boxes >> (lane * 32 / k_rows + j)) & 1u)
+                word |= ((1u << k_rows) - 1u) << (j * k_rows);
           }
           const int past = len.len - (pos0 + lane * 32);  // positions before the end
           stream.valid[g & 7u][lane] =
               past >= 32 ? word : past > 0 ? word & ((1u << past) - 1u) : 0u;
         }
-        if (lane == 0) stream.special[g & 7u] = 0u;
-        auto copy = [&](const CUtensorMap* map, uint32_t at, uint64_t* full) {
-          if (lane == 0) mbar_arrive_expect_tx(full, W::kTileBytes);
-          __syncwarp();
-          if (lane >= boxes) return;
-          at += stage * W::kTileBytes;
-          if (box_rows == 8) {
-            tma_load_box(at + lane * group_bytes, map, row, 0, cur.head, from, full);
+        if (lane == 0) {
+          stream.special[g & 7u] = 0u;
+          mbar_arrive_expect_tx(&stream.k_full[stage], W::kTileBytes);
+        }
+        __syncwarp();
+        if (lane < k_boxes) {
+          const uint32_t at = k_at + stage * W::kTileBytes;
+          if (boxes.k_whole) {
+            tma_load_box(at + lane * k_group, &k_map, row, 0, cur.head, from,
+                         &stream.k_full[stage]);
           } else {
 #pragma unroll
             for (int h = 0; h < kHalves; ++h)
-              tma_load_box(at + h * half_bytes + lane * box_rows * 128, map, row, h, cur.head,
-                           from, full);
+              tma_load_box(at + h * k_half + lane * k_rows * 128, &k_map, row, h, cur.head, from,
+                           &stream.k_full[stage]);
           }
-        };
-        copy(&k_map, k_at, &stream.k_full[stage]);
+        }
         __syncwarp();
+        const int v_from = __shfl_sync(0xffffffffu, from, v_lane);
+        const int v_row = __shfl_sync(0xffffffffu, row, v_lane);
         ok = wait_all(&stream.v_empty[stage], phase_of(g) ^ 1u);
         if (!ok) break;
-        copy(&v_map, v_at, &stream.v_full[stage]);
+        if (lane == 0) mbar_arrive_expect_tx(&stream.v_full[stage], W::kTileBytes);
+        __syncwarp();
+        if (lane < v_boxes)
+          tma_load_box(v_at + stage * W::kTileBytes + lane * v_box, &v_map, v_row, 0, cur.head,
+                       v_from, &stream.v_full[stage]);
         __syncwarp();
       }
     }
@@ -609,23 +654,31 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     // descriptors of this stream's first row tile of Q, and of the stages of keys and values; an
     // operand further on adds its distance / 16
     const uint64_t q_desc = operand_desc(base + x * W::kQBytes, 16, 1024);
-    const uint64_t k_desc = operand_desc(ring + x * W::kRing, 16, group_bytes);
-    const uint64_t v_desc = operand_desc(ring + x * W::kRing + kStages * W::kTileBytes, half_bytes,
-                                         group_bytes);
+    const uint64_t k_desc = operand_desc(ring + x * W::kRing, 16, k_group);
+    const uint64_t v_desc = operand_desc(ring + x * W::kRing + kStages * W::kTileBytes, v_half,
+                                         boxes.v_rows == 8 ? v_box : 1024u);
+    // a tile's values, 16 positions after 16: within a box, or in the next ones
+    uint64_t v_at[kKeys / 16];
+#pragma unroll
+    for (int kt = 0; kt < kKeys / 16; ++kt) {
+      const int r = kt * 16;
+      v_at[kt] = v_desc + (r / boxes.v_rows * v_box + r % boxes.v_rows * 128) / 16;
+    }
+    const uint32_t k_half16 = k_half / 16;
     auto scores = [&](int m, uint32_t g) {  // m: the row tile, of this stream
       const uint64_t a = q_desc + (uint32_t)m * (W::kQBytes / 16);
       const uint64_t b = k_desc + (g % kStages) * (W::kTileBytes / 16);
 #pragma unroll
       for (int kt = 0; kt < D / 16; ++kt)
-        mma_ss(on, s_col(x + m), a + (kt >> 2) * (16384 / 16) + (kt & 3) * 2,
-               b + (kt >> 2) * (half_bytes / 16) + (kt & 3) * 2, kScores, kt > 0);
-      mma_commit(on, &sh.s_full[x + m]);
+        mma_ss(on, s_col(x + m, g), a + (kt >> 2) * (16384 / 16) + (kt & 3) * 2,
+               b + (kt >> 2) * k_half16 + (kt & 3) * 2, kScores, kt > 0);
+      mma_commit(on, &sh.s_full[x + m][g % W::kScores]);
     };
     auto values = [&](int m, uint32_t g, bool add) {
-      const uint64_t b = v_desc + (g % kStages) * (W::kTileBytes / 16);
+      const uint64_t stage = (g % kStages) * (W::kTileBytes / 16);
 #pragma unroll
       for (int kt = 0; kt < kKeys / 16; ++kt)
-        mma_ts(on, o_col(x + m), s_col(x + m) + kt * 8, b + kt * (2 * group_bytes / 16), kValues,
+        mma_ts(on, o_col(x + m), s_col(x + m, g) + kt * 8, v_at[kt] + stage, kValues,
                add || kt > 0);
     };
     uint32_t g = 0, segments = 0;
@@ -639,24 +692,29 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       tc_after_sync();
       for (int m = 0; m < n_tiles; ++m) scores(m, g);
       mma_commit(on, &stream.k_empty[g % kStages]);
+      if (W::kScores == 2 && tiles > 1) {
+        ok = wait_all(&stream.k_full[(g + 1u) % kStages], phase_of(g + 1u));
+        if (!ok) break;
+        scores(0, g + 1u);
+        mma_commit(on, &stream.k_empty[(g + 1u) % kStages]);
+      }
       for (int i = 0; i < tiles && ok; ++i, ++g) {
-        const bool more = i + 1 < tiles;
+        const uint32_t ahead = g + W::kScores;  // takes the place of tile g's scores
+        const bool more = i + W::kScores < tiles;
         for (int m = 0; m < n_tiles; ++m) {
-          ok = wait_all(&sh.p_full[x + m], g & 1u);
+          ok = wait_all(&sh.p_full[x + m][g % W::kScores], score_phase(g));
           if (m == 0) ok = ok && wait_all(&stream.v_full[g % kStages], phase_of(g));
           if (!ok) break;
           tc_after_sync();
           values(m, g, i > 0);
+          mma_commit(on, &sh.o_full[x + m][g & 1u]);
           if (m == n_tiles - 1) mma_commit(on, &stream.v_empty[g % kStages]);
-          if (more) {
-            if (m == 0) ok = wait_all(&stream.k_full[(g + 1u) % kStages], phase_of(g + 1u));
-            if (!ok) break;
-            scores(m, g + 1u);
-          } else {
-            mma_commit(on, &sh.o_full[x + m]);
-          }
+          if (!more) continue;
+          if (m == 0) ok = wait_all(&stream.k_full[ahead % kStages], phase_of(ahead));
+          if (!ok) break;
+          scores(m, ahead);
         }
-        if (ok && more) mma_commit(on, &stream.k_empty[(g + 1u) % kStages]);
+        if (ok && more) mma_commit(on, &stream.k_empty[ahead % kStages]);
       }
       ++segments;
     }
@@ -687,7 +745,8 @@ inline int wide_box_rows(int page, int keys) {
 
 // the map of one cache: 64 dims, rows of a block, blocks of 64 dims, heads, blocks
 template <typename T>
-bool map_cache(CUtensorMap* map, const Params& p, const void* cache, int dim, int box_rows) {
+bool map_cache(CUtensorMap* map, const Params& p, const void* cache, int dim, int box_rows,
+               bool whole) {
   using Encode = decltype(&cuTensorMapEncodeTiled);
   static const Encode encode = [] {
     void* f = nullptr;
@@ -703,8 +762,7 @@ bool map_cache(CUtensorMap* map, const Params& p, const void* cache, int dim, in
                                (cuuint64_t)p.kv_heads, (cuuint64_t)p.n_blocks};
   const cuuint64_t strides[4] = {(cuuint64_t)p.token_stride * 2, 128,
                                  (cuuint64_t)p.head_stride * 2, (cuuint64_t)p.block_stride * 2};
-  const cuuint32_t box[5] = {64, (cuuint32_t)box_rows,
-                             box_rows == 8 ? (cuuint32_t)dim / 64 : 1u, 1, 1};
+  const cuuint32_t box[5] = {64, (cuuint32_t)box_rows, whole ? (cuuint32_t)dim / 64 : 1u, 1, 1};
   const cuuint32_t steps[5] = {1, 1, 1, 1, 1};
   return encode(map,
                 Half<T>::kExponent == 0x7F80u ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
@@ -719,10 +777,15 @@ bool map_cache(CUtensorMap* map, const Params& p, const void* cache, int dim, in
 template <typename T, int D, WideMode kMode>
 bool launch_wide(Params p, int sms, cudaStream_t stream, cudaError_t* error) {
   using W = Wide<D, kMode>;
-  const int box_rows = wide_box_rows(p.page, W::kKeys);
+  const int rows = wide_box_rows(p.page, W::kKeys);
+  if (rows < 8) return false;
+  Boxes boxes;
+  boxes.k_whole = W::kKeys / rows * W::kHalves > W::kKeys / 8;
+  boxes.k_rows = boxes.k_whole ? 8 : rows;
+  boxes.v_rows = rows;
   CUtensorMap k_map, v_map;
-  if (box_rows < 8 || !map_cache<T>(&k_map, p, p.k, D, box_rows) ||
-      !map_cache<T>(&v_map, p, p.v, D, box_rows))
+  if (!map_cache<T>(&k_map, p, p.k, D, boxes.k_rows, boxes.k_whole) ||
+      !map_cache<T>(&v_map, p, p.v, D, boxes.v_rows, true))
     return false;
   p.row_tiles = (p.nodes * p.group + W::kRows - 1) / W::kRows;
   p.max_ctas = wide_ctas(kMode == kPair);
@@ -731,7 +794,7 @@ bool launch_wide(Params p, int sms, cudaStream_t stream, cudaError_t* error) {
   *error = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, W::kSmem);
   if (*error != cudaSuccess) return true;
   const int grid = min(p.max_ctas / W::kStreams, max(sms, p.row_tiles));
-  kernel<<<grid, kWideThreads, W::kSmem, stream>>>(p, k_map, v_map, box_rows);
+  kernel<<<grid, kWideThreads, W::kSmem, stream>>>(p, k_map, v_map, boxes);
   *error = cudaGetLastError();
   if (*error == cudaSuccess)
     *error = launch_join<T, D, kMode == kPair ? 1 : 4>(p, W::kRows, grid * W::kStreams, stream);
