@@ -53,7 +53,7 @@ cudaError_t launch_tree_attention(const void* q, int dtype, int64_t q_req, int64
   p.status = status;
   p.workspace = static_cast<char*>(workspace);
   p.row_tiles = 1;
-  p.max_ctas = p.item_cost = 0;
+  p.max_ctas = p.tile = p.item_cost = 0;
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);

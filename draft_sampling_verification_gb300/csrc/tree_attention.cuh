@@ -30,6 +30,7 @@ struct Params {
   int32_t* status;
   char* workspace;
   int max_ctas;   // ranges that the workspace has room for
+  int tile;       // positions of a tile
   int item_cost;  // an item's start and end, in tiles
   int row_tiles;  // tiles of an item's rows: ceil(nodes * group / rows per CTA)
 };
@@ -143,24 +144,29 @@ struct Start {  // where a team's range begins: `at` into the item, of item_cost
   int b, head, at, tiles;
 };
 
+// The item that is cut first at a team's start, after the team before began
+// it: what the joining kernel has to join there, up to team `last` (-1: the
+// start lies between items, or the item was cut before).
+struct Seam {
+  int b, head, last, none;
+};
+
 struct Workspace {
-  int64_t* total;
-  Start* start;   // [ctas]
+  Seam* seam;     // [ctas], by team
   float2* stats;  // [2 * ctas][rows]: the reference of the exponents, the sum
   float* rows;    // [2 * ctas][rows][dim]
 };
 
 __host__ __device__ inline int64_t workspace_bytes(int rows, int dim, int ctas) {
-  return 64 + (int64_t)ctas * sizeof(Start) +
+  return 32 + (int64_t)ctas * sizeof(Seam) +
          2ll * ctas * rows * (sizeof(float2) + (int64_t)dim * sizeof(float));
 }
 
 __device__ __forceinline__ Workspace carve(char* w, int rows, int ctas) {
   Workspace s;  // every part 32-byte aligned
   w = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(w) + 31) & ~(uintptr_t)31);
-  s.total = reinterpret_cast<int64_t*>(w);
-  s.start = reinterpret_cast<Start*>(w + 32);
-  s.stats = reinterpret_cast<float2*>(w + 32 + ctas * sizeof(Start));
+  s.seam = reinterpret_cast<Seam*>(w);
+  s.stats = reinterpret_cast<float2*>(w + ctas * sizeof(Seam));
   s.rows = reinterpret_cast<float*>(s.stats + 2 * ctas * rows);
   return s;
 }
@@ -187,12 +193,62 @@ __device__ __forceinline__ int tiles_of(const Lengths& r, int tile) {
   return r.len > 0 ? (r.len - 1) / tile + 1 : 1;
 }
 
-// the team whose range holds point x of the axis, and the first point of team c
-__device__ __forceinline__ int owner_of(int64_t x, int64_t total, int teams) {
-  return (int)(((x + 1) * teams - 1) / total);
+// 64 bits by 32: in 32 bits where that is enough, as it nearly always is
+__device__ __forceinline__ int64_t divide(int64_t a, int32_t b) {
+  return a >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
 }
-__device__ __forceinline__ int64_t first_of(int c, int64_t total, int teams) {
-  return (int64_t)c * total / teams;
+
+// The axis cut into ranges that differ by one at most: the first `more` of
+// them have one point more than the others.
+struct Cut {
+  int64_t per;
+  int teams, more;
+  // the first point of team c's range, and the team whose range holds point x
+  __device__ __forceinline__ int64_t first_of(int c) const { return c * per + min(c, more); }
+  __device__ __forceinline__ int owner_of(int64_t x) const {
+    const int64_t head = more * (per + 1);
+    if (x < head) return (int)(per >= INT32_MAX ? x / (per + 1) : divide(x, (int)per + 1));
+    return more + (int)(per >= INT32_MAX ? (x - head) / per : divide(x - head, (int)per));
+  }
+};
+__device__ __forceinline__ Cut cut(int64_t total, int teams) {
+  Cut c;
+  c.teams = (int)min((int64_t)teams, total);
+  c.per = divide(total, c.teams);
+  c.more = (int)(total - c.per * c.teams);
+  return c;
+}
+
+// This thread's part [before, upto) of the axis, that of its share of the
+// requests; returns the axis' length.  All threads of the block call.
+template <int kBlock>
+__device__ __forceinline__ int64_t axis_part(const Params& p, uint64_t* scan, int64_t* before,
+                                             int64_t* upto) {
+  const int per = (p.B + kBlock - 1) / kBlock;
+  const int b0 = min(p.B, (int)threadIdx.x * per), b1 = min(p.B, b0 + per);
+  uint64_t sum = 0, total;
+  for (int b = b0; b < b1; ++b)
+    sum += (uint64_t)(tiles_of(request_lengths(p, b), p.tile) + p.item_cost) * p.kv_heads;
+  *upto = (int64_t)block_inclusive_scan_u64(sum, scan, &total);
+  *before = *upto - (int64_t)sum;
+  return (int64_t)total;
+}
+// where point x of the axis lies, if it is in this thread's part
+template <int kBlock>
+__device__ __forceinline__ bool locate(const Params& p, int64_t before, int64_t upto, int64_t x,
+                                       Start* start) {
+  if (x < before || x >= upto) return false;
+  for (int b = (int)threadIdx.x * ((p.B + kBlock - 1) / kBlock);; ++b) {  // ends by x < upto
+    const int tiles = tiles_of(request_lengths(p, b), p.tile);
+    const int item = tiles + p.item_cost;
+    const int64_t end = before + (int64_t)item * p.kv_heads;
+    if (x < end) {
+      const int head = (int)divide(x - before, item);
+      *start = {b, head, (int)(x - before - (int64_t)head * item), tiles};
+      return true;
+    }
+    before = end;
+  }
 }
 
 // A CTA's way along its range, item by item.
@@ -247,39 +303,31 @@ __device__ __forceinline__ Walk walk_from(const Params& p, const Start& s, int64
 // lengths (0: no work), and where they begin (shared memory, valid after the
 // call).  All threads call.
 template <int kBlock, int kStreams>
-__device__ __forceinline__ void find_range(const Params& p, int tile, const Workspace& ws,
-                                           uint64_t* scan, Start* start, int64_t* range) {
-  const int tid = threadIdx.x;
-  const int per = (p.B + kBlock - 1) / kBlock;
-  const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
-  uint64_t sum = 0, total_u;
-  for (int b = b0; b < b1; ++b)
-    sum += (uint64_t)(tiles_of(request_lengths(p, b), tile) + p.item_cost) * p.kv_heads;
-  const uint64_t upto = block_inclusive_scan_u64(sum, scan, &total_u);
-  const int64_t total = (int64_t)total_u;
-  const int teams = (int)min((int64_t)(gridDim.x * kStreams / p.row_tiles), total);
+__device__ __forceinline__ void find_range(const Params& p, const Workspace& ws, uint64_t* scan,
+                                           Start* start, int64_t* range) {
+  int64_t before, upto;
+  const int64_t total = axis_part<kBlock>(p, scan, &before, &upto);
+  const Cut c = cut(total, gridDim.x * kStreams / p.row_tiles);
 #pragma unroll
   for (int x = 0; x < kStreams; ++x) {
     const int team = blockIdx.x / p.row_tiles * kStreams + x;
     range[x] = 0;
-    if (team >= teams) continue;
-    const int64_t x0 = first_of(team, total, teams);
-    range[x] = first_of(team + 1, total, teams) - x0;
-    int64_t at = (int64_t)(upto - sum);
-    if (x0 < at || x0 >= (int64_t)upto) continue;
-    for (int b = b0; b < b1; ++b) {
-      const int tiles = tiles_of(request_lengths(p, b), tile);
-      const int item = tiles + p.item_cost;
-      const int64_t end = at + (int64_t)item * p.kv_heads;
-      if (x0 < end) {
-        start[x] = {b, (int)((x0 - at) / item), (int)((x0 - at) % item), tiles};
-        if (blockIdx.x % p.row_tiles == 0) ws.start[team] = start[x];
-        break;
-      }
-      at = end;
+    if (team >= c.teams) continue;
+    const int64_t x0 = c.first_of(team);
+    range[x] = c.first_of(team + 1) - x0;
+    if (locate<kBlock>(p, before, upto, x0, &start[x]) && blockIdx.x % p.row_tiles == 0) {
+      const Start at = start[x];
+      Seam seam = {at.b, at.head, -1, 0};
+      const int64_t begin = x0 - at.at + p.item_cost;  // the item's first tile
+      if (at.at > p.item_cost && c.owner_of(begin) == team - 1)
+        seam.last = c.owner_of(begin + at.tiles - 1);
+      ws.seam[team] = seam;
     }
   }
-  if (blockIdx.x == 0 && tid == 0) *ws.total = total;
+  // teams without work: nothing to join
+  for (int t = c.teams + blockIdx.x * kBlock + threadIdx.x; t < (int)gridDim.x * kStreams / p.row_tiles;
+       t += gridDim.x * kBlock)
+    ws.seam[t] = {0, 0, -1, 0};
   __syncthreads();
 }
 
@@ -344,7 +392,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, N8, MW>::kCtas)
   const int mw = warp % MW, kw = warp / MW;
   const Workspace ws = carve(p.workspace, kRows, p.max_ctas);
   int64_t range;
-  find_range<kThreads, 1>(p, S::kTile, ws, s_scan, &s_start, &range);
+  find_range<kThreads, 1>(p, ws, s_scan, &s_start, &range);
   Walk cur = walk_from(p, s_start, range, p.item_cost);
   const int r0 = (blockIdx.x % p.row_tiles) * kRows;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -668,9 +716,9 @@ __global__ void __launch_bounds__(kThreads, Shape<D, N8, MW>::kCtas)
 }
 
 // ------------------------------------------------------- the joining kernel
-// CTA (x, y, z): if the boundary before the range of team x + 1 is the first
-// one inside its item, a block of rows of the item's row tile z is joined
-// from the teams' partial rows, in the teams' order.  A warp takes kRowsAtOnce
+// CTA (x, y, z): a block of rows of row tile z of the item that is first cut
+// between teams x and x + 1, if there is one, is joined from the teams'
+// partial rows, in the teams' order.  A warp takes kRowsAtOnce
 // rows, and kAhead teams' parts of them are in flight together: one row and
 // many parts for the streaming kernel's few rows, cut among many teams; four
 // rows for the wide kernel's.
@@ -678,29 +726,22 @@ constexpr int kJoinThreads = 256;
 
 template <typename T, int D, int kRowsAtOnce>
 __global__ void __launch_bounds__(kJoinThreads)
-    tree_attention_join_kernel(const __grid_constant__ Params p, int rows, int grid) {
+    tree_attention_join_kernel(const __grid_constant__ Params p, int rows) {
   using H = Half<T>;
   constexpr int kPer = D / 32, kJoinUnroll = kRowsAtOnce;
   constexpr int kJoinRows = kJoinThreads / 32 * kRowsAtOnce, kAhead = 8 / kRowsAtOnce;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Workspace ws = carve(p.workspace, rows, p.max_ctas);
-  const int i = blockIdx.x + 1;
-  const int64_t total = *ws.total;
-  const Start at = ws.start[i];  // of a team without work: not looked at
-  const int teams = (int)min((int64_t)(grid / p.row_tiles), total);
-  if (i >= teams) return;
-  if (at.at <= p.item_cost) return;  // before the item's second tile: not split here
-  const int64_t begin = first_of(i, total, teams) - at.at + p.item_cost;
-  const int c0 = owner_of(begin, total, teams);
-  if (c0 != i - 1) return;
-  const int c1 = owner_of(begin + at.tiles - 1, total, teams);
+  const Seam at = ws.seam[blockIdx.x + 1];
+  const int c0 = blockIdx.x, c1 = at.last;  // the item's teams
+  if (c1 < 0) return;
   const int lane = threadIdx.x & 31;
   const int r0 = blockIdx.y * kJoinRows + (threadIdx.x >> 5);
   const int item_rows = p.nodes * p.group - blockIdx.z * rows;  // of this row tile, and more
   const int n_rows = min(rows, item_rows);
-  // the partial rows of team c: its first range's in slot 0, its last's in slot 1
-  auto slot_of = [&](int c) -> int64_t {
-    return (2ll * (c * p.row_tiles + blockIdx.z) + (c == c0 ? 1 : 0)) * rows;
+  // the partial rows of team t: its first range's in slot 0, its last's in slot 1
+  auto slot_of = [&](int t) -> int64_t {
+    return (2ll * (t * p.row_tiles + blockIdx.z) + (t == c0 ? 1 : 0)) * rows;
   };
 
   float top[kJoinUnroll], all[kJoinUnroll], a[kJoinUnroll][kPer];
@@ -708,7 +749,7 @@ __global__ void __launch_bounds__(kJoinThreads)
   for (int u = 0; u < kJoinUnroll; ++u) {
     const int r = min(r0 + u * (kJoinThreads / 32), n_rows - 1);
     top[u] = -INFINITY;
-    for (int c = c0 + lane; c <= c1; c += 32) top[u] = fmaxf(top[u], ws.stats[slot_of(c) + r].x);
+    for (int t = c0 + lane; t <= c1; t += 32) top[u] = fmaxf(top[u], ws.stats[slot_of(t) + r].x);
     all[u] = 0.0f;
 #pragma unroll
     for (int d = 0; d < kPer; ++d) a[u][d] = 0.0f;
@@ -718,14 +759,14 @@ __global__ void __launch_bounds__(kJoinThreads)
     top[u] = warp_reduce(top[u], OpMaxF());
   }
 #pragma unroll kAhead
-  for (int c = c0; c <= c1; ++c) {
+  for (int t = c0; t <= c1; ++t) {
     float2 st[kJoinUnroll];
     float x[kJoinUnroll][kPer];
 #pragma unroll
     for (int u = 0; u < kJoinUnroll; ++u) {
       const int r = min(r0 + u * (kJoinThreads / 32), n_rows - 1);
-      st[u] = ws.stats[slot_of(c) + r];
-      const float* v = ws.rows + (slot_of(c) + r) * D + lane * kPer;
+      st[u] = ws.stats[slot_of(t) + r];
+      const float* v = ws.rows + (slot_of(t) + r) * D + lane * kPer;
       if constexpr (kPer == 2) {
         *reinterpret_cast<float2*>(x[u]) = *reinterpret_cast<const float2*>(v);
       } else {
@@ -784,7 +825,7 @@ cudaError_t launch_join(const Params& p, int rows, int grid, cudaStream_t stream
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, tree_attention_join_kernel<T, D, kRowsAtOnce>, p, rows, grid);
+  return cudaLaunchKernelEx(&cfg, tree_attention_join_kernel<T, D, kRowsAtOnce>, p, rows);
 }
 
 // rows of a streaming CTA for `rows` rows of an item
@@ -808,6 +849,7 @@ cudaError_t launch_shape(Params p, int sms, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   p.max_ctas = kStreamCtas;
   p.item_cost = kStreamCost;
+  p.tile = S::kTile;
   const int grid = min(kStreamCtas, max(sms * S::kCtas, p.row_tiles));
   kernel<<<grid, kThreads, S::kSmem, stream>>>(p);
   e = cudaGetLastError();

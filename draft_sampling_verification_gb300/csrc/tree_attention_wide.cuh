@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   }
   const Workspace ws = carve(p.workspace, W::kRows, p.max_ctas);
   int64_t ranges[W::kStreams];
-  find_range<kWideThreads, W::kStreams>(p, kKeys, ws, sh.scan, sh.start, ranges);
+  find_range<kWideThreads, W::kStreams>(p, ws, sh.scan, sh.start, ranges);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (ranges[0] <= 0) return;  // the second stream's range comes behind the first's
   const int r0 = (blockIdx.x % p.row_tiles) * W::kRows;
@@ -789,6 +789,7 @@ bool launch_wide(Params p, int sms, cudaStream_t stream, cudaError_t* error) {
     return false;
   p.row_tiles = (p.nodes * p.group + W::kRows - 1) / W::kRows;
   p.max_ctas = wide_ctas(kMode == kPair);
+  p.tile = W::kKeys;
   p.item_cost = kMode == kPair ? kPairCost : kMode == kBoth ? kBothCost : kOneCost;
   auto* kernel = tree_attention_wide_kernel<T, D, kMode>;
   *error = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, W::kSmem);
