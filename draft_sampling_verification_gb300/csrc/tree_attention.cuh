@@ -138,6 +138,8 @@ __device__ __forceinline__ uint32_t without_special(uint32_t w) {
 // queries, its first copies and its results take, without which the teams
 // that get many short items end last.  (A pair of ranges in one CTA counts as
 // two CTAs here.)
+// A range is at least kMinRange long: the join of more parts costs more than they save.
+constexpr int kMinRange = 3;
 constexpr int kStreamCost = 5, kPairCost = 2, kBothCost = 5, kOneCost = 1;
 
 struct Start {  // where a team's range begins: `at` into the item, of item_cost + tiles
@@ -213,7 +215,7 @@ struct Cut {
 };
 __device__ __forceinline__ Cut cut(int64_t total, int teams) {
   Cut c;
-  c.teams = (int)min((int64_t)teams, total);
+  c.teams = (int)max(1ll, min((long long)teams, (long long)total / kMinRange));
   c.per = divide(total, c.teams);
   c.more = (int)(total - c.per * c.teams);
   return c;
