@@ -798,7 +798,7 @@ bool launch_wide(Params p, int sms, cudaStream_t stream, cudaError_t* error) {
   kernel<<<grid, kWideThreads, W::kSmem, stream>>>(p, k_map, v_map, boxes);
   *error = cudaGetLastError();
   if (*error == cudaSuccess)
-    *error = launch_join<T, D, kMode == kBoth ? 4 : 1>(p, W::kRows, grid * W::kStreams, stream);
+    *error = launch_join<T, D>(p, W::kRows, grid * W::kStreams, stream);
   return true;
 }
 
