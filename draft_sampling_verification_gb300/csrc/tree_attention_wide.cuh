@@ -128,12 +128,16 @@ __device__ __forceinline__ void tmem_wait_store() {
 // kPair: items of up to 128 rows.  The warpgroups go along two ranges of the
 //   tile axis, each with its own queries and its own copies of keys and
 //   values: two CTAs in one, of which one's starts and results are hidden
-//   behind the other's products.  Bound by HBM.
+//   behind the other's products.  Bound by HBM: 256 items of 4,000 tokens
+//   take 101 us with 24 rows, 118 us with 128 (5.2 and 4.5 TB/s), two
+//   requests of 131,000 tokens 168 us (6.1 TB/s).
 // kBoth: items of more rows.  The warpgroups take two row tiles of one item
 //   and share its keys and values.  Bound by the products (2 * 2 * 128 * 128 *
-//   D operations a row tile and tile of positions).
+//   D operations a row tile and tile of positions): 16 requests with trees of
+//   64 nodes and 8 query heads to a cached head take 159 us, 1.0 PFLOP/s.
 // kOne: head_dim 256, whose accumulators fill half the tensor memory: one
-//   warpgroup, one row tile, 64 positions at a time.
+//   warpgroup, one row tile, 64 positions at a time.  256 items of 4,000
+//   tokens take 198 us with 24 rows (5.3 TB/s).
 //
 // kPair and kOne take 64 positions at a time and keep the scores of two tiles
 // in tensor memory, so that the next tile's products run during a softmax
@@ -220,7 +224,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     asm volatile("prefetch.tensormap [%0];" ::"l"(&k_map) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(&v_map) : "memory");
   }
-  const Workspace ws = carve(p.workspace, W::kRows, p.max_ctas);
+  const Workspace ws = carve(p.workspace, p.part_rows, p.max_ctas);
   int64_t ranges[W::kStreams];
   find_range<kWideThreads, W::kStreams>(p, ws, sh.scan, sh.start, ranges);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -506,7 +510,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       }
       const bool full = cur.whole();
       const int64_t to = (int64_t)cur.b * p.nodes * p.heads + cur.head * p.group + my_row;
-      const int64_t slot = cur.slot(kPaired ? 2 * blockIdx.x + x : blockIdx.x) * W::kRows +
+      const int64_t slot = cur.slot(kPaired ? 2 * blockIdx.x + x : blockIdx.x) * p.part_rows +
                            (kPaired ? 0 : m * 128) + t;
       const float inv = sum == 0.0f ? 0.0f : full ? 1.0f / sum : 1.0f;
       const int chunks = m_rows + (t & ~31) < p.nodes * p.group ? D / 32 : 0;  // of the warp
@@ -788,6 +792,7 @@ bool launch_wide(Params p, int sms, cudaStream_t stream, cudaError_t* error) {
       !map_cache<T>(&v_map, p, p.v, D, boxes.v_rows, true))
     return false;
   p.row_tiles = (p.nodes * p.group + W::kRows - 1) / W::kRows;
+  p.part_rows = part_rows(p.nodes * p.group, W::kRows);
   p.max_ctas = wide_ctas(kMode == kPair);
   p.tile = W::kKeys;
   p.item_cost = kMode == kPair ? kPairCost : kMode == kBoth ? kBothCost : kOneCost;

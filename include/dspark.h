@@ -557,7 +557,8 @@ int dspark_q_validate(const float* q, const int32_t* sparse_ids, const int32_t* 
  * [0, max_new], or more blocks than max_blocks) is refused with BAD_LENGTH
  * and needs none.  taken[0]: the blocks granted, from the front of the list.
  * The lengths and the list stay the caller's: a second call with the same
- * arguments gives the same outputs.
+ * arguments gives the same outputs, and a caller that may drop the step's
+ * tokens takes the granted blocks off its list only when it keeps them.
  *
  * slots[B][max_new]: the slot of new token t of request b (position ctx + t),
  * -1 from new_len on, for a refused request, and where the table entry is
@@ -633,8 +634,8 @@ int dspark_kv_write(const void* k, const void* v, int32_t src_dtype, int64_t src
  * 16-byte aligned and their strides multiples of 8 elements; max_blocks*
  * page_size <= 2^30.  scale finite.
  * workspace: dspark_tree_attention_workspace_bytes(...) bytes of device
- * memory owned by the caller, with no content to keep; calls that may
- * overlap need separate ones.  The result does not depend on the batch's
+ * memory owned by the caller, with no content to keep (3 to 90 MB); calls that
+ * may overlap need separate ones.  The result does not depend on the batch's
  * other requests beyond the order of fp32 sums, and is the same from run to
  * run.
  */

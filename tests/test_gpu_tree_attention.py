@@ -286,6 +286,24 @@ def test_other_stream_stale_workspace_and_repeats(T, heads):
             assert torch.equal(x, y) and torch.equal(x, z)
 
 
+@pytest.mark.parametrize("page", [16, 12])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("T,heads", [(1, 2), (1, 16), (6, 8), (5, 10), (7, 40), (64, 2), (33, 14),
+                                     (64, 16)])
+def test_workspace_bounds(T, heads, dim, page):
+    # few items of many tiles, so that nearly every range leaves partial rows
+    c = Case([9000, 2500], [T, T - T // 3], T, heads=heads, dim=dim, page=page, mask="tree")
+    want = c.run()
+    n = ds.dspark_tree_attention_workspace_bytes(2, T, heads, c.k.shape[2], dim)
+    for at in (256, 272):
+        ws = torch.full((n + 4096,), 90, dtype=torch.uint8, device="cuda")
+        out = [torch.empty_like(t) for t in want]
+        ds.dspark_tree_attention(*c.device(), c.scale, *out, ws[at:at + n])
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(want, out))
+        assert (ws[:at] == 90).all() and (ws[at + n:] == 90).all()
+
+
 def test_in_a_graph():
     c = Case([700, 80], [6, 6], 6)
     a = c.device()
