@@ -152,10 +152,10 @@ __device__ __forceinline__ void tmem_wait_store() {
 //
 // Warps 0-3 and 4-7: softmax, queries and results.  Warps 8 and 9: tensor
 // copies of keys and values, box by box of a block's rows, into a ring of
-// stages.  Warps 10 and 11: issue the products.  (The second of each pair has
-// work under kPair only.)  Q lies in rows of 64 dims (128 bytes, swizzled in
-// groups of eight rows), one block of 64 dims after the other; keys the same;
-// values too, read with their dims as the major axis.
+// stages.  Warps 10 and 11: issue the products of a row tile each.  Q lies in
+// rows of 64 dims (128 bytes, swizzled in groups of eight rows), one block of
+// 64 dims after the other; keys the same; values too, read with their dims as
+// the major axis.
 enum WideMode { kPair, kBoth, kOne };
 
 constexpr int kWideThreads = 384;  // 168 registers a thread: a row's 128 scores and more
@@ -166,11 +166,11 @@ struct Wide {
   static constexpr int kRowTiles = kMode == kOne ? 1 : 2;   // of 128 rows, over all streams
   static constexpr int kRows = kMode == kBoth ? 256 : 128;  // of an item, per CTA
   // positions of a tile, and the tiles whose scores are held
-  static constexpr int kKeys = kMode == kBoth || D == 64 ? 128 : 64;
+  static constexpr int kKeys = kMode == kPair && D == 64 ? 128 : 64;
   static constexpr int kScores = kKeys == 128 ? 1 : 2;
   static constexpr int kHalves = D / 64;
   static constexpr int kQBytes = 128 * D * 2, kTileBytes = kKeys * D * 2;
-  static constexpr int kStages = kMode == kBoth && D == 64 ? 4 : 2;
+  static constexpr int kStages = kMode == kBoth ? 4 : 2;
   static constexpr int kRing = 2 * kStages * kTileBytes;    // keys, then values
   static constexpr int kSmem = kRowTiles * kQBytes + kStreams * kRing + 1024;
 };
@@ -192,7 +192,9 @@ struct WideStream {
 };
 struct WideShared {
   WideStream stream[2];
-  uint64_t q_full[2], s_full[2][2], p_full[2][2], o_full[2][2], drained[2];
+  // p_full by tile number modulo 8: a row tile is less than eight tiles ahead of the other, as
+  // its next scores wait for keys whose place both have left
+  uint64_t q_full[2], s_full[2][2], p_full[2][8], o_full[2][2], drained[2];
   uint64_t scan[32];
   int64_t q_row[256];  // where each row of the CTA begins in Q, from its request and cached head on
   Start start[2];
@@ -241,16 +243,14 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     for (int x = 0; x < W::kStreams; ++x)
       for (int i = 0; i < kStages; ++i) {
         mbar_init(&sh.stream[x].k_full[i], 1);
-        mbar_init(&sh.stream[x].k_empty[i], 1);
+        mbar_init(&sh.stream[x].k_empty[i], n_tiles);
         mbar_init(&sh.stream[x].v_full[i], 1);
-        mbar_init(&sh.stream[x].v_empty[i], 1);
+        mbar_init(&sh.stream[x].v_empty[i], n_tiles);
       }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.q_full[i], 128);
-      for (int j = 0; j < W::kScores; ++j) {
-        mbar_init(&sh.s_full[i][j], 1);
-        mbar_init(&sh.p_full[i][j], 128);
-      }
+      for (int j = 0; j < W::kScores; ++j) mbar_init(&sh.s_full[i][j], 1);
+      for (int j = 0; j < 8; ++j) mbar_init(&sh.p_full[i][j], 128);
       mbar_init(&sh.o_full[i][0], 1);
       mbar_init(&sh.o_full[i][1], 1);
       mbar_init(&sh.drained[i], 1);
@@ -286,8 +286,21 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   auto wait_all = [&](uint64_t* bar, uint32_t phase) -> bool {
     return __all_sync(0xffffffffu, wait(bar, phase));
   };
+  // four waits whose latencies, some 200 cycles each and as long as eight products, overlap; all
+  // lanes wait for the same barriers, so the warp stays together
+  auto wait_each = [&](uint64_t* const (&bar)[4], const uint32_t (&phase)[4]) -> bool {
+    bool done = true;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) done &= mbar_try_wait(bar[i], phase[i]);
+    if (__all_sync(0xffffffffu, done)) return true;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (!wait_all(bar[i], phase[i])) return false;
+    return true;
+  };
   auto phase_of = [](uint32_t g) -> uint32_t { return (g / kStages) & 1u; };
   auto score_phase = [](uint32_t g) -> uint32_t { return (g / W::kScores) & 1u; };
+  auto hand_phase = [](uint32_t g) -> uint32_t { return (g >> 3) & 1u; };
 
   if (warp < 8) {
     // -------------------------------------------------- softmax and results
@@ -490,7 +503,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           fence_async_shared();
         }
         tc_before_sync();
-        mbar_arrive(&sh.p_full[m][tile_no % W::kScores]);
+        mbar_arrive(&sh.p_full[m][tile_no & 7u]);
       }
       // Q is free, as the last scores are done: the next item's first scores
       // are computed while this one's results are written
@@ -498,9 +511,10 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       if (ok) ok = wait_values(tile_no - 1u);
       if (!ok) break;
       tc_after_sync();
-      // nodes lie in the item's last tiles: at most 64 of them, and their last tile's rest
+      // nodes, at most 64, lie in the item's last two tiles (the tiles before these may already
+      // have lent their flags to tiles of the next item)
       bool special = false;
-      for (uint32_t k = 1; k <= min(3, tiles); ++k)
+      for (uint32_t k = 1; k <= min(2, tiles); ++k)
         special |= stream.special[(tile_no - k) & 7u] != 0u;
 
       float sum = sum2.x + sum2.y;
@@ -570,84 +584,115 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       tc_before_sync();  // the accumulators are read: the next item may take them
       cur = ahead;
     }
-  } else if (warp < 8 + W::kStreams) {
+  } else if (warp < 10) {
     // ------------------------------------------------------ keys and values
-    // Lane i copies the tile's box i of keys and of values, a part of one block.
-    const int x = warp - 8;
+    // Lane i copies the tile's box i, a part of one block.  Under kPair a warp
+    // copies the keys and the values of its stream, else warp 8 copies the
+    // keys and warp 9 the values.
+    const int x = kPaired ? warp - 8 : 0;
+    const bool keys = kPaired || warp == 8, values = kPaired || warp == 9;
     WideStream& stream = sh.stream[x];
     const uint32_t k_at = ring + x * W::kRing, v_at = k_at + kStages * W::kTileBytes;
-    const int k_rows = boxes.k_rows, v_rows = boxes.v_rows;  // v_rows a multiple of k_rows
-    const int k_boxes = kKeys / k_rows, v_boxes = kKeys / v_rows;  // at most 16
-    const int v_lane = lane * v_rows / k_rows & 31;  // the keys' box where this lane's values begin
-    uint32_t g = 0;
+    const int k_rows = boxes.k_rows, v_rows = boxes.v_rows;  // powers of two, k_rows at most v_rows
+    const int v_boxes = kKeys / v_rows;
+    const int rows = keys ? k_rows : v_rows, n_boxes = kKeys / rows;  // at most 16
+    const uint32_t all_boxes = (1u << n_boxes) - 1u;
+    const int v_lane = lane * v_rows / rows & 31;  // the box where this lane's values begin
+    const int k_shift = 31 - __clz(k_rows);
+    const int next_row = kKeys % p.page, next_block = kKeys / p.page;  // from tile to tile
+    uint32_t g = 0, k_tiles = 0, v_tiles = 0;  // k_tiles, v_tiles: the tiles copied
     bool ok = true;
     Walk cur = walk_from(p, sh.start[x], ranges[x], p.item_cost);
     while (ok && cur.advance(p, kKeys)) {
       const int tiles = cur.count;
       const Lengths len = cur.len;
       const int first = cur.first * kKeys;
+      // the place of this lane's box: position, entry of the table, row of the block
+      int pos = first + lane * rows, at = pos / p.page, row_ahead = pos - at * p.page;
       const int32_t* table = p.table + cur.b * p.table_ld;
-      auto entry_of = [&](int i) -> int {
-        const int pos = first + i * kKeys + lane * k_rows;
-        return i < tiles && lane < k_boxes && pos < len.len ? __ldg(table + pos / p.page) : -1;
-      };
-      int ahead = entry_of(0);
+      auto entry = [&]() -> int { return lane < n_boxes && pos < len.len ? __ldg(table + at) : -1; };
+      int ahead = entry();
       for (int i = 0; i < tiles; ++i, ++g) {
-        const int pos0 = first + i * kKeys, pos = pos0 + lane * k_rows, block = ahead;
-        ahead = entry_of(i + 1);
+        const int block = ahead, row_here = row_ahead;
+        pos += kKeys;
+        at += next_block;
+        row_ahead += next_row;
+        if (row_ahead >= p.page) {
+          row_ahead -= p.page;
+          ++at;
+        }
+        ahead = entry();
         const bool held = block >= 0 && block < p.n_blocks;
-        const int from = held ? block : p.n_blocks, row = held ? pos % p.page : 0;
-        const uint32_t held_boxes = __ballot_sync(0xffffffffu, held);
+        const int from = held ? block : p.n_blocks, row = held ? row_here : 0;
         const uint32_t stage = g % kStages;
-        ok = wait_all(&stream.k_empty[stage], phase_of(g) ^ 1u);
-        if (!ok) break;
-        if (lane < kKeys / 32) {
-          uint32_t word = 0u;  // positions 32 lane .. of the tile
-          if (k_rows >= 32) {
-            word = (held_boxes >> (lane * 32 / k_rows)) & 1u ? ~0u : 0u;
-          } else {
-            for (int j = 0; j < 32 / k_rows; ++j)
-              if ((held_boxes >> (lane * 32 / k_rows + j)) & 1u)
-                word |= ((1u << k_rows) - 1u) << (j * k_rows);
+        if (keys) {
+          const uint32_t held_boxes = __ballot_sync(0xffffffffu, held);
+          ok = wait_all(&stream.k_empty[stage], phase_of(g) ^ 1u);
+          if (!ok) break;
+          if (lane < kKeys / 32) {
+            uint32_t word = ~0u;  // positions 32 lane .. of the tile
+            if (held_boxes != all_boxes) {
+              const uint32_t mine = held_boxes >> (lane << 5 >> k_shift);
+              word = 0u;
+              if (k_rows >= 32) {
+                word = mine & 1u ? ~0u : 0u;
+              } else {
+                for (int j = 0; j << k_shift < 32; ++j)
+                  if ((mine >> j) & 1u) word |= ((1u << k_rows) - 1u) << (j << k_shift);
+              }
+            }
+            const int past = len.len - (first + i * kKeys + lane * 32);  // positions before the end
+            stream.valid[g & 7u][lane] =
+                past >= 32 ? word : past > 0 ? word & ((1u << past) - 1u) : 0u;
           }
-          const int past = len.len - (pos0 + lane * 32);  // positions before the end
-          stream.valid[g & 7u][lane] =
-              past >= 32 ? word : past > 0 ? word & ((1u << past) - 1u) : 0u;
-        }
-        if (lane == 0) {
-          stream.special[g & 7u] = 0u;
-          mbar_arrive_expect_tx(&stream.k_full[stage], W::kTileBytes);
-        }
-        __syncwarp();
-        if (lane < k_boxes) {
-          const uint32_t at = k_at + stage * W::kTileBytes;
-          if (boxes.k_whole) {
-            tma_load_box(at + lane * k_group, &k_map, row, 0, cur.head, from,
-                         &stream.k_full[stage]);
-          } else {
-#pragma unroll
-            for (int h = 0; h < kHalves; ++h)
-              tma_load_box(at + h * k_half + lane * k_rows * 128, &k_map, row, h, cur.head, from,
+          if (lane == 0) {
+            stream.special[g & 7u] = 0u;
+            mbar_arrive_expect_tx(&stream.k_full[stage], W::kTileBytes);
+          }
+          __syncwarp();
+          if (lane < n_boxes) {
+            const uint32_t to = k_at + stage * W::kTileBytes;
+            if (boxes.k_whole) {
+              tma_load_box(to + lane * k_group, &k_map, row, 0, cur.head, from,
                            &stream.k_full[stage]);
+            } else {
+#pragma unroll
+              for (int h = 0; h < kHalves; ++h)
+                tma_load_box(to + h * k_half + lane * k_rows * 128, &k_map, row, h, cur.head, from,
+                             &stream.k_full[stage]);
+            }
           }
+          k_tiles = g + 1u;
+          __syncwarp();
         }
-        __syncwarp();
-        const int v_from = __shfl_sync(0xffffffffu, from, v_lane);
-        const int v_row = __shfl_sync(0xffffffffu, row, v_lane);
-        ok = wait_all(&stream.v_empty[stage], phase_of(g) ^ 1u);
-        if (!ok) break;
-        if (lane == 0) mbar_arrive_expect_tx(&stream.v_full[stage], W::kTileBytes);
-        __syncwarp();
-        if (lane < v_boxes)
-          tma_load_box(v_at + stage * W::kTileBytes + lane * v_box, &v_map, v_row, 0, cur.head,
-                       v_from, &stream.v_full[stage]);
-        __syncwarp();
+        if (values) {
+          const int v_from = kPaired ? __shfl_sync(0xffffffffu, from, v_lane) : from;
+          const int v_row = kPaired ? __shfl_sync(0xffffffffu, row, v_lane) : row;
+          ok = wait_all(&stream.v_empty[stage], phase_of(g) ^ 1u);
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(&stream.v_full[stage], W::kTileBytes);
+          __syncwarp();
+          if (lane < v_boxes)
+            tma_load_box(v_at + stage * W::kTileBytes + lane * v_box, &v_map, v_row, 0, cur.head,
+                         v_from, &stream.v_full[stage]);
+          v_tiles = g + 1u;
+          __syncwarp();
+        }
       }
     }
-  } else if (warp >= 10 && warp < 10 + W::kStreams) {
+    // no copy is in flight when the CTA ends, which only a wait that expired can leave
+    for (uint32_t i = 0; i < kStages; ++i) {
+      if (i < k_tiles)
+        mbar_wait_bounded(&stream.k_full[(k_tiles - 1u - i) % kStages], phase_of(k_tiles - 1u - i));
+      if (i < v_tiles)
+        mbar_wait_bounded(&stream.v_full[(v_tiles - 1u - i) % kStages], phase_of(v_tiles - 1u - i));
+    }
+  } else if (warp >= 10 && warp < 10 + (kPaired ? 2 : n_tiles)) {
     // ------------------------------------------------------------- products
-    // The warp goes through the loop together; one lane issues.
-    const int x = warp - 10;
+    // A warp for each row tile, so that one's waits pass during the other's
+    // products.  It goes through the loop together; one lane issues.
+    const int m = warp - 10;
+    const int x = kPaired ? m : 0;
     WideStream& stream = sh.stream[x];
     constexpr uint32_t kFormat = H::kExponent == 0x7F80u ? 1u : 0u;  // bf16 or f16
     // fp32 accumulators, both operands of T, 128 rows; for P V the second has its dims outermost
@@ -655,9 +700,9 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     constexpr uint32_t kScores = kCommon | ((uint32_t)(kKeys / 8) << 17);
     constexpr uint32_t kValues = kCommon | (1u << 16) | ((uint32_t)(D / 8) << 17);
     const bool on = elect_one();
-    // descriptors of this stream's first row tile of Q, and of the stages of keys and values; an
-    // operand further on adds its distance / 16
-    const uint64_t q_desc = operand_desc(base + x * W::kQBytes, 16, 1024);
+    // descriptors of this row tile of Q, and of the stages of keys and values; an operand further
+    // on adds its distance / 16
+    const uint64_t q_desc = operand_desc(base + m * W::kQBytes, 16, 1024);
     const uint64_t k_desc = operand_desc(ring + x * W::kRing, 16, k_group);
     const uint64_t v_desc = operand_desc(ring + x * W::kRing + kStages * W::kTileBytes, v_half,
                                          boxes.v_rows == 8 ? v_box : 1024u);
@@ -669,62 +714,62 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       v_at[kt] = v_desc + (r / boxes.v_rows * v_box + r % boxes.v_rows * 128) / 16;
     }
     const uint32_t k_half16 = k_half / 16;
-    auto scores = [&](int m, uint32_t g) {  // m: the row tile, of this stream
-      const uint64_t a = q_desc + (uint32_t)m * (W::kQBytes / 16);
+    auto scores = [&](uint32_t g) {
       const uint64_t b = k_desc + (g % kStages) * (W::kTileBytes / 16);
 #pragma unroll
       for (int kt = 0; kt < D / 16; ++kt)
-        mma_ss(on, s_col(x + m, g), a + (kt >> 2) * (16384 / 16) + (kt & 3) * 2,
+        mma_ss(on, s_col(m, g), q_desc + (kt >> 2) * (16384 / 16) + (kt & 3) * 2,
                b + (kt >> 2) * k_half16 + (kt & 3) * 2, kScores, kt > 0);
-      mma_commit(on, &sh.s_full[x + m][g % W::kScores]);
+      mma_commit(on, &sh.s_full[m][g % W::kScores]);
+      mma_commit(on, &stream.k_empty[g % kStages]);
     };
-    auto values = [&](int m, uint32_t g, bool add) {
+    auto values = [&](uint32_t g, bool add) {
       const uint64_t stage = (g % kStages) * (W::kTileBytes / 16);
 #pragma unroll
       for (int kt = 0; kt < kKeys / 16; ++kt)
-        mma_ts(on, o_col(x + m), s_col(x + m, g) + kt * 8, v_at[kt] + stage, kValues,
-               add || kt > 0);
+        mma_ts(on, o_col(m), s_col(m, g) + kt * 8, v_at[kt] + stage, kValues, add || kt > 0);
+      mma_commit(on, &sh.o_full[m][g & 1u]);
+      mma_commit(on, &stream.v_empty[g % kStages]);
     };
     uint32_t g = 0, segments = 0;
     bool ok = true;
     Walk cur = walk_from(p, sh.start[x], ranges[x], p.item_cost);
     while (ok && cur.advance(p, kKeys)) {
       const int tiles = cur.count;
-      for (int m = 0; m < n_tiles; ++m) ok = ok && wait_all(&sh.q_full[x + m], segments & 1u);
-      ok = ok && wait_all(&stream.k_full[g % kStages], phase_of(g));
-      if (!ok) break;
-      tc_after_sync();
-      for (int m = 0; m < n_tiles; ++m) scores(m, g);
-      mma_commit(on, &stream.k_empty[g % kStages]);
-      if (W::kScores == 2 && tiles > 1) {
-        ok = wait_all(&stream.k_full[(g + 1u) % kStages], phase_of(g + 1u));
+      ok = wait_all(&sh.q_full[m], segments & 1u);
+      for (int i = 0; i < min(W::kScores, tiles) && ok; ++i) {
+        ok = wait_all(&stream.k_full[(g + i) % kStages], phase_of(g + i));
         if (!ok) break;
-        scores(0, g + 1u);
-        mma_commit(on, &stream.k_empty[(g + 1u) % kStages]);
+        tc_after_sync();
+        scores(g + i);
       }
       for (int i = 0; i < tiles && ok; ++i, ++g) {
         const uint32_t ahead = g + W::kScores;  // takes the place of tile g's scores
         const bool more = i + W::kScores < tiles;
-        for (int m = 0; m < n_tiles; ++m) {
-          ok = wait_all(&sh.p_full[x + m][g % W::kScores], score_phase(g));
-          if (m == 0) ok = ok && wait_all(&stream.v_full[g % kStages], phase_of(g));
+        // The weights (and those of the first row tile, which clears the values), the values and,
+        // where their copies run ahead of the scores, the next keys (the values again when there
+        // are none: the barrier of keys read before may have gone on).
+        constexpr bool kEarly = kStages > W::kScores;
+        uint64_t* v_full = &stream.v_full[g % kStages];
+        ok = wait_each({&sh.p_full[m][g & 7u], &sh.p_full[kPaired ? m : 0][g & 7u], v_full,
+                        kEarly && more ? &stream.k_full[ahead % kStages] : v_full},
+                       {hand_phase(g), hand_phase(g), phase_of(g),
+                        phase_of(kEarly && more ? ahead : g)});
+        if (!ok) break;
+        tc_after_sync();
+        values(g, i > 0);
+        if (!more) continue;
+        if constexpr (!kEarly) {
+          ok = wait_all(&stream.k_full[ahead % kStages], phase_of(ahead));
           if (!ok) break;
-          tc_after_sync();
-          values(m, g, i > 0);
-          mma_commit(on, &sh.o_full[x + m][g & 1u]);
-          if (m == n_tiles - 1) mma_commit(on, &stream.v_empty[g % kStages]);
-          if (!more) continue;
-          if (m == 0) ok = wait_all(&stream.k_full[ahead % kStages], phase_of(ahead));
-          if (!ok) break;
-          scores(m, ahead);
         }
-        if (ok && more) mma_commit(on, &stream.k_empty[ahead % kStages]);
+        scores(ahead);
       }
       ++segments;
     }
-    // nothing of this stream's is in flight when its memory is given back
-    mma_commit(on, &sh.drained[x]);
-    mbar_wait_bounded(&sh.drained[x], 0);
+    // nothing of this row tile's is in flight when its memory is given back
+    mma_commit(on, &sh.drained[m]);
+    mbar_wait_bounded(&sh.drained[m], 0);
   }
   __syncwarp();
   tc_before_sync();
