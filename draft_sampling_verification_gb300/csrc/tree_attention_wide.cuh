@@ -192,9 +192,7 @@ struct WideStream {
 };
 struct WideShared {
   WideStream stream[2];
-  // p_full by tile number modulo 8: a row tile is less than eight tiles ahead of the other, as
-  // its next scores wait for keys whose place both have left
-  uint64_t q_full[2], s_full[2][2], p_full[2][8], o_full[2][2], drained[2];
+  uint64_t q_full[2], s_full[2][2], p_full[2][2], o_full[2][2], turn[2], drained[2];
   uint64_t scan[32];
   int64_t q_row[256];  // where each row of the CTA begins in Q, from its request and cached head on
   Start start[2];
@@ -249,10 +247,13 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.q_full[i], 128);
-      for (int j = 0; j < W::kScores; ++j) mbar_init(&sh.s_full[i][j], 1);
-      for (int j = 0; j < 8; ++j) mbar_init(&sh.p_full[i][j], 128);
+      for (int j = 0; j < W::kScores; ++j) {
+        mbar_init(&sh.s_full[i][j], 1);
+        mbar_init(&sh.p_full[i][j], 128);
+      }
       mbar_init(&sh.o_full[i][0], 1);
       mbar_init(&sh.o_full[i][1], 1);
+      mbar_init(&sh.turn[i], 32);
       mbar_init(&sh.drained[i], 1);
     }
     sh.failed = 0u;
@@ -300,7 +301,6 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   };
   auto phase_of = [](uint32_t g) -> uint32_t { return (g / kStages) & 1u; };
   auto score_phase = [](uint32_t g) -> uint32_t { return (g / W::kScores) & 1u; };
-  auto hand_phase = [](uint32_t g) -> uint32_t { return (g >> 3) & 1u; };
 
   if (warp < 8) {
     // -------------------------------------------------- softmax and results
@@ -503,7 +503,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           fence_async_shared();
         }
         tc_before_sync();
-        mbar_arrive(&sh.p_full[m][tile_no & 7u]);
+        mbar_arrive(&sh.p_full[m][tile_no % W::kScores]);
       }
       // Q is free, as the last scores are done: the next item's first scores
       // are computed while this one's results are written
@@ -690,7 +690,9 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   } else if (warp >= 10 && warp < 10 + (kPaired ? 2 : n_tiles)) {
     // ------------------------------------------------------------- products
     // A warp for each row tile, so that one's waits pass during the other's
-    // products.  It goes through the loop together; one lane issues.
+    // products.  Under kBoth the two take turns, tile by tile: products of both
+    // issued side by side would end together, and both warps would wait then.
+    // The warp goes through the loop together; one lane issues.
     const int m = warp - 10;
     const int x = kPaired ? m : 0;
     WideStream& stream = sh.stream[x];
@@ -714,12 +716,16 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       v_at[kt] = v_desc + (r / boxes.v_rows * v_box + r % boxes.v_rows * 128) / 16;
     }
     const uint32_t k_half16 = k_half / 16;
-    auto scores = [&](uint32_t g) {
+    const bool turns = kMode == kBoth && n_tiles == 2;
+    auto scores = [&](uint32_t g, bool pass) {  // pass: gives the turn away
       const uint64_t b = k_desc + (g % kStages) * (W::kTileBytes / 16);
 #pragma unroll
-      for (int kt = 0; kt < D / 16; ++kt)
+      for (int kt = 0; kt < D / 16; ++kt) {
         mma_ss(on, s_col(m, g), q_desc + (kt >> 2) * (16384 / 16) + (kt & 3) * 2,
                b + (kt >> 2) * k_half16 + (kt & 3) * 2, kScores, kt > 0);
+        // half the products take as long as the other warp needs to see it
+        if (kt == D / 32 - 1 && pass) mbar_arrive(&sh.turn[m ^ 1]);
+      }
       mma_commit(on, &sh.s_full[m][g % W::kScores]);
       mma_commit(on, &stream.k_empty[g % kStages]);
     };
@@ -741,29 +747,34 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         ok = wait_all(&stream.k_full[(g + i) % kStages], phase_of(g + i));
         if (!ok) break;
         tc_after_sync();
-        scores(g + i);
+        scores(g + i, false);
       }
       for (int i = 0; i < tiles && ok; ++i, ++g) {
         const uint32_t ahead = g + W::kScores;  // takes the place of tile g's scores
         const bool more = i + W::kScores < tiles;
-        // The weights (and those of the first row tile, which clears the values), the values and,
-        // where their copies run ahead of the scores, the next keys (the values again when there
-        // are none: the barrier of keys read before may have gone on).
+        // The weights, the values, where their copies run ahead of the scores the next keys, and
+        // the turn (the values again where there is none: the barrier of keys read before may have
+        // gone on).  The second row tile's turn also says that the first has cleared the values.
         constexpr bool kEarly = kStages > W::kScores;
         uint64_t* v_full = &stream.v_full[g % kStages];
-        ok = wait_each({&sh.p_full[m][g & 7u], &sh.p_full[kPaired ? m : 0][g & 7u], v_full,
-                        kEarly && more ? &stream.k_full[ahead % kStages] : v_full},
-                       {hand_phase(g), hand_phase(g), phase_of(g),
-                        phase_of(kEarly && more ? ahead : g)});
+        const uint32_t v_phase = phase_of(g);
+        ok = wait_each({&sh.p_full[m][g % W::kScores], v_full,
+                        kEarly && more ? &stream.k_full[ahead % kStages] : v_full,
+                        turns ? &sh.turn[m] : v_full},
+                       {score_phase(g), v_phase, kEarly && more ? phase_of(ahead) : v_phase,
+                        turns ? (g + 1u + m) & 1u : v_phase});
         if (!ok) break;
         tc_after_sync();
         values(g, i > 0);
-        if (!more) continue;
-        if constexpr (!kEarly) {
-          ok = wait_all(&stream.k_full[ahead % kStages], phase_of(ahead));
-          if (!ok) break;
+        if (more) {
+          if constexpr (!kEarly) {
+            ok = wait_all(&stream.k_full[ahead % kStages], phase_of(ahead));
+            if (!ok) break;
+          }
+          scores(ahead, turns);
+        } else if (turns) {
+          mbar_arrive(&sh.turn[m ^ 1]);
         }
-        scores(ahead);
       }
       ++segments;
     }
