@@ -10,7 +10,7 @@ int64_t tree_attention_workspace_bytes(int B, int nodes, int heads, int kv_heads
   const int rows = nodes * (heads / kv_heads), cta_rows = attn::stream_rows(rows, head_dim);
   const int64_t streaming = attn::workspace_bytes(attn::part_rows(rows, cta_rows), head_dim,
                                                   attn::stream_ctas(head_dim, cta_rows));
-  if (rows <= (head_dim == 256 ? attn::kFewRows256 : attn::kFewRows)) return streaming;
+  if (rows <= attn::few_rows(head_dim)) return streaming;
   const bool pair = head_dim != 256 && rows <= 128;
   const int64_t wide =
       attn::workspace_bytes(attn::part_rows(rows, head_dim == 256 || pair ? 128 : 256), head_dim,
@@ -55,7 +55,7 @@ cudaError_t launch_tree_attention(const void* q, int dtype, int64_t q_req, int64
   p.status = status;
   p.workspace = static_cast<char*>(workspace);
   p.row_tiles = 1;
-  p.max_ctas = p.tile = p.item_cost = p.part_rows = 0;
+  p.max_ctas = p.tile = p.item_cost = p.part_rows = p.part_wide = 0;
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);

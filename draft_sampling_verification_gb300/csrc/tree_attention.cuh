@@ -34,6 +34,7 @@ struct Params {
   int item_cost;  // an item's start and end, in tiles
   int row_tiles;  // tiles of an item's rows: ceil(nodes * group / rows per CTA)
   int part_rows;  // rows of a partial result in the workspace
+  int part_wide;  // elements of a row that lie together there, a power of two
 };
 
 // ------------------------------------------------------------ PTX wrappers
@@ -141,7 +142,7 @@ __device__ __forceinline__ uint32_t without_special(uint32_t w) {
 // two CTAs here.)
 // A range is at least kMinRange long: the join of more parts costs more than they save.
 constexpr int kMinRange = 3;
-constexpr int kStreamCost = 5, kPairCost = 2, kBothCost = 5, kOneCost = 1;
+constexpr int kStreamCost = 5, kPairCost = 2, kBothCost = 8, kOneCost = 1;
 
 struct Start {  // where a team's range begins: `at` into the item, of item_cost + tiles
   int b, head, at, tiles;
@@ -157,7 +158,7 @@ struct Seam {
 struct Workspace {
   Seam* seam;     // [ctas], by team
   float2* stats;  // [2 * ctas][rows]: the reference of the exponents, the sum
-  float* rows;    // [2 * ctas][rows][dim]
+  float* rows;    // [2 * ctas][dim / wide][rows][wide]
 };
 
 __host__ __device__ inline int64_t workspace_bytes(int rows, int dim, int ctas) {
@@ -172,6 +173,15 @@ __device__ __forceinline__ Workspace carve(char* w, int rows, int ctas) {
   s.stats = reinterpret_cast<float2*>(w + ctas * sizeof(Seam));
   s.rows = reinterpret_cast<float*>(s.stats + 2 * ctas * rows);
   return s;
+}
+
+// Element d of partial row r of the result whose first row is `slot`.  A row
+// lies in one piece where lanes write along it; in pieces of 8 (32 bytes)
+// where a warp has a row a lane and many rows, so that it writes whole lines
+// (wide trees 148 -> 146 us; elsewhere the joins' reads lose 1 %).
+__device__ __forceinline__ float* part_at(const Workspace& ws, int64_t slot, int rows, int wide,
+                                          int r, int dim, int d) {
+  return ws.rows + slot * dim + ((int64_t)(d / wide) * rows + r) * wide + d % wide;
 }
 
 // a request's tokens: the cached text, and all with its nodes (0 when refused)
@@ -712,7 +722,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, N8, MW>::kCtas)
           p.lse[to] = j.y == 0.0f ? -INFINITY : (j.x + log2f(j.y)) * 0.6931471805599453f;
         }
       } else {
-        *reinterpret_cast<float4*>(ws.rows + (slot + r) * D + d) = a;
+        *reinterpret_cast<float4*>(part_at(ws, slot, p.part_rows, D, r, D, d)) = a;
         if (d == 0) ws.stats[slot + r] = s_joined[r];
       }
     }
@@ -742,13 +752,17 @@ __global__ void __launch_bounds__(kJoinThreads)
   const int r = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5);
   const int row = blockIdx.z * rows + r;
   if (r >= rows || row >= p.nodes * p.group) return;
-  // the partial row of team c: its first range's in slot 0, its last's in slot 1
+  // the first partial row of team c: its first range's in slot 0, its last's in slot 1
   auto part_of = [&](int c) -> int64_t {
-    return (2ll * (c * p.row_tiles + blockIdx.z) + (c == c0 ? 1 : 0)) * p.part_rows + r;
+    return (2ll * (c * p.row_tiles + blockIdx.z) + (c == c0 ? 1 : 0)) * p.part_rows;
   };
 
+  // part_at, with the width's division as a shift
+  const int shift = 31 - __clz(p.part_wide), d0 = lane * kPer;
+  const int offset =
+      ((((d0 >> shift) * p.part_rows) + r) << shift) + (d0 & (p.part_wide - 1));
   float top = -INFINITY;
-  for (int c = c0 + lane; c <= c1; c += 32) top = fmaxf(top, ws.stats[part_of(c)].x);
+  for (int c = c0 + lane; c <= c1; c += 32) top = fmaxf(top, ws.stats[part_of(c) + r].x);
   top = warp_reduce(top, OpMaxF());
   const float safe = top == -INFINITY ? 0.0f : top;
   float all = 0.0f, a[kPer];
@@ -756,8 +770,8 @@ __global__ void __launch_bounds__(kJoinThreads)
   for (int d = 0; d < kPer; ++d) a[d] = 0.0f;
 #pragma unroll kAhead
   for (int c = c0; c <= c1; ++c) {
-    const float2 st = ws.stats[part_of(c)];
-    const float* v = ws.rows + part_of(c) * D + lane * kPer;
+    const float2 st = ws.stats[part_of(c) + r];
+    const float* v = ws.rows + part_of(c) * D + offset;
     float x[kPer];
     if constexpr (kPer == 2) {
       *reinterpret_cast<float2*>(x) = *reinterpret_cast<const float2*>(v);
@@ -813,8 +827,11 @@ inline int stream_rows(int rows, int dim) {
   if (dim == 256) return rows <= 8 ? 8 : rows <= 16 ? 16 : 64;
   return rows <= 24 ? (rows + 7) / 8 * 8 : rows <= 32 ? 32 : 64;
 }
-// rows up to which the streaming kernel is taken, at head_dim 64 and 128, and 256
-constexpr int kFewRows = 16, kFewRows256 = 8;
+// Rows up to which the streaming kernel is taken (256 items of 4,000 tokens / 4,096 of 60, us,
+// against the tensor kernel).  head_dim 64: 16 rows 52 / 38 against 60 / 69, 24 rows 66 / 81
+// against 61 / 75.  128: 8 rows 88 / 62 against 92 / 62, 16 rows 91 / 83 against 93 / 63.  256:
+// 1 row 185 / 120 against 163 / 135, 8 rows 187 / 159 against 166 / 142.
+constexpr int few_rows(int dim) { return dim == 64 ? 16 : dim == 128 ? 8 : 0; }
 // the workspace's ranges, by kernel (160 SMs at most are used), and the rows of
 // each: those that the item has, of a CTA's
 inline int stream_ctas(int dim, int rows) {
@@ -834,6 +851,7 @@ cudaError_t launch_shape(Params p, int sms, cudaStream_t stream) {
                                        S::kSmem);
   if (e != cudaSuccess) return e;
   p.part_rows = part_rows(p.nodes * p.group, S::kRows);
+  p.part_wide = D;
   p.max_ctas = stream_ctas(D, S::kRows);
   p.item_cost = kStreamCost;
   p.tile = S::kTile;

@@ -171,6 +171,7 @@ struct Wide {
   static constexpr int kHalves = D / 64;
   static constexpr int kQBytes = 128 * D * 2, kTileBytes = kKeys * D * 2;
   static constexpr int kStages = kMode == kBoth ? 4 : 2;
+  static constexpr int kPartWide = kMode == kBoth ? 8 : D;  // of a partial row, in one piece
   static constexpr int kRing = 2 * kStages * kTileBytes;    // keys, then values
   static constexpr int kSmem = kRowTiles * kQBytes + kStreams * kRing + 1024;
 };
@@ -219,6 +220,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   const uint32_t k_group = boxes.k_whole ? kHalves * 1024u : 1024u;
   const uint32_t k_half = boxes.k_whole ? 1024u : kKeys * 128u;
   const uint32_t v_half = boxes.v_rows * 128u, v_box = kHalves * v_half;
+  const int v_shift = 31 - __clz(boxes.v_rows);  // a power of two, as k_rows is
 
   if (tid == 0) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(&k_map) : "memory");
@@ -480,24 +482,32 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           const int from = max(0, len.ctx - pos);
           // blocks' rows that the last copy brought; zeros behind them
           const int end =
-              min(kKeys, (len.len - pos + boxes.v_rows - 1) / boxes.v_rows * boxes.v_rows);
-          for (int j = t; j < (end - from) * kChunks; j += 128) {
-            const int r = from + j / kChunks, c = j % kChunks;
-            const uint32_t addr = v_at + r / boxes.v_rows * v_box + (c >> 3) * v_half +
-                                  r % boxes.v_rows * 128 + (((c & 7) ^ (r & 7)) << 4);
-            uint32_t w[4];
-            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                         : "r"(addr)
-                         : "memory");
-            if (any_special<T>(w[0]) || any_special<T>(w[1]) || any_special<T>(w[2]) ||
-                any_special<T>(w[3])) {
-              asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr),
-                           "r"(without_special<T>(w[0])), "r"(without_special<T>(w[1])),
-                           "r"(without_special<T>(w[2])), "r"(without_special<T>(w[3]))
+              min(kKeys, (len.len - pos + boxes.v_rows - 1) & -boxes.v_rows);
+          const int n = (end - from) * kChunks;
+          constexpr int kAtOnce = 4;
+          for (int j0 = t; j0 < n; j0 += 128 * kAtOnce) {
+            uint32_t addr[kAtOnce], w[kAtOnce][4];
+#pragma unroll
+            for (int u = 0; u < kAtOnce; ++u) {
+              const int j = min(j0 + u * 128, n - 1), r = from + j / kChunks, c = j % kChunks;
+              addr[u] = v_at + (r >> v_shift) * v_box + (c >> 3) * v_half +
+                        (r & (boxes.v_rows - 1)) * 128 + (((c & 7) ^ (r & 7)) << 4);
+              asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                           : "=r"(w[u][0]), "=r"(w[u][1]), "=r"(w[u][2]), "=r"(w[u][3])
+                           : "r"(addr[u])
                            : "memory");
-              if (pos + r < len.len) *(volatile uint32_t*)&stream.special[tile_no & 7u] = 1u;
             }
+#pragma unroll
+            for (int u = 0; u < kAtOnce; ++u)
+              if (j0 + u * 128 < n && (any_special<T>(w[u][0]) || any_special<T>(w[u][1]) ||
+                                       any_special<T>(w[u][2]) || any_special<T>(w[u][3]))) {
+                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr[u]),
+                             "r"(without_special<T>(w[u][0])), "r"(without_special<T>(w[u][1])),
+                             "r"(without_special<T>(w[u][2])), "r"(without_special<T>(w[u][3]))
+                             : "memory");
+                if (pos + from + (j0 + u * 128) / kChunks < len.len)
+                  *(volatile uint32_t*)&stream.special[tile_no & 7u] = 1u;
+              }
           }
           __syncwarp();
           fence_async_shared();
@@ -524,8 +534,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       }
       const bool full = cur.whole();
       const int64_t to = (int64_t)cur.b * p.nodes * p.heads + cur.head * p.group + my_row;
-      const int64_t slot = cur.slot(kPaired ? 2 * blockIdx.x + x : blockIdx.x) * p.part_rows +
-                           (kPaired ? 0 : m * 128) + t;
+      const int64_t slot = cur.slot(kPaired ? 2 * blockIdx.x + x : blockIdx.x) * p.part_rows;
+      const int part_row = (kPaired ? 0 : m * 128) + t;
       const float inv = sum == 0.0f ? 0.0f : full ? 1.0f / sum : 1.0f;
       const int chunks = m_rows + (t & ~31) < p.nodes * p.group ? D / 32 : 0;  // of the warp
 #pragma unroll 1
@@ -564,11 +574,11 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                                 H::pack(v[8 * j + 4] * inv, v[8 * j + 5] * inv),
                                 H::pack(v[8 * j + 6] * inv, v[8 * j + 7] * inv));
         } else if (mine) {
-          // whole 32-byte sectors: a warp's rows lie far apart
-          float* out = ws.rows + slot * D + c * 32;
+          constexpr int kWide = W::kPartWide;
+          float* out = part_at(ws, slot, p.part_rows, kWide, part_row, D, c * 32);
 #pragma unroll
           for (int j = 0; j < 32; j += 8)
-            asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(out + j),
+            asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(out + j / kWide * (p.part_rows * kWide) + j % kWide),
                          "f"(v[j]), "f"(v[j + 1]), "f"(v[j + 2]), "f"(v[j + 3]), "f"(v[j + 4]),
                          "f"(v[j + 5]), "f"(v[j + 6]), "f"(v[j + 7])
                          : "memory");
@@ -577,7 +587,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       }
       if (mine) {
         if (!full)
-          ws.stats[slot] = make_float2(ref, sum);
+          ws.stats[slot + part_row] = make_float2(ref, sum);
         else if (p.lse)
           p.lse[to] = sum == 0.0f ? -INFINITY : (ref + log2f(sum)) * 0.6931471805599453f;
       }
@@ -849,6 +859,7 @@ bool launch_wide(Params p, int sms, cudaStream_t stream, cudaError_t* error) {
     return false;
   p.row_tiles = (p.nodes * p.group + W::kRows - 1) / W::kRows;
   p.part_rows = part_rows(p.nodes * p.group, W::kRows);
+  p.part_wide = W::kPartWide;
   p.max_ctas = wide_ctas(kMode == kPair);
   p.tile = W::kKeys;
   p.item_cost = kMode == kPair ? kPairCost : kMode == kBoth ? kBothCost : kOneCost;
@@ -871,14 +882,14 @@ cudaError_t launch_dim(const Params& p, int sms, cudaStream_t stream) {
   const int rows = p.nodes * p.group, shape = stream_rows(rows, D);
   cudaError_t e;
   if constexpr (D == 256) {
-    if (rows > kFewRows256 && launch_wide<T, D, kOne>(p, sms, stream, &e)) return e;
+    if (launch_wide<T, D, kOne>(p, sms, stream, &e)) return e;
     if (shape == 8) return launch_shape<T, D, 1, 1>(p, sms, stream);
     if (shape == 16) return launch_shape<T, D, 2, 1>(p, sms, stream);
     return launch_shape<T, D, 2, 4>(p, sms, stream);
   } else {
     if (rows > 128) {
       if (launch_wide<T, D, kBoth>(p, sms, stream, &e)) return e;
-    } else if (rows > kFewRows) {
+    } else if (rows > few_rows(D)) {
       if (launch_wide<T, D, kPair>(p, sms, stream, &e)) return e;
     }
     if (shape == 8) return launch_shape<T, D, 1, 1>(p, sms, stream);
