@@ -828,8 +828,8 @@ inline int stream_rows(int rows, int dim) {
   return rows <= 24 ? (rows + 7) / 8 * 8 : rows <= 32 ? 32 : 64;
 }
 // Rows up to which the streaming kernel is taken (256 items of 4,000 tokens / 4,096 of 60, us,
-// against the tensor kernel).  head_dim 64: 16 rows 52 / 38 against 60 / 69, 24 rows 66 / 81
-// against 61 / 75.  128: 8 rows 88 / 62 against 92 / 62, 16 rows 91 / 83 against 93 / 63.  256:
+// against the tensor kernel).  head_dim 64: 16 rows 55 / 38 against 59 / 50, 24 rows 67 / 81
+// against 60 / 73.  128: 8 rows 88 / 62 against 92 / 62, 16 rows 91 / 83 against 93 / 63.  256:
 // 1 row 185 / 120 against 163 / 135, 8 rows 187 / 159 against 166 / 142.
 constexpr int few_rows(int dim) { return dim == 64 ? 16 : dim == 128 ? 8 : 0; }
 // the workspace's ranges, by kernel (160 SMs at most are used), and the rows of

@@ -119,32 +119,32 @@ __device__ __forceinline__ void tmem_wait_store() {
 }
 
 // ------------------------------------------------------------ the kernel
-// S = Q K^T into tensor memory for a tile of 128 rows and kKeys positions,
+// S = Q K^T into tensor memory for a tile of 128 rows and 64 positions,
 // softmax by the warpgroup that owns the row tile (a thread per row, so no
 // exchange between threads), the weights back into tensor memory over the
-// scores, O += P V.  Two warpgroups take turns at the tensor cores: while one
-// is in its softmax the products of the other run.
+// scores, O += P V.  The scores of two tiles are held for each row tile, so
+// that the products of the next tile run during a softmax, and two warpgroups
+// share the tensor cores.  (With tiles of 128 positions, whose scores fill
+// the place of two, a row tile's products and softmax wait for one another:
+// 1,024 one-row-tile items of 300 tokens 105 us instead of 86, wide trees 165
+// instead of 146; head_dim 64, 2,048 items of 300 tokens 82 instead of 60.)
 //
 // kPair: items of up to 128 rows.  The warpgroups go along two ranges of the
 //   tile axis, each with its own queries and its own copies of keys and
 //   values: two CTAs in one, of which one's starts and results are hidden
 //   behind the other's products.  Bound by HBM: 256 items of 4,000 tokens
-//   take 101 us with 24 rows, 118 us with 128 (5.2 and 4.5 TB/s), two
-//   requests of 131,000 tokens 168 us (6.1 TB/s).
+//   take 96 us with 24 rows, 114 us with 128 (5.5 and 4.8 TB/s), two
+//   requests of 131,000 tokens 175 us (6.1 TB/s).
 // kBoth: items of more rows.  The warpgroups take two row tiles of one item
-//   and share its keys and values.  Bound by the products (2 * 2 * 128 * 128 *
-//   D operations a row tile and tile of positions): 16 requests with trees of
-//   64 nodes and 8 query heads to a cached head take 159 us, 1.0 PFLOP/s.
+//   and share its keys and values.  Bound by the products (2 * 2 * 128 * 64 *
+//   D operations a row tile and tile of positions) and by their issue: 256
+//   items of 4,000 tokens and 512 rows take 207 us, 1.3 PFLOP/s; 16 requests
+//   with trees of 64 nodes and 8 query heads to a cached head 146 us.  A row
+//   tile's twelve products take 640 cycles, as the scores' operands come at
+//   the rate of shared memory; the two row tiles' take 1,450 in the loop.
 // kOne: head_dim 256, whose accumulators fill half the tensor memory: one
-//   warpgroup, one row tile, 64 positions at a time.  256 items of 4,000
-//   tokens take 198 us with 24 rows (5.3 TB/s).
-//
-// kPair and kOne take 64 positions at a time and keep the scores of two tiles
-// in tensor memory, so that the next tile's products run during a softmax
-// (1,024 one-row-tile items of 300 tokens: 86 us, with tiles of 128 and their
-// scores alone 105).  At head_dim 64 a tile of 64 is too little work for its
-// softmax's latency, and under kBoth the other row tile's products run: a tile
-// has 128 positions.
+//   warpgroup and one row tile.  256 items of 4,000 tokens take 173 us with
+//   24 rows (6.2 TB/s).
 //
 // A score that passes the row's reference by more than 8 has the accumulators
 // rescaled by the softmax warpgroup, once the products before are done; this
@@ -158,19 +158,18 @@ __device__ __forceinline__ void tmem_wait_store() {
 // the major axis.
 enum WideMode { kPair, kBoth, kOne };
 
-constexpr int kWideThreads = 384;  // 168 registers a thread: a row's 128 scores and more
+constexpr int kWideThreads = 384;  // 168 registers a thread: a row's 64 scores, 64 of Q, and more
 
 template <int D, WideMode kMode>
 struct Wide {
   static constexpr int kStreams = kMode == kPair ? 2 : 1;   // ranges of the tile axis
   static constexpr int kRowTiles = kMode == kOne ? 1 : 2;   // of 128 rows, over all streams
   static constexpr int kRows = kMode == kBoth ? 256 : 128;  // of an item, per CTA
-  // positions of a tile, and the tiles whose scores are held
-  static constexpr int kKeys = kMode == kPair && D == 64 ? 128 : 64;
-  static constexpr int kScores = kKeys == 128 ? 1 : 2;
+  static constexpr int kKeys = 64;   // positions of a tile
+  static constexpr int kScores = 2;  // tiles whose scores are held
   static constexpr int kHalves = D / 64;
   static constexpr int kQBytes = 128 * D * 2, kTileBytes = kKeys * D * 2;
-  static constexpr int kStages = kMode == kBoth ? 4 : 2;
+  static constexpr int kStages = kMode == kBoth || D == 64 ? 4 : 2;
   static constexpr int kPartWide = kMode == kBoth ? 8 : D;  // of a partial row, in one piece
   static constexpr int kRing = 2 * kStages * kTileBytes;    // keys, then values
   static constexpr int kSmem = kRowTiles * kQBytes + kStreams * kRing + 1024;
@@ -188,7 +187,7 @@ struct Boxes {
 struct WideStream {
   uint64_t k_full[kWideMaxStages], k_empty[kWideMaxStages];
   uint64_t v_full[kWideMaxStages], v_empty[kWideMaxStages];
-  uint32_t valid[8][4];  // a tile's positions that hold a key, by tile number modulo 8
+  uint32_t valid[8][2];  // a tile's positions that hold a key, by tile number modulo 8
   uint32_t special[8];   // a value of a tile's nodes is an infinity or a NaN
 };
 struct WideShared {
@@ -875,7 +874,7 @@ bool launch_wide(Params p, int sms, cudaStream_t stream, cudaError_t* error) {
 }
 
 // The streaming kernel for few rows, whose products need no tensor memory and
-// whose two CTAs per SM hide one another's starts, and for blocks that have no
+// whose two to four CTAs per SM hide one another's starts, and for blocks that have no
 // tensor copies; else the tensor kernel.
 template <typename T, int D>
 cudaError_t launch_dim(const Params& p, int sms, cudaStream_t stream) {
