@@ -141,7 +141,7 @@ __device__ __forceinline__ void tmem_wait_store() {
 //   items of 4,000 tokens and 512 rows take 207 us, 1.3 PFLOP/s; 16 requests
 //   with trees of 64 nodes and 8 query heads to a cached head 146 us.  A row
 //   tile's twelve products take 640 cycles, as the scores' operands come at
-//   the rate of shared memory; the two row tiles' take 1,450 in the loop.
+//   the rate of shared memory; the two row tiles' take 1,550 in the loop.
 // kOne: head_dim 256, whose accumulators fill half the tensor memory: one
 //   warpgroup and one row tile.  256 items of 4,000 tokens take 173 us with
 //   24 rows (6.2 TB/s).
