@@ -14,6 +14,8 @@
 // us (5.5 TB/s), one request of six rows 5 us.
 #include <cuda_bf16.h>
 
+#include <type_traits>
+
 #define DSPARK_TU 11  // this file's number in the checked build's site codes
 #include "common.cuh"
 
@@ -29,6 +31,8 @@ constexpr uint32_t kCountBits = 0x00FFFFFFu;  // occurrences in the generated te
 constexpr uint32_t kListed = 1u << 31;        // on the list of touched tokens
 constexpr uint32_t kPrompt = 1u << 30;        // occurs in the prompt
 constexpr uint32_t kDrafted = 1u << 29;       // equals one of the drafts
+constexpr uint32_t kRepeated = 1u << 28;      // more than one bias
+constexpr uint32_t kOwner = 0x1FFFFu;         // 65536 - list place of a token's first bias
 
 struct LParams {
   const void* x;
@@ -174,7 +178,7 @@ __global__ void __launch_bounds__(kLThreads, 2) logits_process_kernel(const LPar
   float* bias = reinterpret_cast<float*>(table + p.slice);           // [bias_cap], by list place
   uint16_t* list = reinterpret_cast<uint16_t*>(bias + p.bias_cap);   // [list_cap] touched tokens
   __shared__ int32_t s_draft[DSPARK_MAX_NODES];
-  __shared__ uint32_t s_count, s_biased, s_twice;
+  __shared__ uint32_t s_count, s_biased, s_repeated;
   __shared__ RowPart<T> s_part[DSPARK_MAX_NODES];
   const int tid = threadIdx.x;
   const int b = blockIdx.y;
@@ -222,8 +226,13 @@ __global__ void __launch_bounds__(kLThreads, 2) logits_process_kernel(const LPar
     part.seen = p.row_mask ? p.row_mask[row] : (1ull << (r0 + tid)) - 1ull;
     s_part[tid] = part;
   }
-  if (tid == 0) s_count = s_biased = s_twice = 0u;
+  if (tid == 0) s_count = s_biased = s_repeated = 0u;
   __syncthreads();
+  auto count_biases = [&]() -> int {
+    return p.max_bias > 0 ? max(0, min(p.max_bias, p.n_bias ? p.n_bias[b] : p.max_bias)) : 0;
+  };
+  const int32_t* bias_ids = p.bias_ids + (int64_t)b * p.max_bias;
+  const float* bias_values = p.bias_values + (int64_t)b * p.max_bias;
   // the slice's touched tokens: their counts, and the list of them
   auto count_text = [&](int t0) {
     for (int i = t0; i < p.slice / 4; i += kTextThreads)
@@ -231,35 +240,33 @@ __global__ void __launch_bounds__(kLThreads, 2) logits_process_kernel(const LPar
     if (t0 < p.n_drafts) s_draft[t0] = p.drafts[(int64_t)b * p.n_drafts + t0];
     text_sync();
 
-    // the slice's biases: the first entry of an id owns it and adds up the
-    // later ones in list order; owners come first on the list
-    int n_bias = 0;
-    if (p.max_bias > 0) n_bias = max(0, min(p.max_bias, p.n_bias ? p.n_bias[b] : p.max_bias));
+    // the slice's biases: the first entry of an id owns it, later ones mark
+    // it as repeated; owners come first on the list
+    const int n_bias = count_biases();
     if (n_bias > 0) {
-      const int32_t* ids = p.bias_ids + (int64_t)b * p.max_bias;
-      const float* values = p.bias_values + (int64_t)b * p.max_bias;
       for (int i = t0; i < n_bias; i += kTextThreads) {
-        const uint32_t t = (uint32_t)(ids[i] - v0);
-        if (t < (uint32_t)n && atomicMax(&table[t], 65536u - (uint32_t)i) != 0u) s_twice = 1u;
+        const uint32_t t = (uint32_t)(bias_ids[i] - v0);
+        if (t < (uint32_t)n) atomicMax(&table[t], 65536u - (uint32_t)i);
       }
       text_sync();
-      const bool twice = s_twice != 0u;
       for (int i = t0; i < n_bias; i += kTextThreads) {
-        const uint32_t t = (uint32_t)(ids[i] - v0);
-        if (t >= (uint32_t)n || table[t] != 65536u - (uint32_t)i) continue;
-        float sum = values[i];
-        if (twice)
-          for (int k = i + 1; k < n_bias; ++k)
-            if (ids[k] == ids[i]) sum = __fadd_rn(sum, values[k]);
+        const uint32_t t = (uint32_t)(bias_ids[i] - v0);
+        if (t >= (uint32_t)n) continue;
+        if ((*(volatile uint32_t*)&table[t] & kOwner) != 65536u - (uint32_t)i) {
+          atomicOr(&table[t], kRepeated);
+          s_repeated = 1u;
+          continue;
+        }
         const uint32_t at = atomicAdd(&s_count, 1u);
         if (DSPARK_CHECK(at < (uint32_t)p.bias_cap)) {
           list[at] = (uint16_t)t;
-          bias[at] = sum;
+          bias[at] = bias_values[i];
         }
       }
       text_sync();
       if (t0 == 0) s_biased = s_count;
-      for (int i = t0; i < (int)s_count; i += kTextThreads) table[list[i]] = kListed;
+      for (int i = t0; i < (int)s_count; i += kTextThreads)
+        table[list[i]] = kListed | (table[list[i]] & kRepeated);
       text_sync();
     }
 
@@ -318,14 +325,15 @@ __global__ void __launch_bounds__(kLThreads, 2) logits_process_kernel(const LPar
   __syncthreads();
   const int touched = (int)s_count, n_biased = (int)s_biased;
 
-  // each touched token of each row, from its input
-#pragma unroll 2
-  for (int k = tid; k < touched * rows; k += kLThreads) {
+  // a touched token of a row, from its input; those with more than one bias apart, as the search
+  // for the others in the list keeps the compiler from overlapping two tokens
+  auto touch = [&](int k, auto repeated) {
     const int r = k / touched, i = k - r * touched;
     const RowPart<T>& part = s_part[r];
     const int t = list[i];
-    if (part.words && !((__ldg(part.words + (t >> 5)) >> (t & 31)) & 1u)) continue;
+    if (part.words && !((__ldg(part.words + (t >> 5)) >> (t & 31)) & 1u)) return;
     const uint32_t w = table[t];
+    if (decltype(repeated)::value != ((w & kRepeated) != 0u)) return;
     uint32_t c = w & kCountBits;
     if (w & kDrafted)
       for (int j = 0; j < p.n_drafts; ++j)
@@ -335,8 +343,21 @@ __global__ void __launch_bounds__(kLThreads, 2) logits_process_kernel(const LPar
     y = __fsub_rn(y, __fmul_rn(F, (float)c));
     if (c > 0u) y = __fsub_rn(y, P);
     if (i < n_biased) y = __fadd_rn(y, bias[i]);
+    if constexpr (decltype(repeated)::value) {  // its later biases, one addition each
+      bool first = true;
+      for (int e = 0, n_bias = count_biases(); e < n_bias; ++e) {
+        if (bias_ids[e] != v0 + t) continue;
+        if (!first) y = __fadd_rn(y, bias_values[e]);
+        first = false;
+      }
+    }
     part.out[t] = narrow<T>(y);
-  }
+  };
+#pragma unroll 2
+  for (int k = tid; k < touched * rows; k += kLThreads) touch(k, std::false_type());
+  if (s_repeated)
+    for (int k = tid; k < n_biased * rows; k += kLThreads)
+      touch(k / n_biased * touched + k % n_biased, std::true_type());
 }
 
 cudaError_t launch_logits_process(
