@@ -76,6 +76,20 @@ def _dtype_code(t):
     raise TypeError("logits must be float32 or bfloat16, got %s" % t.dtype)
 
 
+def _uniform(t, dims, what):
+    """(count, step) of what lies along t's first `dims` dimensions: one after the other, `step`
+    apart (0 for one alone).  A dimension of one element may have any stride."""
+    shape, strides, n, step = t.shape, t.stride(), 1, 0
+    for i in range(dims - 1, -1, -1):
+        if shape[i] > 1:
+            if n == 1:
+                step = strides[i]
+            elif n and strides[i] != step * n:
+                raise ValueError("%s must be uniformly strided" % what)
+        n *= shape[i]
+    return n, step
+
+
 def _rows(t):
     """(rows, V, ld) of a logit tensor whose rows are uniformly strided."""
     if t.dim() >= 2 and t.is_contiguous() and t.shape[-1] > 0:
@@ -84,17 +98,8 @@ def _rows(t):
     if t.dim() < 2 or t.stride(-1) != 1:
         raise ValueError("logit rows must be contiguous in their last dimension")
     V = t.shape[-1]
-    ld = t.stride(-2)
-    rows = 1
-    for i in range(t.dim() - 1):
-        rows *= t.shape[i]
-    # leading dimensions must be a plain multiple of the row stride
-    expect = ld
-    for i in range(t.dim() - 2, -1, -1):
-        if t.shape[i] > 1 and t.stride(i) != expect:
-            raise ValueError("logit rows must be uniformly strided")
-        expect *= t.shape[i]
-    return rows, V, ld
+    rows, ld = _uniform(t, t.dim() - 1, "logit rows")
+    return rows, V, ld if rows > 1 else V
 
 
 def _i32(t):
@@ -389,29 +394,27 @@ def _cache_plan(ctx_len, new_len, max_new, page_size, block_table, free_blocks, 
 
 
 def dspark_kv_write(k, v, k_cache, v_cache, slots, rows=None, stream=None):
-    """k, v [.., n_heads, head_dim] (leading dimensions uniformly strided; the same shape and
-    strides), float32 or the caches' type; k_cache, v_cache [n_blocks, page_size, n_heads,
-    head_dim]; slots int32 of n_tokens; rows int32 of n_tokens or None (then n_tokens is the
-    number of source tokens)."""
+    """k, v [.., n_heads, head_dim] (tokens uniformly strided; the same shape and strides), float32
+    or the caches' type; k_cache, v_cache [n_blocks, page_size, n_heads, head_dim]; slots int32 of
+    n_tokens; rows int32 of n_tokens or None (then n_tokens is the number of source tokens)."""
     code, kp, vp, sb, st, sh = _cache_args(k_cache, v_cache)
-    if k.dim() < 3 or v.shape != k.shape or v.stride() != k.stride() or k.stride(-1) != 1:
-        raise ValueError("k and v must have the same shape [.., n_heads, head_dim] and strides, "
-                         "contiguous in head_dim")
+    if k.dim() < 3 or v.shape != k.shape or k.stride(-1) != 1 or v.stride(-1) != 1:
+        raise ValueError("k and v must have the same shape [.., n_heads, head_dim], contiguous in "
+                         "head_dim")
     if k.shape[-2:] != k_cache.shape[-2:]:
         raise ValueError("k and v must have the caches' heads and head_dim")
     if v.dtype is not k.dtype or (k.dtype is not torch.float32 and k.dtype is not k_cache.dtype):
         raise TypeError("k and v must be float32 or of the caches' type")
-    n, step = 1, k.stride(-3)
-    for i in range(k.dim() - 3, -1, -1):
-        if k.shape[i] > 1 and k.stride(i) != step * n:
-            raise ValueError("the tokens of k and v must be uniformly strided")
-        n *= k.shape[i]
+    if v.stride() != k.stride() and any(
+            a != b and size > 1 for a, b, size in zip(k.stride(), v.stride(), k.shape)):
+        raise ValueError("k and v must have the same strides")
+    n, step = _uniform(k, k.dim() - 2, "the tokens of k and v")
     if not (k.is_cuda and v.is_cuda):
         raise ValueError("expected a CUDA tensor")
     if rows is None and slots.numel() != n:
         raise ValueError("slots must hold one slot for each token")
     _call("dspark_kv_write", k.data_ptr(), v.data_ptr(),
-          F32 if k.dtype is torch.float32 else code, step if n > 1 else 0, k.stride(-2), n,
+          F32 if k.dtype is torch.float32 else code, step, k.stride(-2) if k.shape[-2] > 1 else 0, n,
           k.shape[-2], k.shape[-1], kp, vp, code, sb, st, sh, k_cache.shape[0], k_cache.shape[1],
           _arg("slots", slots, torch.int32, slots.shape),
           _arg("rows", rows, torch.int32, slots.shape), slots.numel(), _stream(stream))
