@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import inspect
 
 import torch
 
@@ -503,10 +504,28 @@ def dspark_logits_process(logits, history, prompt_len, history_len, draft_tokens
 
 
 # --------------------------------------------------- allocating helpers
+def _on_stream(helper):
+    """Runs an allocating helper with its `stream` as torch's current one, so that outputs and
+    workspaces are that stream's memory: of another stream's they could be given to its next
+    tensor while the kernels that write them are still to come."""
+    at = list(inspect.signature(helper).parameters).index("stream")
+
+    @functools.wraps(helper)
+    def call(*args, **kw):
+        stream = args[at] if len(args) > at else kw.get("stream")
+        if stream is None:
+            return helper(*args, **kw)
+        with torch.cuda.stream(stream):
+            return helper(*args, **kw)
+
+    return call
+
+
 def _empty(shape, dtype, device):
     return torch.empty(shape, dtype=dtype, device=device)
 
 
+@_on_stream
 def q_build(draft_logits, temperature=None, top_k=0, stream=None):
     """draft_logits [..., V]; returns dict(counts, ids, nnz, status) (rows flattened)."""
     rows, V, _ = _rows(draft_logits)
@@ -523,6 +542,7 @@ def q_build(draft_logits, temperature=None, top_k=0, stream=None):
     return {"counts": counts, "ids": ids, "nnz": nnz, "status": status, "top_k": top_k}
 
 
+@_on_stream
 def q_build_sample(draft_logits, B, depth, seed, temperature=None, top_k=0, request_ids=None,
                    stream=None):
     """Fused q build + draft draw; returns (q dict, tokens [B, depth])."""
@@ -542,6 +562,7 @@ def q_build_sample(draft_logits, B, depth, seed, temperature=None, top_k=0, requ
     return {"counts": counts, "ids": ids, "nnz": nnz, "status": status, "top_k": top_k}, tokens
 
 
+@_on_stream
 def spec_step(draft_logits, target_logits, B, depth, seed, temperature=None, request_ids=None,
               modes=("greedy", "ratio"), stream=None, schedule=0):
     """Fused q build + draft draw + verification (dense q).  Returns (q dict,
@@ -565,6 +586,7 @@ def spec_step(draft_logits, target_logits, B, depth, seed, temperature=None, req
     return q, tokens, outs
 
 
+@_on_stream
 def verify_match(target_logits, draft_tokens, seed, request_ids=None, stream=None):
     """Stochastic verification; returns (accept_len, committed, flags, status)."""
     B, depth = draft_tokens.shape
@@ -578,6 +600,7 @@ def verify_match(target_logits, draft_tokens, seed, request_ids=None, stream=Non
     return acc, com, fl, st
 
 
+@_on_stream
 def q_chain_sample(draft_logits, B, depth, seed, anchors, bias=None, temperature=None,
                    request_ids=None, stream=None):
     """The Markov-conditioned draft chain; returns (q dict, tokens [B, depth],
@@ -594,6 +617,7 @@ def q_chain_sample(draft_logits, B, depth, seed, anchors, bias=None, temperature
     return q, tokens, margins
 
 
+@_on_stream
 def q_build_sample_sharded(draft_logits, B, depth, n_shards, seed, temperature=None, top_k=0,
                            request_ids=None, stream=None):
     """The vocabulary-sharded emulation of q_build_sample."""
@@ -614,6 +638,7 @@ def q_build_sample_sharded(draft_logits, B, depth, n_shards, seed, temperature=N
     return {"counts": counts, "ids": ids, "nnz": nnz, "status": status, "top_k": top_k}, tokens
 
 
+@_on_stream
 def q_pack(q, V, stream=None):
     """Wire form of a q dict from q_build: (q float32 of the counts' shape,
     checksums int64 [n_rows] holding the uint64 bit patterns)."""
@@ -624,6 +649,7 @@ def q_pack(q, V, stream=None):
     return qf, cs
 
 
+@_on_stream
 def q_validate(qf, V, ids=None, nnz=None, top_k=0, tokens=None, expect=None, stream=None):
     """Validation of received q rows: (status int32 [n_rows], recovered counts
     int32 of qf's shape)."""
@@ -633,6 +659,7 @@ def q_validate(qf, V, ids=None, nnz=None, top_k=0, tokens=None, expect=None, str
     return st, counts
 
 
+@_on_stream
 def draft_sample(q, B, depth, V, seed, request_ids=None, stream=None):
     dev = q["counts"].device
     tokens = _empty((B * depth,), torch.int32, dev)
@@ -642,6 +669,7 @@ def draft_sample(q, B, depth, V, seed, request_ids=None, stream=None):
     return tokens.view(B, depth), status.view(B, depth)
 
 
+@_on_stream
 def verify_greedy(target_logits, drafts, stream=None):
     B, depth = drafts.shape
     dev = target_logits.device
@@ -652,6 +680,7 @@ def verify_greedy(target_logits, drafts, stream=None):
     return acc, com, st
 
 
+@_on_stream
 def verify_ratio(target_logits, drafts, q, seed, request_ids=None, stream=None):
     B, depth = drafts.shape
     dev = target_logits.device
@@ -664,6 +693,7 @@ def verify_ratio(target_logits, drafts, q, seed, request_ids=None, stream=None):
     return acc, com, fl, st
 
 
+@_on_stream
 def verify_stats(flags, stream=None):
     """Counts of the requests with each DSPARK_FLAG_* bit in flags [B]: a
     tensor [3] (ambiguous decisions, draws near a boundary, degenerate
@@ -673,6 +703,7 @@ def verify_stats(flags, stream=None):
     return stats
 
 
+@_on_stream
 def target_probs(target_logits, want_p=True, stream=None):
     rows, V, _ = _rows(target_logits)
     dev = target_logits.device
@@ -683,6 +714,7 @@ def target_probs(target_logits, want_p=True, stream=None):
     return p, am, st
 
 
+@_on_stream
 def cache_plan(ctx_len, new_len, max_new, page_size, block_table, free_blocks, n_free=None,
                parents=None, stream=None):
     """Grants the step's blocks and maps its new tokens; returns dict(block_table (the caller's,
@@ -709,15 +741,11 @@ def kv_write(k, v, k_cache, v_cache, slots, rows=None, stream=None):
     return k_cache, v_cache
 
 
+@_on_stream
 def tree_attention(q, k_cache, v_cache, block_table, ctx_len, n_nodes, tree_mask=None, scale=None,
                    stream=None):
     """Attention of the nodes over the cache (scale 1 / sqrt(head_dim) when None); returns (out
-    like q, lse [B, nodes, n_heads], status [B]).  Outputs and workspace are allocated on
-    `stream`."""
-    if stream is not None:  # the workspace is given back when this returns
-        with torch.cuda.stream(stream):
-            return tree_attention(q, k_cache, v_cache, block_table, ctx_len, n_nodes, tree_mask,
-                                  scale)
+    like q, lse [B, nodes, n_heads], status [B])."""
     B, nodes, heads, dim = q.shape
     dev = q.device
     out = _empty((B, nodes, heads, dim), q.dtype, dev)
@@ -727,10 +755,11 @@ def tree_attention(q, k_cache, v_cache, block_table, ctx_len, n_nodes, tree_mask
                 torch.uint8, dev)
     _tree_attention(q, k_cache, v_cache, block_table, ctx_len, n_nodes, tree_mask,
                     dim ** -0.5 if scale is None else scale, out.data_ptr(), lse.data_ptr(),
-                    st.data_ptr(), ws.data_ptr(), None)
+                    st.data_ptr(), ws.data_ptr(), stream)
     return out, lse, st
 
 
+@_on_stream
 def logits_process(logits, history=None, prompt_len=None, history_len=None, draft_tokens=None,
                    row_mask=None, repetition=None, frequency=None, presence=None, bias_ids=None,
                    bias_values=None, n_bias=None, mask_words=None, mask_rows=None, out=None,
