@@ -369,6 +369,9 @@ def dspark_cache_plan(ctx_len, new_len, max_new, page_size, block_table, free_bl
                 _arg("slots", slots, i32, cells), _arg("positions", positions, i32, cells),
                 _arg("tree_mask", tree_mask, torch.int64, cells), _arg("taken", taken, i32, (1,)),
                 _arg("req_status", req_status, i32, cells[:1]), stream)
+    if not cells[0] and taken is not None:  # nothing is launched for an empty batch
+        with torch.cuda.stream(stream):
+            taken.zero_()
 
 
 def _table_args(block_table, B):
@@ -415,8 +418,8 @@ def dspark_kv_write(k, v, k_cache, v_cache, slots, rows=None, stream=None):
     if rows is None and slots.numel() != n:
         raise ValueError("slots must hold one slot for each token")
     _call("dspark_kv_write", k.data_ptr(), v.data_ptr(),
-          F32 if k.dtype is torch.float32 else code, step, k.stride(-2) if k.shape[-2] > 1 else 0, n,
-          k.shape[-2], k.shape[-1], kp, vp, code, sb, st, sh, k_cache.shape[0], k_cache.shape[1],
+          F32 if k.dtype is torch.float32 else code, step,
+          k.stride(-2) if k.shape[-2] > 1 else 0, n, k.shape[-2], k.shape[-1], kp, vp, code, sb, st, sh, k_cache.shape[0], k_cache.shape[1],
           _arg("slots", slots, torch.int32, slots.shape),
           _arg("rows", rows, torch.int32, slots.shape), slots.numel(), _stream(stream))
 
@@ -728,6 +731,8 @@ def cache_plan(ctx_len, new_len, max_new, page_size, block_table, free_blocks, n
     _cache_plan(ctx_len, new_len, max_new, page_size, block_table, free_blocks, n_free, parents,
                 slots.data_ptr(), positions.data_ptr(), None if mask is None else mask.data_ptr(),
                 taken.data_ptr(), status.data_ptr(), stream)
+    if not B:
+        taken.zero_()
     out = {"block_table": block_table, "slots": slots, "positions": positions, "taken": taken,
            "status": status}
     if mask is not None:

@@ -571,6 +571,8 @@ int dspark_q_validate(const float* q, const int32_t* sparse_ids, const int32_t* 
  * Both need max_new <= DSPARK_MAX_NODES (DSPARK_ERR_SIZE otherwise).  A
  * request with a parent out of range keeps its blocks and slots and gets
  * BAD_TREE, masks 0 and positions -1.
+ * B == 0: nothing is launched and nothing written, taken[0] neither; an empty
+ * batch takes no block.
  * n_free: device int32, read as at most max_free, the list's length (NULL:
  * max_free).  Limits: 1 <= page_size <= DSPARK_MAX_PAGE, max_new in [1, 2^24],
  * max_blocks >= 1, table_ld >= max_blocks, max_blocks*page_size <= 2^30,
