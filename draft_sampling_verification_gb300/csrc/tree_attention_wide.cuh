@@ -654,6 +654,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             stream.valid[g & 7u][lane] =
                 past >= 32 ? word : past > 0 ? word & ((1u << past) - 1u) : 0u;
           }
+          __syncwarp();  // lane 0's arrival stands for both lanes' words
           if (lane == 0) {
             stream.special[g & 7u] = 0u;
             mbar_arrive_expect_tx(&stream.k_full[stage], W::kTileBytes);
