@@ -277,16 +277,23 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   };
   auto o_col = [&](int m) -> uint32_t { return tmem + 256u + 128u * m; };
 
-  // a bounded wait; once one expires, every later one of the CTA gives up at once
-  auto wait = [&](uint64_t* bar, uint32_t phase) -> bool {
-    if (mbar_try_wait(bar, phase)) return true;
-    if (*(volatile uint32_t*)&sh.failed) return false;
-    if (mbar_wait_bounded(bar, phase)) return true;
-    *(volatile uint32_t*)&sh.failed = 1u;
-    return false;
-  };
+  // A bounded wait of a whole warp; once one expires, every later one of the CTA gives up at once.
+  // The lanes poll and leave together: each branch is on a vote of all of them.  So the warp is
+  // whole when it goes on to products, whose operands lie in its uniform registers.
   auto wait_all = [&](uint64_t* bar, uint32_t phase) -> bool {
-    return __all_sync(0xffffffffu, wait(bar, phase));
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, phase))) return true;
+    const uint64_t t0 = global_ns();
+    uint32_t nap = 32;
+    while (!__any_sync(0xffffffffu, *(volatile uint32_t*)&sh.failed)) {
+      if (__all_sync(0xffffffffu, mbar_try_wait(bar, phase))) return true;
+      if (__any_sync(0xffffffffu, global_ns() - t0 >= kWaitLimitNs)) {
+        *(volatile uint32_t*)&sh.failed = 1u;
+        break;
+      }
+      if (nap > 32u) __nanosleep(nap);
+      nap = nap < 1024u ? 2u * nap : 1024u;
+    }
+    return false;
   };
   // four waits whose latencies, some 200 cycles each and as long as eight products, overlap; all
   // lanes wait for the same barriers, so the warp stays together
