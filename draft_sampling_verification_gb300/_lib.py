@@ -55,6 +55,7 @@ SIGNATURES = {
     "dspark_logits_process": [_P, _I32, _I64, _I32, _I32, _I32, _P, _I64, _P, _P, _P, _I32, _P, _P,
                               _P, _P, _P, _P, _I32, _P, _P, _I64, _I32, _P, _P, _I64, _P, _P],
     "dspark_debug_exp_weights": [_P, _I64, _P, _P, _P],
+    "dspark_debug_stall_attention": [_I32],
     "dspark_debug_philox": [_P, _U64, _I64, _P, _P],
     "dspark_debug_alloc_scale": [_P, _I64, _P, _P, _P, _P, _P],
     "dspark_debug_wait": [_I32, _P, _U32, _P, _P],

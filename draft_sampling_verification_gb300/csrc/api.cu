@@ -98,6 +98,11 @@ cudaError_t launch_logits_process(
     int64_t mask_ld, int n_masks, const int32_t* mask_rows, void* out, int64_t ld_out,
     int32_t* status, cudaStream_t stream);
 #ifdef DSPARK_CHECKED
+namespace attn {
+cudaError_t stall_64(uint32_t v);
+cudaError_t stall_128(uint32_t v);
+cudaError_t stall_256(uint32_t v);
+}  // namespace attn
 cudaError_t dspark_check_collect_cache(uint32_t* out);
 cudaError_t dspark_check_collect_logits(uint32_t* out);
 cudaError_t dspark_check_collect_chain(uint32_t* out);
@@ -168,6 +173,18 @@ int dspark_checked_status(uint32_t* out) {
 #else
   out[2] = 0u;
   return 0;
+#endif
+}
+
+int dspark_debug_stall_attention(int32_t cta) {
+  if (cta < -1) return DSPARK_ERR_ARG;
+#ifdef DSPARK_CHECKED
+  const uint32_t v = (uint32_t)(cta + 1);
+  for (auto set : {dspark::attn::stall_64, dspark::attn::stall_128, dspark::attn::stall_256})
+    if (const cudaError_t e = set(v)) return (int)e;
+  return 0;
+#else
+  return cta < 0 ? 0 : DSPARK_ERR_ARG;
 #endif
 }
 

@@ -35,6 +35,7 @@ struct Params {
   int row_tiles;  // tiles of an item's rows: ceil(nodes * group / rows per CTA)
   int part_rows;  // rows of a partial result in the workspace
   int part_wide;  // elements of a row that lie together there, a power of two
+  bool waits;     // the kernel's waits can expire: each CTA writes its Lost
 };
 
 // ------------------------------------------------------------ PTX wrappers
@@ -155,14 +156,21 @@ struct Seam {
   int b, head, last, none;
 };
 
+// The requests of a CTA's range when one of its waits expired (none: first > last).  Their
+// status is written by the joining kernel, after every CTA that may have called them well.
+struct Lost {
+  int first, last;
+};
+
 struct Workspace {
   Seam* seam;     // [ctas], by team
+  Lost* lost;     // [ctas]
   float2* stats;  // [2 * ctas][rows]: the reference of the exponents, the sum
   float* rows;    // [2 * ctas][dim / wide][rows][wide]
 };
 
 __host__ __device__ inline int64_t workspace_bytes(int rows, int dim, int ctas) {
-  return 32 + (int64_t)ctas * sizeof(Seam) +
+  return 32 + (int64_t)ctas * (sizeof(Seam) + sizeof(Lost)) +
          2ll * ctas * rows * (sizeof(float2) + (int64_t)dim * sizeof(float));
 }
 
@@ -170,7 +178,8 @@ __device__ __forceinline__ Workspace carve(char* w, int rows, int ctas) {
   Workspace s;  // every part 32-byte aligned
   w = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(w) + 31) & ~(uintptr_t)31);
   s.seam = reinterpret_cast<Seam*>(w);
-  s.stats = reinterpret_cast<float2*>(w + ctas * sizeof(Seam));
+  s.lost = reinterpret_cast<Lost*>(w + ctas * sizeof(Seam));
+  s.stats = reinterpret_cast<float2*>(w + ctas * (sizeof(Seam) + sizeof(Lost)));
   s.rows = reinterpret_cast<float*>(s.stats + 2 * ctas * rows);
   return s;
 }
@@ -735,7 +744,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, N8, MW>::kCtas)
 // between teams x and x + 1, if there is one, are joined from the teams'
 // partial rows, in the teams' order.  A warp takes a row, and kAhead teams'
 // parts of it are in flight together: its time is the latency of reading them
-// (6 us of 104 at 256 items of 4,000 tokens on 304 ranges).
+// (6 us of 104 at 256 items of 4,000 tokens on 304 ranges).  CTA (x, 0, 0)
+// also gives the requests that team x lost their status.
 constexpr int kJoinThreads = 256;
 
 template <typename T, int D>
@@ -745,9 +755,13 @@ __global__ void __launch_bounds__(kJoinThreads)
   constexpr int kPer = D / 32, kAhead = 8;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Workspace ws = carve(p.workspace, p.part_rows, p.max_ctas);
-  const Seam at = ws.seam[blockIdx.x + 1];
+  const Seam at = ws.seam[min(blockIdx.x + 1, gridDim.x - 1)];
+  if (p.waits && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x < p.row_tiles) {
+    const Lost lost = ws.lost[blockIdx.x * p.row_tiles + threadIdx.x];
+    for (int b = lost.first; b <= lost.last; ++b) p.status[b] = DSPARK_ST_TIMEOUT;
+  }
   const int c0 = blockIdx.x, c1 = at.last;  // the item's teams
-  if (c1 < 0) return;
+  if (c1 < 0 || blockIdx.x + 1 == gridDim.x) return;
   const int lane = threadIdx.x & 31;
   const int r = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5);
   const int row = blockIdx.z * rows + r;
@@ -808,10 +822,10 @@ __global__ void __launch_bounds__(kJoinThreads)
 template <typename T, int D>
 cudaError_t launch_join(const Params& p, int rows, int grid, cudaStream_t stream) {
   const int teams = grid / p.row_tiles;
-  if (teams == 1) return cudaSuccess;
+  if (teams == 1 && !p.waits) return cudaSuccess;
   cudaLaunchConfig_t cfg = {};
   const int used = min(rows, p.nodes * p.group);
-  cfg.gridDim = dim3(teams - 1, (used + kJoinThreads / 32 - 1) / (kJoinThreads / 32), p.row_tiles);
+  cfg.gridDim = dim3(teams, (used + kJoinThreads / 32 - 1) / (kJoinThreads / 32), p.row_tiles);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -855,6 +869,7 @@ cudaError_t launch_shape(Params p, int sms, cudaStream_t stream) {
   p.max_ctas = stream_ctas(D, S::kRows);
   p.item_cost = kStreamCost;
   p.tile = S::kTile;
+  p.waits = false;
   const int grid = min(p.max_ctas, max(sms * S::kCtas, p.row_tiles));
   kernel<<<grid, kThreads, S::kSmem, stream>>>(p);
   e = cudaGetLastError();

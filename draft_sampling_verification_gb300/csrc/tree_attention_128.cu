@@ -10,5 +10,7 @@ cudaError_t launch_128(const Params& p, int dtype, int sms, cudaStream_t stream)
                               : launch_dim<__half, 128>(p, sms, stream);
 }
 
+DSPARK_STALL_SETTER(128)
+
 }  // namespace attn
 }  // namespace dspark

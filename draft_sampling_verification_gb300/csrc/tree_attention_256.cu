@@ -10,5 +10,7 @@ cudaError_t launch_256(const Params& p, int dtype, int sms, cudaStream_t stream)
                               : launch_dim<__half, 256>(p, sms, stream);
 }
 
+DSPARK_STALL_SETTER(256)
+
 }  // namespace attn
 }  // namespace dspark

@@ -10,5 +10,7 @@ cudaError_t launch_64(const Params& p, int dtype, int sms, cudaStream_t stream) 
                               : launch_dim<__half, 64>(p, sms, stream);
 }
 
+DSPARK_STALL_SETTER(64)
+
 }  // namespace attn
 }  // namespace dspark

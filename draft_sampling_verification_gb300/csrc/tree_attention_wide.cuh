@@ -8,6 +8,18 @@
 
 #include "tree_attention.cuh"
 
+// The checked build can leave one CTA of the kernel without its copies, so that its waits expire:
+// dspark_debug_stall_attention.
+#ifdef DSPARK_CHECKED
+static __device__ uint32_t g_stalled;  // the CTA + 1
+#define DSPARK_STALLED(cta) (*(volatile uint32_t*)&g_stalled == (cta) + 1u)
+#define DSPARK_STALL_SETTER(dim) \
+  cudaError_t stall_##dim(uint32_t v) { return cudaMemcpyToSymbol(g_stalled, &v, 4); }
+#else
+#define DSPARK_STALLED(cta) false
+#define DSPARK_STALL_SETTER(dim)
+#endif
+
 namespace dspark {
 namespace attn {
 
@@ -229,7 +241,10 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   int64_t ranges[W::kStreams];
   find_range<kWideThreads, W::kStreams>(p, ws, sh.scan, sh.start, ranges);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (ranges[0] <= 0) return;  // the second stream's range comes behind the first's
+  if (ranges[0] <= 0) {  // the second stream's range comes behind the first's
+    if (tid < W::kStreams) ws.lost[blockIdx.x * W::kStreams + tid] = {0, -1};
+    return;
+  }
   const int r0 = (blockIdx.x % p.row_tiles) * W::kRows;
   // row tiles of one stream
   const int n_tiles = kMode == kBoth && p.nodes * p.group - r0 > 128 ? 2 : 1;
@@ -617,7 +632,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     const int k_shift = 31 - __clz(k_rows);
     const int next_row = kKeys % p.page, next_block = kKeys / p.page;  // from tile to tile
     uint32_t g = 0, k_tiles = 0, v_tiles = 0;  // k_tiles, v_tiles: the tiles copied
-    bool ok = true;
+    bool ok = !DSPARK_STALLED(blockIdx.x);
     Walk cur = walk_from(p, sh.start[x], ranges[x], p.item_cost);
     while (ok && cur.advance(p, kKeys)) {
       const int tiles = cur.count;
@@ -806,9 +821,31 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     tc_after_sync();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
   }
-  if (sh.failed && tid < W::kStreams) {  // the requests of this range are refused
-    for (Walk cur = walk_from(p, sh.start[tid], ranges[tid], p.item_cost); cur.advance(p, kKeys);)
-      p.status[cur.b] = DSPARK_ST_TIMEOUT;
+  // After a wait that expired the requests of the range are refused.  What the CTA has written of
+  // them may be unfinished: NaN takes its place, and in the parts the joining kernel's sums.
+  for (int x = 0; x < W::kStreams; ++x) {
+    Lost lost = {0, -1};
+    if (sh.failed && ranges[x] > 0) {
+      Walk cur = walk_from(p, sh.start[x], ranges[x], p.item_cost);
+      lost.first = cur.b;
+      while (cur.advance(p, kKeys)) {
+        lost.last = cur.b;
+        const int64_t slot = cur.slot(blockIdx.x * W::kStreams + x) * p.part_rows;
+        for (int r = tid; r < min(W::kRows, p.nodes * p.group - r0); r += kWideThreads) {
+          const int node = (r0 + r) / p.group;
+          const int64_t to = ((int64_t)cur.b * p.nodes + node) * p.heads + cur.head * p.group +
+                             r0 + r - node * p.group;
+          if (!cur.whole()) {
+            ws.stats[slot + r] = make_float2(NAN, NAN);
+            continue;
+          }
+          for (int d = 0; d < D; d += 2)
+            *reinterpret_cast<uint32_t*>(static_cast<T*>(p.out) + to * D + d) = H::pack(NAN, NAN);
+          if (p.lse) p.lse[to] = NAN;
+        }
+      }
+    }
+    if (tid == 0) ws.lost[blockIdx.x * W::kStreams + x] = lost;
   }
 }
 
@@ -869,6 +906,7 @@ bool launch_wide(Params p, int sms, cudaStream_t stream, cudaError_t* error) {
   p.part_wide = W::kPartWide;
   p.max_ctas = wide_ctas(kMode == kPair);
   p.tile = W::kKeys;
+  p.waits = true;
   p.item_cost = kMode == kPair ? kPairCost : kMode == kBoth ? kBothCost : kOneCost;
   auto* kernel = tree_attention_wide_kernel<T, D, kMode>;
   *error = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, W::kSmem);

@@ -630,7 +630,9 @@ int dspark_kv_write(const void* k, const void* v, int32_t src_dtype, int64_t src
  * [head_dim] contiguous, of q's dtype; lse [B][nodes][n_heads] fp32 (may be
  * NULL).  dtype: DSPARK_BF16 or DSPARK_F16, for q, both caches and out.
  * req_status[B]: BAD_LENGTH for ctx < 0, n_nodes outside [0, nodes] or more
- * tokens than max_blocks*page_size (every row of the request gets out 0).
+ * tokens than max_blocks*page_size (every row of the request gets out 0);
+ * TIMEOUT for a request that shares a kernel range with a wait that expired
+ * (2 s): its rows hold their result or NaN, out and lse alike.
  * Limits: head_dim 64, 128 or 256; 1 <= nodes <= DSPARK_MAX_NODES; n_heads a
  * multiple of n_kv_heads, at most 64 times it; q, out, caches and workspace
  * 16-byte aligned and their strides multiples of 8 elements; max_blocks*

@@ -87,6 +87,16 @@ int dspark_checked_status(uint32_t* out);
  */
 int dspark_debug_check_selftest(void* stream);
 
+/*
+ * In the checked build, the later dspark_tree_attention calls whose kernel
+ * has waits (the tensor kernel) leave CTA `cta` without its copies of keys
+ * and values, until a call with cta = -1: its waits for them expire (2 s), it
+ * ends, and its requests get DSPARK_ST_TIMEOUT.  The normal build has no such
+ * switch: DSPARK_ERR_ARG for cta >= 0.  Host; ordered as a copy to the device
+ * on the default stream.
+ */
+int dspark_debug_stall_attention(int32_t cta);
+
 #ifdef __cplusplus
 }
 #endif
