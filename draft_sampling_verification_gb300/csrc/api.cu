@@ -104,6 +104,9 @@ cudaError_t stall_128(uint32_t v);
 cudaError_t stall_256(uint32_t v);
 }  // namespace attn
 cudaError_t dspark_check_collect_cache(uint32_t* out);
+cudaError_t dspark_check_collect_tree_attention_64(uint32_t* out);
+cudaError_t dspark_check_collect_tree_attention_128(uint32_t* out);
+cudaError_t dspark_check_collect_tree_attention_256(uint32_t* out);
 cudaError_t dspark_check_collect_logits(uint32_t* out);
 cudaError_t dspark_check_collect_chain(uint32_t* out);
 cudaError_t dspark_check_collect_debug(uint32_t* out);
@@ -162,6 +165,9 @@ int dspark_checked_status(uint32_t* out) {
   cudaError_t e = cudaSuccess;
   cudaError_t (*collect[])(uint32_t*) = {
       dspark::dspark_check_collect_cache, dspark::dspark_check_collect_logits,
+      dspark::dspark_check_collect_tree_attention_64,
+      dspark::dspark_check_collect_tree_attention_128,
+      dspark::dspark_check_collect_tree_attention_256,
       dspark::dspark_check_collect_chain, dspark::dspark_check_collect_debug,
       dspark::dspark_check_collect_q_dense, dspark::dspark_check_collect_q_topk,
       dspark::dspark_check_collect_q_wire, dspark::dspark_check_collect_sample,

@@ -281,6 +281,11 @@ __global__ void __launch_bounds__(kWriteThreads) kv_write_kernel(const WritePara
       const int j = j0 + u * lanes;
       if (j >= p.per) continue;
       const int head = j / p.vecs, d = (j - head * p.vecs) * 8;
+      if (!DSPARK_CHECK(block < p.n_blocks && slot - block * p.page < p.page &&
+                        (head + 1) * p.vecs <= p.per && d / 8 < p.vecs && row < p.n_src)) {
+        at[u] = -1;
+        continue;
+      }
       const int64_t from = head * p.src_head + d;
       at[u] = to + head * p.head_stride + d;
 #pragma unroll
@@ -291,7 +296,7 @@ __global__ void __launch_bounds__(kWriteThreads) kv_write_kernel(const WritePara
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      if (j0 + u * lanes >= p.per) continue;
+      if (j0 + u * lanes >= p.per || !DSPARK_CHECK(at[u] >= 0)) continue;
       *reinterpret_cast<uint4*>(static_cast<T*>(p.k_cache) + at[u]) = stored<T>(a[u]);
       *reinterpret_cast<uint4*>(static_cast<T*>(p.v_cache) + at[u]) = stored<T>(c[u]);
     }

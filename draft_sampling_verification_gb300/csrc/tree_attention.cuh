@@ -193,6 +193,15 @@ __device__ __forceinline__ float* part_at(const Workspace& ws, int64_t slot, int
   return ws.rows + slot * dim + ((int64_t)(d / wide) * rows + r) * wide + d % wide;
 }
 
+// Bounds of the checked build: row r of the partial result at `slot`, and a row of out and lse.
+__device__ __forceinline__ bool part_held(const Params& p, int64_t slot, int r) {
+  return r >= 0 && r < p.part_rows && slot >= 0 && slot % p.part_rows == 0 &&
+         slot < 2ll * p.max_ctas * p.part_rows;
+}
+__device__ __forceinline__ bool row_held(const Params& p, int64_t to) {
+  return to >= 0 && to < (int64_t)p.B * p.nodes * p.heads;
+}
+
 // a request's tokens: the cached text, and all with its nodes (0 when refused)
 struct Lengths {
   int ctx, len, nodes;
@@ -343,13 +352,15 @@ __device__ __forceinline__ void find_range(const Params& p, const Workspace& ws,
       const int64_t begin = x0 - at.at + p.item_cost;  // the item's first tile
       if (at.at > p.item_cost && c.owner_of(begin) == team - 1)
         seam.last = c.owner_of(begin + at.tiles - 1);
-      ws.seam[team] = seam;
+      if (DSPARK_CHECK(team < p.max_ctas && at.b < p.B && at.head < p.kv_heads &&
+                       seam.last < c.teams))
+        ws.seam[team] = seam;
     }
   }
   // teams without work: nothing to join
   for (int t = c.teams + blockIdx.x * kBlock + threadIdx.x; t < (int)gridDim.x * kStreams / p.row_tiles;
        t += gridDim.x * kBlock)
-    ws.seam[t] = {0, 0, -1, 0};
+    if (DSPARK_CHECK(t < p.max_ctas)) ws.seam[t] = {0, 0, -1, 0};
   __syncthreads();
 }
 
@@ -441,7 +452,10 @@ __global__ void __launch_bounds__(kThreads, Shape<D, N8, MW>::kCtas)
     const int64_t head_off = kvh * p.head_stride;
     auto entry_of = [&](int step) -> int {  // the block of this lane's position in a step
       const int pos = first + step * S::kTile + (whole ? 0 : (lane & 15));
-      return step < tiles && pos < len.len ? __ldg(table + pos / p.page) : -1;
+      return step < tiles && pos < len.len &&
+                     DSPARK_CHECK(pos >= 0 && pos / p.page < p.max_blocks && cur.b < p.B)
+                 ? __ldg(table + pos / p.page)
+                 : -1;
     };
     auto issue = [&](int step, int block) {
       const int pos = first + step * S::kTile;
@@ -459,7 +473,10 @@ __global__ void __launch_bounds__(kThreads, Shape<D, N8, MW>::kCtas)
       for (int i = 0; i < kKeys * kChunks / (32 * MW); ++i) {
         const int at = (i * MW + mw) * 32 + lane;
         const int row = at / kChunks, chunk = at % kChunks;
-        const bool on = (valid >> row) & 1u;
+        // a step of whole blocks lies in one of them
+        const bool on = ((valid >> row) & 1u) &&
+                        DSPARK_CHECK(kvh < p.kv_heads && pos + row < len.len &&
+                                     (!whole || pos % p.page + row < p.page));
         const int64_t row_off = whole ? off + row * p.token_stride
                                       : __shfl_sync(0xffffffffu, (long long)off, row);
         const int64_t from = on ? row_off + head_off + chunk * 8 : 0;
@@ -481,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, N8, MW>::kCtas)
     for (int r = tid; r < kRows; r += kThreads) {
       const int row = r0 + r, node = row / p.group;
       uint64_t m = 0;
-      if (row < live) {
+      if (row < live && DSPARK_CHECK(node < p.nodes && cur.b < p.B)) {
         m = p.mask ? p.mask[(int64_t)cur.b * p.nodes + node] : ~0ull >> (63 - node);
       }
       s_mask[r] = m;
@@ -493,10 +510,11 @@ __global__ void __launch_bounds__(kThreads, Shape<D, N8, MW>::kCtas)
       const int node = row / p.group, h = kvh * p.group + row - node * p.group;
       const T* from = static_cast<const T*>(p.q) + cur.b * p.q_req + node * p.q_node +
                       h * p.q_head + (lane & 3) * 2;
+      const bool has = row < live && DSPARK_CHECK(cur.b < p.B && node < p.nodes && h < p.heads);
 #pragma unroll
       for (int kt = 0; kt < D / 16; ++kt) {
-        q[kt][n][0] = row < live ? __ldg(reinterpret_cast<const uint32_t*>(from + kt * 16)) : 0u;
-        q[kt][n][1] = row < live ? __ldg(reinterpret_cast<const uint32_t*>(from + kt * 16 + 8)) : 0u;
+        q[kt][n][0] = has ? __ldg(reinterpret_cast<const uint32_t*>(from + kt * 16)) : 0u;
+        q[kt][n][1] = has ? __ldg(reinterpret_cast<const uint32_t*>(from + kt * 16 + 8)) : 0u;
       }
     }
     float o[D / 16][N8][4];
@@ -722,6 +740,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, N8, MW>::kCtas)
         const int row = r0 + r, node = row / p.group;
         const int64_t to = ((int64_t)cur.b * p.nodes + node) * p.heads + kvh * p.group + row -
                            node * p.group;
+        if (!DSPARK_CHECK(row_held(p, to))) continue;
         uint2 w;
         w.x = H::pack(a.x, a.y);
         w.y = H::pack(a.z, a.w);
@@ -730,7 +749,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, N8, MW>::kCtas)
           const float2 j = s_joined[r];
           p.lse[to] = j.y == 0.0f ? -INFINITY : (j.x + log2f(j.y)) * 0.6931471805599453f;
         }
-      } else {
+      } else if (DSPARK_CHECK(part_held(p, slot, r))) {
         *reinterpret_cast<float4*>(part_at(ws, slot, p.part_rows, D, r, D, d)) = a;
         if (d == 0) ws.stats[slot + r] = s_joined[r];
       }
@@ -755,8 +774,10 @@ __global__ void __launch_bounds__(kJoinThreads)
   constexpr int kPer = D / 32, kAhead = 8;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Workspace ws = carve(p.workspace, p.part_rows, p.max_ctas);
+  if (!DSPARK_CHECK(gridDim.x <= p.max_ctas)) return;
   const Seam at = ws.seam[min(blockIdx.x + 1, gridDim.x - 1)];
-  if (p.waits && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x < p.row_tiles) {
+  if (p.waits && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x < p.row_tiles &&
+      DSPARK_CHECK(blockIdx.x * p.row_tiles + threadIdx.x < p.max_ctas)) {
     const Lost lost = ws.lost[blockIdx.x * p.row_tiles + threadIdx.x];
     for (int b = lost.first; b <= lost.last; ++b) p.status[b] = DSPARK_ST_TIMEOUT;
   }
@@ -775,6 +796,9 @@ __global__ void __launch_bounds__(kJoinThreads)
   const int shift = 31 - __clz(p.part_wide), d0 = lane * kPer;
   const int offset =
       ((((d0 >> shift) * p.part_rows) + r) << shift) + (d0 & (p.part_wide - 1));
+  if (!DSPARK_CHECK(c1 < gridDim.x && part_held(p, part_of(c0), r) &&
+                    part_held(p, part_of(c1), r) && offset + kPer <= p.part_rows * D))
+    return;
   float top = -INFINITY;
   for (int c = c0 + lane; c <= c1; c += 32) top = fmaxf(top, ws.stats[part_of(c) + r].x);
   top = warp_reduce(top, OpMaxF());
@@ -801,6 +825,7 @@ __global__ void __launch_bounds__(kJoinThreads)
   }
   const int node = row / p.group, h = at.head * p.group + row - node * p.group;
   const int64_t to = ((int64_t)at.b * p.nodes + node) * p.heads + h;
+  if (!DSPARK_CHECK(row_held(p, to))) return;
   const float inv = all == 0.0f ? 0.0f : 1.0f / all;
   uint32_t w[kPer / 2];
 #pragma unroll

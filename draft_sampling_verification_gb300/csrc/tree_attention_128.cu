@@ -1,5 +1,6 @@
 // tree_attention_128.cu -- the attention kernels of tree_attention.cuh for
 // head_dim 128.
+#define DSPARK_TU 13  // this file's number in the checked build's site codes
 #include "tree_attention_wide.cuh"
 
 namespace dspark {
@@ -13,4 +14,7 @@ cudaError_t launch_128(const Params& p, int dtype, int sms, cudaStream_t stream)
 DSPARK_STALL_SETTER(128)
 
 }  // namespace attn
+
+DSPARK_CHECK_COLLECTOR(tree_attention_128)
+
 }  // namespace dspark

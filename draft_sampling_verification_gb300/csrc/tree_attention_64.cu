@@ -1,5 +1,6 @@
 // tree_attention_64.cu -- the attention kernels of tree_attention.cuh for
 // head_dim 64.
+#define DSPARK_TU 12  // this file's number in the checked build's site codes
 #include "tree_attention_wide.cuh"
 
 namespace dspark {
@@ -13,4 +14,7 @@ cudaError_t launch_64(const Params& p, int dtype, int sms, cudaStream_t stream) 
 DSPARK_STALL_SETTER(64)
 
 }  // namespace attn
+
+DSPARK_CHECK_COLLECTOR(tree_attention_64)
+
 }  // namespace dspark

@@ -242,7 +242,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   find_range<kWideThreads, W::kStreams>(p, ws, sh.scan, sh.start, ranges);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (ranges[0] <= 0) {  // the second stream's range comes behind the first's
-    if (tid < W::kStreams) ws.lost[blockIdx.x * W::kStreams + tid] = {0, -1};
+    if (tid < W::kStreams && DSPARK_CHECK(blockIdx.x * W::kStreams + tid < p.max_ctas))
+      ws.lost[blockIdx.x * W::kStreams + tid] = {0, -1};
     return;
   }
   const int r0 = (blockIdx.x % p.row_tiles) * W::kRows;
@@ -363,6 +364,9 @@ __global__ void __launch_bounds__(kWideThreads, 1)
 #pragma unroll
       for (int part = 0; part < kChunks / kPart; ++part) {
         uint4 q[kPart];
+        if (!DSPARK_CHECK(w.b < p.B && w.head < p.kv_heads && m_rows - r0 >= 0 &&
+                          m_rows - r0 + t / kChunks + (kChunks - 1) * kStep < W::kRows))
+          continue;
 #pragma unroll
         for (int i = 0; i < kPart; ++i)
           q[i] = __ldg(reinterpret_cast<const uint4*>(from + q_row[(part * kPart + i) * kStep]));
@@ -371,6 +375,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           const int r = (part * kPart + i) * kStep + t / kChunks;
           const uint32_t keep = r < live ? ~0u : 0u;
           const uint32_t to = q_at + (c >> 3) * 16384 + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+          if (!DSPARK_CHECK(to + 16 <= ring)) continue;
           asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to),
                        "r"((q[i].x ^ flip) & keep), "r"((q[i].y ^ flip) & keep),
                        "r"((q[i].z ^ flip) & keep), "r"((q[i].w ^ flip) & keep)
@@ -404,7 +409,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       if (more) prefetch_q(ahead);
       const bool idle = m_rows + (t & ~31) >= live;  // no row of this warp has a node
       uint64_t mask = 0;
-      if (row < live)
+      if (row < live && DSPARK_CHECK(node < p.nodes && cur.b < p.B))
         mask = p.mask ? p.mask[(int64_t)cur.b * p.nodes + node] : ~0ull >> (63 - node);
       float ref = -INFINITY;
       float2 sum2 = make_float2(0.0f, 0.0f);
@@ -513,6 +518,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
               const int j = min(j0 + u * 128, n - 1), r = from + j / kChunks, c = j % kChunks;
               addr[u] = v_at + (r >> v_shift) * v_box + (c >> 3) * v_half +
                         (r & (boxes.v_rows - 1)) * 128 + (((c & 7) ^ (r & 7)) << 4);
+              if (!DSPARK_CHECK(addr[u] >= v_at && addr[u] + 16 <= v_at + W::kTileBytes))
+                addr[u] = v_at;
               asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                            : "=r"(w[u][0]), "=r"(w[u][1]), "=r"(w[u][2]), "=r"(w[u][3])
                            : "r"(addr[u])
@@ -574,6 +581,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           for (int k = 0; k < len.nodes; ++k) {
             const int at = len.ctx + k, tile = at / kKeys;
             if (!((mask >> k) & 1ull) || tile < cur.first || tile >= cur.first + tiles) continue;
+            if (!DSPARK_CHECK(at / p.page < p.max_blocks && cur.b < p.B)) continue;
             const int block = p.table[cur.b * p.table_ld + at / p.page];
             if (block < 0 || block >= p.n_blocks) continue;
             const T* from = static_cast<const T*>(p.v) + block * p.block_stride +
@@ -586,7 +594,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             }
           }
         }
-        if (mine && full) {
+        if (mine && full && DSPARK_CHECK(row_held(p, to))) {
           uint4* out = reinterpret_cast<uint4*>(static_cast<T*>(p.out) + to * D + c * 32);
 #pragma unroll
           for (int j = 0; j < 4; ++j)
@@ -594,7 +602,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                                 H::pack(v[8 * j + 2] * inv, v[8 * j + 3] * inv),
                                 H::pack(v[8 * j + 4] * inv, v[8 * j + 5] * inv),
                                 H::pack(v[8 * j + 6] * inv, v[8 * j + 7] * inv));
-        } else if (mine) {
+        } else if (mine && DSPARK_CHECK(!full && part_held(p, slot, part_row))) {
           constexpr int kWide = W::kPartWide;
           float* out = part_at(ws, slot, p.part_rows, kWide, part_row, D, c * 32);
 #pragma unroll
@@ -606,7 +614,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         }
         __syncwarp();
       }
-      if (mine) {
+      if (mine && DSPARK_CHECK(full ? row_held(p, to) : part_held(p, slot, part_row))) {
         if (!full)
           ws.stats[slot + part_row] = make_float2(ref, sum);
         else if (p.lse)
@@ -641,7 +649,12 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       // the place of this lane's box: position, entry of the table, row of the block
       int pos = first + lane * rows, at = pos / p.page, row_ahead = pos - at * p.page;
       const int32_t* table = p.table + cur.b * p.table_ld;
-      auto entry = [&]() -> int { return lane < n_boxes && pos < len.len ? __ldg(table + at) : -1; };
+      auto entry = [&]() -> int {
+        return lane < n_boxes && pos < len.len &&
+                       DSPARK_CHECK(at == pos / p.page && at < p.max_blocks && cur.b < p.B)
+                   ? __ldg(table + at)
+                   : -1;
+      };
       int ahead = entry();
       for (int i = 0; i < tiles; ++i, ++g) {
         const int block = ahead, row_here = row_ahead;
@@ -682,7 +695,12 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             mbar_arrive_expect_tx(&stream.k_full[stage], W::kTileBytes);
           }
           __syncwarp();
-          if (lane < n_boxes) {
+          // rows of one block, and a place inside the stage
+          if (lane < n_boxes && DSPARK_CHECK(row + k_rows <= p.page && cur.head < p.kv_heads &&
+                                             lane * (boxes.k_whole ? k_group : k_rows * 128u) +
+                                                     (boxes.k_whole ? k_group : k_rows * 128u) <=
+                                                 (boxes.k_whole ? W::kTileBytes : k_half) &&
+                                             stage < kStages)) {
             const uint32_t to = k_at + stage * W::kTileBytes;
             if (boxes.k_whole) {
               tma_load_box(to + lane * k_group, &k_map, row, 0, cur.head, from,
@@ -704,7 +722,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           if (!ok) break;
           if (lane == 0) mbar_arrive_expect_tx(&stream.v_full[stage], W::kTileBytes);
           __syncwarp();
-          if (lane < v_boxes)
+          if (lane < v_boxes && DSPARK_CHECK(v_row + v_rows <= p.page && cur.head < p.kv_heads &&
+                                             (lane + 1) * v_box <= W::kTileBytes))
             tma_load_box(v_at + stage * W::kTileBytes + lane * v_box, &v_map, v_row, 0, cur.head,
                          v_from, &stream.v_full[stage]);
           v_tiles = g + 1u;
@@ -835,6 +854,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           const int node = (r0 + r) / p.group;
           const int64_t to = ((int64_t)cur.b * p.nodes + node) * p.heads + cur.head * p.group +
                              r0 + r - node * p.group;
+          if (!DSPARK_CHECK(cur.whole() ? row_held(p, to) : part_held(p, slot, r))) continue;
           if (!cur.whole()) {
             ws.stats[slot + r] = make_float2(NAN, NAN);
             continue;
@@ -845,7 +865,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         }
       }
     }
-    if (tid == 0) ws.lost[blockIdx.x * W::kStreams + x] = lost;
+    if (tid == 0 && DSPARK_CHECK(blockIdx.x * W::kStreams + x < p.max_ctas))
+      ws.lost[blockIdx.x * W::kStreams + x] = lost;
   }
 }
 
