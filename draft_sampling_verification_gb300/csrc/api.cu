@@ -705,7 +705,8 @@ int dspark_cache_plan(const int32_t* ctx_len, const int32_t* new_len, int32_t B,
                       int32_t* positions, uint64_t* tree_mask, int32_t* taken,
                       int32_t* req_status, void* stream) {
   const NvtxRange nvtx_range("dspark_cache_plan");
-  if (B < 0 || max_new < 1 || page_size < 1 || page_size > DSPARK_MAX_PAGE || max_blocks < 1 ||
+  if (B < 0 || B > DSPARK_MAX_PLANNED || max_new < 1 || page_size < 1 ||
+      page_size > DSPARK_MAX_PAGE || max_blocks < 1 ||
       table_ld < max_blocks || max_free < 0 ||
       (int64_t)max_blocks * page_size > DSPARK_MAX_TOKENS ||
       max_new > (1 << 24) || (int64_t)B * max_new > INT32_MAX)

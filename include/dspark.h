@@ -542,6 +542,7 @@ int dspark_q_validate(const float* q, const int32_t* sparse_ids, const int32_t* 
 #define DSPARK_MAX_NODES 64          /* nodes of a request's tree            */
 #define DSPARK_MAX_PAGE 1024         /* token rows of a block                */
 #define DSPARK_MAX_TOKENS 1073741824 /* positions of a request's table, 2^30 */
+#define DSPARK_MAX_PLANNED 1048576   /* requests of a plan, 2^20             */
 
 /*
  * dspark_cache_plan -- grants blocks to the requests of a step and maps their
@@ -576,7 +577,7 @@ int dspark_q_validate(const float* q, const int32_t* sparse_ids, const int32_t* 
  * n_free: device int32, read as at most max_free, the list's length (NULL:
  * max_free).  Limits: 1 <= page_size <= DSPARK_MAX_PAGE, max_new in [1, 2^24],
  * max_blocks >= 1, table_ld >= max_blocks, max_blocks*page_size <= 2^30,
- * B*max_new < 2^31, max_free >= 0.
+ * B <= DSPARK_MAX_PLANNED, B*max_new < 2^31, max_free >= 0.
  */
 int dspark_cache_plan(const int32_t* ctx_len, const int32_t* new_len, int32_t B, int32_t max_new,
                       int32_t page_size, int32_t* block_table, int64_t table_ld,
