@@ -786,7 +786,8 @@ int dspark_tree_attention(const void* q, int32_t dtype, int64_t q_req_stride,
       (int64_t)max_blocks * page_size > DSPARK_MAX_TOKENS ||
       q_req_stride < 0 || q_node_stride < 0 || q_head_stride < 0)
     return DSPARK_ERR_SIZE;
-  if (!(scale > -3.0e38f && scale < 3.0e38f)) return DSPARK_ERR_ARG;
+  // times log2(e) it has to stay finite, or a score of 0 would become NaN
+  if (!(scale > -2.3e38f && scale < 2.3e38f)) return DSPARK_ERR_ARG;
   if (B == 0) return 0;
   if (!q || !k_cache || !v_cache || !block_table || !ctx_len || !n_nodes || !out || !req_status ||
       !workspace)

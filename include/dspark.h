@@ -637,7 +637,7 @@ int dspark_kv_write(const void* k, const void* v, int32_t src_dtype, int64_t src
  * Limits: head_dim 64, 128 or 256; 1 <= nodes <= DSPARK_MAX_NODES; n_heads a
  * multiple of n_kv_heads, at most 64 times it; q, out, caches and workspace
  * 16-byte aligned and their strides multiples of 8 elements; max_blocks*
- * page_size <= 2^30.  scale finite.
+ * page_size <= 2^30.  |scale| < 2.3e38 (DSPARK_ERR_ARG otherwise).
  * workspace: dspark_tree_attention_workspace_bytes(...) bytes of device
  * memory owned by the caller, with no content to keep (3 to 90 MB); calls that
  * may overlap need separate ones.  The result does not depend on the batch's
