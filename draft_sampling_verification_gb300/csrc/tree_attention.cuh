@@ -776,69 +776,72 @@ __global__ void __launch_bounds__(kJoinThreads)
   const Workspace ws = carve(p.workspace, p.part_rows, p.max_ctas);
   if (!DSPARK_CHECK(gridDim.x <= p.max_ctas)) return;
   const Seam at = ws.seam[min(blockIdx.x + 1, gridDim.x - 1)];
+  // read at the start, as its latency would follow the rows', and used at the end
+  Lost lost = {0, -1};
   if (p.waits && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x < p.row_tiles &&
-      DSPARK_CHECK(blockIdx.x * p.row_tiles + threadIdx.x < p.max_ctas)) {
-    const Lost lost = ws.lost[blockIdx.x * p.row_tiles + threadIdx.x];
-    for (int b = lost.first; b <= lost.last; ++b) p.status[b] = DSPARK_ST_TIMEOUT;
-  }
-  const int c0 = blockIdx.x, c1 = at.last;  // the item's teams
-  if (c1 < 0 || blockIdx.x + 1 == gridDim.x) return;
-  const int lane = threadIdx.x & 31;
-  const int r = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5);
-  const int row = blockIdx.z * rows + r;
-  if (r >= rows || row >= p.nodes * p.group) return;
-  // the first partial row of team c: its first range's in slot 0, its last's in slot 1
-  auto part_of = [&](int c) -> int64_t {
-    return (2ll * (c * p.row_tiles + blockIdx.z) + (c == c0 ? 1 : 0)) * p.part_rows;
-  };
+      DSPARK_CHECK(blockIdx.x * p.row_tiles + threadIdx.x < p.max_ctas))
+    lost = ws.lost[blockIdx.x * p.row_tiles + threadIdx.x];
+  [&] {
+    const int c0 = blockIdx.x, c1 = blockIdx.x + 1 < gridDim.x ? at.last : -1;  // the item's teams
+    if (c1 < 0) return;
+    const int lane = threadIdx.x & 31;
+    const int r = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5);
+    const int row = blockIdx.z * rows + r;
+    if (r >= rows || row >= p.nodes * p.group) return;
+    // the first partial row of team c: its first range's in slot 0, its last's in slot 1
+    auto part_of = [&](int c) -> int64_t {
+      return (2ll * (c * p.row_tiles + blockIdx.z) + (c == c0 ? 1 : 0)) * p.part_rows;
+    };
 
-  // part_at, with the width's division as a shift
-  const int shift = 31 - __clz(p.part_wide), d0 = lane * kPer;
-  const int offset =
-      ((((d0 >> shift) * p.part_rows) + r) << shift) + (d0 & (p.part_wide - 1));
-  if (!DSPARK_CHECK(c1 < gridDim.x && part_held(p, part_of(c0), r) &&
-                    part_held(p, part_of(c1), r) && offset + kPer <= p.part_rows * D))
-    return;
-  float top = -INFINITY;
-  for (int c = c0 + lane; c <= c1; c += 32) top = fmaxf(top, ws.stats[part_of(c) + r].x);
-  top = warp_reduce(top, OpMaxF());
-  const float safe = top == -INFINITY ? 0.0f : top;
-  float all = 0.0f, a[kPer];
+    // part_at, with the width's division as a shift
+    const int shift = 31 - __clz(p.part_wide), d0 = lane * kPer;
+    const int offset =
+        ((((d0 >> shift) * p.part_rows) + r) << shift) + (d0 & (p.part_wide - 1));
+    if (!DSPARK_CHECK(c1 < gridDim.x && part_held(p, part_of(c0), r) &&
+                      part_held(p, part_of(c1), r) && offset + kPer <= p.part_rows * D))
+      return;
+    float top = -INFINITY;
+    for (int c = c0 + lane; c <= c1; c += 32) top = fmaxf(top, ws.stats[part_of(c) + r].x);
+    top = warp_reduce(top, OpMaxF());
+    const float safe = top == -INFINITY ? 0.0f : top;
+    float all = 0.0f, a[kPer];
 #pragma unroll
-  for (int d = 0; d < kPer; ++d) a[d] = 0.0f;
+    for (int d = 0; d < kPer; ++d) a[d] = 0.0f;
 #pragma unroll kAhead
-  for (int c = c0; c <= c1; ++c) {
-    const float2 st = ws.stats[part_of(c) + r];
-    const float* v = ws.rows + part_of(c) * D + offset;
-    float x[kPer];
-    if constexpr (kPer == 2) {
-      *reinterpret_cast<float2*>(x) = *reinterpret_cast<const float2*>(v);
-    } else {
+    for (int c = c0; c <= c1; ++c) {
+      const float2 st = ws.stats[part_of(c) + r];
+      const float* v = ws.rows + part_of(c) * D + offset;
+      float x[kPer];
+      if constexpr (kPer == 2) {
+        *reinterpret_cast<float2*>(x) = *reinterpret_cast<const float2*>(v);
+      } else {
 #pragma unroll
-      for (int d = 0; d < kPer; d += 4)
-        *reinterpret_cast<float4*>(x + d) = *reinterpret_cast<const float4*>(v + d);
+        for (int d = 0; d < kPer; d += 4)
+          *reinterpret_cast<float4*>(x + d) = *reinterpret_cast<const float4*>(v + d);
+      }
+      const float f = exp2_approx(st.x - safe);
+      all += st.y * f;
+#pragma unroll
+      for (int d = 0; d < kPer; ++d) a[d] += x[d] * f;
     }
-    const float f = exp2_approx(st.x - safe);
-    all += st.y * f;
+    const int node = row / p.group, h = at.head * p.group + row - node * p.group;
+    const int64_t to = ((int64_t)at.b * p.nodes + node) * p.heads + h;
+    if (!DSPARK_CHECK(row_held(p, to))) return;
+    const float inv = all == 0.0f ? 0.0f : 1.0f / all;
+    uint32_t w[kPer / 2];
 #pragma unroll
-    for (int d = 0; d < kPer; ++d) a[d] += x[d] * f;
-  }
-  const int node = row / p.group, h = at.head * p.group + row - node * p.group;
-  const int64_t to = ((int64_t)at.b * p.nodes + node) * p.heads + h;
-  if (!DSPARK_CHECK(row_held(p, to))) return;
-  const float inv = all == 0.0f ? 0.0f : 1.0f / all;
-  uint32_t w[kPer / 2];
-#pragma unroll
-  for (int d = 0; d < kPer; d += 2) w[d / 2] = H::pack(a[d] * inv, a[d + 1] * inv);
-  uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<T*>(p.out) + to * D) + lane * (kPer / 2);
-  if constexpr (kPer == 2)
-    *out = w[0];
-  else if constexpr (kPer == 4)
-    *reinterpret_cast<uint2*>(out) = make_uint2(w[0], w[1]);
-  else
-    *reinterpret_cast<uint4*>(out) = make_uint4(w[0], w[1], w[2], w[3]);
-  if (lane == 0 && p.lse)
-    p.lse[to] = all == 0.0f ? -INFINITY : (top + log2f(all)) * 0.6931471805599453f;
+    for (int d = 0; d < kPer; d += 2) w[d / 2] = H::pack(a[d] * inv, a[d + 1] * inv);
+    uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<T*>(p.out) + to * D) + lane * (kPer / 2);
+    if constexpr (kPer == 2)
+      *out = w[0];
+    else if constexpr (kPer == 4)
+      *reinterpret_cast<uint2*>(out) = make_uint2(w[0], w[1]);
+    else
+      *reinterpret_cast<uint4*>(out) = make_uint4(w[0], w[1], w[2], w[3]);
+    if (lane == 0 && p.lse)
+      p.lse[to] = all == 0.0f ? -INFINITY : (top + log2f(all)) * 0.6931471805599453f;
+  }();
+  for (int b = lost.first; b <= lost.last; ++b) p.status[b] = DSPARK_ST_TIMEOUT;
 }
 
 // ---------------------------------------------------------------- launches

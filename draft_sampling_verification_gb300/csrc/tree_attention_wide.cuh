@@ -241,11 +241,9 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   int64_t ranges[W::kStreams];
   find_range<kWideThreads, W::kStreams>(p, ws, sh.scan, sh.start, ranges);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (ranges[0] <= 0) {  // the second stream's range comes behind the first's
-    if (tid < W::kStreams && DSPARK_CHECK(blockIdx.x * W::kStreams + tid < p.max_ctas))
-      ws.lost[blockIdx.x * W::kStreams + tid] = {0, -1};
-    return;
-  }
+  if (tid < W::kStreams && DSPARK_CHECK(blockIdx.x * W::kStreams + tid < p.max_ctas))
+    ws.lost[blockIdx.x * W::kStreams + tid] = {0, -1};
+  if (ranges[0] <= 0) return;  // the second stream's range comes behind the first's
   const int r0 = (blockIdx.x % p.row_tiles) * W::kRows;
   // row tiles of one stream
   const int n_tiles = kMode == kBoth && p.nodes * p.group - r0 > 128 ? 2 : 1;
@@ -842,27 +840,26 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   }
   // After a wait that expired the requests of the range are refused.  What the CTA has written of
   // them may be unfinished: NaN takes its place, and in the parts the joining kernel's sums.
+  if (!sh.failed) return;
   for (int x = 0; x < W::kStreams; ++x) {
-    Lost lost = {0, -1};
-    if (sh.failed && ranges[x] > 0) {
-      Walk cur = walk_from(p, sh.start[x], ranges[x], p.item_cost);
-      lost.first = cur.b;
-      while (cur.advance(p, kKeys)) {
-        lost.last = cur.b;
-        const int64_t slot = cur.slot(blockIdx.x * W::kStreams + x) * p.part_rows;
-        for (int r = tid; r < min(W::kRows, p.nodes * p.group - r0); r += kWideThreads) {
-          const int node = (r0 + r) / p.group;
-          const int64_t to = ((int64_t)cur.b * p.nodes + node) * p.heads + cur.head * p.group +
-                             r0 + r - node * p.group;
-          if (!DSPARK_CHECK(cur.whole() ? row_held(p, to) : part_held(p, slot, r))) continue;
-          if (!cur.whole()) {
-            ws.stats[slot + r] = make_float2(NAN, NAN);
-            continue;
-          }
-          for (int d = 0; d < D; d += 2)
-            *reinterpret_cast<uint32_t*>(static_cast<T*>(p.out) + to * D + d) = H::pack(NAN, NAN);
-          if (p.lse) p.lse[to] = NAN;
+    if (ranges[x] <= 0) continue;
+    Walk cur = walk_from(p, sh.start[x], ranges[x], p.item_cost);
+    Lost lost = {cur.b, -1};
+    while (cur.advance(p, kKeys)) {
+      lost.last = cur.b;
+      const int64_t slot = cur.slot(blockIdx.x * W::kStreams + x) * p.part_rows;
+      for (int r = tid; r < min(W::kRows, p.nodes * p.group - r0); r += kWideThreads) {
+        const int node = (r0 + r) / p.group;
+        const int64_t to = ((int64_t)cur.b * p.nodes + node) * p.heads + cur.head * p.group + r0 +
+                           r - node * p.group;
+        if (!DSPARK_CHECK(cur.whole() ? row_held(p, to) : part_held(p, slot, r))) continue;
+        if (!cur.whole()) {
+          ws.stats[slot + r] = make_float2(NAN, NAN);
+          continue;
         }
+        for (int d = 0; d < D; d += 2)
+          *reinterpret_cast<uint32_t*>(static_cast<T*>(p.out) + to * D + d) = H::pack(NAN, NAN);
+        if (p.lse) p.lse[to] = NAN;
       }
     }
     if (tid == 0 && DSPARK_CHECK(blockIdx.x * W::kStreams + x < p.max_ctas))
