@@ -419,7 +419,8 @@ def dspark_kv_write(k, v, k_cache, v_cache, slots, rows=None, stream=None):
         raise ValueError("slots must hold one slot for each token")
     _call("dspark_kv_write", k.data_ptr(), v.data_ptr(),
           F32 if k.dtype is torch.float32 else code, step,
-          k.stride(-2) if k.shape[-2] > 1 else 0, n, k.shape[-2], k.shape[-1], kp, vp, code, sb, st, sh, k_cache.shape[0], k_cache.shape[1],
+          k.stride(-2) if k.shape[-2] > 1 else 0, n, k.shape[-2], k.shape[-1], kp, vp, code, sb,
+          st, sh, k_cache.shape[0], k_cache.shape[1],
           _arg("slots", slots, torch.int32, slots.shape),
           _arg("rows", rows, torch.int32, slots.shape), slots.numel(), _stream(stream))
 
@@ -510,7 +511,8 @@ def dspark_logits_process(logits, history, prompt_len, history_len, draft_tokens
 def _on_stream(helper):
     """Runs an allocating helper with its `stream` as torch's current one, so that outputs and
     workspaces are that stream's memory: of another stream's they could be given to its next
-    tensor while the kernels that write them are still to come."""
+    tensor while the kernels that write them are still to come.  (The helpers of a few us enter
+    the stream themselves: this wrapper costs 0.3.)"""
     at = list(inspect.signature(helper).parameters).index("stream")
 
     @functools.wraps(helper)
@@ -717,12 +719,15 @@ def target_probs(target_logits, want_p=True, stream=None):
     return p, am, st
 
 
-@_on_stream
 def cache_plan(ctx_len, new_len, max_new, page_size, block_table, free_blocks, n_free=None,
                parents=None, stream=None):
     """Grants the step's blocks and maps its new tokens; returns dict(block_table (the caller's,
     updated), slots, positions [B, max_new], taken [1], status [B]) and, for max_new <= 64,
     tree_mask int64 [B, max_new]."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return cache_plan(ctx_len, new_len, max_new, page_size, block_table, free_blocks,
+                              n_free, parents)
     B, dev, i32 = ctx_len.shape[0], ctx_len.device, torch.int32
     slots, taken, status = (_empty((B, max_new), i32, dev), _empty((1,), i32, dev),
                             _empty((B,), i32, dev))
@@ -746,11 +751,14 @@ def kv_write(k, v, k_cache, v_cache, slots, rows=None, stream=None):
     return k_cache, v_cache
 
 
-@_on_stream
 def tree_attention(q, k_cache, v_cache, block_table, ctx_len, n_nodes, tree_mask=None, scale=None,
                    stream=None):
     """Attention of the nodes over the cache (scale 1 / sqrt(head_dim) when None); returns (out
     like q, lse [B, nodes, n_heads], status [B])."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return tree_attention(q, k_cache, v_cache, block_table, ctx_len, n_nodes, tree_mask,
+                                  scale)
     B, nodes, heads, dim = q.shape
     dev = q.device
     out = _empty((B, nodes, heads, dim), q.dtype, dev)
@@ -764,13 +772,17 @@ def tree_attention(q, k_cache, v_cache, block_table, ctx_len, n_nodes, tree_mask
     return out, lse, st
 
 
-@_on_stream
 def logits_process(logits, history=None, prompt_len=None, history_len=None, draft_tokens=None,
                    row_mask=None, repetition=None, frequency=None, presence=None, bias_ids=None,
                    bias_values=None, n_bias=None, mask_words=None, mask_rows=None, out=None,
                    stream=None):
     """Penalties, biases and grammar masks on logits [B, rows, V]; returns (out (a new tensor when
     None; logits itself for in place), status [B])."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return logits_process(logits, history, prompt_len, history_len, draft_tokens, row_mask,
+                                  repetition, frequency, presence, bias_ids, bias_values, n_bias,
+                                  mask_words, mask_rows, out)
     if out is None:
         out = _empty(logits.shape, logits.dtype, logits.device)
     st = _empty((logits.shape[0],), torch.int32, logits.device)
