@@ -8,9 +8,10 @@
 // slice of the vocabulary of one request: it scans the text once, counts the
 // slice's tokens in shared memory (integer atomics: the counts do not depend
 // on their order), lists the touched ones, and goes with list and counts over
-// its share of the request's rows.  Bound by HBM; slices are long, since each
+// its share of the request's rows; tokens with more than one bias, which are
+// added in list order, in a pass of their own.  Bound by HBM; slices are long, since each
 // scans the whole text and has its own start and end.  256 requests of six
-// bf16 rows of 129,280 under masks take 136 us (5.8 TB/s), 64 of fp32 rows 72
+// bf16 rows of 129,280 under masks take 135 us (5.9 TB/s), 64 of fp32 rows 72
 // us (5.5 TB/s), one request of six rows 5 us.
 #include <cuda_bf16.h>
 

@@ -74,6 +74,14 @@ __device__ __forceinline__ float exp2_approx(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// The 16-bit types.  The softmax weights are rounded to the inputs' type for
+// the second product: the tensor instructions take both operands in one type,
+// and a second product for what the rounding leaves over would cost as much
+// as the first.  A weight is off by half a step, u of it (2^-8 bf16, 2^-11
+// f16), so a result by at most u sum p|v|, as much as by its own rounding
+// (against 64 bits 1.2 to 1.35 times the error of fp32 weights, bf16 2.1e-3
+// relative).  The sum is taken before the rounding, as lse would be off by u
+// after it.
 template <typename T>
 struct Half;
 template <>
@@ -140,7 +148,14 @@ __device__ __forceinline__ uint32_t without_special(uint32_t w) {
 // counts for item_cost tiles more, ahead of its first: the time that its
 // queries, its first copies and its results take, without which the teams
 // that get many short items end last.  (A pair of ranges in one CTA counts as
-// two CTAs here.)
+// two CTAs here.)  The costs by kernel, from what an item takes beside its
+// tiles, and requests of mixed lengths at 0, about half, the value and double
+// of it (us): streaming, 64 requests of 300 to 8,000 tokens and 4 rows, 113,
+// 103, 107, 113 (of 300 tokens 66, 66, 67, 68); kPair, the same with 24 rows,
+// 115, 112, 113, 114; kBoth, 64 of 30 to 1,000 tokens and 512 rows, 138, 95,
+// 89, 100 (head_dim 64: 98, 69, 74, 84); kOne, 64 of 300 to 8,000 tokens, 219
+// at 0, 210 at 1, 204 at 2, 206 at 4.  The streaming and kOne values are not
+// their best.
 // A range is at least kMinRange long: the join of more parts costs more than they save.
 constexpr int kMinRange = 3;
 constexpr int kStreamCost = 5, kPairCost = 2, kBothCost = 8, kOneCost = 1;
@@ -358,8 +373,8 @@ __device__ __forceinline__ void find_range(const Params& p, const Workspace& ws,
     }
   }
   // teams without work: nothing to join
-  for (int t = c.teams + blockIdx.x * kBlock + threadIdx.x; t < (int)gridDim.x * kStreams / p.row_tiles;
-       t += gridDim.x * kBlock)
+  for (int t = c.teams + blockIdx.x * kBlock + threadIdx.x;
+       t < (int)gridDim.x * kStreams / p.row_tiles; t += gridDim.x * kBlock)
     if (DSPARK_CHECK(t < p.max_ctas)) ws.seam[t] = {0, 0, -1, 0};
   __syncthreads();
 }
@@ -388,7 +403,7 @@ __device__ __forceinline__ void find_range(const Params& p, const Workspace& ws,
 //
 // Bound by HBM: 16 steps of 8 KB are in flight per SM at head_dim 128.  256
 // items of 4,000 tokens and 8 rows take 90 us (5.8 TB/s), two requests of
-// 100,000 tokens 132 us (6.2 TB/s).
+// 100,000 tokens 133 us (6.1 TB/s).
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kKeys = 16;
@@ -729,7 +744,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, N8, MW>::kCtas)
 #pragma unroll
         for (int g = 0; g < KW; ++g) {
           const float f = s_factor[g][r];
-          const float4 v = *reinterpret_cast<const float4*>(joined + (g * kRows + r) * S::kPitch + d);
+          const float4 v =
+              *reinterpret_cast<const float4*>(joined + (g * kRows + r) * S::kPitch + d);
           a.x += v.x * f;
           a.y += v.y * f;
           a.z += v.z * f;
@@ -831,7 +847,8 @@ __global__ void __launch_bounds__(kJoinThreads)
     uint32_t w[kPer / 2];
 #pragma unroll
     for (int d = 0; d < kPer; d += 2) w[d / 2] = H::pack(a[d] * inv, a[d + 1] * inv);
-    uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<T*>(p.out) + to * D) + lane * (kPer / 2);
+    uint32_t* out =
+        reinterpret_cast<uint32_t*>(static_cast<T*>(p.out) + to * D) + lane * (kPer / 2);
     if constexpr (kPer == 2)
       *out = w[0];
     else if constexpr (kPer == 4)
@@ -872,7 +889,9 @@ inline int stream_rows(int rows, int dim) {
 // Rows up to which the streaming kernel is taken (256 items of 4,000 tokens / 4,096 of 60, us,
 // against the tensor kernel).  head_dim 64: 16 rows 55 / 38 against 59 / 50, 24 rows 67 / 81
 // against 60 / 73.  128: 8 rows 88 / 62 against 92 / 62, 16 rows 91 / 83 against 93 / 63.  256:
-// 1 row 185 / 120 against 163 / 135, 8 rows 187 / 159 against 166 / 142.
+// 1 row 185 / 120 against 163 / 135, 8 rows 187 / 159 against 166 / 142.  These are batches: one
+// request alone, of 4,000 tokens with 24 rows at head_dim 64, takes 16.2 streaming and 16.9 in the
+// tensor kernel.
 constexpr int few_rows(int dim) { return dim == 64 ? 16 : dim == 128 ? 8 : 0; }
 // the workspace's ranges, by kernel (160 SMs at most are used), and the rows of
 // each: those that the item has, of a CTA's

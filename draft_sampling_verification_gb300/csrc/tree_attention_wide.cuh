@@ -139,24 +139,26 @@ __device__ __forceinline__ void tmem_wait_store() {
 // share the tensor cores.  (With tiles of 128 positions, whose scores fill
 // the place of two, a row tile's products and softmax wait for one another:
 // 1,024 one-row-tile items of 300 tokens 105 us instead of 86, wide trees 165
-// instead of 146; head_dim 64, 2,048 items of 300 tokens 82 instead of 60.)
+// instead of 146 at that time; head_dim 64, 2,048 items of 300 tokens 82
+// instead of 60.)
 //
 // kPair: items of up to 128 rows.  The warpgroups go along two ranges of the
 //   tile axis, each with its own queries and its own copies of keys and
 //   values: two CTAs in one, of which one's starts and results are hidden
 //   behind the other's products.  Bound by HBM: 256 items of 4,000 tokens
-//   take 96 us with 24 rows, 114 us with 128 (5.5 and 4.8 TB/s), two
-//   requests of 131,000 tokens 175 us (6.1 TB/s).
+//   take 95 us with 24 rows, 113 us with 128 (5.6 and 4.8 TB/s), two
+//   requests of 131,000 tokens 174 us (6.2 TB/s).
 // kBoth: items of more rows.  The warpgroups take two row tiles of one item
 //   and share its keys and values.  Bound by the products (2 * 2 * 128 * 64 *
 //   D operations a row tile and tile of positions) and by their issue: 256
-//   items of 4,000 tokens and 512 rows take 207 us, 1.3 PFLOP/s; 16 requests
-//   with trees of 64 nodes and 8 query heads to a cached head 146 us.  A row
+//   items of 4,000 tokens and 512 rows take 205 us, 1.3 PFLOP/s; 16 requests
+//   with trees of 64 nodes and 8 query heads to a cached head 134 to 140 us.  A row
 //   tile's twelve products take 640 cycles, as the scores' operands come at
 //   the rate of shared memory; the two row tiles' take 1,550 in the loop.
 // kOne: head_dim 256, whose accumulators fill half the tensor memory: one
 //   warpgroup and one row tile.  256 items of 4,000 tokens take 173 us with
-//   24 rows (6.2 TB/s).
+//   24 rows (6.1 TB/s), 466 us with 512, whose four row tiles are four CTAs
+//   that copy the same keys, three of them from L2.
 //
 // A score that passes the row's reference by more than 8 has the accumulators
 // rescaled by the softmax warpgroup, once the products before are done; this
@@ -605,7 +607,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           float* out = part_at(ws, slot, p.part_rows, kWide, part_row, D, c * 32);
 #pragma unroll
           for (int j = 0; j < 32; j += 8)
-            asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(out + j / kWide * (p.part_rows * kWide) + j % kWide),
+            asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(
+                             out + j / kWide * (p.part_rows * kWide) + j % kWide),
                          "f"(v[j]), "f"(v[j + 1]), "f"(v[j + 2]), "f"(v[j + 3]), "f"(v[j + 4]),
                          "f"(v[j + 5]), "f"(v[j + 6]), "f"(v[j + 7])
                          : "memory");

@@ -598,9 +598,9 @@ int dspark_cache_plan(const int32_t* ctx_len, const int32_t* new_len, int32_t B,
  * or DSPARK_F16; src_dtype the same, or DSPARK_F32, rounded to the nearest
  * (ties to even) as it is written.  With rows and slots a committed path's
  * nodes can be written again to the positions that follow the text.
- * head_dim a multiple of 8 in [8, 1024]; all four pointers 16-byte aligned,
- * source and cache strides multiples of 16 bytes (DSPARK_ERR_ALIGN);
- * n_blocks*page_size < 2^31.
+ * head_dim a multiple of 8 in [8, 1024]; n_heads in [1, 65,535]; all four
+ * pointers 16-byte aligned, source and cache strides multiples of 16 bytes
+ * (DSPARK_ERR_ALIGN); n_blocks*page_size < 2^31.
  */
 int dspark_kv_write(const void* k, const void* v, int32_t src_dtype, int64_t src_token_stride,
                     int64_t src_head_stride, int32_t n_src, int32_t n_heads, int32_t head_dim,
@@ -624,7 +624,9 @@ int dspark_kv_write(const void* k, const void* v, int32_t src_dtype, int64_t src
  * not see do not reach it, whatever they hold.
  * Products take the 16-bit inputs; scores, maxima, sums and accumulators are
  * fp32; the softmax weights are rounded to the inputs' type for the second
- * product (the sum is taken before that), and out is rounded once.
+ * product (the sum is taken before that), and out is rounded once.  What lies
+ * 2^-24 below a row's accumulator is lost to it, as in any fp32 sum: where one
+ * key outweighs 100,000 others by 2^25 each, their 0.3 % in all.
  *
  * q: element (request, node, head, d) at request*q_req_stride +
  * node*q_node_stride + head*q_head_stride + d.  out [B][nodes][n_heads]
@@ -634,12 +636,13 @@ int dspark_kv_write(const void* k, const void* v, int32_t src_dtype, int64_t src
  * tokens than max_blocks*page_size (every row of the request gets out 0);
  * TIMEOUT for a request that shares a kernel range with a wait that expired
  * (2 s): its rows hold their result or NaN, out and lse alike.
- * Limits: head_dim 64, 128 or 256; 1 <= nodes <= DSPARK_MAX_NODES; n_heads a
- * multiple of n_kv_heads, at most 64 times it; q, out, caches and workspace
+ * Limits: head_dim 64, 128 or 256; 1 <= nodes <= DSPARK_MAX_NODES; B <=
+ * 65,535; n_kv_heads <= 1,024; n_heads a multiple of it, at most 64 times it;
+ * n_blocks*page_size < 2^31; strides >= 0; q, out, caches and workspace
  * 16-byte aligned and their strides multiples of 8 elements; max_blocks*
  * page_size <= 2^30.  |scale| < 2.3e38 (DSPARK_ERR_ARG otherwise).
  * workspace: dspark_tree_attention_workspace_bytes(...) bytes of device
- * memory owned by the caller, with no content to keep (3 to 90 MB); calls that
+ * memory owned by the caller, with no content to keep (2.6 to 43 MB); calls that
  * may overlap need separate ones.  The result does not depend on the batch's
  * other requests beyond the order of fp32 sums, and is the same from run to
  * run.
@@ -685,7 +688,7 @@ int dspark_tree_attention(const void* q, int32_t dtype, int64_t q_req_stride,
  * mask_words NULL: no masks.  history, history_len NULL: no text;
  * prompt_len NULL: all of it generated.  Lengths are read as at least 0 and
  * at most history_ld, max_bias; prompt_len as at most history_len.
- * req_status[B].  Limits: rows in [1, DSPARK_MAX_NODES], n_drafts in
+ * req_status[B].  Limits: B <= 65,535, rows in [1, DSPARK_MAX_NODES], n_drafts in
  * [0, DSPARK_MAX_NODES], 0 <= history_ld < 2^24, 0 <= max_bias <= 65535.
  */
 int dspark_logits_process(const void* logits, int32_t dtype, int64_t ld, int32_t B, int32_t rows,
