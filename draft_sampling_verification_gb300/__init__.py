@@ -4,7 +4,8 @@ Thin Python binding of the C ABI in ``include/dspark.h``: the functions named
 like the C calls (``dspark_q_build``, ``dspark_draft_sample``,
 ``dspark_verify_greedy``, ``dspark_verify_ratio``, ``dspark_target_probs``,
 ``dspark_cache_plan``, ``dspark_kv_write``, ``dspark_tree_attention``,
-``dspark_logits_process``)
+``dspark_logits_process``, ``dspark_qk_rotate``, ``dspark_rotate_write``,
+``dspark_latent_write``, ``dspark_latent_attention``)
 take torch CUDA tensors, pass their device pointers, sizes and the current
 stream to libdspark.so, and raise on a nonzero return.  Every step of the
 path runs in the library's CUDA kernels; torch only provides device memory
@@ -27,6 +28,7 @@ ST_OK, ST_NONFINITE, ST_ZERO_MASS, ST_ALLOC_INCONSISTENT = 0, 1, 2, 3
 ST_BAD_TEMPERATURE, ST_BAD_Q, ST_BAD_DRAFT, ST_TIMEOUT, ST_INTERNAL = 4, 5, 6, 7, 8
 ST_BAD_CHECKSUM, ST_NO_BLOCKS, ST_BAD_LENGTH, ST_BAD_TREE, ST_BAD_PENALTY = 9, 10, 11, 12, 13
 MAX_NODES = 64
+ROPE_PLAIN, ROPE_LINEAR, ROPE_PARTS = 0, 1, 2
 FLAG_AMBIG_ACCEPT, FLAG_NEAR_BOUNDARY, FLAG_DEGENERATE = 1, 2, 4
 SCHEDULE_AUTO, SCHEDULE_ONE_LAUNCH, SCHEDULE_SEPARATE = 0, 1, 2
 PURPOSE_PROPOSAL, PURPOSE_ACCEPT, PURPOSE_RESIDUAL, PURPOSE_BONUS, PURPOSE_MATCH = 0, 1, 2, 3, 4
@@ -42,7 +44,10 @@ __all__ = ["dspark_q_build", "dspark_q_build_sample", "dspark_draft_sample", "ds
            "draft_sample", "verify_greedy", "verify_ratio", "target_probs", "q_build_sample",
            "spec_step", "version", "dspark_cache_plan", "cache_plan", "dspark_kv_write", "kv_write",
            "dspark_tree_attention", "dspark_tree_attention_workspace_bytes", "tree_attention",
-           "dspark_logits_process", "logits_process"]
+           "dspark_logits_process", "logits_process", "dspark_rope_table", "rope_table",
+           "dspark_qk_rotate", "qk_rotate", "dspark_rotate_write", "rotate_write",
+           "dspark_latent_write", "latent_write", "dspark_latent_attention",
+           "dspark_latent_attention_workspace_bytes", "latent_attention"]
 
 
 def version() -> str:
@@ -507,6 +512,218 @@ def dspark_logits_process(logits, history, prompt_len, history_len, draft_tokens
           _arg("req_status", req_status, i32, one), _stream(stream))
 
 
+def dspark_rope_table(rot_dim, base, scaling, factor, original_len, low, high, inv_freq, table):
+    """table: host int64 [rot_dim / 2] (holding the uint64 turns); inv_freq: host float64
+    [rot_dim / 2] or None.  The one call that needs no GPU."""
+    pairs = (rot_dim // 2,)
+    for name, t, dtype in (("inv_freq", inv_freq, torch.float64), ("table", table, torch.int64)):
+        if t is not None and (t.dtype is not dtype or tuple(t.shape) != pairs):
+            raise ValueError("%s must be %s of shape %s" % (name, dtype, pairs))
+    _call("dspark_rope_table", int(rot_dim), float(base), int(scaling), float(factor),
+          float(original_len), float(low), float(high), _host(inv_freq), _host(table))
+
+
+_ELEMENTS = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
+
+
+def _head_args(name, t):
+    """(dtype code, pointer, token stride, head stride, tokens, heads, head_dim) of a tensor
+    [.., n_heads, head_dim] whose tokens are uniformly strided."""
+    if t.dtype not in _ELEMENTS:
+        raise TypeError("%s must be float32, bfloat16 or float16, got %s" % (name, t.dtype))
+    shape, strides = t.shape, t.stride()
+    if len(shape) < 3 or (strides[-1] != 1 and shape[-1] > 1) or not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor [.., n_heads, head_dim], contiguous in head_dim"
+                         % name)
+    n, step = _uniform(t, len(shape) - 2, "the tokens of " + name)
+    return (_ELEMENTS[t.dtype], t.data_ptr(), step, strides[-2] if shape[-2] > 1 else 0, n,
+            shape[-2], shape[-1])
+
+
+def _written(name, t, heads):
+    """Refuses an output whose elements share a place, by the arguments of _head_args."""
+    _, _, token, head, n, n_heads, dim = heads
+    if (n_heads > 1 and head < dim) or (n > 1 and token < dim):
+        raise ValueError("the tokens and heads of %s must not overlap" % name)
+
+
+def _table_arg(table, rot_start):
+    """(pointer, rot_start, rot_dim) of a rotation's table (None: no rotation)."""
+    if table is None:
+        return None, 0, 0
+    return _arg("table", table, torch.int64, table.shape), rot_start, 2 * table.numel()
+
+
+def dspark_qk_rotate(q, k, positions, table, q_weight, k_weight, eps, rot_start, interleaved,
+                     magnitude, q_out, k_out, stream=None):
+    """q, k [.., n_heads, head_dim] (either may be None, with its output) of one type, with the
+    same tokens and head_dim; positions int32 of n_tokens; table int64 [rot_dim / 2] of
+    rope_table, on the device, or None (norms alone); weights float32 [head_dim] or None; q_out,
+    k_out like q, k in shape, of one type: the sources' or, for float32 sources, a 16-bit one."""
+    none = (0, None, 0, 0, 0, 0, 0)
+    a, b = (none if t is None else _head_args(n, t) for n, t in (("q", q), ("k", k)))
+    some = a if q is not None else b
+    if some is none:
+        raise ValueError("q or k is needed")
+    if q is not None and k is not None and (a[0] != b[0] or a[4] != b[4] or a[6] != b[6]):
+        raise ValueError("q and k must have the same type, tokens and head_dim")
+    outs = []
+    for name, t, o, x in (("q_out", q, q_out, a), ("k_out", k, k_out, b)):
+        if t is None:
+            outs.append(none)
+            continue
+        outs.append(_head_args(name, o))
+        if o.shape != t.shape:
+            raise ValueError("%s must have its source's shape" % name)
+        _written(name, o, outs[-1])
+    if q is not None and k is not None and outs[0][0] != outs[1][0]:
+        raise TypeError("q_out and k_out must have the same type")
+    code = outs[0][0] if q is not None else outs[1][0]
+    n, dim = some[4], some[6]
+    tp, start, rot = _table_arg(table, rot_start)
+    _call("dspark_qk_rotate", a[1], b[1], some[0], a[2], a[3], b[2], b[3], n, a[5], b[5], dim,
+          _arg("q_weight", q_weight, torch.float32, (dim,)),
+          _arg("k_weight", k_weight, torch.float32, (dim,)), eps,
+          _positions(positions, n), tp, start, rot, int(interleaved), magnitude, outs[0][1],
+          outs[0][2], outs[0][3], outs[1][1], outs[1][2], outs[1][3], code, _stream(stream))
+
+
+def _positions(positions, n):
+    if positions.numel() != n:
+        raise ValueError("positions must hold one position for each token")
+    return _arg("positions", positions, torch.int32, positions.shape)
+
+
+def dspark_rotate_write(q, k, v, positions, table, k_cache, v_cache, slots, rows, q_weight,
+                        k_weight, eps, rot_start, interleaved, magnitude, q_out, stream=None):
+    """q [.., n_heads, head_dim] or None (with q_out), k, v [.., n_kv_heads, head_dim] of the same
+    strides, all float32 or the caches' type; positions, slots int32 of n_tokens; rows int32 of
+    n_tokens (q None) or None (then n_tokens is the number of tokens of k, and of q); the caches as
+    in dspark_kv_write; q_out like q, of the caches' type; the rest as in dspark_qk_rotate."""
+    code, kp, vp, sb, st, sh = _cache_args(k_cache, v_cache)
+    x = _head_args("k", k)
+    if v.shape != k.shape or v.dtype is not k.dtype or not v.is_cuda:
+        raise ValueError("k and v must be CUDA tensors of the same shape and type")
+    if v.stride() != k.stride() and any(
+            i != j and size > 1 for i, j, size in zip(k.stride(), v.stride(), k.shape)):
+        raise ValueError("k and v must have the same strides")
+    if k.shape[-2:] != k_cache.shape[-2:]:
+        raise ValueError("k and v must have the caches' heads and head_dim")
+    if x[0] != F32 and x[0] != code:
+        raise TypeError("q, k and v must be float32 or of the caches' type")
+    n, dim = slots.numel(), x[6]
+    if rows is None and n != x[4]:
+        raise ValueError("slots must hold one slot for each token")
+    a = o = (0, None, 0, 0, 0, 0, 0)
+    if q is not None:
+        a, o = _head_args("q", q), _head_args("q_out", q_out)
+        if a[0] != x[0] or a[4] != n or a[6] != dim:
+            raise ValueError("q and k must have the same type, tokens and head_dim")
+        if q_out.shape != q.shape or o[0] != code:
+            raise ValueError("q_out must have q's shape and the caches' type")
+        _written("q_out", q_out, o)
+    tp, start, rot = _table_arg(table, rot_start)
+    _call("dspark_rotate_write", a[1], x[1], v.data_ptr(), x[0], a[2], a[3], x[2], x[3], x[4],
+          a[5], x[5], dim, _arg("q_weight", q_weight, torch.float32, (dim,)),
+          _arg("k_weight", k_weight, torch.float32, (dim,)), eps, _positions(positions, n), tp,
+          start, rot, int(interleaved), magnitude, o[1], o[2], o[3], kp, vp, code, sb, st, sh,
+          k_cache.shape[0], k_cache.shape[1], _arg("slots", slots, torch.int32, slots.shape),
+          _arg("rows", rows, torch.int32, slots.shape), n, _stream(stream))
+
+
+def _latent_cache_args(cache):
+    """(dtype code, pointer, block stride, token stride) of a cache [n_blocks, page_size, width]."""
+    if cache.dtype not in _HALF:
+        raise TypeError("the cache must be bfloat16 or float16")
+    if cache.dim() != 3 or cache.stride(2) != 1 or not cache.is_cuda:
+        raise ValueError("the cache must be a CUDA tensor [n_blocks, page_size, latent_dim + "
+                         "rope_dim], contiguous in its last dimension")
+    blocks, page, width = cache.shape
+    # a dimension of one element may have any stride
+    token = cache.stride(1) if page > 1 else width
+    return (_HALF[cache.dtype], cache.data_ptr(),
+            cache.stride(0) if blocks > 1 else max(token, page * token), token)
+
+
+def _token_args(name, t):
+    """(pointer, token stride, tokens, width) of a tensor [.., width] of uniformly strided tokens."""
+    if t.dim() < 2 or (t.stride(-1) != 1 and t.shape[-1] > 1) or not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor [.., width], contiguous in its last dimension"
+                         % name)
+    n, step = _uniform(t, t.dim() - 1, "the tokens of " + name)
+    return t.data_ptr(), step, n, t.shape[-1]
+
+
+def dspark_latent_write(c, k_rope, positions, table, cache, slots, rows, weight, eps, interleaved,
+                        magnitude, stream=None):
+    """c [.., latent_dim] and k_rope [.., rope_dim] (None: rope_dim 0) of the same tokens, float32
+    or the cache's type; cache [n_blocks, page_size, latent_dim + rope_dim]; positions, slots int32
+    of n_tokens; rows int32 of n_tokens or None (then n_tokens is the number of source tokens);
+    table int64 [rope_dim / 2] of rope_table, on the device; weight float32 [latent_dim] or None."""
+    code, cp, sb, st = _latent_cache_args(cache)
+    p, step, n_src, latent = _token_args("c", c)
+    rp, r_step, rope = None, 0, 0
+    if k_rope is not None:
+        rp, r_step, n_rope, rope = _token_args("k_rope", k_rope)
+        if n_rope != n_src or k_rope.dtype is not c.dtype:
+            raise ValueError("c and k_rope must have the same tokens and type")
+        if table is None or 2 * table.numel() != rope:
+            raise ValueError("table must hold one entry for each pair of k_rope")
+    if c.dtype is not torch.float32 and c.dtype is not cache.dtype:
+        raise TypeError("c must be float32 or of the cache's type")
+    if cache.shape[2] != latent + rope:
+        raise ValueError("the cache's rows must hold c and k_rope")
+    n = slots.numel()
+    if rows is None and n != n_src:
+        raise ValueError("slots must hold one slot for each token")
+    _call("dspark_latent_write", p, step, rp, r_step, _ELEMENTS[c.dtype], n_src, latent, rope,
+          _arg("weight", weight, torch.float32, (latent,)), eps, _positions(positions, n),
+          _table_arg(table, 0)[0] if rope else None, int(interleaved), magnitude, cp, code, sb, st,
+          cache.shape[0], cache.shape[1], _arg("slots", slots, torch.int32, slots.shape),
+          _arg("rows", rows, torch.int32, slots.shape), n, _stream(stream))
+
+
+@functools.lru_cache(maxsize=256)
+def dspark_latent_attention_workspace_bytes(B, nodes, n_heads, latent_dim):
+    return int(_lib.load().dspark_latent_attention_workspace_bytes(B, nodes, n_heads, latent_dim))
+
+
+def dspark_latent_attention(q, cache, block_table, ctx_len, n_nodes, latent_dim, tree_mask, scale,
+                            out, lse, req_status, workspace, stream=None):
+    """q [B, nodes, n_heads, latent_dim + rope_dim] (strided, contiguous in its last dimension) of
+    the cache's type; cache [n_blocks, page_size, latent_dim + rope_dim]; out [B, nodes, n_heads,
+    latent_dim] and lse float32 [B, nodes, n_heads] (or None) contiguous; workspace: uint8, at
+    least dspark_latent_attention_workspace_bytes bytes; the rest as in dspark_tree_attention."""
+    B, nodes, heads = q.shape[:3]
+    need = dspark_latent_attention_workspace_bytes(B, nodes, heads, latent_dim)
+    if workspace.numel() * workspace.element_size() < need:
+        raise ValueError("the workspace is too small")
+    _latent_attention(q, cache, block_table, ctx_len, n_nodes, latent_dim, tree_mask, scale,
+                      _arg("out", out, q.dtype, (B, nodes, heads, latent_dim)),
+                      _arg("lse", lse, torch.float32, (B, nodes, heads)),
+                      _arg("req_status", req_status, torch.int32, (B,)), _ptr(workspace), stream)
+
+
+def _latent_attention(q, cache, block_table, ctx_len, n_nodes, latent_dim, tree_mask, scale, out,
+                      lse, req_status, workspace, stream):
+    """The call, with outputs and workspace as pointers."""
+    code, cp, sb, st = _latent_cache_args(cache)
+    i32, strides = torch.int32, q.stride()
+    if q.dim() != 4 or q.dtype is not cache.dtype or strides[3] != 1 or not q.is_cuda:
+        raise ValueError("q must be a CUDA tensor [B, nodes, n_heads, latent_dim + rope_dim] of "
+                         "the cache's type, contiguous in its last dimension")
+    B, nodes, heads, width = q.shape
+    n_blocks, page, row = cache.shape
+    if row != width:
+        raise ValueError("q and the cache's rows must have the same width")
+    table, ld, wide = _table_args(block_table, B)
+    _call("dspark_latent_attention", q.data_ptr(), code, strides[0], strides[1], strides[2], B,
+          nodes, heads, latent_dim, width - latent_dim, cp, sb, st, n_blocks, page, table, ld,
+          wide, _arg("ctx_len", ctx_len, i32, (B,)), _arg("n_nodes", n_nodes, i32, (B,)),
+          _arg("tree_mask", tree_mask, torch.int64, (B, nodes)), scale, out, lse, req_status,
+          workspace, _stream(stream))
+
+
 # --------------------------------------------------- allocating helpers
 def _on_stream(helper):
     """Runs an allocating helper with its `stream` as torch's current one, so that outputs and
@@ -790,3 +1007,81 @@ def logits_process(logits, history=None, prompt_len=None, history_len=None, draf
                           repetition, frequency, presence, bias_ids, bias_values, n_bias,
                           mask_words, mask_rows, out, st, stream)
     return out, st
+
+
+_SCALINGS = {None: ROPE_PLAIN, "linear": ROPE_LINEAR, "parts": ROPE_PARTS}
+
+
+def rope_table(rot_dim, base=10000.0, scaling=None, factor=1.0, original_len=1.0, low=1.0,
+               high=32.0, inv_freq=None, device=None):
+    """The table of a rotation of rot_dim elements, int64 [rot_dim / 2] on the device (the current
+    CUDA device when None), made once and kept.  scaling: None, "linear" or "parts"; inv_freq:
+    radians a position, a sequence or a tensor, in place of base's."""
+    if scaling not in _SCALINGS:
+        raise ValueError("scaling must be None, 'linear' or 'parts', got %r" % (scaling,))
+    if inv_freq is not None:
+        inv_freq = torch.as_tensor(inv_freq).detach().to("cpu", torch.float64).contiguous()
+    table = torch.empty((rot_dim // 2,), dtype=torch.int64)
+    dspark_rope_table(rot_dim, base, _SCALINGS[scaling], factor, original_len, low, high, inv_freq,
+                      table)
+    return table.to("cuda" if device is None else device)
+
+
+def qk_rotate(q, k, positions, table, q_weight=None, k_weight=None, eps=1e-6, rot_start=0,
+              interleaved=False, magnitude=1.0, out=None, stream=None):
+    """Norms (with weights) and rotates queries and keys [.., n_heads, head_dim] (either may be
+    None) by their tokens' positions; returns (q_out, k_out): new tensors, or the pair `out`, which
+    may be (q, k) themselves."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return qk_rotate(q, k, positions, table, q_weight, k_weight, eps, rot_start,
+                             interleaved, magnitude, out)
+    if out is None:
+        out = tuple(None if t is None else _empty(t.shape, t.dtype, t.device) for t in (q, k))
+    dspark_qk_rotate(q, k, positions, table, q_weight, k_weight, eps, rot_start, interleaved,
+                     magnitude, out[0], out[1], stream)
+    return out[0], out[1]
+
+
+def rotate_write(q, k, v, positions, table, k_cache, v_cache, slots, rows=None, q_weight=None,
+                 k_weight=None, eps=1e-6, rot_start=0, interleaved=False, magnitude=1.0, out=None,
+                 stream=None):
+    """qk_rotate whose keys go to their slots of the cache, with the values; returns (q_out (a new
+    tensor of the caches' type, `out`, or None without q), k_cache, v_cache)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return rotate_write(q, k, v, positions, table, k_cache, v_cache, slots, rows, q_weight,
+                                k_weight, eps, rot_start, interleaved, magnitude, out)
+    if out is None and q is not None:
+        out = _empty(q.shape, k_cache.dtype, q.device)
+    dspark_rotate_write(q, k, v, positions, table, k_cache, v_cache, slots, rows, q_weight,
+                        k_weight, eps, rot_start, interleaved, magnitude, out, stream)
+    return out, k_cache, v_cache
+
+
+def latent_write(c, k_rope, positions, table, cache, slots, rows=None, weight=None, eps=1e-6,
+                 interleaved=False, magnitude=1.0, stream=None):
+    """Writes tokens' normed latent vectors and rotated parts into their slots; returns the cache."""
+    dspark_latent_write(c, k_rope, positions, table, cache, slots, rows, weight, eps, interleaved,
+                        magnitude, stream)
+    return cache
+
+
+def latent_attention(q, cache, block_table, ctx_len, n_nodes, latent_dim, scale, tree_mask=None,
+                     stream=None):
+    """Attention of the nodes over a latent cache, absorbed form; returns (out [B, nodes, n_heads,
+    latent_dim], lse [B, nodes, n_heads], status [B])."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return latent_attention(q, cache, block_table, ctx_len, n_nodes, latent_dim, scale,
+                                    tree_mask)
+    B, nodes, heads = q.shape[:3]
+    dev = q.device
+    out = _empty((B, nodes, heads, latent_dim), q.dtype, dev)
+    lse = _empty((B, nodes, heads), torch.float32, dev)
+    st = _empty((B,), torch.int32, dev)
+    ws = _empty((dspark_latent_attention_workspace_bytes(B, nodes, heads, latent_dim),),
+                torch.uint8, dev)
+    _latent_attention(q, cache, block_table, ctx_len, n_nodes, latent_dim, tree_mask, scale,
+                      out.data_ptr(), lse.data_ptr(), st.data_ptr(), ws.data_ptr(), stream)
+    return out, lse, st

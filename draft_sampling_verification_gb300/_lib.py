@@ -17,7 +17,7 @@ HEADERS = [os.path.join(INCLUDE, "dspark.h"), os.path.join(INCLUDE, "dspark_debu
 
 _P = ctypes.c_void_p
 _I32, _I64, _U64, _U32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_uint64, ctypes.c_uint32
-_F32 = ctypes.c_float
+_F32, _F64 = ctypes.c_float, ctypes.c_double
 
 SIGNATURES = {
     "dspark_q_build": [_P, _I32, _I64, _I32, _I32, _P, _I32, _P, _P, _P, _P, _P],
@@ -52,6 +52,17 @@ SIGNATURES = {
     "dspark_tree_attention": [_P, _I32, _I64, _I64, _I64, _I32, _I32, _I32, _I32, _I32, _P, _P,
                               _I64, _I64, _I64, _I32, _I32, _P, _I64, _I32, _P, _P, _P, _F32, _P,
                               _P, _P, _P, _P],
+    "dspark_rope_table": [_I32, _F64, _I32, _F64, _F64, _F64, _F64, _P, _P],
+    "dspark_qk_rotate": [_P, _P, _I32, _I64, _I64, _I64, _I64, _I32, _I32, _I32, _I32, _P, _P, _F32,
+                         _P, _P, _I32, _I32, _I32, _F32, _P, _I64, _I64, _P, _I64, _I64, _I32, _P],
+    "dspark_rotate_write": [_P, _P, _P, _I32, _I64, _I64, _I64, _I64, _I32, _I32, _I32, _I32, _P,
+                            _P, _F32, _P, _P, _I32, _I32, _I32, _F32, _P, _I64, _I64, _P, _P, _I32,
+                            _I64, _I64, _I64, _I32, _I32, _P, _P, _I32, _P],
+    "dspark_latent_write": [_P, _I64, _P, _I64, _I32, _I32, _I32, _I32, _P, _F32, _P, _P, _I32,
+                            _F32, _P, _I32, _I64, _I64, _I32, _I32, _P, _P, _I32, _P],
+    "dspark_latent_attention": [_P, _I32, _I64, _I64, _I64, _I32, _I32, _I32, _I32, _I32, _P, _I64,
+                                _I64, _I32, _I32, _P, _I64, _I32, _P, _P, _P, _F32, _P, _P, _P, _P,
+                                _P],
     "dspark_logits_process": [_P, _I32, _I64, _I32, _I32, _I32, _P, _I64, _P, _P, _P, _I32, _P, _P,
                               _P, _P, _P, _P, _I32, _P, _P, _I64, _I32, _P, _P, _I64, _P, _P],
     "dspark_debug_exp_weights": [_P, _I64, _P, _P, _P],
@@ -95,6 +106,8 @@ def load(path: str = LIB_PATH):
             lib.dspark_spec_step_host_staging_bytes.restype = ctypes.c_int64
             lib.dspark_tree_attention_workspace_bytes.argtypes = [_I32, _I32, _I32, _I32, _I32]
             lib.dspark_tree_attention_workspace_bytes.restype = ctypes.c_int64
+            lib.dspark_latent_attention_workspace_bytes.argtypes = [_I32, _I32, _I32, _I32]
+            lib.dspark_latent_attention_workspace_bytes.restype = ctypes.c_int64
             lib.dspark_version.argtypes = []
             lib.dspark_version.restype = ctypes.c_char_p
             _lib = lib

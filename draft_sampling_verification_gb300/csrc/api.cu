@@ -2,6 +2,8 @@
 // code only: argument checks (nothing is launched on a bad argument), then
 // one kernel launch on the caller's stream.  No allocation, no host sync.
 #include <nvtx3/nvToolsExt.h>
+#include <cfloat>
+#include <cmath>
 #include <cstdint>
 #include <cuda_runtime.h>
 
@@ -89,6 +91,35 @@ cudaError_t launch_tree_attention(const void* q, int dtype, int64_t q_req, int64
                                   int max_blocks, const int32_t* ctx, const int32_t* n_nodes,
                                   const uint64_t* mask, float scale, void* out, float* lse,
                                   int32_t* status, void* workspace, cudaStream_t stream);
+void rope_table(int rot_dim, double base, int scaling, double factor, double original_len,
+                double low, double high, const double* inv_freq, uint64_t* table);
+cudaError_t launch_rotate(const void* q, const void* k, const void* v, int src_dtype,
+                          int64_t q_token, int64_t q_head, int64_t k_token, int64_t k_head,
+                          int n_src, int n_tokens, int heads, int kv_heads, int dim,
+                          const float* q_weight, const float* k_weight, float eps,
+                          const int32_t* positions, const uint64_t* table, int rot_start,
+                          int rot_dim, bool interleaved, float magnitude, void* q_out,
+                          int64_t qo_token, int64_t qo_head, void* k_out, void* v_out,
+                          int dst_dtype, int64_t block_stride, int64_t ko_token, int64_t ko_head,
+                          int n_blocks, int page, const int32_t* slots, const int32_t* src_rows,
+                          cudaStream_t stream);
+cudaError_t launch_latent_write(const void* c, int64_t c_token, const void* r, int64_t r_token,
+                                int src_dtype, int n_src, int latent, int rope,
+                                const float* weight, float eps, const int32_t* positions,
+                                const uint64_t* table, bool interleaved, float magnitude,
+                                void* cache, int cache_dtype, int64_t block_stride,
+                                int64_t token_stride, int n_blocks, int page,
+                                const int32_t* slots, const int32_t* src_rows, int n_tokens,
+                                cudaStream_t stream);
+int64_t latent_attention_workspace_bytes(int B, int nodes, int heads, int latent);
+cudaError_t launch_latent_attention(const void* q, int dtype, int64_t q_req, int64_t q_node,
+                                    int64_t q_head, int B, int nodes, int heads, int latent,
+                                    int rope, const void* cache, int64_t block_stride,
+                                    int64_t token_stride, int n_blocks, int page,
+                                    const int32_t* table, int64_t table_ld, int max_blocks,
+                                    const int32_t* ctx, const int32_t* n_nodes,
+                                    const uint64_t* mask, float scale, void* out, float* lse,
+                                    int32_t* status, void* workspace, cudaStream_t stream);
 cudaError_t launch_logits_process(
     const void* x, int dtype, int64_t ld, int B, int rows, int V, const int32_t* history,
     int64_t history_ld, const int32_t* prompt_len, const int32_t* history_len,
@@ -108,6 +139,8 @@ cudaError_t dspark_check_collect_tree_attention_64(uint32_t* out);
 cudaError_t dspark_check_collect_tree_attention_128(uint32_t* out);
 cudaError_t dspark_check_collect_tree_attention_256(uint32_t* out);
 cudaError_t dspark_check_collect_logits(uint32_t* out);
+cudaError_t dspark_check_collect_rotate(uint32_t* out);
+cudaError_t dspark_check_collect_latent_attention(uint32_t* out);
 cudaError_t dspark_check_collect_chain(uint32_t* out);
 cudaError_t dspark_check_collect_debug(uint32_t* out);
 cudaError_t dspark_check_collect_q_dense(uint32_t* out);
@@ -165,6 +198,7 @@ int dspark_checked_status(uint32_t* out) {
   cudaError_t e = cudaSuccess;
   cudaError_t (*collect[])(uint32_t*) = {
       dspark::dspark_check_collect_cache, dspark::dspark_check_collect_logits,
+      dspark::dspark_check_collect_rotate, dspark::dspark_check_collect_latent_attention,
       dspark::dspark_check_collect_tree_attention_64,
       dspark::dspark_check_collect_tree_attention_128,
       dspark::dspark_check_collect_tree_attention_256,
@@ -803,6 +837,232 @@ int dspark_tree_attention(const void* q, int32_t dtype, int64_t q_req_stride,
       head_dim, k_cache, v_cache, block_stride, token_stride, head_stride, n_blocks, page_size,
       block_table, table_ld, max_blocks, ctx_len, n_nodes, tree_mask, scale, out, lse, req_status,
       workspace, static_cast<cudaStream_t>(stream)));
+}
+
+static bool positive(double v) { return v > 0.0 && v <= DBL_MAX; }
+
+int dspark_rope_table(int32_t rot_dim, double base, int32_t scaling, double factor,
+                      double original_len, double low, double high, const double* inv_freq,
+                      uint64_t* table) {
+  if (rot_dim < 8 || rot_dim > DSPARK_MAX_HEAD || rot_dim % 8) return DSPARK_ERR_SIZE;
+  if (!table) return DSPARK_ERR_NULL;
+  if (!aligned(table, 8) || !aligned_or_null(inv_freq, 8)) return DSPARK_ERR_ALIGN;
+  if (scaling < DSPARK_ROPE_PLAIN || scaling > DSPARK_ROPE_PARTS) return DSPARK_ERR_ARG;
+  if (!inv_freq && !positive(base)) return DSPARK_ERR_ARG;
+  if (scaling != DSPARK_ROPE_PLAIN && !positive(factor)) return DSPARK_ERR_ARG;
+  if (scaling == DSPARK_ROPE_PARTS &&
+      (!positive(original_len) || !positive(high - low) || !(low >= -DBL_MAX && low <= DBL_MAX)))
+    return DSPARK_ERR_ARG;
+  for (int32_t i = 0; i < rot_dim / 2; ++i) {
+    const double f = inv_freq ? inv_freq[i] : std::pow(base, -2.0 * i / rot_dim);
+    // beyond 2^31 turns a position a double has no fraction worth the name
+    if (!(f >= 0.0 && f < 1.3e10 && f / (scaling ? factor : 1.0) < 1.3e10)) return DSPARK_ERR_ARG;
+  }
+  dspark::rope_table(rot_dim, base, scaling, factor, original_len, low, high, inv_freq, table);
+  return 0;
+}
+
+// the sizes of a rotation; dtypes: src fp32 or dst
+static int check_rotation(int32_t src_dtype, int32_t dst_dtype, int32_t n_tokens, int32_t n_heads,
+                          int32_t n_kv_heads, int32_t head_dim, int32_t rot_start,
+                          int32_t rot_dim, float eps, float magnitude) {
+  for (int32_t d : {src_dtype, dst_dtype})
+    if (d != DSPARK_F32 && d != DSPARK_BF16 && d != DSPARK_F16) return DSPARK_ERR_DTYPE;
+  if (src_dtype != DSPARK_F32 && src_dtype != dst_dtype) return DSPARK_ERR_DTYPE;
+  if (n_tokens < 0 || n_heads < 0 || n_kv_heads < 0 || (int64_t)n_heads + n_kv_heads > 65535 ||
+      head_dim < 8 || head_dim > DSPARK_MAX_HEAD || head_dim % 8 || rot_start < 0 ||
+      rot_start % 8 || rot_dim < 0 || rot_dim % 8 || rot_start + rot_dim > head_dim)
+    return DSPARK_ERR_SIZE;
+  if (!(eps >= 0.0f && eps <= FLT_MAX) || !(magnitude >= -FLT_MAX && magnitude <= FLT_MAX))
+    return DSPARK_ERR_ARG;
+  return 0;
+}
+
+// a tensor of heads: aligned to 16 bytes, as its strides
+static bool aligned_heads(const void* p, int32_t dtype, int64_t token, int64_t head) {
+  const int unit = 16 / esize(dtype);
+  return aligned(p, 16) && token % unit == 0 && head % unit == 0;
+}
+
+int dspark_qk_rotate(const void* q, const void* k, int32_t src_dtype, int64_t q_token_stride,
+                     int64_t q_head_stride, int64_t k_token_stride, int64_t k_head_stride,
+                     int32_t n_tokens, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim,
+                     const float* q_weight, const float* k_weight, float eps,
+                     const int32_t* positions, const uint64_t* table, int32_t rot_start,
+                     int32_t rot_dim, int32_t interleaved, float magnitude, void* q_out,
+                     int64_t qo_token_stride, int64_t qo_head_stride, void* k_out,
+                     int64_t ko_token_stride, int64_t ko_head_stride, int32_t out_dtype,
+                     void* stream) {
+  const NvtxRange nvtx_range("dspark_qk_rotate");
+  if (int e = check_rotation(src_dtype, out_dtype, n_tokens, n_heads, n_kv_heads, head_dim,
+                             rot_start, rot_dim, eps, magnitude))
+    return e;
+  if (n_heads && (q_token_stride < 0 || q_head_stride < 0 || qo_token_stride < 0 ||
+                  qo_head_stride < 0))
+    return DSPARK_ERR_SIZE;
+  if (n_kv_heads && (k_token_stride < 0 || k_head_stride < 0 || ko_token_stride < 0 ||
+                     ko_head_stride < 0))
+    return DSPARK_ERR_SIZE;
+  if (n_tokens == 0 || n_heads + n_kv_heads == 0) return 0;
+  if ((n_heads && (!q || !q_out)) || (n_kv_heads && (!k || !k_out)) || !positions ||
+      (rot_dim && !table))
+    return DSPARK_ERR_NULL;
+  if (n_heads && (!aligned_heads(q, src_dtype, q_token_stride, q_head_stride) ||
+                  !aligned_heads(q_out, out_dtype, qo_token_stride, qo_head_stride)))
+    return DSPARK_ERR_ALIGN;
+  if (n_kv_heads && (!aligned_heads(k, src_dtype, k_token_stride, k_head_stride) ||
+                     !aligned_heads(k_out, out_dtype, ko_token_stride, ko_head_stride)))
+    return DSPARK_ERR_ALIGN;
+  if (!aligned(positions, 4) || !aligned_or_null(table, 8) || !aligned_or_null(q_weight, 4) ||
+      !aligned_or_null(k_weight, 4))
+    return DSPARK_ERR_ALIGN;
+  // in place: the same elements at the same places
+  if (n_heads && q == q_out && (src_dtype != out_dtype || q_token_stride != qo_token_stride ||
+                                q_head_stride != qo_head_stride))
+    return DSPARK_ERR_ARG;
+  if (n_kv_heads && k == k_out && (src_dtype != out_dtype || k_token_stride != ko_token_stride ||
+                                   k_head_stride != ko_head_stride))
+    return DSPARK_ERR_ARG;
+  return launch_result(dspark::launch_rotate(
+      q, k, nullptr, src_dtype, q_token_stride, q_head_stride, k_token_stride, k_head_stride,
+      n_tokens, n_tokens, n_heads, n_kv_heads, head_dim, n_heads ? q_weight : nullptr,
+      n_kv_heads ? k_weight : nullptr, eps, positions, table, rot_start, rot_dim,
+      interleaved != 0, magnitude, q_out, qo_token_stride, qo_head_stride, k_out, nullptr,
+      out_dtype, 0, ko_token_stride, ko_head_stride, 0, 1, nullptr, nullptr,
+      static_cast<cudaStream_t>(stream)));
+}
+
+int dspark_rotate_write(const void* q, const void* k, const void* v, int32_t src_dtype,
+                        int64_t q_token_stride, int64_t q_head_stride, int64_t kv_token_stride,
+                        int64_t kv_head_stride, int32_t n_src, int32_t n_heads,
+                        int32_t n_kv_heads, int32_t head_dim, const float* q_weight,
+                        const float* k_weight, float eps, const int32_t* positions,
+                        const uint64_t* table, int32_t rot_start, int32_t rot_dim,
+                        int32_t interleaved, float magnitude, void* q_out,
+                        int64_t qo_token_stride, int64_t qo_head_stride, void* k_cache,
+                        void* v_cache, int32_t cache_dtype, int64_t block_stride,
+                        int64_t token_stride, int64_t head_stride, int32_t n_blocks,
+                        int32_t page_size, const int32_t* slots, const int32_t* rows,
+                        int32_t n_tokens, void* stream) {
+  const NvtxRange nvtx_range("dspark_rotate_write");
+  if (int e = check_cache(n_blocks, page_size, cache_dtype, block_stride, token_stride,
+                          head_stride))
+    return e;
+  if (int e = check_rotation(src_dtype, cache_dtype, n_tokens, n_heads, n_kv_heads, head_dim,
+                             rot_start, rot_dim, eps, magnitude))
+    return e;
+  if (n_src < 0 || n_kv_heads < 1 || kv_token_stride < 0 || kv_head_stride < 0 ||
+      (n_heads && (q_token_stride < 0 || q_head_stride < 0 || qo_token_stride < 0 ||
+                   qo_head_stride < 0)))
+    return DSPARK_ERR_SIZE;
+  if (rows && n_heads) return DSPARK_ERR_ARG;
+  if (n_tokens == 0 || (n_src == 0 && n_heads == 0)) return 0;
+  if (!k || !v || !k_cache || !v_cache || !slots || !positions || (rot_dim && !table) ||
+      (n_heads && (!q || !q_out)))
+    return DSPARK_ERR_NULL;
+  if (!aligned_heads(k, src_dtype, kv_token_stride, kv_head_stride) || !aligned(v, 16) ||
+      !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
+      (n_heads && (!aligned_heads(q, src_dtype, q_token_stride, q_head_stride) ||
+                   !aligned_heads(q_out, cache_dtype, qo_token_stride, qo_head_stride))) ||
+      !aligned(slots, 4) || !aligned_or_null(rows, 4) || !aligned(positions, 4) ||
+      !aligned_or_null(table, 8) || !aligned_or_null(q_weight, 4) ||
+      !aligned_or_null(k_weight, 4))
+    return DSPARK_ERR_ALIGN;
+  if (n_heads && q == q_out && (src_dtype != cache_dtype || q_token_stride != qo_token_stride ||
+                                q_head_stride != qo_head_stride))
+    return DSPARK_ERR_ARG;
+  return launch_result(dspark::launch_rotate(
+      q, k, v, src_dtype, q_token_stride, q_head_stride, kv_token_stride, kv_head_stride, n_src,
+      n_tokens, n_heads, n_kv_heads, head_dim, n_heads ? q_weight : nullptr, k_weight, eps,
+      positions, table, rot_start, rot_dim, interleaved != 0, magnitude, q_out, qo_token_stride,
+      qo_head_stride, k_cache, v_cache, cache_dtype, block_stride, token_stride, head_stride,
+      n_blocks, page_size, slots, rows, static_cast<cudaStream_t>(stream)));
+}
+
+static int check_latent(int32_t latent_dim, int32_t rope_dim) {
+  if (latent_dim < 64 || latent_dim > DSPARK_MAX_LATENT || latent_dim % 64 || rope_dim < 0 ||
+      rope_dim > DSPARK_MAX_LATENT_ROPE || rope_dim % 8)
+    return DSPARK_ERR_SIZE;
+  return 0;
+}
+
+int dspark_latent_write(const void* c, int64_t c_token_stride, const void* r,
+                        int64_t r_token_stride, int32_t src_dtype, int32_t n_src,
+                        int32_t latent_dim, int32_t rope_dim, const float* weight, float eps,
+                        const int32_t* positions, const uint64_t* table, int32_t interleaved,
+                        float magnitude, void* cache, int32_t cache_dtype, int64_t block_stride,
+                        int64_t token_stride, int32_t n_blocks, int32_t page_size,
+                        const int32_t* slots, const int32_t* rows, int32_t n_tokens,
+                        void* stream) {
+  const NvtxRange nvtx_range("dspark_latent_write");
+  if (int e = check_cache(n_blocks, page_size, cache_dtype, block_stride, token_stride, 0))
+    return e;
+  if (src_dtype != DSPARK_F32 && src_dtype != cache_dtype) return DSPARK_ERR_DTYPE;
+  if (int e = check_latent(latent_dim, rope_dim)) return e;
+  if (n_src < 0 || n_tokens < 0 || c_token_stride < 0 || (rope_dim && r_token_stride < 0))
+    return DSPARK_ERR_SIZE;
+  if (!(eps >= 0.0f && eps <= FLT_MAX) || !(magnitude >= -FLT_MAX && magnitude <= FLT_MAX))
+    return DSPARK_ERR_ARG;
+  if (n_tokens == 0 || n_src == 0) return 0;
+  if (!c || !cache || !slots || !positions || (rope_dim && (!r || !table))) return DSPARK_ERR_NULL;
+  if (!aligned_heads(c, src_dtype, c_token_stride, 0) ||
+      (rope_dim && !aligned_heads(r, src_dtype, r_token_stride, 0)) || !aligned(cache, 16) ||
+      !aligned(slots, 4) || !aligned_or_null(rows, 4) || !aligned(positions, 4) ||
+      !aligned_or_null(table, 8) || !aligned_or_null(weight, 4))
+    return DSPARK_ERR_ALIGN;
+  return launch_result(dspark::launch_latent_write(
+      c, c_token_stride, r, r_token_stride, src_dtype, n_src, latent_dim, rope_dim, weight, eps,
+      positions, table, interleaved != 0, magnitude, cache, cache_dtype, block_stride,
+      token_stride, n_blocks, page_size, slots, rows, n_tokens,
+      static_cast<cudaStream_t>(stream)));
+}
+
+static int check_latent_rows(int32_t B, int32_t nodes, int32_t n_heads, int32_t latent_dim) {
+  if (B < 0 || B > 65535 || nodes < 1 || nodes > DSPARK_MAX_NODES || n_heads < 1 ||
+      n_heads > DSPARK_MAX_LATENT_HEADS)
+    return DSPARK_ERR_SIZE;
+  return check_latent(latent_dim, 0);
+}
+
+int64_t dspark_latent_attention_workspace_bytes(int32_t B, int32_t nodes, int32_t n_heads,
+                                                int32_t latent_dim) {
+  if (check_latent_rows(B, nodes, n_heads, latent_dim)) return 0;
+  return dspark::latent_attention_workspace_bytes(B, nodes, n_heads, latent_dim);
+}
+
+int dspark_latent_attention(const void* q, int32_t dtype, int64_t q_req_stride,
+                            int64_t q_node_stride, int64_t q_head_stride, int32_t B,
+                            int32_t nodes, int32_t n_heads, int32_t latent_dim,
+                            int32_t rope_dim, const void* cache, int64_t block_stride,
+                            int64_t token_stride, int32_t n_blocks, int32_t page_size,
+                            const int32_t* block_table, int64_t table_ld, int32_t max_blocks,
+                            const int32_t* ctx_len, const int32_t* n_nodes,
+                            const uint64_t* tree_mask, float scale, void* out, float* lse,
+                            int32_t* req_status, void* workspace, void* stream) {
+  const NvtxRange nvtx_range("dspark_latent_attention");
+  if (int e = check_cache(n_blocks, page_size, dtype, block_stride, token_stride, 0)) return e;
+  if (int e = check_latent_rows(B, nodes, n_heads, latent_dim)) return e;
+  if (int e = check_latent(latent_dim, rope_dim)) return e;
+  if (page_size % 8 || token_stride < latent_dim + rope_dim || block_stride < token_stride ||
+      token_stride >= (1ll << 39) || block_stride >= (1ll << 39) || max_blocks < 1 ||
+      table_ld < max_blocks || (int64_t)max_blocks * page_size > DSPARK_MAX_TOKENS ||
+      q_req_stride < 0 || q_node_stride < 0 || q_head_stride < 0)
+    return DSPARK_ERR_SIZE;
+  // times log2(e) it has to stay finite, or a score of 0 would become NaN
+  if (!(scale > -2.3e38f && scale < 2.3e38f)) return DSPARK_ERR_ARG;
+  if (B == 0) return 0;
+  if (!q || !cache || !block_table || !ctx_len || !n_nodes || !out || !req_status || !workspace)
+    return DSPARK_ERR_NULL;
+  if (q_req_stride % 8 || q_node_stride % 8 || q_head_stride % 8 || !aligned(q, 16) ||
+      !aligned(cache, 16) || !aligned(out, 16) || !aligned(workspace, 16) ||
+      !aligned(block_table, 4) || !aligned(ctx_len, 4) || !aligned(n_nodes, 4) ||
+      !aligned_or_null(tree_mask, 8) || !aligned_or_null(lse, 4) || !aligned(req_status, 4))
+    return DSPARK_ERR_ALIGN;
+  return launch_result(dspark::launch_latent_attention(
+      q, dtype, q_req_stride, q_node_stride, q_head_stride, B, nodes, n_heads, latent_dim,
+      rope_dim, cache, block_stride, token_stride, n_blocks, page_size, block_table, table_ld,
+      max_blocks, ctx_len, n_nodes, tree_mask, scale, out, lse, req_status, workspace,
+      static_cast<cudaStream_t>(stream)));
 }
 
 int dspark_logits_process(const void* logits, int32_t dtype, int64_t ld, int32_t B, int32_t rows,

@@ -543,6 +543,15 @@ int dspark_q_validate(const float* q, const int32_t* sparse_ids, const int32_t* 
 #define DSPARK_MAX_PAGE 1024         /* token rows of a block                */
 #define DSPARK_MAX_TOKENS 1073741824 /* positions of a request's table, 2^30 */
 #define DSPARK_MAX_PLANNED 1048576   /* requests of a plan, 2^20             */
+#define DSPARK_MAX_HEAD 256          /* elements of a rotated head           */
+#define DSPARK_MAX_LATENT 512        /* elements of a latent vector          */
+#define DSPARK_MAX_LATENT_ROPE 64    /* rotated elements beside it           */
+#define DSPARK_MAX_LATENT_HEADS 128  /* query heads over a latent cache      */
+
+/* scalings of a rotation's frequencies */
+#define DSPARK_ROPE_PLAIN 0
+#define DSPARK_ROPE_LINEAR 1         /* every frequency / factor             */
+#define DSPARK_ROPE_PARTS 2          /* by the turns over the original length */
 
 /*
  * dspark_cache_plan -- grants blocks to the requests of a step and maps their
@@ -701,6 +710,147 @@ int dspark_logits_process(const void* logits, int32_t dtype, int64_t ld, int32_t
                           const int32_t* n_bias, const uint32_t* mask_words, int64_t mask_ld,
                           int32_t n_masks, const int32_t* mask_rows, void* out, int64_t ld_out,
                           int32_t* req_status, void* stream);
+
+/*
+ * dspark_rope_table -- the frequencies of a position rotation, as turns per
+ * position in 0.64 fixed point: table[rot_dim / 2], on the HOST (the caller
+ * copies it to the device and keeps it).  position * table[i] modulo 2^64 is
+ * the angle exactly, however far the position.
+ *
+ * f_i = inv_freq[i] radians a position, or (NULL) base^(-2 i / rot_dim).
+ * DSPARK_ROPE_LINEAR: f_i / factor.  DSPARK_ROPE_PARTS: with the turns
+ * r = original_len * f_i / (2 pi) and keep = clamp((r - low) / (high - low),
+ * 0, 1), f_i * (keep + (1 - keep) / factor) (Peng et al., "YaRN", 2023,
+ * "NTK-by-parts"): frequencies of many turns stay, those of few are divided.
+ * inv_freq: host, may be NULL.  rot_dim a multiple of 8 in [8,
+ * DSPARK_MAX_HEAD]; base > 0, factor > 0 and, for PARTS, original_len > 0
+ * and high > low, all finite, as every f_i (DSPARK_ERR_ARG otherwise).
+ */
+int dspark_rope_table(int32_t rot_dim, double base, int32_t scaling, double factor,
+                      double original_len, double low, double high, const double* inv_freq,
+                      uint64_t* table);
+
+/*
+ * dspark_qk_rotate -- norms of queries and keys for each head and their
+ * rotation by position, in one pass.
+ *
+ * Per token and head, with x its head_dim elements, all in fp32:
+ *   y = x * rsqrt(mean(x^2) + eps) * weight  (weight NULL: y = x);
+ *   pair i of the rotated part, y's rot_dim elements from rot_start on:
+ *   (a, b) -> ((a cos - b sin) * magnitude, (b cos + a sin) * magnitude) at
+ *   the angle positions[token] * f_i, with elements 2i and 2i + 1 as a and b
+ *   (interleaved != 0) or i and i + rot_dim / 2 (interleaved == 0);
+ *   rounded once to out_dtype.
+ * Elements outside the rotated part are normed only.  rot_dim 0 (table may
+ * be NULL): norms alone.  A token with a negative position is padding: its
+ * outputs are 0 and nothing of it is read.
+ *
+ * Source element (token, head, d) at token*token_stride + head*head_stride +
+ * d, queries and keys with strides of their own, so both may be views of one
+ * projection's output; outputs the same.  An output may be its source itself
+ * (of the same dtype and strides, DSPARK_ERR_ARG otherwise) and must not
+ * overlap a source else.  n_heads or n_kv_heads may be 0 (then q, k and what
+ * belongs to them are not looked at).  src_dtype DSPARK_F32, _BF16 or _F16;
+ * out_dtype the same, or a 16-bit type for fp32 sources (DSPARK_ERR_DTYPE).
+ * Weights fp32 [head_dim]; eps >= 0; head_dim a multiple of 8 in [8,
+ * DSPARK_MAX_HEAD]; rot_start and rot_dim multiples of 8, rot_start + rot_dim
+ * <= head_dim; heads at most 65,535 in all.  Sources and outputs 16-byte
+ * aligned, their strides multiples of 16 bytes (DSPARK_ERR_ALIGN).
+ */
+int dspark_qk_rotate(const void* q, const void* k, int32_t src_dtype, int64_t q_token_stride,
+                     int64_t q_head_stride, int64_t k_token_stride, int64_t k_head_stride,
+                     int32_t n_tokens, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim,
+                     const float* q_weight, const float* k_weight, float eps,
+                     const int32_t* positions, const uint64_t* table, int32_t rot_start,
+                     int32_t rot_dim, int32_t interleaved, float magnitude, void* q_out,
+                     int64_t qo_token_stride, int64_t qo_head_stride, void* k_out,
+                     int64_t ko_token_stride, int64_t ko_head_stride, int32_t out_dtype,
+                     void* stream);
+
+/*
+ * dspark_rotate_write -- dspark_qk_rotate whose keys go to their slots of the
+ * paged cache, with the values beside them (as dspark_kv_write stores them):
+ * what a step does between its projections and dspark_tree_attention.
+ *
+ * Token i of n_tokens has positions[i] and slots[i]; its keys and values are
+ * source token src = rows ? rows[i] : i of n_src.  They are skipped for a
+ * negative position, a slot outside [0, n_blocks*page_size) or a source
+ * outside [0, n_src).  Two tokens with one slot leave either one's elements.
+ * Queries: of token i, rotated to q_out of the caches' dtype; n_heads 0: none
+ * (q, q_out not looked at), and always so with rows (DSPARK_ERR_ARG
+ * otherwise).  k and v have the same strides.  src_dtype the caches' dtype or
+ * DSPARK_F32.  Sizes, alignments and the caches' layout as above;
+ * n_blocks*page_size < 2^31.
+ */
+int dspark_rotate_write(const void* q, const void* k, const void* v, int32_t src_dtype,
+                        int64_t q_token_stride, int64_t q_head_stride, int64_t kv_token_stride,
+                        int64_t kv_head_stride, int32_t n_src, int32_t n_heads,
+                        int32_t n_kv_heads, int32_t head_dim, const float* q_weight,
+                        const float* k_weight, float eps, const int32_t* positions,
+                        const uint64_t* table, int32_t rot_start, int32_t rot_dim,
+                        int32_t interleaved, float magnitude, void* q_out,
+                        int64_t qo_token_stride, int64_t qo_head_stride, void* k_cache,
+                        void* v_cache, int32_t cache_dtype, int64_t block_stride,
+                        int64_t token_stride, int64_t head_stride, int32_t n_blocks,
+                        int32_t page_size, const int32_t* slots, const int32_t* rows,
+                        int32_t n_tokens, void* stream);
+
+/*
+ * The latent cache: n_blocks blocks of page_size rows, one row a token for
+ * all its heads: latent_dim elements from which every head's keys and values
+ * are made by products, then rope_dim rotated elements that every head's key
+ * ends with.  Element (block, row, d) at block*block_stride +
+ * row*token_stride + d.
+ *
+ * dspark_latent_write -- writes rows of n_tokens tokens into it: row =
+ * [ c * rsqrt(mean(c^2) + eps) * weight (weight NULL: c) | rotated r ], in
+ * fp32, rounded once, with c [latent_dim] and r [rope_dim] of source token
+ * src = rows ? rows[i] : i; rotation, interleaved, table and magnitude as in
+ * dspark_qk_rotate at positions[i].  A token with a negative position, a slot
+ * outside the cache or a source outside [0, n_src) is skipped.
+ * latent_dim a multiple of 64 in [64, DSPARK_MAX_LATENT]; rope_dim a multiple
+ * of 8 in [0, DSPARK_MAX_LATENT_ROPE] (0: r and table not looked at).
+ * src_dtype the cache's or DSPARK_F32.  Alignments as above.
+ */
+int dspark_latent_write(const void* c, int64_t c_token_stride, const void* r,
+                        int64_t r_token_stride, int32_t src_dtype, int32_t n_src,
+                        int32_t latent_dim, int32_t rope_dim, const float* weight, float eps,
+                        const int32_t* positions, const uint64_t* table, int32_t interleaved,
+                        float magnitude, void* cache, int32_t cache_dtype, int64_t block_stride,
+                        int64_t token_stride, int32_t n_blocks, int32_t page_size,
+                        const int32_t* slots, const int32_t* rows, int32_t n_tokens,
+                        void* stream);
+
+/*
+ * dspark_latent_attention -- dspark_tree_attention over a latent cache, in
+ * the absorbed form: the heads' key products are in the queries already, the
+ * value products are left to the caller.
+ *
+ * With row_i the latent_dim + rope_dim elements of position i, s_i = scale *
+ * q . row_i over the seen positions; out = sum_i exp(s_i - lse)
+ * row_i[0 .. latent_dim), lse = log sum exp s_i.  Which positions a node
+ * sees, what a row that sees nothing gets, the precision, req_status and the
+ * workspace are as in dspark_tree_attention; every head reads the same rows.
+ * q: element (request, node, head, d), d < latent_dim + rope_dim, with
+ * strides; out [B][nodes][n_heads][latent_dim] contiguous; lse
+ * [B][nodes][n_heads] (may be NULL).
+ * Limits: latent_dim a multiple of 64 in [64, DSPARK_MAX_LATENT], rope_dim a
+ * multiple of 8 in [0, DSPARK_MAX_LATENT_ROPE]; n_heads in [1,
+ * DSPARK_MAX_LATENT_HEADS]; page_size a multiple of 8; token_stride >=
+ * latent_dim + rope_dim; block_stride >= token_stride; strides below 2^39
+ * elements; the others as in dspark_tree_attention.
+ */
+int64_t dspark_latent_attention_workspace_bytes(int32_t B, int32_t nodes, int32_t n_heads,
+                                                int32_t latent_dim);
+int dspark_latent_attention(const void* q, int32_t dtype, int64_t q_req_stride,
+                            int64_t q_node_stride, int64_t q_head_stride, int32_t B,
+                            int32_t nodes, int32_t n_heads, int32_t latent_dim,
+                            int32_t rope_dim, const void* cache, int64_t block_stride,
+                            int64_t token_stride, int32_t n_blocks, int32_t page_size,
+                            const int32_t* block_table, int64_t table_ld, int32_t max_blocks,
+                            const int32_t* ctx_len, const int32_t* n_nodes,
+                            const uint64_t* tree_mask, float scale, void* out, float* lse,
+                            int32_t* req_status, void* workspace, void* stream);
 
 /* Library build identifier (static string, host). */
 const char* dspark_version(void);
