@@ -133,6 +133,7 @@ namespace attn {
 cudaError_t stall_64(uint32_t v);
 cudaError_t stall_128(uint32_t v);
 cudaError_t stall_256(uint32_t v);
+cudaError_t stall_latent(uint32_t v);
 }  // namespace attn
 cudaError_t dspark_check_collect_cache(uint32_t* out);
 cudaError_t dspark_check_collect_tree_attention_64(uint32_t* out);
@@ -220,7 +221,8 @@ int dspark_debug_stall_attention(int32_t cta) {
   if (cta < -1) return DSPARK_ERR_ARG;
 #ifdef DSPARK_CHECKED
   const uint32_t v = (uint32_t)(cta + 1);
-  for (auto set : {dspark::attn::stall_64, dspark::attn::stall_128, dspark::attn::stall_256})
+  for (auto set : {dspark::attn::stall_64, dspark::attn::stall_128, dspark::attn::stall_256,
+                   dspark::attn::stall_latent})
     if (const cudaError_t e = set(v)) return (int)e;
   return 0;
 #else

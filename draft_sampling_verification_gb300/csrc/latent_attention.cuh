@@ -1,0 +1,857 @@
+// latent_attention.cuh -- the kernels of dspark_latent_attention.  Division of
+// work, walk along it and workspace are those of tree_attention.cuh, with an
+// item for each (request, tile of 128 rows).
+#pragma once
+
+#include "tree_attention_wide.cuh"
+
+namespace dspark {
+namespace attn {
+
+struct LatentParams : Params {
+  int latent, width;  // of a row of the cache: its values, all of it
+};
+
+// ------------------------------------------- a pair of CTAs and its barriers
+// The address of this CTA's shared address `addr` in CTA `rank` of the pair.
+__device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+}
+__device__ __forceinline__ void cluster_fence() {
+  asm volatile("fence.acq_rel.cluster;" ::: "memory");
+}
+__device__ __forceinline__ void pair_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void pair_arrive_expect_tx(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t phase) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(phase)
+      : "memory");
+  return ok != 0u;
+}
+__device__ __forceinline__ void pair_store(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+// one box of the cache, from element x of row r of block b, into this CTA, completing on a barrier
+// of either CTA; what lies beyond a row's width or the cache is 0
+__device__ __forceinline__ void pair_load_box(uint32_t dst, const CUtensorMap* map, int x, int r,
+                                              int b, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".cta_group::2 [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(r), "r"(b), "r"(bar)
+      : "memory");
+}
+// d (+)= a b over the pair, a's rows and b's columns from both CTAs' shared memory
+__device__ __forceinline__ void pair_mma(bool on, uint32_t d, uint64_t a, uint64_t b,
+                                         uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add), "r"((uint32_t)on)
+      : "memory");
+}
+// arrives on `bar` in both CTAs once every product issued before it is done
+__device__ __forceinline__ void pair_commit(bool on, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+      "[%0], %2;\n\t}" ::"r"(smem_u32(bar)),
+      "r"((uint32_t)on), "h"((uint16_t)3)
+      : "memory");
+}
+// whether any of the 256 softmax threads says so; all of them call
+__device__ __forceinline__ bool any_of_256(bool v) {
+  uint32_t r;
+  __syncwarp();
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\tbarrier.cta.red.or.pred.aligned q, 1, 256, "
+      "p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)v)
+      : "memory");
+  return r != 0u;
+}
+
+// ------------------------------------------------------------ the kernel
+// A pair of CTAs takes 128 rows of an item, 64 a CTA, and goes over the keys
+// in tiles of 128 positions.  512 dims of fp32 accumulators for 128 rows
+// would fill the tensor memory of one SM; with products of the pair
+// (cta_group::2, 128 rows) a CTA's 64 rows take its 128 lanes twice: half of
+// a product's columns in lanes 0-63, the other half in lanes 64-127, so that
+// 64 columns hold the scores of 128 positions and 256 the accumulators.
+//
+// S = Q K^T: each CTA brings its 64 rows of Q and 64 of the tile's rows of
+// the cache, in groups of three chunks of 64 elements (24 KB) that are freed
+// one by one.  O += P V: each CTA brings its rows' weights (through shared
+// memory) and its half of the values' dims for all 128 positions, in pieces
+// of 64 positions.  The scores of the next tile are computed before the
+// values of this one, while the softmax of this one runs.
+//
+// Warps 0-7: softmax; a thread has a row's scores of 32 positions, so four
+// threads share a row: the threads vote whether any score passes its row's
+// reference by more than 8, and only then exchange maxima and rescale.  Also
+// queries and results.  Warps 8 and 9: tensor copies of keys and of values.
+// Warp 10 of CTA 0 issues the pair's products.
+constexpr int kLatentKeys = 128;  // positions of a tile
+constexpr int kLatentThreads = 384;
+constexpr int kLatentCost = 3;
+
+template <int DV>
+struct Latent {
+  static constexpr int kHalf = DV / 2;            // values' dims of a CTA
+  static constexpr int kChunks = DV / 64 + 1;     // of 64 elements, of a row of the cache
+  static constexpr int kGroup = 3;                // chunks that come together
+  static constexpr int kKSlots = DV == 512 ? 3 : 4;
+  static constexpr int kVSlots = DV == 512 ? 2 : 4;  // pieces of 64 positions
+  static constexpr int kVParts = kHalf / 64;      // chunks of a piece
+  static constexpr int kChunkBytes = 64 * 128;
+  static constexpr int kKBytes = kGroup * kChunkBytes, kVBytes = kVParts * kChunkBytes;
+  static constexpr int kQBytes = kChunks * kChunkBytes;
+  static constexpr int kPBytes = 64 * kLatentKeys * 2;
+  static constexpr int kSmem = kQBytes + kKSlots * kKBytes + kVSlots * kVBytes + kPBytes + 1024;
+};
+
+struct LatentShared {
+  uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
+  uint64_t q_full, s_full[2], p_full, o_full, v_go, drained;
+  uint64_t scan[32];
+  // by tile number modulo 16: a narrow row's keys are copied up to 7 tiles ahead of the results
+  uint32_t valid[16][4];  // a tile's positions that hold a key
+  uint32_t special[16];   // a value of a tile's nodes is an infinity or a NaN
+  Start start;
+  uint32_t tmem;
+  uint32_t failed;  // a wait expired
+  uint32_t peer_failed, issued[2], peer_issued[2];
+};
+
+template <typename T, int DV>
+__global__ void __launch_bounds__(kLatentThreads, 1) __cluster_dims__(2, 1, 1)
+    latent_attention_kernel(const __grid_constant__ LatentParams p,
+                            const __grid_constant__ CUtensorMap map, int rows) {
+  using H = Half<T>;
+  using L = Latent<DV>;
+  constexpr int kKeys = kLatentKeys;
+  extern __shared__ unsigned char smem_raw[];
+  __shared__ LatentShared sh;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t rank = cluster_rank();
+  const int pair = blockIdx.x / 2, pairs = gridDim.x / 2;
+  const uint32_t q_at = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  const uint32_t k_at = q_at + L::kQBytes, v_at = k_at + L::kKSlots * L::kKBytes;
+  const uint32_t p_at = v_at + L::kVSlots * L::kVBytes;
+  const int chunks = (p.width + 63) / 64, groups = (chunks + L::kGroup - 1) / L::kGroup;
+  const int all_rows = p.nodes * p.heads;
+
+  if (tid == 0) asm volatile("prefetch.tensormap [%0];" ::"l"(&map) : "memory");
+  const Workspace ws = carve(p.workspace, p.part_rows, p.max_ctas);
+  int64_t range;
+  find_range<kLatentThreads, 1>(p, ws, sh.scan, &sh.start, &range, pair, pairs, rank == 0);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (tid == 0 && rank == 0 && DSPARK_CHECK(pair < p.max_ctas)) ws.lost[pair] = {0, -1};
+  if (range <= 0) return;  // both CTAs
+
+  if (tid == 0) {
+    for (int i = 0; i < L::kKSlots; ++i) {
+      mbar_init(&sh.k_full[i], 2);
+      mbar_init(&sh.k_empty[i], 1);
+    }
+    for (int i = 0; i < L::kVSlots; ++i) {
+      mbar_init(&sh.v_full[i], 2);
+      mbar_init(&sh.v_empty[i], 1);
+    }
+    mbar_init(&sh.q_full, 16);
+    mbar_init(&sh.s_full[0], 1);
+    mbar_init(&sh.s_full[1], 1);
+    mbar_init(&sh.p_full, 16);
+    mbar_init(&sh.o_full, 1);
+    mbar_init(&sh.v_go, 1);
+    mbar_init(&sh.drained, 1);
+    sh.failed = sh.peer_failed = 0u;
+    sh.issued[0] = sh.issued[1] = sh.peer_issued[0] = sh.peer_issued[1] = 0u;
+    mbar_init_fence();
+  }
+  if (warp == 10) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                     smem_u32(&sh.tmem))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  tc_before_sync();
+  __syncthreads();
+  cluster_sync();
+  tc_after_sync();
+  const uint32_t tmem = sh.tmem;
+  auto s_col = [&](uint32_t g) -> uint32_t { return tmem + (g & 1u) * 64u; };
+  const uint32_t o_col = tmem + 128u;
+
+  // bounded waits of a whole warp, as in tree_attention_wide_kernel
+  auto wait_all = [&](uint64_t* bar, uint32_t phase) -> bool {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, phase))) return true;
+    const uint64_t t0 = global_ns();
+    uint32_t nap = 32;
+    while (!__any_sync(0xffffffffu, *(volatile uint32_t*)&sh.failed)) {
+      if (__all_sync(0xffffffffu, mbar_try_wait(bar, phase))) return true;
+      if (__any_sync(0xffffffffu, global_ns() - t0 >= kWaitLimitNs)) {
+        *(volatile uint32_t*)&sh.failed = 1u;
+        break;
+      }
+      if (nap > 32u) __nanosleep(nap);
+      nap = nap < 1024u ? 2u * nap : 1024u;
+    }
+    return false;
+  };
+
+  if (warp < 8) {
+    // -------------------------------------------------- softmax and results
+    const int t = tid & 127, wg = tid >> 7;   // lane of tensor memory; which columns
+    const int row = t & 63, half = t >> 6;    // of this CTA's rows; positions and dims from 64, DV/2
+    const int word = half * 2 + wg;           // this thread's 32 positions of a tile
+    const uint32_t lanes = (uint32_t)(t & ~31) << 16;
+    const uint32_t oc = o_col + wg * (DV / 4) + lanes;
+    // as in tree_attention_wide_kernel: a negative scale goes into Q's sign
+    const uint32_t flip = p.scale2 < 0.0f ? 0x80008000u : 0u;
+    const float scale = fmaxf(fabsf(p.scale2), 1.17549435e-38f);
+    const uint32_t q_full = in_cta(smem_u32(&sh.q_full), 0), p_full = in_cta(smem_u32(&sh.p_full), 0);
+    const uint32_t v_go = in_cta(smem_u32(&sh.v_go), 1);
+    const uint32_t special_there = in_cta(smem_u32(sh.special), rank ^ 1u);
+    // four floats a row, in the place of the weights between two products
+    const uint32_t exchange = p_at + row * 16;
+    uint32_t tile_no = 0, o_done = 0, goes = 0;  // o_done: products of values waited for
+    bool bad = false;                            // a wait of this warp expired
+
+    auto fill_q = [&](const Walk& w) {
+      constexpr int kPieces = L::kChunks * 8, kEach = 64 * kPieces / 256, kBatch = kEach / 2;
+      const int first = w.head * 128 + (int)rank * 64, live = w.len.nodes * p.heads;
+      const T* from = static_cast<const T*>(p.q) + w.b * p.q_req;
+#pragma unroll
+      for (int part = 0; part < 2; ++part) {
+        uint4 q[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          const int at = tid + (part * kBatch + i) * 256, r = at / kPieces, c = at % kPieces;
+          q[i] = make_uint4(0u, 0u, 0u, 0u);
+          if (first + r < live && c * 8 < p.width &&
+              DSPARK_CHECK(w.b < p.B && first + r < all_rows)) {
+            const int node = (first + r) / p.heads;
+            q[i] = __ldg(reinterpret_cast<const uint4*>(
+                from + node * p.q_node + (int64_t)(first + r - node * p.heads) * p.q_head + c * 8));
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          const int at = tid + (part * kBatch + i) * 256, r = at / kPieces, c = at % kPieces;
+          const uint32_t to = q_at + (c >> 3) * L::kChunkBytes + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+          if (!DSPARK_CHECK(to + 16 <= k_at)) continue;
+          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(q[i].x ^ flip),
+                       "r"(q[i].y ^ flip), "r"(q[i].z ^ flip), "r"(q[i].w ^ flip)
+                       : "memory");
+        }
+      }
+      fence_async_shared();
+      __syncwarp();
+      if (lane == 0) pair_arrive(q_full);
+    };
+    auto wait_values = [&]() {  // for the last product of values that was handed over
+      bad = bad || !wait_all(&sh.o_full, o_done & 1u);
+      ++o_done;
+      tc_after_sync();
+    };
+    auto put = [&](float v) {
+      asm volatile("st.shared.f32 [%0], %1;" ::"r"(exchange + word * 4), "f"(v) : "memory");
+    };
+    auto get = [&]() -> float4 {
+      float4 v;
+      asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                   : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                   : "r"(exchange)
+                   : "memory");
+      return v;
+    };
+    // Whether one of the eight warps is lost: what each of them asks at the same barrier, so that
+    // they leave together.
+    auto lost = [&]() -> bool { return any_of_256(bad); };
+
+    Walk cur = walk_from(p, sh.start, range, p.item_cost);
+    bool more = cur.advance(p, kKeys), ok = true;
+    if (more) fill_q(cur);
+    while (ok && more) {
+      const int tiles = cur.count;
+      const Lengths len = cur.len;
+      const int live = len.nodes * p.heads;
+      const int item_row = cur.head * 128 + (int)rank * 64 + row;
+      if (tid == 0 && rank == 0 && cur.head == 0 && cur.first == 0)
+        p.status[cur.b] = len.bad ? DSPARK_ST_BAD_LENGTH : DSPARK_ST_OK;
+      Walk ahead = cur;
+      more = ahead.advance(p, kKeys);
+      const bool idle = item_row - (t & 31) >= live;  // no row of this warp has a node
+      const int node = item_row / p.heads;
+      uint64_t mask = 0;
+      if (item_row < live && DSPARK_CHECK(node < p.nodes && cur.b < p.B))
+        mask = p.mask ? p.mask[(int64_t)cur.b * p.nodes + node] : ~0ull >> (63 - node);
+      float ref = -INFINITY;
+      float2 sum2 = make_float2(0.0f, 0.0f);
+      for (int i = 0; i < tiles; ++i, ++tile_no) {
+        bad = bad || !wait_all(&sh.s_full[tile_no & 1u], (tile_no >> 1) & 1u);
+        tc_after_sync();
+        const int pos = (cur.first + i) * kKeys;
+        const bool nodes_here = pos + kKeys > len.ctx;
+        float v[32];
+        float top = -INFINITY;
+        if (!idle && !bad) {
+          tmem_load32(v, s_col(tile_no) + wg * 32 + lanes);
+          uint32_t w = sh.valid[tile_no & 15u][word];
+          tmem_wait_load();
+          if (nodes_here) {
+            const int node0 = pos + word * 32 - len.ctx;  // the node of the first position
+            if (node0 >= 0)
+              w &= node0 < 64 ? (uint32_t)(mask >> node0) : 0u;
+            else if (node0 > -32)
+              w &= (uint32_t)(mask << -node0) | ((1u << -node0) - 1u);
+          }
+          if (!__all_sync(0xffffffffu, w == ~0u)) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (!((w >> j) & 1u)) v[j] = -INFINITY;
+          }
+          float m4[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+          for (int j = 4; j < 28; j += 8) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) m4[k] = fmaxf(fmaxf(m4[k], v[j + k]), v[j + 4 + k]);
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) m4[k] = fmaxf(m4[k], v[28 + k]);
+          top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * scale;
+        }
+        bool waited = i == 0;  // the product before, of which the weights' place is free
+        if (any_of_256(bad || top > ref + kSlack)) {
+          if (!waited) wait_values();
+          waited = true;
+          put(top);
+          if (lost()) {
+            ok = false;
+            break;
+          }
+          const float4 tops = get();
+          top = fmaxf(fmaxf(fmaxf(tops.x, tops.y), fmaxf(tops.z, tops.w)), ref);
+          const float f = top == -INFINITY ? 1.0f : exp2_approx(ref - top);
+          ref = top;
+          sum2.x *= f;
+          sum2.y *= f;
+          if (i > 0 && !idle) {
+#pragma unroll 1
+            for (int c = 0; c < DV / 64; ++c) {
+              uint32_t a[16];
+              tmem_load16(a, oc + c * 16);
+              tmem_wait_load();
+#pragma unroll
+              for (int j = 0; j < 16; ++j) a[j] = __float_as_uint(__uint_as_float(a[j]) * f);
+              tmem_store16(oc + c * 16, a);
+            }
+            tmem_wait_store();
+          }
+          any_of_256(false);  // all have read before the weights take the place
+        }
+        uint32_t w16[16];
+        if (!idle) {
+          const float2 off = f2(ref == -INFINITY ? 0.0f : -ref), by = f2(scale);
+          float2 part2 = make_float2(0.0f, 0.0f);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            float2 e = fma2_rn(make_float2(v[2 * j], v[2 * j + 1]), by, off);
+            e.x = exp2_approx(e.x);
+            e.y = exp2_approx(e.y);
+            if (j & 1)
+              part2 = add2_rn(part2, e);
+            else
+              sum2 = add2_rn(sum2, e);
+            w16[j] = H::pack(e.x, e.y);
+          }
+          sum2 = add2_rn(sum2, part2);
+        }
+        if (!waited) wait_values();
+        if (!idle) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
+                             p_at + half * 8192 + row * 128 + (((wg * 4 + j) ^ (row & 7)) << 4)),
+                         "r"(w16[4 * j]), "r"(w16[4 * j + 1]), "r"(w16[4 * j + 2]),
+                         "r"(w16[4 * j + 3])
+                         : "memory");
+        }
+        if (nodes_here) {
+          // Rows from the first node on, which some rows see and others do not, and what lies
+          // behind the end: infinities and NaN are cleared, as 0 times them would reach rows that
+          // do not see them.  CTA 1 learns from CTA 0 that its values are there.
+          const uint32_t piece = tile_no * 2u;
+          if (rank == 0) {
+#pragma unroll
+            for (uint32_t s = 0; s < 2; ++s)
+              bad = bad || !wait_all(&sh.v_full[(piece + s) % L::kVSlots],
+                                     ((piece + s) / L::kVSlots) & 1u);
+            if (tid == 0) {
+              cluster_fence();
+              pair_arrive(v_go);
+            }
+          } else {
+            bad = bad || !wait_all(&sh.v_go, goes & 1u);
+            cluster_fence();
+          }
+          ++goes;
+          const int from = max(0, len.ctx - pos);
+          // blocks' rows that the last copy brought; zeros behind them
+          const int end = min(kKeys, (len.len - pos + rows - 1) & -rows);
+          constexpr int kPer = L::kHalf / 8;  // 16-byte pieces of a position
+          for (int j = tid; j < (end - from) * kPer && !bad; j += 256) {
+            const int r = from + j / kPer, c = j % kPer;
+            const uint32_t slot = (piece + (r >> 6)) % L::kVSlots;
+            const uint32_t addr = v_at + slot * L::kVBytes + (c >> 3) * L::kChunkBytes +
+                                  (r & 63) * 128 + (((c & 7) ^ (r & 7)) << 4);
+            if (!DSPARK_CHECK(addr >= v_at && addr + 16 <= p_at)) continue;
+            uint32_t x[4];
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+                         : "r"(addr)
+                         : "memory");
+            if (any_special<T>(x[0]) || any_special<T>(x[1]) || any_special<T>(x[2]) ||
+                any_special<T>(x[3])) {
+              asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr),
+                           "r"(without_special<T>(x[0])), "r"(without_special<T>(x[1])),
+                           "r"(without_special<T>(x[2])), "r"(without_special<T>(x[3]))
+                           : "memory");
+              if (pos + r < len.len) {
+                *(volatile uint32_t*)&sh.special[tile_no & 15u] = 1u;
+                pair_store(special_there + (tile_no & 15u) * 4, 1u);
+                cluster_fence();
+              }
+            }
+          }
+        }
+        fence_async_shared();
+        tc_before_sync();
+        __syncwarp();
+        if (lane == 0) pair_arrive(p_full);
+      }
+      if (!ok) break;
+      // Q is free, as the last scores are done
+      if (more) fill_q(ahead);
+      wait_values();
+      float sum = sum2.x + sum2.y;
+      if (item_row >= live) {  // a row of no node: its zero query saw the text all the same
+        ref = -INFINITY;
+        sum = 0.0f;
+      }
+      put(sum);
+      if (lost()) break;
+      const float4 sums = get();
+      sum = (sums.x + sums.y) + (sums.z + sums.w);
+      bool special = false;
+      for (uint32_t k = 1; k <= min(2, tiles); ++k)
+        special |= *(volatile uint32_t*)&sh.special[(tile_no - k) & 15u] != 0u;
+
+      const bool mine = item_row < all_rows, full = cur.whole();
+      const int64_t to = (int64_t)cur.b * all_rows + item_row;
+      const int64_t slot = cur.slot(pair) * p.part_rows;
+      const int part_row = (int)rank * 64 + row;
+      const float inv = sum == 0.0f ? 0.0f : full ? 1.0f / sum : 1.0f;
+      const int d0 = half * L::kHalf + wg * (DV / 4);  // this thread's dims
+      const int pieces = item_row - (t & 31) < all_rows ? DV / 128 : 0;
+#pragma unroll 1
+      for (int c = 0; c < pieces; ++c) {
+        const int d = d0 + c * 32;
+        if (d >= p.latent) break;  // of the whole warp
+        float v[32];
+        tmem_load32(v, oc + c * 32);
+        tmem_wait_load();
+        if (item_row >= live) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = 0.0f;
+        }
+        if (special) {
+          // infinities and NaN, left out of the product, reach the rows that see their key
+#pragma unroll 1
+          for (int k = 0; k < len.nodes; ++k) {
+            const int at = len.ctx + k, tile = at / kKeys;
+            if (!((mask >> k) & 1ull) || tile < cur.first || tile >= cur.first + tiles) continue;
+            if (!DSPARK_CHECK(at / p.page < p.max_blocks && cur.b < p.B)) continue;
+            const int block = p.table[cur.b * p.table_ld + at / p.page];
+            if (block < 0 || block >= p.n_blocks) continue;
+            const T* from = static_cast<const T*>(p.k) + block * p.block_stride +
+                            (int64_t)(at % p.page) * p.token_stride + d;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              const uint32_t bits = __ldg(reinterpret_cast<const unsigned short*>(from) + j);
+              if (any_special<T>(bits)) v[j] += H::widen(bits);
+            }
+          }
+        }
+        if (mine && full && DSPARK_CHECK(row_held(p, to))) {
+          uint4* out = reinterpret_cast<uint4*>(static_cast<T*>(p.out) + to * p.latent + d);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            out[j] = make_uint4(H::pack(v[8 * j] * inv, v[8 * j + 1] * inv),
+                                H::pack(v[8 * j + 2] * inv, v[8 * j + 3] * inv),
+                                H::pack(v[8 * j + 4] * inv, v[8 * j + 5] * inv),
+                                H::pack(v[8 * j + 6] * inv, v[8 * j + 7] * inv));
+        } else if (mine && DSPARK_CHECK(!full && part_held(p, slot, part_row))) {
+          float* out = part_at(ws, slot, p.part_rows, 8, part_row, DV, d);
+#pragma unroll
+          for (int j = 0; j < 32; j += 8)
+            asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(
+                             out + j / 8 * (p.part_rows * 8)),
+                         "f"(v[j]), "f"(v[j + 1]), "f"(v[j + 2]), "f"(v[j + 3]), "f"(v[j + 4]),
+                         "f"(v[j + 5]), "f"(v[j + 6]), "f"(v[j + 7])
+                         : "memory");
+        }
+        __syncwarp();
+      }
+      if (mine && word == 0 && DSPARK_CHECK(full ? row_held(p, to) : part_held(p, slot, part_row))) {
+        if (!full)
+          ws.stats[slot + part_row] = make_float2(ref, sum);
+        else if (p.lse)
+          p.lse[to] = sum == 0.0f ? -INFINITY : (ref + log2f(sum)) * 0.6931471805599453f;
+      }
+      tc_before_sync();  // the accumulators are read: the next item may take them
+      cur = ahead;
+    }
+  } else if (warp < 10) {
+    // ------------------------------------------------------ keys and values
+    // A box is `rows` rows of one block, 64 elements wide.  Lane i holds the place of the tile's
+    // i-th run of rows; of a copy, lane i takes the i-th box: run i % per_half of 64 positions,
+    // chunk i / per_half.
+    const bool keys = warp == 8;
+    const int runs = kKeys / rows, per_half = runs / 2;  // powers of two, at most 16 and 8
+    const int shift = 31 - __clz(rows), half_shift = 31 - __clz(per_half);
+    const int next_row = kKeys % p.page, next_block = kKeys / p.page;
+    const uint32_t all_runs = (1u << runs) - 1u;
+    const int run = lane & (per_half - 1), chunk = lane >> half_shift;
+    const uint32_t box_at = chunk * L::kChunkBytes + run * rows * 128;
+    uint32_t g = 0, issued = 0, slot = 0, phase = 0;
+    bool ok = !DSPARK_STALLED(blockIdx.x);
+    Walk cur = walk_from(p, sh.start, range, p.item_cost);
+    while (ok && cur.advance(p, kKeys)) {
+      const int tiles = cur.count;
+      const Lengths len = cur.len;
+      int pos = cur.first * kKeys + lane * rows, at = pos / p.page, row_ahead = pos - at * p.page;
+      const int32_t* table = p.table + cur.b * p.table_ld;
+      auto entry = [&]() -> int {
+        return lane < runs && pos < len.len &&
+                       DSPARK_CHECK(at == pos / p.page && at < p.max_blocks && cur.b < p.B)
+                   ? __ldg(table + at)
+                   : -1;
+      };
+      int ahead = entry();
+      for (int i = 0; i < tiles && ok; ++i, ++g) {
+        const int block = ahead, row_here = row_ahead;
+        pos += kKeys;
+        at += next_block;
+        row_ahead += next_row;
+        if (row_ahead >= p.page) {
+          row_ahead -= p.page;
+          ++at;
+        }
+        ahead = entry();
+        const bool held = block >= 0 && block < p.n_blocks;
+        const int from = held ? block : p.n_blocks, row = held ? row_here : 0;
+        if (keys) {
+          const uint32_t held_runs = __ballot_sync(0xffffffffu, held);
+          const int b = __shfl_sync(0xffffffffu, from, (int)rank * per_half + run);
+          const int r = __shfl_sync(0xffffffffu, row, (int)rank * per_half + run);
+          for (int c = 0; c < chunks; c += L::kGroup) {
+            const int here = min(L::kGroup, chunks - c);
+            ok = wait_all(&sh.k_empty[slot], phase ^ 1u);
+            if (!ok) break;
+            if (c == 0) {
+              if (lane < 4) {
+                uint32_t word = ~0u;  // positions 32 lane .. of the tile
+                if (held_runs != all_runs) {
+                  const uint32_t mine = held_runs >> (lane << 5 >> shift);
+                  word = 0u;
+                  if (rows >= 32) {
+                    word = mine & 1u ? ~0u : 0u;
+                  } else {
+                    for (int j = 0; j << shift < 32; ++j)
+                      if ((mine >> j) & 1u) word |= ((1u << rows) - 1u) << (j << shift);
+                  }
+                }
+                const int past = len.len - ((cur.first + i) * kKeys + lane * 32);
+                sh.valid[g & 15u][lane] = past >= 32 ? word
+                                          : past > 0 ? word & ((1u << past) - 1u)
+                                                     : 0u;
+              }
+              if (lane == 0) sh.special[g & 15u] = 0u;
+              __syncwarp();
+            }
+            const uint32_t bar = in_cta(smem_u32(&sh.k_full[slot]), 0);
+            if (lane == 0) pair_arrive_expect_tx(bar, here * L::kChunkBytes);
+            __syncwarp();
+            if (chunk < here && DSPARK_CHECK(r + rows <= p.page && slot < L::kKSlots &&
+                                             box_at + rows * 128 <= L::kKBytes))
+              pair_load_box(k_at + slot * L::kKBytes + box_at, &map, (c + chunk) * 64, r, b, bar);
+            ++issued;
+            if (++slot == L::kKSlots) slot = 0, phase ^= 1u;
+            __syncwarp();
+          }
+        } else {
+          for (int s = 0; s < 2; ++s) {  // 64 positions
+            const int b = __shfl_sync(0xffffffffu, from, s * per_half + run);
+            const int r = __shfl_sync(0xffffffffu, row, s * per_half + run);
+            ok = wait_all(&sh.v_empty[slot], phase ^ 1u);
+            if (!ok) break;
+            const uint32_t bar = in_cta(smem_u32(&sh.v_full[slot]), 0);
+            if (lane == 0) pair_arrive_expect_tx(bar, L::kVBytes);
+            __syncwarp();
+            if (chunk < L::kVParts && DSPARK_CHECK(r + rows <= p.page && slot < L::kVSlots &&
+                                                   box_at + rows * 128 <= L::kVBytes))
+              pair_load_box(v_at + slot * L::kVBytes + box_at, &map,
+                            (int)rank * L::kHalf + chunk * 64, r, b, bar);
+            ++issued;
+            if (++slot == L::kVSlots) slot = 0, phase ^= 1u;
+            __syncwarp();
+          }
+        }
+      }
+    }
+    if (lane == 0) sh.issued[warp - 8] = issued;
+  } else if (warp == 10 && rank == 0) {
+    // ------------------------------------------------------------- products
+    // The warp goes through the loop together; one lane issues.
+    constexpr uint32_t kFormat = H::kExponent == 0x7F80u ? 1u : 0u;  // bf16 or f16
+    // fp32 accumulators, both operands of T, 128 rows; for P V the second has its dims outermost
+    constexpr uint32_t kCommon = (1u << 4) | (kFormat << 7) | (kFormat << 10) | (8u << 24);
+    constexpr uint32_t kScores = kCommon | ((uint32_t)(kKeys / 8) << 17);
+    constexpr uint32_t kValues = kCommon | (1u << 16) | (32u << 17);  // 256 dims, 128 a CTA
+    const bool on = elect_one();
+    const uint64_t q_desc = operand_desc(q_at, 16, 1024), k_desc = operand_desc(k_at, 16, 1024);
+    const uint64_t p_desc = operand_desc(p_at, 16, 1024);
+    const uint64_t v_desc = operand_desc(v_at, L::kChunkBytes, 1024);
+    // the barriers of a product's operands are looked at together, as a look takes some 200 cycles
+    auto all_of = [](uint32_t bits) { return __reduce_and_sync(0xffffffffu, bits); };
+    uint32_t k_slot = 0, k_phase = 0, v_slot = 0, v_phase = 0;
+    auto scores = [&](uint32_t g) -> bool {
+      uint32_t ready = 0, slot = k_slot, phase = k_phase;
+#pragma unroll
+      for (int x = 0; x < 3; ++x) {
+        if (x < groups && mbar_test(&sh.k_full[slot], phase)) ready |= 1u << x;
+        if (++slot == L::kKSlots) slot = 0, phase ^= 1u;
+      }
+      ready = all_of(ready);
+      for (int x = 0; x < groups; ++x) {
+        if (!((ready >> x) & 1u) && !wait_all(&sh.k_full[k_slot], k_phase)) return false;
+        tc_after_sync();
+        uint64_t a = q_desc + x * (L::kKBytes / 16);
+        uint64_t b = k_desc + k_slot * (L::kKBytes / 16);
+#pragma unroll
+        for (int c = 0; c < L::kGroup; ++c) {
+          const int left = p.width - (x * L::kGroup + c) * 64;  // zeros lie behind a row's end
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (k * 16 < left)
+              pair_mma(on, s_col(g), a + k * 2, b + k * 2, kScores, x + c + k > 0);
+          a += L::kChunkBytes / 16;
+          b += L::kChunkBytes / 16;
+        }
+        pair_commit(on, &sh.k_empty[k_slot]);
+        if (++k_slot == L::kKSlots) k_slot = 0, k_phase ^= 1u;
+      }
+      pair_commit(on, &sh.s_full[g & 1u]);
+      return true;
+    };
+    auto values = [&](uint32_t g, bool add) -> bool {
+      uint32_t ready = 0, slot = v_slot, phase = v_phase;
+      if (mbar_test(&sh.p_full, g & 1u)) ready |= 4u;
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        if (mbar_test(&sh.v_full[slot], phase)) ready |= 1u << s;
+        if (++slot == L::kVSlots) slot = 0, phase ^= 1u;
+      }
+      ready = all_of(ready);
+      if (!(ready & 4u) && !wait_all(&sh.p_full, g & 1u)) return false;
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        if (!((ready >> s) & 1u) && !wait_all(&sh.v_full[v_slot], v_phase)) return false;
+        tc_after_sync();
+        const uint64_t a = p_desc + s * (8192 / 16);
+        const uint64_t b = v_desc + v_slot * (L::kVBytes / 16);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+          for (int j = 0; j < DV / 256; ++j)
+            pair_mma(on, o_col + j * 128, a + k * 2, b + k * (2048 / 16) +
+                     j * (2 * L::kChunkBytes / 16), kValues, add || s + k > 0);
+        pair_commit(on, &sh.v_empty[v_slot]);
+        if (++v_slot == L::kVSlots) v_slot = 0, v_phase ^= 1u;
+      }
+      pair_commit(on, &sh.o_full);
+      return true;
+    };
+    uint32_t g = 0, segments = 0;
+    bool ok = true;
+    Walk cur = walk_from(p, sh.start, range, p.item_cost);
+    while (ok && cur.advance(p, kKeys)) {
+      const int tiles = cur.count;
+      ok = wait_all(&sh.q_full, segments & 1u);
+      if (!ok) break;
+      tc_after_sync();
+      ok = scores(g);
+      for (int i = 0; i < tiles && ok; ++i, ++g) {
+        if (i + 1 < tiles) ok = scores(g + 1);
+        ok = ok && values(g, i > 0);
+      }
+      ++segments;
+    }
+    // nothing is in flight when the tensor memory is given back
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t@q tcgen05.commit.cta_group::2"
+        ".mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(&sh.drained)),
+        "r"((uint32_t)on)
+        : "memory");
+    mbar_wait_bounded(&sh.drained, 0);
+  }
+  __syncwarp();
+  tc_before_sync();
+  __syncthreads();
+  if (tid == 0) {
+    pair_store(in_cta(smem_u32(&sh.peer_failed), rank ^ 1u), sh.failed);
+    pair_store(in_cta(smem_u32(&sh.peer_issued[0]), rank ^ 1u), sh.issued[0]);
+    pair_store(in_cta(smem_u32(&sh.peer_issued[1]), rank ^ 1u), sh.issued[1]);
+  }
+  __syncwarp();
+  cluster_sync();
+  tc_after_sync();
+  const bool failed = sh.failed || sh.peer_failed;
+  // After a wait that expired copies may be in flight.  CTA 0, whose barriers they complete on,
+  // arrives in place of a CTA that did not come to a copy and waits for what the other one asked
+  // for; without such a wait every copy has been multiplied.
+  if (failed && rank == 0 && (warp == 8 || warp == 9)) {
+    const uint32_t slots = warp == 8 ? L::kKSlots : L::kVSlots;
+    uint64_t* full = warp == 8 ? sh.k_full : sh.v_full;
+    const uint32_t a = sh.issued[warp - 8], b = sh.peer_issued[warp - 8];
+    const uint32_t most = a > b ? a : b, least = a > b ? b : a;
+    for (uint32_t n = most > slots ? most - slots : 0u; n < most; ++n) {
+      if (n >= least && lane == 0) pair_arrive(in_cta(smem_u32(&full[n % slots]), 0));
+      __syncwarp();
+      mbar_wait_bounded(&full[n % slots], (n / slots) & 1u);
+    }
+  }
+  __syncwarp();
+  cluster_sync();
+  if (warp == 10)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  // The requests of the range are refused; what the pair has written of them may be unfinished:
+  // NaN takes its place, and in the parts the joining kernel's sums.
+  if (!failed) return;
+  Walk cur = walk_from(p, sh.start, range, p.item_cost);
+  Lost lost = {cur.b, -1};
+  while (cur.advance(p, kKeys)) {
+    lost.last = cur.b;
+    const int64_t slot = cur.slot(pair) * p.part_rows;
+    const int first = cur.head * 128 + (int)rank * 64;
+    for (int r = tid; r < min(64, all_rows - first); r += kLatentThreads) {
+      const int64_t to = (int64_t)cur.b * all_rows + first + r;
+      const int part_row = (int)rank * 64 + r;
+      if (!DSPARK_CHECK(cur.whole() ? row_held(p, to) : part_held(p, slot, part_row))) continue;
+      if (!cur.whole()) {
+        ws.stats[slot + part_row] = make_float2(NAN, NAN);
+        continue;
+      }
+      for (int d = 0; d < p.latent; d += 2)
+        *reinterpret_cast<uint32_t*>(static_cast<T*>(p.out) + to * p.latent + d) =
+            H::pack(NAN, NAN);
+      if (p.lse) p.lse[to] = NAN;
+    }
+  }
+  if (tid == 0 && rank == 0 && DSPARK_CHECK(pair < p.max_ctas)) ws.lost[pair] = lost;
+}
+
+// ------------------------------------------------------- the joining kernel
+// CTA (x, y): eight rows of the item that is first cut between pairs x and
+// x + 1, if there is one, joined from the pairs' partial rows in the pairs'
+// order, a warp a row.  CTA (x, 0) also gives the requests that pair x lost
+// their status.
+template <typename T, int DV>
+__global__ void __launch_bounds__(kJoinThreads)
+    latent_join_kernel(const __grid_constant__ LatentParams p) {
+  using H = Half<T>;
+  constexpr int kPieces = DV / 256;  // of eight dims, of a lane
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const Workspace ws = carve(p.workspace, p.part_rows, p.max_ctas);
+  if (!DSPARK_CHECK(gridDim.x <= p.max_ctas)) return;
+  const Seam at = ws.seam[min(blockIdx.x + 1, gridDim.x - 1)];
+  Lost lost = {0, -1};
+  if (blockIdx.y == 0 && threadIdx.x == 0) lost = ws.lost[blockIdx.x];
+  [&] {
+    const int c0 = blockIdx.x, c1 = blockIdx.x + 1 < gridDim.x ? at.last : -1;  // the item's pairs
+    if (c1 < 0) return;
+    const int lane = threadIdx.x & 31;
+    const int r = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5);
+    const int row = at.head * 128 + r, all_rows = p.nodes * p.heads;
+    if (r >= p.part_rows || row >= all_rows) return;
+    auto part_of = [&](int c) -> int64_t { return (2ll * c + (c == c0 ? 1 : 0)) * p.part_rows; };
+    if (!DSPARK_CHECK(c1 < gridDim.x && part_held(p, part_of(c0), r) && part_held(p, part_of(c1), r)))
+      return;
+    float top = -INFINITY;
+    for (int c = c0 + lane; c <= c1; c += 32) top = fmaxf(top, ws.stats[part_of(c) + r].x);
+    top = warp_reduce(top, OpMaxF());
+    const float safe = top == -INFINITY ? 0.0f : top;
+    float all = 0.0f, a[kPieces][8];
+#pragma unroll
+    for (int k = 0; k < kPieces; ++k)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) a[k][j] = 0.0f;
+#pragma unroll 4
+    for (int c = c0; c <= c1; ++c) {
+      const float2 st = ws.stats[part_of(c) + r];
+      float x[kPieces][8];
+#pragma unroll
+      for (int k = 0; k < kPieces; ++k) {
+        const float* v = part_at(ws, part_of(c), p.part_rows, 8, r, DV, (k * 32 + lane) * 8);
+        *reinterpret_cast<float4*>(x[k]) = *reinterpret_cast<const float4*>(v);
+        *reinterpret_cast<float4*>(x[k] + 4) = *reinterpret_cast<const float4*>(v + 4);
+      }
+      const float f = exp2_approx(st.x - safe);
+      all += st.y * f;
+#pragma unroll
+      for (int k = 0; k < kPieces; ++k)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) a[k][j] += x[k][j] * f;
+    }
+    const int64_t to = (int64_t)at.b * all_rows + row;
+    if (!DSPARK_CHECK(row_held(p, to))) return;
+    const float inv = all == 0.0f ? 0.0f : 1.0f / all;
+#pragma unroll
+    for (int k = 0; k < kPieces; ++k) {
+      const int d = (k * 32 + lane) * 8;
+      if (d >= p.latent) continue;
+      *reinterpret_cast<uint4*>(static_cast<T*>(p.out) + to * p.latent + d) =
+          make_uint4(H::pack(a[k][0] * inv, a[k][1] * inv), H::pack(a[k][2] * inv, a[k][3] * inv),
+                     H::pack(a[k][4] * inv, a[k][5] * inv), H::pack(a[k][6] * inv, a[k][7] * inv));
+    }
+    if (lane == 0 && p.lse)
+      p.lse[to] = all == 0.0f ? -INFINITY : (top + log2f(all)) * 0.6931471805599453f;
+  }();
+  for (int b = lost.first; b <= lost.last; ++b) p.status[b] = DSPARK_ST_TIMEOUT;
+}
+
+}  // namespace attn
+}  // namespace dspark

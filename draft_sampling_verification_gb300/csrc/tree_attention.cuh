@@ -348,20 +348,22 @@ __device__ __forceinline__ Walk walk_from(const Params& p, const Start& s, int64
 // This CTA's ranges of the tile axis, kStreams of them side by side: their
 // lengths (0: no work), and where they begin (shared memory, valid after the
 // call).  All threads call.
+// `ctas` CTAs share the axis, of which this is number `cta`; `writes` says whether it notes seams.
 template <int kBlock, int kStreams>
 __device__ __forceinline__ void find_range(const Params& p, const Workspace& ws, uint64_t* scan,
-                                           Start* start, int64_t* range) {
+                                           Start* start, int64_t* range, int cta, int ctas,
+                                           bool writes) {
   int64_t before, upto;
   const int64_t total = axis_part<kBlock>(p, scan, &before, &upto);
-  const Cut c = cut(total, gridDim.x * kStreams / p.row_tiles);
+  const Cut c = cut(total, ctas * kStreams / p.row_tiles);
 #pragma unroll
   for (int x = 0; x < kStreams; ++x) {
-    const int team = blockIdx.x / p.row_tiles * kStreams + x;
+    const int team = cta / p.row_tiles * kStreams + x;
     range[x] = 0;
     if (team >= c.teams) continue;
     const int64_t x0 = c.first_of(team);
     range[x] = c.first_of(team + 1) - x0;
-    if (locate<kBlock>(p, before, upto, x0, &start[x]) && blockIdx.x % p.row_tiles == 0) {
+    if (locate<kBlock>(p, before, upto, x0, &start[x]) && writes) {
       const Start at = start[x];
       Seam seam = {at.b, at.head, -1, 0};
       const int64_t begin = x0 - at.at + p.item_cost;  // the item's first tile
@@ -373,10 +375,16 @@ __device__ __forceinline__ void find_range(const Params& p, const Workspace& ws,
     }
   }
   // teams without work: nothing to join
-  for (int t = c.teams + blockIdx.x * kBlock + threadIdx.x;
-       t < (int)gridDim.x * kStreams / p.row_tiles; t += gridDim.x * kBlock)
+  for (int t = c.teams + cta * kBlock + threadIdx.x; t < ctas * kStreams / p.row_tiles;
+       t += ctas * kBlock)
     if (DSPARK_CHECK(t < p.max_ctas)) ws.seam[t] = {0, 0, -1, 0};
   __syncthreads();
+}
+template <int kBlock, int kStreams>
+__device__ __forceinline__ void find_range(const Params& p, const Workspace& ws, uint64_t* scan,
+                                           Start* start, int64_t* range) {
+  find_range<kBlock, kStreams>(p, ws, scan, start, range, blockIdx.x, gridDim.x,
+                               blockIdx.x % p.row_tiles == 0);
 }
 
 // ------------------------------------------------------ the streaming kernel

@@ -878,10 +878,8 @@ inline int wide_box_rows(int page, int keys) {
   return rows;
 }
 
-// the map of one cache: 64 dims, rows of a block, blocks of 64 dims, heads, blocks
-template <typename T>
-bool map_cache(CUtensorMap* map, const Params& p, const void* cache, int dim, int box_rows,
-               bool whole) {
+// the driver's encoder of tensor maps, NULL where there is none
+inline auto encode_tiled() {
   using Encode = decltype(&cuTensorMapEncodeTiled);
   static const Encode encode = [] {
     void* f = nullptr;
@@ -892,6 +890,14 @@ bool map_cache(CUtensorMap* map, const Params& p, const void* cache, int dim, in
       f = nullptr;
     return reinterpret_cast<Encode>(f);
   }();
+  return encode;
+}
+
+// the map of one cache: 64 dims, rows of a block, blocks of 64 dims, heads, blocks
+template <typename T>
+bool map_cache(CUtensorMap* map, const Params& p, const void* cache, int dim, int box_rows,
+               bool whole) {
+  const auto encode = encode_tiled();
   if (!encode) return false;
   const cuuint64_t sizes[5] = {64, (cuuint64_t)p.page, (cuuint64_t)dim / 64,
                                (cuuint64_t)p.kv_heads, (cuuint64_t)p.n_blocks};
