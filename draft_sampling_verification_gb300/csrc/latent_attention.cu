@@ -4,6 +4,8 @@
 // are in latent_attention.cuh.
 #define DSPARK_TU 16  // this file's number in the checked build's site codes
 
+#include <tuple>
+
 #include "latent_attention.cuh"
 
 namespace dspark {
@@ -15,35 +17,69 @@ constexpr int kMaxPairs = 80;  // 160 SMs at most are used
 int values_dim(int latent) { return latent <= 256 ? 256 : 512; }  // of the kernel
 int latent_part_rows(int rows) { return rows >= 128 ? 128 : (rows + 7) / 8 * 8; }
 
-template <typename T>
-bool map_rows(CUtensorMap* map, const LatentParams& p, int rows) {
+// a map of 16-bit elements; the innermost dimension is dense
+template <typename T, int N>
+bool encode_map(CUtensorMap* map, const void* base, const cuuint64_t (&sizes)[N],
+                const int64_t (&strides)[N - 1], const cuuint32_t (&box)[N],
+                CUtensorMapSwizzle swizzle) {
   const auto encode = encode_tiled();
   if (!encode) return false;
-  const cuuint64_t sizes[3] = {(cuuint64_t)p.width, (cuuint64_t)p.page, (cuuint64_t)p.n_blocks};
-  const cuuint64_t strides[2] = {(cuuint64_t)p.token_stride * 2, (cuuint64_t)p.block_stride * 2};
-  const cuuint32_t box[3] = {64, (cuuint32_t)rows, 1};
-  const cuuint32_t steps[3] = {1, 1, 1};
+  cuuint64_t bytes[N - 1];
+  cuuint32_t steps[N];
+  for (int i = 0; i < N - 1; ++i) bytes[i] = (cuuint64_t)strides[i] * 2;
+  for (int i = 0; i < N; ++i) steps[i] = 1;
   return encode(map,
                 Half<T>::kExponent == 0x7F80u ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                               : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
-                3, const_cast<void*>(p.k), sizes, strides, box, steps,
-                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                N, const_cast<void*>(base), sizes, bytes, box, steps,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename T, int DV>
+bool make_maps(LatentMaps* m, const LatentParams& p) {
+  using L = Latent<DV>;
+  const auto swizzle = CU_TENSOR_MAP_SWIZZLE_128B;
+  const cuuint64_t width = p.width, page = p.page, blocks = p.n_blocks, B = p.B;
+  const cuuint64_t rows = (cuuint64_t)p.nodes * p.heads;
+  m->rows = wide_box_rows(p.page, 64);
+  // keys in one copy a group, or in eight of eight rows where those are fewer than by chunks
+  m->k_rows = m->rows == 64 ? 64 : m->rows <= 16 ? 8 : 0;
+  const cuuint32_t run = m->rows, k_run = m->k_rows ? m->k_rows : 8;
+  bool ok = encode_map<T, 3>(&m->tail, p.k, {width, page, blocks}, {p.token_stride, p.block_stride},
+                             {64, run, 1}, swizzle);
+  for (auto [map, box_rows, chunks] : {std::tuple{&m->keys, k_run, (int)L::kGroup},
+                                       std::tuple{&m->values, run, (int)L::kVParts}})
+    ok = ok && encode_map<T, 4>(map, p.k, {64, page, width / 64, blocks},
+                                {p.token_stride, 64, p.block_stride},
+                                {64, box_rows, (cuuint32_t)chunks, 1}, swizzle);
+  ok = ok && encode_map<T, 3>(&m->out, p.out, {(cuuint64_t)p.latent, rows, B},
+                              {p.latent, (int64_t)rows * p.latent}, {32, 32, 1},
+                              CU_TENSOR_MAP_SWIZZLE_64B);
+  // Q by tensor copies where a request's rows are uniformly strided (and not broadcast); a negative
+  // scale goes into its sign, which a copy cannot change
+  const int64_t row = p.heads > 1 ? p.q_head : p.nodes > 1 ? p.q_node : p.width;
+  const int64_t request = p.B > 1 ? p.q_req : row * (int64_t)rows;
+  m->q_copies = p.scale2 >= 0.0f && (p.heads == 1 || p.nodes == 1 || p.q_node == row * p.heads) &&
+                row > 0 && request > 0 && row < (1ll << 38) && request < (1ll << 38);
+  if (m->q_copies)
+    ok = ok && encode_map<T, 3>(&m->q, p.q, {width, rows, B}, {row, request}, {64, 64, 1}, swizzle);
+  else
+    m->q = m->out;  // not used
+  return ok;
 }
 
 template <typename T, int DV>
 cudaError_t launch(const LatentParams& p, int sms, cudaStream_t stream) {
   using L = Latent<DV>;
-  const int rows = wide_box_rows(p.page, 64);
-  CUtensorMap map;
-  if (!map_rows<T>(&map, p, rows)) return cudaErrorInvalidValue;
+  LatentMaps maps;
+  if (!make_maps<T, DV>(&maps, p)) return cudaErrorInvalidValue;
   auto* kernel = latent_attention_kernel<T, DV>;
   cudaError_t e =
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
   if (e != cudaSuccess) return e;
   const int pairs = min(kMaxPairs, max(1, sms / 2));
-  kernel<<<2 * pairs, kLatentThreads, L::kSmem, stream>>>(p, map, rows);
+  kernel<<<2 * pairs, kLatentThreads, L::kSmem, stream>>>(p, maps);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   // launched while that one runs, waits on the device for its end

@@ -51,8 +51,8 @@ __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t phase) {
 __device__ __forceinline__ void pair_store(uint32_t addr, uint32_t v) {
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
-// one box of the cache, from element x of row r of block b, into this CTA, completing on a barrier
-// of either CTA; what lies beyond a row's width or the cache is 0
+// Tensor copies into this CTA that complete on a barrier of either; what lies beyond the map is 0.
+// From element x of row r of block b (or of request b of Q):
 __device__ __forceinline__ void pair_load_box(uint32_t dst, const CUtensorMap* map, int x, int r,
                                               int b, uint32_t bar) {
   asm volatile(
@@ -60,6 +60,29 @@ __device__ __forceinline__ void pair_load_box(uint32_t dst, const CUtensorMap* m
       ".cta_group::2 [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
       "l"(map), "r"(x), "r"(r), "r"(b), "r"(bar)
       : "memory");
+}
+// several chunks of 64 elements, from chunk c on
+__device__ __forceinline__ void pair_load_chunks(uint32_t dst, const CUtensorMap* map, int r, int c,
+                                                 int b, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".cta_group::2 [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(map), "r"(0), "r"(r), "r"(c), "r"(b), "r"(bar)
+      : "memory");
+}
+// 32 rows of 32 elements of the result, from element x of row r of request b
+__device__ __forceinline__ void store_box(const CUtensorMap* map, int x, int r, int b,
+                                          uint32_t src) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];"
+               "\n\tcp.async.bulk.commit_group;" ::"l"(map),
+               "r"(x), "r"(r), "r"(b), "r"(src)
+               : "memory");
+}
+__device__ __forceinline__ void stores_read() {  // the shared memory of this thread's is free
+  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+}
+__device__ __forceinline__ void stores_done() {
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 // d (+)= a b over the pair, a's rows and b's columns from both CTAs' shared memory
 __device__ __forceinline__ void pair_mma(bool on, uint32_t d, uint64_t a, uint64_t b,
@@ -133,7 +156,7 @@ struct Latent {
 
 struct LatentShared {
   uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
-  uint64_t q_full, s_full[2], p_full, o_full, v_go, drained;
+  uint64_t q_full, q_empty, s_full[2], p_full, o_full, v_go, drained;
   uint64_t scan[32];
   // by tile number modulo 16: a narrow row's keys are copied up to 7 tiles ahead of the results
   uint32_t valid[16][4];  // a tile's positions that hold a key
@@ -141,13 +164,25 @@ struct LatentShared {
   Start start;
   uint32_t tmem;
   uint32_t failed;  // a wait expired
-  uint32_t peer_failed, issued[2], peer_issued[2];
+  uint32_t peer_failed, issued[3], peer_issued[3];  // copies of keys, values, queries
+};
+
+// The maps of the tensor copies, and the shapes of their boxes.
+struct LatentMaps {
+  CUtensorMap tail;    // {elements, rows of a block, blocks}, a chunk of `rows` rows
+  CUtensorMap keys;    // {64, rows of a block, whole chunks, blocks}, kGroup chunks of k_rows rows
+  CUtensorMap values;  // the same, a CTA's values of `rows` rows
+  CUtensorMap q;       // {elements, rows of a request, requests}, a chunk of 64 rows
+  CUtensorMap out;     // the same, 32 elements of 32 rows
+  int rows;            // of a block that are copied together: 8, 16, 32 or 64
+  int k_rows;          // 64 or 8; 0: keys are copied chunk by chunk
+  int q_copies;        // Q has a map
 };
 
 template <typename T, int DV>
 __global__ void __launch_bounds__(kLatentThreads, 1) __cluster_dims__(2, 1, 1)
     latent_attention_kernel(const __grid_constant__ LatentParams p,
-                            const __grid_constant__ CUtensorMap map, int rows) {
+                            const __grid_constant__ LatentMaps maps) {
   using H = Half<T>;
   using L = Latent<DV>;
   constexpr int kKeys = kLatentKeys;
@@ -160,9 +195,20 @@ __global__ void __launch_bounds__(kLatentThreads, 1) __cluster_dims__(2, 1, 1)
   const uint32_t k_at = q_at + L::kQBytes, v_at = k_at + L::kKSlots * L::kKBytes;
   const uint32_t p_at = v_at + L::kVSlots * L::kVBytes;
   const int chunks = (p.width + 63) / 64, groups = (chunks + L::kGroup - 1) / L::kGroup;
-  const int all_rows = p.nodes * p.heads;
+  const int all_rows = p.nodes * p.heads, rows = maps.rows;
+  // Where a copied group of keys lies: runs of k_rows rows, each with its chunks one after the
+  // other; chunk after chunk where it is copied so.  Values: runs of `rows` rows, each with its
+  // chunks one after the other.
+  const int whole_groups = maps.k_rows ? p.width / 64 / L::kGroup : 0;
+  const uint32_t k_chunk = maps.k_rows == 8 ? 1024u : L::kChunkBytes;
+  const uint32_t k_eight = maps.k_rows == 8 ? L::kGroup * 1024u : 1024u;  // rows
+  const uint32_t v_chunk = rows * 128u, v_run = L::kVParts * v_chunk;
+  const int shift = 31 - __clz(rows);  // a power of two
 
-  if (tid == 0) asm volatile("prefetch.tensormap [%0];" ::"l"(&map) : "memory");
+  if (tid < 5)
+    asm volatile("prefetch.tensormap [%0];" ::"l"(
+                     reinterpret_cast<const CUtensorMap*>(&maps) + tid)
+                 : "memory");
   const Workspace ws = carve(p.workspace, p.part_rows, p.max_ctas);
   int64_t range;
   find_range<kLatentThreads, 1>(p, ws, sh.scan, &sh.start, &range, pair, pairs, rank == 0);
@@ -179,7 +225,8 @@ __global__ void __launch_bounds__(kLatentThreads, 1) __cluster_dims__(2, 1, 1)
       mbar_init(&sh.v_full[i], 2);
       mbar_init(&sh.v_empty[i], 1);
     }
-    mbar_init(&sh.q_full, 16);
+    mbar_init(&sh.q_full, maps.q_copies ? 2 : 16);
+    mbar_init(&sh.q_empty, 1);
     mbar_init(&sh.s_full[0], 1);
     mbar_init(&sh.s_full[1], 1);
     mbar_init(&sh.p_full, 16);
@@ -187,7 +234,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1) __cluster_dims__(2, 1, 1)
     mbar_init(&sh.v_go, 1);
     mbar_init(&sh.drained, 1);
     sh.failed = sh.peer_failed = 0u;
-    sh.issued[0] = sh.issued[1] = sh.peer_issued[0] = sh.peer_issued[1] = 0u;
+    for (int i = 0; i < 3; ++i) sh.issued[i] = sh.peer_issued[i] = 0u;
     mbar_init_fence();
   }
   if (warp == 10) {
@@ -293,7 +340,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1) __cluster_dims__(2, 1, 1)
 
     Walk cur = walk_from(p, sh.start, range, p.item_cost);
     bool more = cur.advance(p, kKeys), ok = true;
-    if (more) fill_q(cur);
+    if (more && !maps.q_copies) fill_q(cur);
     while (ok && more) {
       const int tiles = cur.count;
       const Lengths len = cur.len;
@@ -341,7 +388,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1) __cluster_dims__(2, 1, 1)
           }
 #pragma unroll
           for (int k = 0; k < 4; ++k) m4[k] = fmaxf(m4[k], v[28 + k]);
-          top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * scale;
+          if (item_row < live) top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * scale;
         }
         bool waited = i == 0;  // the product before, of which the weights' place is free
         if (any_of_256(bad || top > ref + kSlack)) {
@@ -425,8 +472,9 @@ __global__ void __launch_bounds__(kLatentThreads, 1) __cluster_dims__(2, 1, 1)
           for (int j = tid; j < (end - from) * kPer && !bad; j += 256) {
             const int r = from + j / kPer, c = j % kPer;
             const uint32_t slot = (piece + (r >> 6)) % L::kVSlots;
-            const uint32_t addr = v_at + slot * L::kVBytes + (c >> 3) * L::kChunkBytes +
-                                  (r & 63) * 128 + (((c & 7) ^ (r & 7)) << 4);
+            const uint32_t addr = v_at + slot * L::kVBytes + ((r & 63) >> shift) * v_run +
+                                  (c >> 3) * v_chunk + (r & (rows - 1)) * 128 +
+                                  (((c & 7) ^ (r & 7)) << 4);
             if (!DSPARK_CHECK(addr >= v_at && addr + 16 <= p_at)) continue;
             uint32_t x[4];
             asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
@@ -454,7 +502,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1) __cluster_dims__(2, 1, 1)
       }
       if (!ok) break;
       // Q is free, as the last scores are done
-      if (more) fill_q(ahead);
+      if (more && !maps.q_copies) fill_q(ahead);
       wait_values();
       float sum = sum2.x + sum2.y;
       if (item_row >= live) {  // a row of no node: its zero query saw the text all the same
@@ -476,6 +524,8 @@ __global__ void __launch_bounds__(kLatentThreads, 1) __cluster_dims__(2, 1, 1)
       const float inv = sum == 0.0f ? 0.0f : full ? 1.0f / sum : 1.0f;
       const int d0 = half * L::kHalf + wg * (DV / 4);  // this thread's dims
       const int pieces = item_row - (t & 31) < all_rows ? DV / 128 : 0;
+      const uint32_t staged = p_at + warp * 2048;  // 32 rows of 64 bytes, swizzled
+      if (full) any_of_256(false);  // all have read the sums, in whose place results are staged
 #pragma unroll 1
       for (int c = 0; c < pieces; ++c) {
         const int d = d0 + c * 32;
@@ -505,15 +555,23 @@ __global__ void __launch_bounds__(kLatentThreads, 1) __cluster_dims__(2, 1, 1)
             }
           }
         }
-        if (mine && full && DSPARK_CHECK(row_held(p, to))) {
-          uint4* out = reinterpret_cast<uint4*>(static_cast<T*>(p.out) + to * p.latent + d);
+        if (full) {  // by tensor copies: a thread's 64 bytes of a row would be half a line each
+          if (lane == 0) stores_read();
+          __syncwarp();
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            out[j] = make_uint4(H::pack(v[8 * j] * inv, v[8 * j + 1] * inv),
-                                H::pack(v[8 * j + 2] * inv, v[8 * j + 3] * inv),
-                                H::pack(v[8 * j + 4] * inv, v[8 * j + 5] * inv),
-                                H::pack(v[8 * j + 6] * inv, v[8 * j + 7] * inv));
-        } else if (mine && DSPARK_CHECK(!full && part_held(p, slot, part_row))) {
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
+                             staged + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)),
+                         "r"(H::pack(v[8 * j] * inv, v[8 * j + 1] * inv)),
+                         "r"(H::pack(v[8 * j + 2] * inv, v[8 * j + 3] * inv)),
+                         "r"(H::pack(v[8 * j + 4] * inv, v[8 * j + 5] * inv)),
+                         "r"(H::pack(v[8 * j + 6] * inv, v[8 * j + 7] * inv))
+                         : "memory");
+          fence_async_shared();
+          __syncwarp();
+          if (lane == 0 && DSPARK_CHECK(cur.b < p.B && item_row < all_rows && d + 32 <= p.latent))
+            store_box(&maps.out, d, item_row, cur.b, staged);
+        } else if (mine && DSPARK_CHECK(part_held(p, slot, part_row))) {
           float* out = part_at(ws, slot, p.part_rows, 8, part_row, DV, d);
 #pragma unroll
           for (int j = 0; j < 32; j += 8)
@@ -532,20 +590,24 @@ __global__ void __launch_bounds__(kLatentThreads, 1) __cluster_dims__(2, 1, 1)
           p.lse[to] = sum == 0.0f ? -INFINITY : (ref + log2f(sum)) * 0.6931471805599453f;
       }
       tc_before_sync();  // the accumulators are read: the next item may take them
+      if (lane == 0) stores_read();  // before this warp's next vote, so before weights lie there
+      __syncwarp();
       cur = ahead;
     }
+    if (lane == 0) stores_done();
   } else if (warp < 10) {
     // ------------------------------------------------------ keys and values
-    // A box is `rows` rows of one block, 64 elements wide.  Lane i holds the place of the tile's
-    // i-th run of rows; of a copy, lane i takes the i-th box: run i % per_half of 64 positions,
-    // chunk i / per_half.
+    // Lane i holds the place of the tile's i-th run of `rows` rows of one block.  Of a copy chunk by
+    // chunk, lane i takes run i % per_half of 64 positions and chunk i / per_half; of a copy of
+    // whole groups or of values, the lanes before per_half or 64 / k_rows take a run each.
     const bool keys = warp == 8;
     const int runs = kKeys / rows, per_half = runs / 2;  // powers of two, at most 16 and 8
-    const int shift = 31 - __clz(rows), half_shift = 31 - __clz(per_half);
+    const int half_shift = 31 - __clz(per_half);
     const int next_row = kKeys % p.page, next_block = kKeys / p.page;
     const uint32_t all_runs = (1u << runs) - 1u;
     const int run = lane & (per_half - 1), chunk = lane >> half_shift;
-    const uint32_t box_at = chunk * L::kChunkBytes + run * rows * 128;
+    // boxes of eight rows: this lane's run, and its first row there
+    const int eight = lane & 7, eight_run = eight * 8 >> shift, eight_row = eight * 8 & (rows - 1);
     uint32_t g = 0, issued = 0, slot = 0, phase = 0;
     bool ok = !DSPARK_STALLED(blockIdx.x);
     Walk cur = walk_from(p, sh.start, range, p.item_cost);
@@ -575,13 +637,16 @@ __global__ void __launch_bounds__(kLatentThreads, 1) __cluster_dims__(2, 1, 1)
         const int from = held ? block : p.n_blocks, row = held ? row_here : 0;
         if (keys) {
           const uint32_t held_runs = __ballot_sync(0xffffffffu, held);
-          const int b = __shfl_sync(0xffffffffu, from, (int)rank * per_half + run);
-          const int r = __shfl_sync(0xffffffffu, row, (int)rank * per_half + run);
-          for (int c = 0; c < chunks; c += L::kGroup) {
-            const int here = min(L::kGroup, chunks - c);
+          const int at_run = (int)rank * per_half;
+          const int b = __shfl_sync(0xffffffffu, from, at_run + run);
+          const int r = __shfl_sync(0xffffffffu, row, at_run + run);
+          const int b8 = __shfl_sync(0xffffffffu, from, at_run + eight_run);
+          const int r8 = __shfl_sync(0xffffffffu, row, at_run + eight_run) + eight_row;
+          for (int x = 0; x < groups; ++x) {
+            const int c = x * L::kGroup, here = min(L::kGroup, chunks - c);
             ok = wait_all(&sh.k_empty[slot], phase ^ 1u);
             if (!ok) break;
-            if (c == 0) {
+            if (x == 0) {
               if (lane < 4) {
                 uint32_t word = ~0u;  // positions 32 lane .. of the tile
                 if (held_runs != all_runs) {
@@ -605,9 +670,18 @@ __global__ void __launch_bounds__(kLatentThreads, 1) __cluster_dims__(2, 1, 1)
             const uint32_t bar = in_cta(smem_u32(&sh.k_full[slot]), 0);
             if (lane == 0) pair_arrive_expect_tx(bar, here * L::kChunkBytes);
             __syncwarp();
-            if (chunk < here && DSPARK_CHECK(r + rows <= p.page && slot < L::kKSlots &&
-                                             box_at + rows * 128 <= L::kKBytes))
-              pair_load_box(k_at + slot * L::kKBytes + box_at, &map, (c + chunk) * 64, r, b, bar);
+            const uint32_t to = k_at + slot * L::kKBytes;
+            if (!DSPARK_CHECK(r + rows <= p.page && slot < L::kKSlots && r8 + 8 <= p.page)) {
+            } else if (x < whole_groups) {
+              if (maps.k_rows == 8) {
+                if (lane < 8) pair_load_chunks(to + lane * k_eight, &maps.keys, r8, c, b8, bar);
+              } else if (lane == 0) {
+                pair_load_chunks(to, &maps.keys, r, c, b, bar);
+              }
+            } else if (chunk < here) {
+              pair_load_box(to + chunk * L::kChunkBytes + run * rows * 128, &maps.tail,
+                            (c + chunk) * 64, r, b, bar);
+            }
             ++issued;
             if (++slot == L::kKSlots) slot = 0, phase ^= 1u;
             __syncwarp();
@@ -621,10 +695,10 @@ __global__ void __launch_bounds__(kLatentThreads, 1) __cluster_dims__(2, 1, 1)
             const uint32_t bar = in_cta(smem_u32(&sh.v_full[slot]), 0);
             if (lane == 0) pair_arrive_expect_tx(bar, L::kVBytes);
             __syncwarp();
-            if (chunk < L::kVParts && DSPARK_CHECK(r + rows <= p.page && slot < L::kVSlots &&
-                                                   box_at + rows * 128 <= L::kVBytes))
-              pair_load_box(v_at + slot * L::kVBytes + box_at, &map,
-                            (int)rank * L::kHalf + chunk * 64, r, b, bar);
+            if (lane < per_half && DSPARK_CHECK(r + rows <= p.page && slot < L::kVSlots &&
+                                                (run + 1) * v_run <= L::kVBytes))
+              pair_load_chunks(v_at + slot * L::kVBytes + run * v_run, &maps.values, r,
+                               (int)rank * L::kVParts, b, bar);
             ++issued;
             if (++slot == L::kVSlots) slot = 0, phase ^= 1u;
             __syncwarp();
@@ -642,50 +716,61 @@ __global__ void __launch_bounds__(kLatentThreads, 1) __cluster_dims__(2, 1, 1)
     constexpr uint32_t kScores = kCommon | ((uint32_t)(kKeys / 8) << 17);
     constexpr uint32_t kValues = kCommon | (1u << 16) | (32u << 17);  // 256 dims, 128 a CTA
     const bool on = elect_one();
-    const uint64_t q_desc = operand_desc(q_at, 16, 1024), k_desc = operand_desc(k_at, 16, 1024);
-    const uint64_t p_desc = operand_desc(p_at, 16, 1024);
-    const uint64_t v_desc = operand_desc(v_at, L::kChunkBytes, 1024);
-    // the barriers of a product's operands are looked at together, as a look takes some 200 cycles
-    auto all_of = [](uint32_t bits) { return __reduce_and_sync(0xffffffffu, bits); };
+    const uint64_t q_desc = operand_desc(q_at, 16, 1024), p_desc = operand_desc(p_at, 16, 1024);
+    const uint64_t k_desc = operand_desc(k_at, 16, 1024), k_whole = operand_desc(k_at, 16, k_eight);
+    // a piece of values, 16 positions after 16: within a run, or in the next ones
+    const uint64_t v_desc = operand_desc(v_at, v_chunk, rows == 8 ? v_run : 1024u);
+    uint32_t v_step[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v_step[k] = ((16 * k >> shift) * v_run + (16 * k & (rows - 1)) * 128) / 16;
     uint32_t k_slot = 0, k_phase = 0, v_slot = 0, v_phase = 0;
-    auto scores = [&](uint32_t g) -> bool {
+    // The barriers of the next products' operands are looked at together and ahead, behind the
+    // products of a group: a look takes some 160 cycles.
+    auto look = [](uint32_t bits) { return __reduce_and_sync(0xffffffffu, bits); };
+    auto look_keys = [&]() -> uint32_t {
       uint32_t ready = 0, slot = k_slot, phase = k_phase;
 #pragma unroll
       for (int x = 0; x < 3; ++x) {
         if (x < groups && mbar_test(&sh.k_full[slot], phase)) ready |= 1u << x;
         if (++slot == L::kKSlots) slot = 0, phase ^= 1u;
       }
-      ready = all_of(ready);
-      for (int x = 0; x < groups; ++x) {
-        if (!((ready >> x) & 1u) && !wait_all(&sh.k_full[k_slot], k_phase)) return false;
-        tc_after_sync();
-        uint64_t a = q_desc + x * (L::kKBytes / 16);
-        uint64_t b = k_desc + k_slot * (L::kKBytes / 16);
-#pragma unroll
-        for (int c = 0; c < L::kGroup; ++c) {
-          const int left = p.width - (x * L::kGroup + c) * 64;  // zeros lie behind a row's end
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (k * 16 < left)
-              pair_mma(on, s_col(g), a + k * 2, b + k * 2, kScores, x + c + k > 0);
-          a += L::kChunkBytes / 16;
-          b += L::kChunkBytes / 16;
-        }
-        pair_commit(on, &sh.k_empty[k_slot]);
-        if (++k_slot == L::kKSlots) k_slot = 0, k_phase ^= 1u;
-      }
-      pair_commit(on, &sh.s_full[g & 1u]);
-      return true;
+      return look(ready);
     };
-    auto values = [&](uint32_t g, bool add) -> bool {
-      uint32_t ready = 0, slot = v_slot, phase = v_phase;
-      if (mbar_test(&sh.p_full, g & 1u)) ready |= 4u;
+    auto look_values = [&](uint32_t g) -> uint32_t {
+      uint32_t ready = mbar_test(&sh.p_full, g & 1u) ? 4u : 0u, slot = v_slot, phase = v_phase;
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         if (mbar_test(&sh.v_full[slot], phase)) ready |= 1u << s;
         if (++slot == L::kVSlots) slot = 0, phase ^= 1u;
       }
-      ready = all_of(ready);
+      return look(ready);
+    };
+    // group x of tile g's scores
+    auto scores = [&](uint32_t g, int x, bool ready) -> bool {
+      if (!ready && !wait_all(&sh.k_full[k_slot], k_phase)) return false;
+      tc_after_sync();
+      const bool whole = x < whole_groups;
+      const uint64_t a = q_desc + x * (L::kKBytes / 16);
+      const uint64_t b = (whole ? k_whole : k_desc) + k_slot * (L::kKBytes / 16);
+      const uint32_t step = (whole ? k_chunk : L::kChunkBytes) / 16;
+      const int here = chunks - x * L::kGroup;
+      auto chunk = [&](int c) {  // zeros lie behind a row's end
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          pair_mma(on, s_col(g), a + c * (L::kChunkBytes / 16) + k * 2, b + c * step + k * 2,
+                   kScores, c + k > 0 || x > 0);
+      };
+      if (here >= L::kGroup) {  // without a branch between its products
+#pragma unroll
+        for (int c = 0; c < L::kGroup; ++c) chunk(c);
+      } else {
+        for (int c = 0; c < here; ++c) chunk(c);
+      }
+      pair_commit(on, &sh.k_empty[k_slot]);
+      if (++k_slot == L::kKSlots) k_slot = 0, k_phase ^= 1u;
+      return true;
+    };
+    auto values = [&](uint32_t g, bool add, uint32_t ready) -> bool {
       if (!(ready & 4u) && !wait_all(&sh.p_full, g & 1u)) return false;
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
@@ -697,8 +782,8 @@ __global__ void __launch_bounds__(kLatentThreads, 1) __cluster_dims__(2, 1, 1)
         for (int k = 0; k < 4; ++k)
 #pragma unroll
           for (int j = 0; j < DV / 256; ++j)
-            pair_mma(on, o_col + j * 128, a + k * 2, b + k * (2048 / 16) +
-                     j * (2 * L::kChunkBytes / 16), kValues, add || s + k > 0);
+            pair_mma(on, o_col + j * 128, a + k * 2, b + v_step[k] + j * (2 * v_chunk / 16), kValues,
+                     add || s + k > 0);
         pair_commit(on, &sh.v_empty[v_slot]);
         if (++v_slot == L::kVSlots) v_slot = 0, v_phase ^= 1u;
       }
@@ -713,10 +798,22 @@ __global__ void __launch_bounds__(kLatentThreads, 1) __cluster_dims__(2, 1, 1)
       ok = wait_all(&sh.q_full, segments & 1u);
       if (!ok) break;
       tc_after_sync();
-      ok = scores(g);
+      uint32_t ready = look_keys();
+      for (int x = 0; x < groups && ok; ++x) ok = scores(g, x, (ready >> x) & 1u);
+      pair_commit(on, &sh.s_full[g & 1u]);
+      if (tiles == 1) pair_commit(on, &sh.q_empty);
       for (int i = 0; i < tiles && ok; ++i, ++g) {
-        if (i + 1 < tiles) ok = scores(g + 1);
-        ok = ok && values(g, i > 0);
+        uint32_t values_ready = 0;
+        if (i + 1 < tiles) {
+          ready = look_keys();
+          for (int x = 0; x < groups && ok; ++x) {
+            if (x + 1 == groups) values_ready = look_values(g);
+            ok = scores(g + 1, x, (ready >> x) & 1u);
+          }
+          pair_commit(on, &sh.s_full[(g + 1) & 1u]);
+          if (i + 2 == tiles) pair_commit(on, &sh.q_empty);
+        }
+        ok = ok && values(g, i > 0, values_ready);
       }
       ++segments;
     }
@@ -727,14 +824,32 @@ __global__ void __launch_bounds__(kLatentThreads, 1) __cluster_dims__(2, 1, 1)
         "r"((uint32_t)on)
         : "memory");
     mbar_wait_bounded(&sh.drained, 0);
+  } else if (warp == 11 && maps.q_copies) {
+    // -------------------------------------------------------------- queries
+    uint32_t segments = 0;
+    bool ok = true;
+    Walk cur = walk_from(p, sh.start, range, p.item_cost);
+    while (ok && cur.advance(p, kKeys)) {
+      ok = wait_all(&sh.q_empty, (segments & 1u) ^ 1u);  // the scores of the item before are done
+      if (!ok) break;
+      const uint32_t bar = in_cta(smem_u32(&sh.q_full), 0);
+      if (lane == 0) pair_arrive_expect_tx(bar, chunks * L::kChunkBytes);
+      __syncwarp();
+      if (lane < chunks && DSPARK_CHECK(cur.b < p.B && cur.head < p.kv_heads && lane < L::kChunks))
+        pair_load_box(q_at + lane * L::kChunkBytes, &maps.q, lane * 64,
+                      cur.head * 128 + (int)rank * 64, cur.b, bar);
+      ++segments;
+      __syncwarp();
+    }
+    if (lane == 0) sh.issued[2] = segments;
   }
   __syncwarp();
   tc_before_sync();
   __syncthreads();
   if (tid == 0) {
     pair_store(in_cta(smem_u32(&sh.peer_failed), rank ^ 1u), sh.failed);
-    pair_store(in_cta(smem_u32(&sh.peer_issued[0]), rank ^ 1u), sh.issued[0]);
-    pair_store(in_cta(smem_u32(&sh.peer_issued[1]), rank ^ 1u), sh.issued[1]);
+    for (int i = 0; i < 3; ++i)
+      pair_store(in_cta(smem_u32(&sh.peer_issued[i]), rank ^ 1u), sh.issued[i]);
   }
   __syncwarp();
   cluster_sync();
@@ -743,10 +858,11 @@ __global__ void __launch_bounds__(kLatentThreads, 1) __cluster_dims__(2, 1, 1)
   // After a wait that expired copies may be in flight.  CTA 0, whose barriers they complete on,
   // arrives in place of a CTA that did not come to a copy and waits for what the other one asked
   // for; without such a wait every copy has been multiplied.
-  if (failed && rank == 0 && (warp == 8 || warp == 9)) {
-    const uint32_t slots = warp == 8 ? L::kKSlots : L::kVSlots;
-    uint64_t* full = warp == 8 ? sh.k_full : sh.v_full;
-    const uint32_t a = sh.issued[warp - 8], b = sh.peer_issued[warp - 8];
+  if (failed && rank == 0 && warp >= 8 && warp != 10) {
+    const int of = warp == 11 ? 2 : warp - 8;
+    const uint32_t slots = of == 0 ? L::kKSlots : of == 1 ? L::kVSlots : 1;
+    uint64_t* full = of == 0 ? sh.k_full : of == 1 ? sh.v_full : &sh.q_full;
+    const uint32_t a = sh.issued[of], b = sh.peer_issued[of];
     const uint32_t most = a > b ? a : b, least = a > b ? b : a;
     for (uint32_t n = most > slots ? most - slots : 0u; n < most; ++n) {
       if (n >= least && lane == 0) pair_arrive(in_cta(smem_u32(&full[n % slots]), 0));
