@@ -84,8 +84,9 @@ cudaError_t launch(const LatentParams& p, int sms, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   // launched while that one runs, waits on the device for its end
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(pairs, (p.part_rows + kJoinThreads / 32 - 1) / (kJoinThreads / 32));
-  cfg.blockDim = dim3(kJoinThreads);
+  constexpr int kRows = kLatentJoinThreads / 32 / (DV / 256);  // of a CTA
+  cfg.gridDim = dim3(pairs, (p.part_rows + kRows - 1) / kRows);
+  cfg.blockDim = dim3(kLatentJoinThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

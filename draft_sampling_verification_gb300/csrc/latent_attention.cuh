@@ -209,13 +209,6 @@ __global__ void __launch_bounds__(kLatentThreads, 1) __cluster_dims__(2, 1, 1)
     asm volatile("prefetch.tensormap [%0];" ::"l"(
                      reinterpret_cast<const CUtensorMap*>(&maps) + tid)
                  : "memory");
-  const Workspace ws = carve(p.workspace, p.part_rows, p.max_ctas);
-  int64_t range;
-  find_range<kLatentThreads, 1>(p, ws, sh.scan, &sh.start, &range, pair, pairs, rank == 0);
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (tid == 0 && rank == 0 && DSPARK_CHECK(pair < p.max_ctas)) ws.lost[pair] = {0, -1};
-  if (range <= 0) return;  // both CTAs
-
   if (tid == 0) {
     for (int i = 0; i < L::kKSlots; ++i) {
       mbar_init(&sh.k_full[i], 2);
@@ -243,11 +236,21 @@ __global__ void __launch_bounds__(kLatentThreads, 1) __cluster_dims__(2, 1, 1)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
+  const Workspace ws = carve(p.workspace, p.part_rows, p.max_ctas);
+  int64_t range;
+  find_range<kLatentThreads, 1>(p, ws, sh.scan, &sh.start, &range, pair, pairs, rank == 0);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (tid == 0 && rank == 0 && DSPARK_CHECK(pair < p.max_ctas)) ws.lost[pair] = {0, -1};
   tc_before_sync();
   __syncthreads();
   cluster_sync();
   tc_after_sync();
   const uint32_t tmem = sh.tmem;
+  if (range <= 0) {  // both CTAs
+    if (warp == 10)
+      asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    return;
+  }
   auto s_col = [&](uint32_t g) -> uint32_t { return tmem + (g & 1u) * 64u; };
   const uint32_t o_col = tmem + 128u;
 
@@ -572,11 +575,10 @@ __global__ void __launch_bounds__(kLatentThreads, 1) __cluster_dims__(2, 1, 1)
           if (lane == 0 && DSPARK_CHECK(cur.b < p.B && item_row < all_rows && d + 32 <= p.latent))
             store_box(&maps.out, d, item_row, cur.b, staged);
         } else if (mine && DSPARK_CHECK(part_held(p, slot, part_row))) {
-          float* out = part_at(ws, slot, p.part_rows, 8, part_row, DV, d);
+          float* out = ws.rows + (slot + part_row) * DV + d;
 #pragma unroll
           for (int j = 0; j < 32; j += 8)
-            asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(
-                             out + j / 8 * (p.part_rows * 8)),
+            asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(out + j),
                          "f"(v[j]), "f"(v[j + 1]), "f"(v[j + 2]), "f"(v[j + 3]), "f"(v[j + 4]),
                          "f"(v[j + 5]), "f"(v[j + 6]), "f"(v[j + 7])
                          : "memory");
@@ -901,15 +903,18 @@ __global__ void __launch_bounds__(kLatentThreads, 1) __cluster_dims__(2, 1, 1)
 }
 
 // ------------------------------------------------------- the joining kernel
-// CTA (x, y): eight rows of the item that is first cut between pairs x and
-// x + 1, if there is one, joined from the pairs' partial rows in the pairs'
-// order, a warp a row.  CTA (x, 0) also gives the requests that pair x lost
-// their status.
+// The item that is first cut between pairs x and x + 1, if there is one, is
+// joined from the pairs' partial rows, in the pairs' order: a warp takes 256
+// dims of a row, so that the parts of a long item, some 20, come in three
+// rounds of loads.  CTA (x, 0) also gives the requests that pair x lost their
+// status.
+constexpr int kLatentJoinThreads = 128;
+
 template <typename T, int DV>
-__global__ void __launch_bounds__(kJoinThreads)
+__global__ void __launch_bounds__(kLatentJoinThreads)
     latent_join_kernel(const __grid_constant__ LatentParams p) {
   using H = Half<T>;
-  constexpr int kPieces = DV / 256;  // of eight dims, of a lane
+  constexpr int kSlices = DV / 256, kRows = kLatentJoinThreads / 32 / kSlices, kAhead = 8;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Workspace ws = carve(p.workspace, p.part_rows, p.max_ctas);
   if (!DSPARK_CHECK(gridDim.x <= p.max_ctas)) return;
@@ -919,51 +924,55 @@ __global__ void __launch_bounds__(kJoinThreads)
   [&] {
     const int c0 = blockIdx.x, c1 = blockIdx.x + 1 < gridDim.x ? at.last : -1;  // the item's pairs
     if (c1 < 0) return;
-    const int lane = threadIdx.x & 31;
-    const int r = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int r = blockIdx.y * kRows + warp / kSlices, d = warp % kSlices * 256 + lane * 4;
     const int row = at.head * 128 + r, all_rows = p.nodes * p.heads;
     if (r >= p.part_rows || row >= all_rows) return;
     auto part_of = [&](int c) -> int64_t { return (2ll * c + (c == c0 ? 1 : 0)) * p.part_rows; };
     if (!DSPARK_CHECK(c1 < gridDim.x && part_held(p, part_of(c0), r) && part_held(p, part_of(c1), r)))
       return;
+    const int64_t to = (int64_t)at.b * all_rows + row;
+    if (!DSPARK_CHECK(row_held(p, to))) return;
     float top = -INFINITY;
     for (int c = c0 + lane; c <= c1; c += 32) top = fmaxf(top, ws.stats[part_of(c) + r].x);
     top = warp_reduce(top, OpMaxF());
     const float safe = top == -INFINITY ? 0.0f : top;
-    float all = 0.0f, a[kPieces][8];
-#pragma unroll
-    for (int k = 0; k < kPieces; ++k)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) a[k][j] = 0.0f;
-#pragma unroll 4
-    for (int c = c0; c <= c1; ++c) {
-      const float2 st = ws.stats[part_of(c) + r];
-      float x[kPieces][8];
-#pragma unroll
-      for (int k = 0; k < kPieces; ++k) {
-        const float* v = part_at(ws, part_of(c), p.part_rows, 8, r, DV, (k * 32 + lane) * 8);
-        *reinterpret_cast<float4*>(x[k]) = *reinterpret_cast<const float4*>(v);
-        *reinterpret_cast<float4*>(x[k] + 4) = *reinterpret_cast<const float4*>(v + 4);
-      }
+    float all = 0.0f;
+    float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f), b = a;
+    for (int base = c0; base <= c1; base += 32) {  // 32 parts, whose factors the lanes hold
+      float2 st = make_float2(-INFINITY, 0.0f);
+      if (base + lane <= c1) st = ws.stats[part_of(base + lane) + r];
       const float f = exp2_approx(st.x - safe);
-      all += st.y * f;
+      for (int c = base; c <= min(c1, base + 31); c += kAhead) {
+        float4 x[kAhead], y[kAhead];
 #pragma unroll
-      for (int k = 0; k < kPieces; ++k)
+        for (int u = 0; u < kAhead; ++u) {
+          x[u] = y[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          if (c + u > c1) continue;
+          const float4* v =
+              reinterpret_cast<const float4*>(ws.rows + (part_of(c + u) + r) * DV + d);
+          x[u] = v[0];
+          y[u] = v[32];
+        }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) a[k][j] += x[k][j] * f;
+        for (int u = 0; u < kAhead; ++u) {
+          if (c + u > c1) continue;
+          const float w = __shfl_sync(0xffffffffu, f, c + u - base);
+          all += __shfl_sync(0xffffffffu, st.y, c + u - base) * w;
+          a = make_float4(a.x + x[u].x * w, a.y + x[u].y * w, a.z + x[u].z * w, a.w + x[u].w * w);
+          b = make_float4(b.x + y[u].x * w, b.y + y[u].y * w, b.z + y[u].z * w, b.w + y[u].w * w);
+        }
+      }
     }
-    const int64_t to = (int64_t)at.b * all_rows + row;
-    if (!DSPARK_CHECK(row_held(p, to))) return;
     const float inv = all == 0.0f ? 0.0f : 1.0f / all;
-#pragma unroll
-    for (int k = 0; k < kPieces; ++k) {
-      const int d = (k * 32 + lane) * 8;
-      if (d >= p.latent) continue;
-      *reinterpret_cast<uint4*>(static_cast<T*>(p.out) + to * p.latent + d) =
-          make_uint4(H::pack(a[k][0] * inv, a[k][1] * inv), H::pack(a[k][2] * inv, a[k][3] * inv),
-                     H::pack(a[k][4] * inv, a[k][5] * inv), H::pack(a[k][6] * inv, a[k][7] * inv));
-    }
-    if (lane == 0 && p.lse)
+    T* out = static_cast<T*>(p.out) + to * p.latent + d;
+    if (d < p.latent)
+      *reinterpret_cast<uint2*>(out) =
+          make_uint2(H::pack(a.x * inv, a.y * inv), H::pack(a.z * inv, a.w * inv));
+    if (d + 128 < p.latent)
+      *reinterpret_cast<uint2*>(out + 128) =
+          make_uint2(H::pack(b.x * inv, b.y * inv), H::pack(b.z * inv, b.w * inv));
+    if (d == 0 && p.lse)
       p.lse[to] = all == 0.0f ? -INFINITY : (top + log2f(all)) * 0.6931471805599453f;
   }();
   for (int b = lost.first; b <= lost.last; ++b) p.status[b] = DSPARK_ST_TIMEOUT;
