@@ -38,16 +38,6 @@ __device__ __forceinline__ void pair_arrive_expect_tx(uint32_t bar, uint32_t byt
   asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
                : "memory");
 }
-__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t phase) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(phase)
-      : "memory");
-  return ok != 0u;
-}
 __device__ __forceinline__ void pair_store(uint32_t addr, uint32_t v) {
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
@@ -133,10 +123,10 @@ __device__ __forceinline__ bool any_of_256(bool v) {
 // Warps 0-7: softmax; a thread has a row's scores of 32 positions, so four
 // threads share a row: the threads vote whether any score passes its row's
 // reference by more than 8, and only then exchange maxima and rescale.  Also
-// queries and results.  Warps 8 and 9: tensor copies of keys and of values.
-// Warp 10 of CTA 0 issues the pair's products.
+// results.  Warp 8: tensor copies of keys; warp 9: of queries and values.  Warps
+// 10 and 11 of CTA 0 issue the pair's products.
 constexpr int kLatentKeys = 128;  // positions of a tile
-constexpr int kLatentThreads = 384;
+constexpr int kLatentThreads = 384;  // 168 registers a thread; from 416 on it is 128, and spills
 constexpr int kLatentCost = 3;
 
 template <int DV>
@@ -156,7 +146,7 @@ struct Latent {
 
 struct LatentShared {
   uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
-  uint64_t q_full, q_empty, s_full[2], p_full, o_full, v_go, drained;
+  uint64_t q_full, q_empty, s_full[2], p_full[2], o_full, v_go, drained;
   uint64_t scan[32];
   // by tile number modulo 16: a narrow row's keys are copied up to 7 tiles ahead of the results
   uint32_t valid[16][4];  // a tile's positions that hold a key
@@ -220,12 +210,13 @@ __global__ void __launch_bounds__(kLatentThreads, 1) __cluster_dims__(2, 1, 1)
     }
     mbar_init(&sh.q_full, maps.q_copies ? 2 : 16);
     mbar_init(&sh.q_empty, 1);
-    mbar_init(&sh.s_full[0], 1);
-    mbar_init(&sh.s_full[1], 1);
-    mbar_init(&sh.p_full, 16);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.s_full[i], 1);
+      mbar_init(&sh.p_full[i], 16);
+    }
     mbar_init(&sh.o_full, 1);
     mbar_init(&sh.v_go, 1);
-    mbar_init(&sh.drained, 1);
+    mbar_init(&sh.drained, 2);
     sh.failed = sh.peer_failed = 0u;
     for (int i = 0; i < 3; ++i) sh.issued[i] = sh.peer_issued[i] = 0u;
     mbar_init_fence();
@@ -281,7 +272,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1) __cluster_dims__(2, 1, 1)
     // as in tree_attention_wide_kernel: a negative scale goes into Q's sign
     const uint32_t flip = p.scale2 < 0.0f ? 0x80008000u : 0u;
     const float scale = fmaxf(fabsf(p.scale2), 1.17549435e-38f);
-    const uint32_t q_full = in_cta(smem_u32(&sh.q_full), 0), p_full = in_cta(smem_u32(&sh.p_full), 0);
+    const uint32_t q_full = in_cta(smem_u32(&sh.q_full), 0), p_full = in_cta(smem_u32(&sh.p_full[0]), 0);
     const uint32_t v_go = in_cta(smem_u32(&sh.v_go), 1);
     const uint32_t special_there = in_cta(smem_u32(sh.special), rank ^ 1u);
     // four floats a row, in the place of the weights between two products
@@ -501,7 +492,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1) __cluster_dims__(2, 1, 1)
         fence_async_shared();
         tc_before_sync();
         __syncwarp();
-        if (lane == 0) pair_arrive(p_full);
+        if (lane == 0) pair_arrive(p_full + (tile_no & 1u) * 8u);
       }
       if (!ok) break;
       // Q is free, as the last scores are done
@@ -610,10 +601,24 @@ __global__ void __launch_bounds__(kLatentThreads, 1) __cluster_dims__(2, 1, 1)
     const int run = lane & (per_half - 1), chunk = lane >> half_shift;
     // boxes of eight rows: this lane's run, and its first row there
     const int eight = lane & 7, eight_run = eight * 8 >> shift, eight_row = eight * 8 & (rows - 1);
-    uint32_t g = 0, issued = 0, slot = 0, phase = 0;
+    uint32_t g = 0, issued = 0, slot = 0, phase = 0, segments = 0;
     bool ok = !DSPARK_STALLED(blockIdx.x);
     Walk cur = walk_from(p, sh.start, range, p.item_cost);
     while (ok && cur.advance(p, kKeys)) {
+      if (!keys && maps.q_copies) {
+        // the item's queries, once the scores of the item before are done, which is before any
+        // place of values is free
+        ok = wait_all(&sh.q_empty, (segments & 1u) ^ 1u);
+        if (!ok) break;
+        const uint32_t bar = in_cta(smem_u32(&sh.q_full), 0);
+        if (lane == 0) pair_arrive_expect_tx(bar, chunks * L::kChunkBytes);
+        __syncwarp();
+        if (lane < chunks && DSPARK_CHECK(cur.b < p.B && cur.head < p.kv_heads && lane < L::kChunks))
+          pair_load_box(q_at + lane * L::kChunkBytes, &maps.q, lane * 64,
+                        cur.head * 128 + (int)rank * 64, cur.b, bar);
+        ++segments;
+        __syncwarp();
+      }
       const int tiles = cur.count;
       const Lengths len = cur.len;
       int pos = cur.first * kKeys + lane * rows, at = pos / p.page, row_ahead = pos - at * p.page;
@@ -708,116 +713,93 @@ __global__ void __launch_bounds__(kLatentThreads, 1) __cluster_dims__(2, 1, 1)
         }
       }
     }
-    if (lane == 0) sh.issued[warp - 8] = issued;
-  } else if (warp == 10 && rank == 0) {
+    if (lane == 0) {
+      sh.issued[warp - 8] = issued;
+      if (!keys) sh.issued[2] = segments;
+    }
+  } else if (rank == 0) {
     // ------------------------------------------------------------- products
-    // The warp goes through the loop together; one lane issues.
+    // A warp for the scores and one for the values, so that one's waits, 200 cycles each where the
+    // tensor cores hold some 100 cycles of products ahead, pass during the other's products.  A
+    // warp goes through its loop together; one lane issues.
     constexpr uint32_t kFormat = H::kExponent == 0x7F80u ? 1u : 0u;  // bf16 or f16
     // fp32 accumulators, both operands of T, 128 rows; for P V the second has its dims outermost
     constexpr uint32_t kCommon = (1u << 4) | (kFormat << 7) | (kFormat << 10) | (8u << 24);
     constexpr uint32_t kScores = kCommon | ((uint32_t)(kKeys / 8) << 17);
     constexpr uint32_t kValues = kCommon | (1u << 16) | (32u << 17);  // 256 dims, 128 a CTA
     const bool on = elect_one();
-    const uint64_t q_desc = operand_desc(q_at, 16, 1024), p_desc = operand_desc(p_at, 16, 1024);
-    const uint64_t k_desc = operand_desc(k_at, 16, 1024), k_whole = operand_desc(k_at, 16, k_eight);
-    // a piece of values, 16 positions after 16: within a run, or in the next ones
-    const uint64_t v_desc = operand_desc(v_at, v_chunk, rows == 8 ? v_run : 1024u);
-    uint32_t v_step[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) v_step[k] = ((16 * k >> shift) * v_run + (16 * k & (rows - 1)) * 128) / 16;
-    uint32_t k_slot = 0, k_phase = 0, v_slot = 0, v_phase = 0;
-    // The barriers of the next products' operands are looked at together and ahead, behind the
-    // products of a group: a look takes some 160 cycles.
-    auto look = [](uint32_t bits) { return __reduce_and_sync(0xffffffffu, bits); };
-    auto look_keys = [&]() -> uint32_t {
-      uint32_t ready = 0, slot = k_slot, phase = k_phase;
-#pragma unroll
-      for (int x = 0; x < 3; ++x) {
-        if (x < groups && mbar_test(&sh.k_full[slot], phase)) ready |= 1u << x;
-        if (++slot == L::kKSlots) slot = 0, phase ^= 1u;
-      }
-      return look(ready);
-    };
-    auto look_values = [&](uint32_t g) -> uint32_t {
-      uint32_t ready = mbar_test(&sh.p_full, g & 1u) ? 4u : 0u, slot = v_slot, phase = v_phase;
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        if (mbar_test(&sh.v_full[slot], phase)) ready |= 1u << s;
-        if (++slot == L::kVSlots) slot = 0, phase ^= 1u;
-      }
-      return look(ready);
-    };
-    // group x of tile g's scores
-    auto scores = [&](uint32_t g, int x, bool ready) -> bool {
-      if (!ready && !wait_all(&sh.k_full[k_slot], k_phase)) return false;
-      tc_after_sync();
-      const bool whole = x < whole_groups;
-      const uint64_t a = q_desc + x * (L::kKBytes / 16);
-      const uint64_t b = (whole ? k_whole : k_desc) + k_slot * (L::kKBytes / 16);
-      const uint32_t step = (whole ? k_chunk : L::kChunkBytes) / 16;
-      const int here = chunks - x * L::kGroup;
-      auto chunk = [&](int c) {  // zeros lie behind a row's end
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          pair_mma(on, s_col(g), a + c * (L::kChunkBytes / 16) + k * 2, b + c * step + k * 2,
-                   kScores, c + k > 0 || x > 0);
-      };
-      if (here >= L::kGroup) {  // without a branch between its products
-#pragma unroll
-        for (int c = 0; c < L::kGroup; ++c) chunk(c);
-      } else {
-        for (int c = 0; c < here; ++c) chunk(c);
-      }
-      pair_commit(on, &sh.k_empty[k_slot]);
-      if (++k_slot == L::kKSlots) k_slot = 0, k_phase ^= 1u;
-      return true;
-    };
-    auto values = [&](uint32_t g, bool add, uint32_t ready) -> bool {
-      if (!(ready & 4u) && !wait_all(&sh.p_full, g & 1u)) return false;
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        if (!((ready >> s) & 1u) && !wait_all(&sh.v_full[v_slot], v_phase)) return false;
-        tc_after_sync();
-        const uint64_t a = p_desc + s * (8192 / 16);
-        const uint64_t b = v_desc + v_slot * (L::kVBytes / 16);
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-#pragma unroll
-          for (int j = 0; j < DV / 256; ++j)
-            pair_mma(on, o_col + j * 128, a + k * 2, b + v_step[k] + j * (2 * v_chunk / 16), kValues,
-                     add || s + k > 0);
-        pair_commit(on, &sh.v_empty[v_slot]);
-        if (++v_slot == L::kVSlots) v_slot = 0, v_phase ^= 1u;
-      }
-      pair_commit(on, &sh.o_full);
-      return true;
-    };
-    uint32_t g = 0, segments = 0;
+    uint32_t g = 0, slot = 0, phase = 0;
     bool ok = true;
     Walk cur = walk_from(p, sh.start, range, p.item_cost);
-    while (ok && cur.advance(p, kKeys)) {
-      const int tiles = cur.count;
-      ok = wait_all(&sh.q_full, segments & 1u);
-      if (!ok) break;
-      tc_after_sync();
-      uint32_t ready = look_keys();
-      for (int x = 0; x < groups && ok; ++x) ok = scores(g, x, (ready >> x) & 1u);
-      pair_commit(on, &sh.s_full[g & 1u]);
-      if (tiles == 1) pair_commit(on, &sh.q_empty);
-      for (int i = 0; i < tiles && ok; ++i, ++g) {
-        uint32_t values_ready = 0;
-        if (i + 1 < tiles) {
-          ready = look_keys();
+    if (warp == 10) {
+      const uint64_t q_desc = operand_desc(q_at, 16, 1024), k_desc = operand_desc(k_at, 16, 1024);
+      const uint64_t k_whole = operand_desc(k_at, 16, k_eight);
+      uint32_t segments = 0;
+      while (ok && cur.advance(p, kKeys)) {
+        ok = wait_all(&sh.q_full, segments & 1u);
+        for (int i = 0; i < cur.count && ok; ++i, ++g) {
+          // the scores two tiles before have been read
+          if (g >= 2) ok = wait_all(&sh.p_full[g & 1u], (g >> 1) + 1u & 1u);
           for (int x = 0; x < groups && ok; ++x) {
-            if (x + 1 == groups) values_ready = look_values(g);
-            ok = scores(g + 1, x, (ready >> x) & 1u);
+            ok = wait_all(&sh.k_full[slot], phase);
+            if (!ok) break;
+            tc_after_sync();
+            const bool whole = x < whole_groups;
+            const uint64_t a = q_desc + x * (L::kKBytes / 16);
+            const uint64_t b = (whole ? k_whole : k_desc) + slot * (L::kKBytes / 16);
+            const uint32_t step = (whole ? k_chunk : L::kChunkBytes) / 16;
+            const int here = chunks - x * L::kGroup;
+            auto chunk = [&](int c) {  // zeros lie behind a row's end
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                pair_mma(on, s_col(g), a + c * (L::kChunkBytes / 16) + k * 2, b + c * step + k * 2,
+                         kScores, c + k > 0 || x > 0);
+            };
+            if (here >= L::kGroup) {  // without a branch between its products
+#pragma unroll
+              for (int c = 0; c < L::kGroup; ++c) chunk(c);
+            } else {
+              for (int c = 0; c < here; ++c) chunk(c);
+            }
+            pair_commit(on, &sh.k_empty[slot]);
+            if (++slot == L::kKSlots) slot = 0, phase ^= 1u;
           }
-          pair_commit(on, &sh.s_full[(g + 1) & 1u]);
-          if (i + 2 == tiles) pair_commit(on, &sh.q_empty);
+          if (!ok) break;
+          pair_commit(on, &sh.s_full[g & 1u]);
+          if (i + 1 == cur.count) pair_commit(on, &sh.q_empty);
         }
-        ok = ok && values(g, i > 0, values_ready);
+        ++segments;
       }
-      ++segments;
+    } else {
+      const uint64_t p_desc = operand_desc(p_at, 16, 1024);
+      // a piece of values, 16 positions after 16: within a run, or in the next ones
+      const uint64_t v_desc = operand_desc(v_at, v_chunk, rows == 8 ? v_run : 1024u);
+      uint32_t step[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        step[k] = ((16 * k >> shift) * v_run + (16 * k & (rows - 1)) * 128) / 16;
+      while (ok && cur.advance(p, kKeys)) {
+        for (int i = 0; i < cur.count && ok; ++i, ++g) {
+          ok = wait_all(&sh.p_full[g & 1u], (g >> 1) & 1u);
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            ok = ok && wait_all(&sh.v_full[slot], phase);
+            if (!ok) break;
+            tc_after_sync();
+            const uint64_t a = p_desc + s * (8192 / 16);
+            const uint64_t b = v_desc + slot * (L::kVBytes / 16);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+              for (int j = 0; j < DV / 256; ++j)
+                pair_mma(on, o_col + j * 128, a + k * 2, b + step[k] + j * (2 * v_chunk / 16),
+                         kValues, i > 0 || s + k > 0);
+            pair_commit(on, &sh.v_empty[slot]);
+            if (++slot == L::kVSlots) slot = 0, phase ^= 1u;
+          }
+          if (ok) pair_commit(on, &sh.o_full);
+        }
+      }
     }
     // nothing is in flight when the tensor memory is given back
     asm volatile(
@@ -826,24 +808,6 @@ __global__ void __launch_bounds__(kLatentThreads, 1) __cluster_dims__(2, 1, 1)
         "r"((uint32_t)on)
         : "memory");
     mbar_wait_bounded(&sh.drained, 0);
-  } else if (warp == 11 && maps.q_copies) {
-    // -------------------------------------------------------------- queries
-    uint32_t segments = 0;
-    bool ok = true;
-    Walk cur = walk_from(p, sh.start, range, p.item_cost);
-    while (ok && cur.advance(p, kKeys)) {
-      ok = wait_all(&sh.q_empty, (segments & 1u) ^ 1u);  // the scores of the item before are done
-      if (!ok) break;
-      const uint32_t bar = in_cta(smem_u32(&sh.q_full), 0);
-      if (lane == 0) pair_arrive_expect_tx(bar, chunks * L::kChunkBytes);
-      __syncwarp();
-      if (lane < chunks && DSPARK_CHECK(cur.b < p.B && cur.head < p.kv_heads && lane < L::kChunks))
-        pair_load_box(q_at + lane * L::kChunkBytes, &maps.q, lane * 64,
-                      cur.head * 128 + (int)rank * 64, cur.b, bar);
-      ++segments;
-      __syncwarp();
-    }
-    if (lane == 0) sh.issued[2] = segments;
   }
   __syncwarp();
   tc_before_sync();
