@@ -146,7 +146,12 @@ struct Latent {
 
 struct LatentShared {
   uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
-  uint64_t q_full, q_empty, s_full[2], p_full[2], o_full, v_go, drained;
+  uint64_t q_full, q_empty, drained;
+  // by tile number modulo 2: the scores are there, and have been read
+  uint64_t s_full[2], s_empty[2];
+  // by half of a tile's positions: the weights are there (and by tile number modulo 2), have been
+  // multiplied; the values are there for CTA 1 to look at
+  uint64_t p_full[2][2], o_full[2], v_go[2];
   uint64_t scan[32];
   // by tile number modulo 16: a narrow row's keys are copied up to 7 tiles ahead of the results
   uint32_t valid[16][4];  // a tile's positions that hold a key
@@ -212,10 +217,12 @@ __global__ void __launch_bounds__(kLatentThreads, 1) __cluster_dims__(2, 1, 1)
     mbar_init(&sh.q_empty, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.s_full[i], 1);
-      mbar_init(&sh.p_full[i], 16);
+      mbar_init(&sh.s_empty[i], 16);
+      mbar_init(&sh.p_full[i][0], 8);
+      mbar_init(&sh.p_full[i][1], 8);
+      mbar_init(&sh.o_full[i], 1);
+      mbar_init(&sh.v_go[i], 1);
     }
-    mbar_init(&sh.o_full, 1);
-    mbar_init(&sh.v_go, 1);
     mbar_init(&sh.drained, 2);
     sh.failed = sh.peer_failed = 0u;
     for (int i = 0; i < 3; ++i) sh.issued[i] = sh.peer_issued[i] = 0u;
@@ -272,12 +279,14 @@ __global__ void __launch_bounds__(kLatentThreads, 1) __cluster_dims__(2, 1, 1)
     // as in tree_attention_wide_kernel: a negative scale goes into Q's sign
     const uint32_t flip = p.scale2 < 0.0f ? 0x80008000u : 0u;
     const float scale = fmaxf(fabsf(p.scale2), 1.17549435e-38f);
-    const uint32_t q_full = in_cta(smem_u32(&sh.q_full), 0), p_full = in_cta(smem_u32(&sh.p_full[0]), 0);
-    const uint32_t v_go = in_cta(smem_u32(&sh.v_go), 1);
+    const uint32_t q_full = in_cta(smem_u32(&sh.q_full), 0);
+    const uint32_t p_full = in_cta(smem_u32(&sh.p_full[half][0]), 0);
+    const uint32_t s_empty = in_cta(smem_u32(&sh.s_empty[0]), 0);
+    const uint32_t v_go = in_cta(smem_u32(&sh.v_go[half]), 1);
     const uint32_t special_there = in_cta(smem_u32(sh.special), rank ^ 1u);
     // four floats a row, in the place of the weights between two products
     const uint32_t exchange = p_at + row * 16;
-    uint32_t tile_no = 0, o_done = 0, goes = 0;  // o_done: products of values waited for
+    uint32_t tile_no = 0, goes = 0;
     bool bad = false;                            // a wait of this warp expired
 
     auto fill_q = [&](const Walk& w) {
@@ -312,10 +321,15 @@ __global__ void __launch_bounds__(kLatentThreads, 1) __cluster_dims__(2, 1, 1)
       __syncwarp();
       if (lane == 0) pair_arrive(q_full);
     };
-    auto wait_values = [&]() {  // for the last product of values that was handed over
-      bad = bad || !wait_all(&sh.o_full, o_done & 1u);
-      ++o_done;
+    // For the products with half h of tile g's weights, or with both.  The phase before has been
+    // seen by this warp, or by one that has voted with it since: no phase is taken for another.
+    auto wait_half = [&](int h, uint32_t g) {
+      bad = bad || !wait_all(&sh.o_full[h], g & 1u);
       tc_after_sync();
+    };
+    auto wait_values = [&](uint32_t g) {
+      wait_half(0, g);
+      wait_half(1, g);
     };
     auto put = [&](float v) {
       asm volatile("st.shared.f32 [%0], %1;" ::"r"(exchange + word * 4), "f"(v) : "memory");
@@ -358,10 +372,11 @@ __global__ void __launch_bounds__(kLatentThreads, 1) __cluster_dims__(2, 1, 1)
         const bool nodes_here = pos + kKeys > len.ctx;
         float v[32];
         float top = -INFINITY;
-        if (!idle && !bad) {
+        if (!idle) {
           tmem_load32(v, s_col(tile_no) + wg * 32 + lanes);
           uint32_t w = sh.valid[tile_no & 15u][word];
           tmem_wait_load();
+          tc_before_sync();
           if (nodes_here) {
             const int node0 = pos + word * 32 - len.ctx;  // the node of the first position
             if (node0 >= 0)
@@ -384,9 +399,11 @@ __global__ void __launch_bounds__(kLatentThreads, 1) __cluster_dims__(2, 1, 1)
           for (int k = 0; k < 4; ++k) m4[k] = fmaxf(m4[k], v[28 + k]);
           if (item_row < live) top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * scale;
         }
-        bool waited = i == 0;  // the product before, of which the weights' place is free
+        __syncwarp();
+        if (lane == 0) pair_arrive(s_empty + (tile_no & 1u) * 8u);
+        bool waited = i == 0;  // for the products before, of which the weights' place is free
         if (any_of_256(bad || top > ref + kSlack)) {
-          if (!waited) wait_values();
+          if (!waited) wait_values(tile_no - 1u);
           waited = true;
           put(top);
           if (lost()) {
@@ -430,7 +447,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1) __cluster_dims__(2, 1, 1)
           }
           sum2 = add2_rn(sum2, part2);
         }
-        if (!waited) wait_values();
+        if (!waited) wait_half(half, tile_no - 1u);
         if (!idle) {
 #pragma unroll
           for (int j = 0; j < 4; ++j)
@@ -444,29 +461,26 @@ __global__ void __launch_bounds__(kLatentThreads, 1) __cluster_dims__(2, 1, 1)
           // Rows from the first node on, which some rows see and others do not, and what lies
           // behind the end: infinities and NaN are cleared, as 0 times them would reach rows that
           // do not see them.  CTA 1 learns from CTA 0 that its values are there.
-          const uint32_t piece = tile_no * 2u;
+          // Each half's threads clear the positions that their weights belong to.
+          const uint32_t piece = tile_no * 2u + half, slot = piece % L::kVSlots;
           if (rank == 0) {
-#pragma unroll
-            for (uint32_t s = 0; s < 2; ++s)
-              bad = bad || !wait_all(&sh.v_full[(piece + s) % L::kVSlots],
-                                     ((piece + s) / L::kVSlots) & 1u);
-            if (tid == 0) {
+            bad = bad || !wait_all(&sh.v_full[slot], (piece / L::kVSlots) & 1u);
+            if (t == half * 64 && wg == 0) {
               cluster_fence();
               pair_arrive(v_go);
             }
           } else {
-            bad = bad || !wait_all(&sh.v_go, goes & 1u);
+            bad = bad || !wait_all(&sh.v_go[half], goes & 1u);
             cluster_fence();
           }
           ++goes;
-          const int from = max(0, len.ctx - pos);
+          const int from = max(0, len.ctx - pos - half * 64);
           // blocks' rows that the last copy brought; zeros behind them
-          const int end = min(kKeys, (len.len - pos + rows - 1) & -rows);
+          const int end = min(64, (len.len - pos - half * 64 + rows - 1) & -rows);
           constexpr int kPer = L::kHalf / 8;  // 16-byte pieces of a position
-          for (int j = tid; j < (end - from) * kPer && !bad; j += 256) {
+          for (int j = wg * 64 + row; j < (end - from) * kPer && !bad; j += 128) {
             const int r = from + j / kPer, c = j % kPer;
-            const uint32_t slot = (piece + (r >> 6)) % L::kVSlots;
-            const uint32_t addr = v_at + slot * L::kVBytes + ((r & 63) >> shift) * v_run +
+            const uint32_t addr = v_at + slot * L::kVBytes + (r >> shift) * v_run +
                                   (c >> 3) * v_chunk + (r & (rows - 1)) * 128 +
                                   (((c & 7) ^ (r & 7)) << 4);
             if (!DSPARK_CHECK(addr >= v_at && addr + 16 <= p_at)) continue;
@@ -481,7 +495,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1) __cluster_dims__(2, 1, 1)
                            "r"(without_special<T>(x[0])), "r"(without_special<T>(x[1])),
                            "r"(without_special<T>(x[2])), "r"(without_special<T>(x[3]))
                            : "memory");
-              if (pos + r < len.len) {
+              if (pos + half * 64 + r < len.len) {
                 *(volatile uint32_t*)&sh.special[tile_no & 15u] = 1u;
                 pair_store(special_there + (tile_no & 15u) * 4, 1u);
                 cluster_fence();
@@ -497,7 +511,8 @@ __global__ void __launch_bounds__(kLatentThreads, 1) __cluster_dims__(2, 1, 1)
       if (!ok) break;
       // Q is free, as the last scores are done
       if (more && !maps.q_copies) fill_q(ahead);
-      wait_values();
+      if (lost()) break;
+      wait_values(tile_no - 1u);
       float sum = sum2.x + sum2.y;
       if (item_row >= live) {  // a row of no node: its zero query saw the text all the same
         ref = -INFINITY;
@@ -739,7 +754,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1) __cluster_dims__(2, 1, 1)
         ok = wait_all(&sh.q_full, segments & 1u);
         for (int i = 0; i < cur.count && ok; ++i, ++g) {
           // the scores two tiles before have been read
-          if (g >= 2) ok = wait_all(&sh.p_full[g & 1u], (g >> 1) + 1u & 1u);
+          if (g >= 2) ok = wait_all(&sh.s_empty[g & 1u], (g >> 1) + 1u & 1u);
           for (int x = 0; x < groups && ok; ++x) {
             ok = wait_all(&sh.k_full[slot], phase);
             if (!ok) break;
@@ -780,10 +795,10 @@ __global__ void __launch_bounds__(kLatentThreads, 1) __cluster_dims__(2, 1, 1)
         step[k] = ((16 * k >> shift) * v_run + (16 * k & (rows - 1)) * 128) / 16;
       while (ok && cur.advance(p, kKeys)) {
         for (int i = 0; i < cur.count && ok; ++i, ++g) {
-          ok = wait_all(&sh.p_full[g & 1u], (g >> 1) & 1u);
 #pragma unroll
           for (int s = 0; s < 2; ++s) {
-            ok = ok && wait_all(&sh.v_full[slot], phase);
+            ok = ok && wait_all(&sh.v_full[slot], phase) &&
+                 wait_all(&sh.p_full[s][g & 1u], (g >> 1) & 1u);
             if (!ok) break;
             tc_after_sync();
             const uint64_t a = p_desc + s * (8192 / 16);
@@ -795,9 +810,9 @@ __global__ void __launch_bounds__(kLatentThreads, 1) __cluster_dims__(2, 1, 1)
                 pair_mma(on, o_col + j * 128, a + k * 2, b + step[k] + j * (2 * v_chunk / 16),
                          kValues, i > 0 || s + k > 0);
             pair_commit(on, &sh.v_empty[slot]);
+            pair_commit(on, &sh.o_full[s]);
             if (++slot == L::kVSlots) slot = 0, phase ^= 1u;
           }
-          if (ok) pair_commit(on, &sh.o_full);
         }
       }
     }
