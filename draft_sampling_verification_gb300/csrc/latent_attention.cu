@@ -20,8 +20,7 @@ int latent_part_rows(int rows) { return rows >= 128 ? 128 : (rows + 7) / 8 * 8; 
 // a map of 16-bit elements; the innermost dimension is dense
 template <typename T, int N>
 bool encode_map(CUtensorMap* map, const void* base, const cuuint64_t (&sizes)[N],
-                const int64_t (&strides)[N - 1], const cuuint32_t (&box)[N],
-                CUtensorMapSwizzle swizzle) {
+                const int64_t (&strides)[N - 1], const cuuint32_t (&box)[N]) {
   const auto encode = encode_tiled();
   if (!encode) return false;
   cuuint64_t bytes[N - 1];
@@ -32,14 +31,13 @@ bool encode_map(CUtensorMap* map, const void* base, const cuuint64_t (&sizes)[N]
                 Half<T>::kExponent == 0x7F80u ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                               : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
                 N, const_cast<void*>(base), sizes, bytes, box, steps,
-                CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <typename T, int DV>
 bool make_maps(LatentMaps* m, const LatentParams& p) {
   using L = Latent<DV>;
-  const auto swizzle = CU_TENSOR_MAP_SWIZZLE_128B;
   const cuuint64_t width = p.width, page = p.page, blocks = p.n_blocks, B = p.B;
   const cuuint64_t rows = (cuuint64_t)p.nodes * p.heads;
   m->rows = wide_box_rows(p.page, 64);
@@ -47,15 +45,12 @@ bool make_maps(LatentMaps* m, const LatentParams& p) {
   m->k_rows = m->rows == 64 ? 64 : m->rows <= 16 ? 8 : 0;
   const cuuint32_t run = m->rows, k_run = m->k_rows ? m->k_rows : 8;
   bool ok = encode_map<T, 3>(&m->tail, p.k, {width, page, blocks}, {p.token_stride, p.block_stride},
-                             {64, run, 1}, swizzle);
+                             {64, run, 1});
   for (auto [map, box_rows, chunks] : {std::tuple{&m->keys, k_run, (int)L::kGroup},
                                        std::tuple{&m->values, run, (int)L::kVParts}})
     ok = ok && encode_map<T, 4>(map, p.k, {64, page, width / 64, blocks},
                                 {p.token_stride, 64, p.block_stride},
-                                {64, box_rows, (cuuint32_t)chunks, 1}, swizzle);
-  ok = ok && encode_map<T, 3>(&m->out, p.out, {(cuuint64_t)p.latent, rows, B},
-                              {p.latent, (int64_t)rows * p.latent}, {32, 32, 1},
-                              CU_TENSOR_MAP_SWIZZLE_64B);
+                                {64, box_rows, (cuuint32_t)chunks, 1});
   // Q by tensor copies where a request's rows are uniformly strided (and not broadcast); a negative
   // scale goes into its sign, which a copy cannot change
   const int64_t row = p.heads > 1 ? p.q_head : p.nodes > 1 ? p.q_node : p.width;
@@ -63,9 +58,9 @@ bool make_maps(LatentMaps* m, const LatentParams& p) {
   m->q_copies = p.scale2 >= 0.0f && (p.heads == 1 || p.nodes == 1 || p.q_node == row * p.heads) &&
                 row > 0 && request > 0 && row < (1ll << 38) && request < (1ll << 38);
   if (m->q_copies)
-    ok = ok && encode_map<T, 3>(&m->q, p.q, {width, rows, B}, {row, request}, {64, 64, 1}, swizzle);
+    ok = ok && encode_map<T, 3>(&m->q, p.q, {width, rows, B}, {row, request}, {64, 64, 1});
   else
-    m->q = m->out;  // not used
+    m->q = m->tail;  // not used
   return ok;
 }
 

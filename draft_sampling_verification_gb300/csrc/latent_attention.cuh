@@ -60,20 +60,6 @@ __device__ __forceinline__ void pair_load_chunks(uint32_t dst, const CUtensorMap
       "l"(map), "r"(0), "r"(r), "r"(c), "r"(b), "r"(bar)
       : "memory");
 }
-// 32 rows of 32 elements of the result, from element x of row r of request b
-__device__ __forceinline__ void store_box(const CUtensorMap* map, int x, int r, int b,
-                                          uint32_t src) {
-  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];"
-               "\n\tcp.async.bulk.commit_group;" ::"l"(map),
-               "r"(x), "r"(r), "r"(b), "r"(src)
-               : "memory");
-}
-__device__ __forceinline__ void stores_read() {  // the shared memory of this thread's is free
-  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-}
-__device__ __forceinline__ void stores_done() {
-  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-}
 // d (+)= a b over the pair, a's rows and b's columns from both CTAs' shared memory
 __device__ __forceinline__ void pair_mma(bool on, uint32_t d, uint64_t a, uint64_t b,
                                          uint32_t idesc, bool add) {
@@ -147,8 +133,8 @@ struct Latent {
 struct LatentShared {
   uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
   uint64_t q_full, q_empty, drained;
-  // by tile number modulo 2: the scores are there, and have been read
-  uint64_t s_full[2], s_empty[2];
+  // by tile number modulo 2: the scores are there; the first products of scores, of values are issued
+  uint64_t s_full[2], s_turn[2], v_turn[2];
   // by half of a tile's positions: the weights are there (and by tile number modulo 2), have been
   // multiplied; the values are there for CTA 1 to look at
   uint64_t p_full[2][2], o_full[2], v_go[2];
@@ -168,7 +154,6 @@ struct LatentMaps {
   CUtensorMap keys;    // {64, rows of a block, whole chunks, blocks}, kGroup chunks of k_rows rows
   CUtensorMap values;  // the same, a CTA's values of `rows` rows
   CUtensorMap q;       // {elements, rows of a request, requests}, a chunk of 64 rows
-  CUtensorMap out;     // the same, 32 elements of 32 rows
   int rows;            // of a block that are copied together: 8, 16, 32 or 64
   int k_rows;          // 64 or 8; 0: keys are copied chunk by chunk
   int q_copies;        // Q has a map
@@ -200,7 +185,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1) __cluster_dims__(2, 1, 1)
   const uint32_t v_chunk = rows * 128u, v_run = L::kVParts * v_chunk;
   const int shift = 31 - __clz(rows);  // a power of two
 
-  if (tid < 5)
+  if (tid < 4)
     asm volatile("prefetch.tensormap [%0];" ::"l"(
                      reinterpret_cast<const CUtensorMap*>(&maps) + tid)
                  : "memory");
@@ -217,7 +202,8 @@ __global__ void __launch_bounds__(kLatentThreads, 1) __cluster_dims__(2, 1, 1)
     mbar_init(&sh.q_empty, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.s_full[i], 1);
-      mbar_init(&sh.s_empty[i], 16);
+      mbar_init(&sh.s_turn[i], 32);
+      mbar_init(&sh.v_turn[i], 32);
       mbar_init(&sh.p_full[i][0], 8);
       mbar_init(&sh.p_full[i][1], 8);
       mbar_init(&sh.o_full[i], 1);
@@ -281,7 +267,6 @@ __global__ void __launch_bounds__(kLatentThreads, 1) __cluster_dims__(2, 1, 1)
     const float scale = fmaxf(fabsf(p.scale2), 1.17549435e-38f);
     const uint32_t q_full = in_cta(smem_u32(&sh.q_full), 0);
     const uint32_t p_full = in_cta(smem_u32(&sh.p_full[half][0]), 0);
-    const uint32_t s_empty = in_cta(smem_u32(&sh.s_empty[0]), 0);
     const uint32_t v_go = in_cta(smem_u32(&sh.v_go[half]), 1);
     const uint32_t special_there = in_cta(smem_u32(sh.special), rank ^ 1u);
     // four floats a row, in the place of the weights between two products
@@ -399,8 +384,6 @@ __global__ void __launch_bounds__(kLatentThreads, 1) __cluster_dims__(2, 1, 1)
           for (int k = 0; k < 4; ++k) m4[k] = fmaxf(m4[k], v[28 + k]);
           if (item_row < live) top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * scale;
         }
-        __syncwarp();
-        if (lane == 0) pair_arrive(s_empty + (tile_no & 1u) * 8u);
         bool waited = i == 0;  // for the products before, of which the weights' place is free
         if (any_of_256(bad || top > ref + kSlack)) {
           if (!waited) wait_values(tile_no - 1u);
@@ -564,8 +547,8 @@ __global__ void __launch_bounds__(kLatentThreads, 1) __cluster_dims__(2, 1, 1)
             }
           }
         }
-        if (full) {  // by tensor copies: a thread's 64 bytes of a row would be half a line each
-          if (lane == 0) stores_read();
+        if (full) {
+          // turned in shared memory, so that four lanes write 64 bytes of a row
           __syncwarp();
 #pragma unroll
           for (int j = 0; j < 4; ++j)
@@ -576,10 +559,19 @@ __global__ void __launch_bounds__(kLatentThreads, 1) __cluster_dims__(2, 1, 1)
                          "r"(H::pack(v[8 * j + 4] * inv, v[8 * j + 5] * inv)),
                          "r"(H::pack(v[8 * j + 6] * inv, v[8 * j + 7] * inv))
                          : "memory");
-          fence_async_shared();
           __syncwarp();
-          if (lane == 0 && DSPARK_CHECK(cur.b < p.B && item_row < all_rows && d + 32 <= p.latent))
-            store_box(&maps.out, d, item_row, cur.b, staged);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int r = k * 8 + (lane >> 2), j = lane & 3, there = item_row - lane + r;
+            uint4 x;
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+                         : "r"(staged + r * 64 + ((j ^ ((r >> 1) & 3)) << 4))
+                         : "memory");
+            if (there < all_rows && DSPARK_CHECK(row_held(p, to - lane + r) && d + 32 <= p.latent))
+              *reinterpret_cast<uint4*>(static_cast<T*>(p.out) + (to - lane + r) * p.latent + d +
+                                        j * 8) = x;
+          }
         } else if (mine && DSPARK_CHECK(part_held(p, slot, part_row))) {
           float* out = ws.rows + (slot + part_row) * DV + d;
 #pragma unroll
@@ -598,11 +590,8 @@ __global__ void __launch_bounds__(kLatentThreads, 1) __cluster_dims__(2, 1, 1)
           p.lse[to] = sum == 0.0f ? -INFINITY : (ref + log2f(sum)) * 0.6931471805599453f;
       }
       tc_before_sync();  // the accumulators are read: the next item may take them
-      if (lane == 0) stores_read();  // before this warp's next vote, so before weights lie there
-      __syncwarp();
       cur = ahead;
     }
-    if (lane == 0) stores_done();
   } else if (warp < 10) {
     // ------------------------------------------------------ keys and values
     // Lane i holds the place of the tile's i-th run of `rows` rows of one block.  Of a copy chunk by
@@ -735,7 +724,10 @@ __global__ void __launch_bounds__(kLatentThreads, 1) __cluster_dims__(2, 1, 1)
   } else if (rank == 0) {
     // ------------------------------------------------------------- products
     // A warp for the scores and one for the values, so that one's waits, 200 cycles each where the
-    // tensor cores hold some 100 cycles of products ahead, pass during the other's products.  A
+    // tensor cores hold some 100 cycles of products ahead, pass during the other's products.  They
+    // take turns: tile g's scores behind tile g - 2's values, which have read the weights that
+    // were its scores' place, and tile g's values behind tile g + 1's scores (of the same item).
+    // Products of both side by side would end together, and the softmax would wait for both.  A
     // warp goes through its loop together; one lane issues.
     constexpr uint32_t kFormat = H::kExponent == 0x7F80u ? 1u : 0u;  // bf16 or f16
     // fp32 accumulators, both operands of T, 128 rows; for P V the second has its dims outermost
@@ -753,10 +745,9 @@ __global__ void __launch_bounds__(kLatentThreads, 1) __cluster_dims__(2, 1, 1)
       while (ok && cur.advance(p, kKeys)) {
         ok = wait_all(&sh.q_full, segments & 1u);
         for (int i = 0; i < cur.count && ok; ++i, ++g) {
-          // the scores two tiles before have been read
-          if (g >= 2) ok = wait_all(&sh.s_empty[g & 1u], (g >> 1) + 1u & 1u);
           for (int x = 0; x < groups && ok; ++x) {
-            ok = wait_all(&sh.k_full[slot], phase);
+            ok = wait_all(&sh.k_full[slot], phase) &&
+                 (x > 0 || g < 2 || wait_all(&sh.v_turn[g & 1u], (g >> 1) + 1u & 1u));
             if (!ok) break;
             tc_after_sync();
             const bool whole = x < whole_groups;
@@ -777,6 +768,8 @@ __global__ void __launch_bounds__(kLatentThreads, 1) __cluster_dims__(2, 1, 1)
               for (int c = 0; c < here; ++c) chunk(c);
             }
             pair_commit(on, &sh.k_empty[slot]);
+            // the other warp needs as long to see it as the rest takes
+            if (x == 0) mbar_arrive(&sh.s_turn[g & 1u]);
             if (++slot == L::kKSlots) slot = 0, phase ^= 1u;
           }
           if (!ok) break;
@@ -798,7 +791,9 @@ __global__ void __launch_bounds__(kLatentThreads, 1) __cluster_dims__(2, 1, 1)
 #pragma unroll
           for (int s = 0; s < 2; ++s) {
             ok = ok && wait_all(&sh.v_full[slot], phase) &&
-                 wait_all(&sh.p_full[s][g & 1u], (g >> 1) & 1u);
+                 wait_all(&sh.p_full[s][g & 1u], (g >> 1) & 1u) &&
+                 (s > 0 || i + 1 == cur.count ||
+                  wait_all(&sh.s_turn[(g + 1) & 1u], ((g + 1) >> 1) & 1u));
             if (!ok) break;
             tc_after_sync();
             const uint64_t a = p_desc + s * (8192 / 16);
@@ -811,6 +806,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1) __cluster_dims__(2, 1, 1)
                          kValues, i > 0 || s + k > 0);
             pair_commit(on, &sh.v_empty[slot]);
             pair_commit(on, &sh.o_full[s]);
+            if (s == 0) mbar_arrive(&sh.v_turn[g & 1u]);
             if (++slot == L::kVSlots) slot = 0, phase ^= 1u;
           }
         }
@@ -884,16 +880,15 @@ __global__ void __launch_bounds__(kLatentThreads, 1) __cluster_dims__(2, 1, 1)
 // ------------------------------------------------------- the joining kernel
 // The item that is first cut between pairs x and x + 1, if there is one, is
 // joined from the pairs' partial rows, in the pairs' order: a warp takes 256
-// dims of a row, so that the parts of a long item, some 20, come in three
-// rounds of loads.  CTA (x, 0) also gives the requests that pair x lost their
+// dims of a row, four parts in flight together.  CTA (x, 0) also gives the requests that pair x lost their
 // status.
 constexpr int kLatentJoinThreads = 128;
 
 template <typename T, int DV>
-__global__ void __launch_bounds__(kLatentJoinThreads)
+__global__ void __launch_bounds__(kLatentJoinThreads, 8)
     latent_join_kernel(const __grid_constant__ LatentParams p) {
   using H = Half<T>;
-  constexpr int kSlices = DV / 256, kRows = kLatentJoinThreads / 32 / kSlices, kAhead = 8;
+  constexpr int kSlices = DV / 256, kRows = kLatentJoinThreads / 32 / kSlices, kAhead = 4;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Workspace ws = carve(p.workspace, p.part_rows, p.max_ctas);
   if (!DSPARK_CHECK(gridDim.x <= p.max_ctas)) return;
