@@ -605,6 +605,8 @@ __global__ void __launch_bounds__(kLatentThreads, 1) __cluster_dims__(2, 1, 1)
     const int run = lane & (per_half - 1), chunk = lane >> half_shift;
     // boxes of eight rows: this lane's run, and its first row there
     const int eight = lane & 7, eight_run = eight * 8 >> shift, eight_row = eight * 8 & (rows - 1);
+    const uint32_t k_full = in_cta(smem_u32(sh.k_full), 0), v_full = in_cta(smem_u32(sh.v_full), 0);
+    const bool dense = p.token_stride == p.width;  // runs lie in one piece
     uint32_t g = 0, issued = 0, slot = 0, phase = 0, segments = 0;
     bool ok = !DSPARK_STALLED(blockIdx.x);
     Walk cur = walk_from(p, sh.start, range, p.item_cost);
@@ -653,35 +655,29 @@ __global__ void __launch_bounds__(kLatentThreads, 1) __cluster_dims__(2, 1, 1)
           const int r = __shfl_sync(0xffffffffu, row, at_run + run);
           const int b8 = __shfl_sync(0xffffffffu, from, at_run + eight_run);
           const int r8 = __shfl_sync(0xffffffffu, row, at_run + eight_run) + eight_row;
+          if (lane < 4) {
+            uint32_t word = ~0u;  // positions 32 lane .. of the tile
+            if (held_runs != all_runs) {
+              const uint32_t mine = held_runs >> (lane << 5 >> shift);
+              word = 0u;
+              if (rows >= 32) {
+                word = mine & 1u ? ~0u : 0u;
+              } else {
+                for (int j = 0; j << shift < 32; ++j)
+                  if ((mine >> j) & 1u) word |= ((1u << rows) - 1u) << (j << shift);
+              }
+            }
+            const int past = len.len - ((cur.first + i) * kKeys + lane * 32);
+            sh.valid[g & 15u][lane] = past >= 32 ? word : past > 0 ? word & ((1u << past) - 1u) : 0u;
+          }
+          if (lane == 0) sh.special[g & 15u] = 0u;
+          __syncwarp();  // lane 0's arrivals stand for all lanes' words
           for (int x = 0; x < groups; ++x) {
             const int c = x * L::kGroup, here = min(L::kGroup, chunks - c);
+            const uint32_t bar = k_full + slot * 8u, to = k_at + slot * L::kKBytes;
             ok = wait_all(&sh.k_empty[slot], phase ^ 1u);
             if (!ok) break;
-            if (x == 0) {
-              if (lane < 4) {
-                uint32_t word = ~0u;  // positions 32 lane .. of the tile
-                if (held_runs != all_runs) {
-                  const uint32_t mine = held_runs >> (lane << 5 >> shift);
-                  word = 0u;
-                  if (rows >= 32) {
-                    word = mine & 1u ? ~0u : 0u;
-                  } else {
-                    for (int j = 0; j << shift < 32; ++j)
-                      if ((mine >> j) & 1u) word |= ((1u << rows) - 1u) << (j << shift);
-                  }
-                }
-                const int past = len.len - ((cur.first + i) * kKeys + lane * 32);
-                sh.valid[g & 15u][lane] = past >= 32 ? word
-                                          : past > 0 ? word & ((1u << past) - 1u)
-                                                     : 0u;
-              }
-              if (lane == 0) sh.special[g & 15u] = 0u;
-              __syncwarp();
-            }
-            const uint32_t bar = in_cta(smem_u32(&sh.k_full[slot]), 0);
             if (lane == 0) pair_arrive_expect_tx(bar, here * L::kChunkBytes);
-            __syncwarp();
-            const uint32_t to = k_at + slot * L::kKBytes;
             if (!DSPARK_CHECK(r + rows <= p.page && slot < L::kKSlots && r8 + 8 <= p.page)) {
             } else if (x < whole_groups) {
               if (maps.k_rows == 8) {
@@ -697,15 +693,22 @@ __global__ void __launch_bounds__(kLatentThreads, 1) __cluster_dims__(2, 1, 1)
             if (++slot == L::kKSlots) slot = 0, phase ^= 1u;
             __syncwarp();
           }
+          // The next tile's rows on their way to L2: the ring holds one tile, and an HBM latency
+          // more from a place's release to its next keys would show.
+          if (dense && lane >= at_run && lane < at_run + per_half && ahead >= 0 &&
+              ahead < p.n_blocks && DSPARK_CHECK(row_ahead + rows <= p.page))
+            l2_prefetch_bulk(static_cast<const T*>(p.k) + ahead * p.block_stride +
+                                 (int64_t)row_ahead * p.token_stride,
+                             rows * p.width * 2);
+          __syncwarp();
         } else {
           for (int s = 0; s < 2; ++s) {  // 64 positions
             const int b = __shfl_sync(0xffffffffu, from, s * per_half + run);
             const int r = __shfl_sync(0xffffffffu, row, s * per_half + run);
+            const uint32_t bar = v_full + slot * 8u;
             ok = wait_all(&sh.v_empty[slot], phase ^ 1u);
             if (!ok) break;
-            const uint32_t bar = in_cta(smem_u32(&sh.v_full[slot]), 0);
             if (lane == 0) pair_arrive_expect_tx(bar, L::kVBytes);
-            __syncwarp();
             if (lane < per_half && DSPARK_CHECK(r + rows <= p.page && slot < L::kVSlots &&
                                                 (run + 1) * v_run <= L::kVBytes))
               pair_load_chunks(v_at + slot * L::kVBytes + run * v_run, &maps.values, r,
