@@ -42,7 +42,6 @@ namespace {
 constexpr int kRotThreads = 256;
 constexpr int kRotTokens = 4;  // of a CTA, 64 threads each
 constexpr int kRotLanes = kRotThreads / kRotTokens;
-constexpr int kRotAhead = 4;   // rows of a group in flight
 constexpr int kMaxRot = 256;
 
 struct RotateParams {
@@ -151,50 +150,93 @@ __device__ __forceinline__ Place place_of(int lane, int rot_start, int rot_dim) 
   return {rot_start + 4 * j, rot_start + rot_dim / 2 + 4 * j, 4 * j};
 }
 
-// Bound by HBM: every element is read once and written once, a row of a head
-// by dim / 8 lanes, the turns of a token computed once for all its heads.
-template <typename Src, typename Dst, bool kInterleaved>
-__global__ void __launch_bounds__(kRotThreads) rotate_kernel(const RotateParams p) {
+// Heads [h0, h1) of a token, a head's row by 2^lane_bits lanes, two rows of a group in flight.
+// kTurned: queries or keys, normed by `weight` (NULL: not) and turned; else values, copied.  All
+// lanes of a warp call with the same range.
+template <typename Src, typename Dst, bool kInterleaved, bool kTurned>
+__device__ __forceinline__ void rotate_heads(const RotateParams& p, const Src* from, int64_t src_head,
+                                             Dst* to, int64_t dst_head, int h0, int h1,
+                                             const float* weight, const Place& at, bool write,
+                                             bool read, const float (&c)[4], const float (&s)[4]) {
   using In = Quad<Src>;
   using Out = Quad<Dst>;
+  constexpr int kAhead = 2;
+  const int lanes = 1 << p.lane_bits, groups = kRotLanes >> p.lane_bits;
+  const int group = (int)(threadIdx.x % kRotLanes) >> p.lane_bits;
+  float4 wa, wb;
+  if (kTurned && weight) {  // aligned to 4 bytes only
+    wa = make_float4(weight[at.a], weight[at.a + 1], weight[at.a + 2], weight[at.a + 3]);
+    wb = make_float4(weight[at.b], weight[at.b + 1], weight[at.b + 2], weight[at.b + 3]);
+  }
+  for (int first = h0; first < h1; first += kAhead * groups) {
+    typename In::Load x[kAhead][2];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int h = first + u * groups + group;
+      x[u][0] = x[u][1] = typename In::Load{};
+      if (read && h < h1 && DSPARK_CHECK(at.a + 4 <= p.dim && at.b + 4 <= p.dim)) {
+        x[u][0] = __ldcs(reinterpret_cast<const typename In::Load*>(from + h * src_head + at.a));
+        x[u][1] = __ldcs(reinterpret_cast<const typename In::Load*>(from + h * src_head + at.b));
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int h = first + u * groups + group;
+      float4 a = In::widen(x[u][0]), b = In::widen(x[u][1]);
+      if constexpr (kTurned) {
+        if (weight) {
+          float sum = a.x * a.x + a.y * a.y + a.z * a.z + a.w * a.w;
+          sum += b.x * b.x + b.y * b.y + b.z * b.z + b.w * b.w;
+          for (int m = lanes >> 1; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+          const float f = rsqrtf(sum / (float)p.dim + p.eps);
+          a = scale4(a, f, wa);
+          b = scale4(b, f, wb);
+        }
+        if (at.pair >= 0) turn8<kInterleaved>(a, b, c, s);
+      }
+      if (!write || h >= h1 || !DSPARK_CHECK(at.a + 4 <= p.dim && at.b + 4 <= p.dim)) continue;
+      if (!read) a = b = make_float4(0.0f, 0.0f, 0.0f, 0.0f);  // padding
+      *reinterpret_cast<typename Out::Load*>(to + h * dst_head + at.a) = Out::round(a);
+      *reinterpret_cast<typename Out::Load*>(to + h * dst_head + at.b) = Out::round(b);
+    }
+  }
+}
+
+// Bound by HBM: every element is read once and written once, the turns of a token computed once for
+// all its heads.  Few registers, so that four or five CTAs of an SM hide one another's starts: 16,384
+// tokens of 48 rows of 128, fp32 to bf16, take 98 us (6.2 TB/s; with five CTAs 100, and with all of
+// a token's rows in one loop, 106 registers and two CTAs 141); 384 tokens in bf16 6.6 us (with four
+// CTAs 8.8).
+template <typename Src, typename Dst, bool kInterleaved>
+__global__ void __launch_bounds__(kRotThreads, sizeof(Src) == 4 ? 4 : 5)
+    rotate_kernel(const RotateParams p) {
   __shared__ float2 turns[kRotTokens][kMaxRot / 2];
   const int sub = threadIdx.x / kRotLanes, t = threadIdx.x % kRotLanes;
   const int64_t token = (int64_t)blockIdx.x * kRotTokens + sub;
   const bool mine = token < p.n_tokens;
   const int position = mine ? p.positions[token] : -1;
   const bool live = position >= 0;
-  for (int i = t; i < p.rot_dim / 2; i += kRotLanes)
-    if (live && DSPARK_CHECK(i < kMaxRot / 2))
-      turns[sub][i] = turn_of(position, p.table[i], p.magnitude);
+  for (int i = t; i < p.rot_dim / 2; i += kRotLanes) {
+    const uint64_t entry = __ldg(p.table + i);  // beside the position's load
+    if (live && DSPARK_CHECK(i < kMaxRot / 2)) turns[sub][i] = turn_of(position, entry, p.magnitude);
+  }
 
-  const int lanes = 1 << p.lane_bits, groups = kRotLanes >> p.lane_bits;
-  const int lane = t & (lanes - 1), group = t >> p.lane_bits;
+  const int lane = t & ((1 << p.lane_bits) - 1);
   const bool inside = lane < p.dim / 8;
   const Place at = place_of<kInterleaved>(inside ? lane : 0, p.rot_start, p.rot_dim);
-  const float4 ones = make_float4(1.0f, 1.0f, 1.0f, 1.0f);
-  float4 qa = ones, qb = ones, ka = ones, kb = ones;
-  auto weight = [&](const float* w, int d) {  // the weights need not be aligned to more than 4
-    return make_float4(w[d], w[d + 1], w[d + 2], w[d + 3]);
-  };
-  if (p.q_weight) qa = weight(p.q_weight, at.a), qb = weight(p.q_weight, at.b);
-  if (p.k_weight) ka = weight(p.k_weight, at.a), kb = weight(p.k_weight, at.b);
 
   // the token's source, and the place of its keys and values
   const int64_t src = p.src_rows && mine ? p.src_rows[token] : token;
-  bool store = live && src >= 0 && src < p.n_src;
+  bool store = mine && src >= 0 && src < p.n_src;
   int64_t to = token * p.ko_token;
   if (p.slots) {
     const int slot = mine ? p.slots[token] : -1;
-    store = store && slot >= 0 && slot < p.n_blocks * p.page;
+    store = store && live && slot >= 0 && slot < p.n_blocks * p.page;
     const int block = store ? slot / p.page : 0;
-    to = store ? block * p.block_stride + (int64_t)(slot - block * p.page) * p.ko_token : 0;
+    to = block * p.block_stride + (int64_t)(slot - block * p.page) * p.ko_token;
   }
-  const Src* q = static_cast<const Src*>(p.q) + (mine ? token * p.q_token : 0);
-  const Src* k = static_cast<const Src*>(p.k) + (store ? src * p.k_token : 0);
-  const Src* v = static_cast<const Src*>(p.v) + (store ? src * p.k_token : 0);
-  Dst* q_out = static_cast<Dst*>(p.q_out) + (mine ? token * p.qo_token : 0);
-  Dst* k_out = static_cast<Dst*>(p.k_out) + to;
-  Dst* v_out = static_cast<Dst*>(p.v_out) + to;
+  if (!store) to = 0;
+  store = store && inside;
 
   __syncthreads();
   float c[4], s[4];
@@ -204,55 +246,23 @@ __global__ void __launch_bounds__(kRotThreads) rotate_kernel(const RotateParams 
     c[i] = turn.x;
     s[i] = turn.y;
   }
-  const int begin = blockIdx.y * p.per, end = min(p.rows, begin + p.per);
-  const float by_dim = 1.0f / (float)p.dim;
-  const bool norms = p.q_weight || p.k_weight;
-  for (int r0 = begin; r0 < end; r0 += kRotAhead * groups) {
-    typename In::Load x[kRotAhead][2];
-    Dst* out[kRotAhead];
-    bool read[kRotAhead];
-#pragma unroll
-    for (int u = 0; u < kRotAhead; ++u) {
-      const int r = r0 + u * groups + group;
-      const bool is_q = r < p.heads, is_v = r >= p.heads + p.kv_heads;
-      const int h = is_q ? r : is_v ? r - p.heads - p.kv_heads : r - p.heads;
-      const Src* from = is_q ? q + h * p.q_head : (is_v ? v : k) + h * p.k_head;
-      const bool here = mine && inside && r < end;
-      // padding's queries and, without a cache, its keys become 0
-      out[u] = is_q ? q_out + h * p.qo_head : (is_v ? v_out : k_out) + h * p.ko_head;
-      if (!here || (!is_q && p.slots && !store) || !DSPARK_CHECK(r < p.rows && at.b + 4 <= p.dim))
-        out[u] = nullptr;
-      read[u] = out[u] && live;
-      if (read[u]) {
-        x[u][0] = __ldcs(reinterpret_cast<const typename In::Load*>(from + at.a));
-        x[u][1] = __ldcs(reinterpret_cast<const typename In::Load*>(from + at.b));
-      } else {
-        x[u][0] = x[u][1] = typename In::Load{};
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < kRotAhead; ++u) {
-      const int r = r0 + u * groups + group;
-      const bool is_q = r < p.heads, is_v = r >= p.heads + p.kv_heads;
-      float4 a = In::widen(x[u][0]), b = In::widen(x[u][1]);
-      if (norms) {
-        float sum = a.x * a.x + a.y * a.y + a.z * a.z + a.w * a.w;
-        sum += b.x * b.x + b.y * b.y + b.z * b.z + b.w * b.w;
-        for (int m = lanes >> 1; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
-        const bool on = is_q ? p.q_weight != nullptr : !is_v && p.k_weight != nullptr;
-        if (on) {
-          const float f = rsqrtf(sum * by_dim + p.eps);
-          a = scale4(a, f, is_q ? qa : ka);
-          b = scale4(b, f, is_q ? qb : kb);
-        }
-      }
-      if (at.pair >= 0 && !is_v) turn8<kInterleaved>(a, b, c, s);
-      if (!out[u]) continue;
-      if (!read[u]) a = b = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      *reinterpret_cast<typename Out::Load*>(out[u] + at.a) = Out::round(a);
-      *reinterpret_cast<typename Out::Load*>(out[u] + at.b) = Out::round(b);
-    }
-  }
+  // this CTA's rows of a token: queries, keys and values one after the other
+  const int begin = blockIdx.y * p.per, end = min(p.rows, begin + p.per), keys = p.heads + p.kv_heads;
+  if (begin < p.heads)
+    rotate_heads<Src, Dst, kInterleaved, true>(
+        p, static_cast<const Src*>(p.q) + (mine ? token * p.q_token : 0), p.q_head,
+        static_cast<Dst*>(p.q_out) + (mine ? token * p.qo_token : 0), p.qo_head, begin,
+        min(end, p.heads), p.q_weight, at, mine && inside, live && inside, c, s);
+  const int64_t from = store ? src * p.k_token : 0;
+  if (begin < keys && end > p.heads)
+    rotate_heads<Src, Dst, kInterleaved, true>(
+        p, static_cast<const Src*>(p.k) + from, p.k_head, static_cast<Dst*>(p.k_out) + to, p.ko_head,
+        max(begin - p.heads, 0), min(end - p.heads, p.kv_heads), p.k_weight, at, store,
+        store && live, c, s);
+  if (end > keys)
+    rotate_heads<Src, Dst, kInterleaved, false>(
+        p, static_cast<const Src*>(p.v) + from, p.k_head, static_cast<Dst*>(p.v_out) + to, p.ko_head,
+        max(begin - keys, 0), end - keys, nullptr, at, store, store, c, s);
 }
 
 // -------------------------------------------------- rows of a latent cache
@@ -429,9 +439,9 @@ cudaError_t launch_rotate(const void* q, const void* k, const void* v, int src_d
   const int64_t tiles = ((int64_t)n_tokens + kRotTokens - 1) / kRotTokens;
   const int groups = kRotLanes >> p.lane_bits;
   // few tokens: a token's rows go to several CTAs
-  int splits = 1;
   const int most = (p.rows + groups - 1) / groups;
-  while (tiles * splits < 608 && splits * 2 <= most) splits *= 2;
+  const int64_t wanted = (608 + tiles - 1) / tiles;
+  const int splits = wanted < most ? (int)wanted : most;
   p.per = (p.rows + splits - 1) / splits;
   const dim3 grid((unsigned)tiles, (unsigned)((p.rows + p.per - 1) / p.per));
   return by_types<LaunchRotate>(src_dtype, dst_dtype, interleaved, p, grid, stream);
