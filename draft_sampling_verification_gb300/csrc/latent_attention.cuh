@@ -910,35 +910,40 @@ __global__ void __launch_bounds__(kLatentJoinThreads, 8)
       return;
     const int64_t to = (int64_t)at.b * all_rows + row;
     if (!DSPARK_CHECK(row_held(p, to))) return;
-    float top = -INFINITY;
-    for (int c = c0 + lane; c <= c1; c += 32) top = fmaxf(top, ws.stats[part_of(c) + r].x);
+    // kAhead parts of the row, beside the loads of what they are weighted with
+    float4 x[kAhead], y[kAhead];
+    auto load = [&](int c) {
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const float4* v = reinterpret_cast<const float4*>(
+            ws.rows + (part_of(min(c + u, c1)) + r) * DV + d);
+        x[u] = __ldcs(v);
+        y[u] = __ldcs(v + 32);
+      }
+    };
+    load(c0);
+    float2 st = make_float2(-INFINITY, 0.0f);  // of the lane's part
+    if (c0 + lane <= c1) st = ws.stats[part_of(c0 + lane) + r];
+    float top = st.x;
+    for (int c = c0 + 32 + lane; c <= c1; c += 32) top = fmaxf(top, ws.stats[part_of(c) + r].x);
     top = warp_reduce(top, OpMaxF());
     const float safe = top == -INFINITY ? 0.0f : top;
-    float all = 0.0f;
+    float f = exp2_approx(st.x - safe), all = 0.0f;
     float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f), b = a;
-    for (int base = c0; base <= c1; base += 32) {  // 32 parts, whose factors the lanes hold
-      float2 st = make_float2(-INFINITY, 0.0f);
-      if (base + lane <= c1) st = ws.stats[part_of(base + lane) + r];
-      const float f = exp2_approx(st.x - safe);
-      for (int c = base; c <= min(c1, base + 31); c += kAhead) {
-        float4 x[kAhead], y[kAhead];
+    for (int c = c0; c <= c1; c += kAhead) {
+      if (c > c0) load(c);
+      if (c > c0 && (c - c0) % 32 == 0) {  // the next 32 parts, whose factors the lanes hold
+        st = make_float2(-INFINITY, 0.0f);
+        if (c + lane <= c1) st = ws.stats[part_of(c + lane) + r];
+        f = exp2_approx(st.x - safe);
+      }
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-          x[u] = y[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          if (c + u > c1) continue;
-          const float4* v =
-              reinterpret_cast<const float4*>(ws.rows + (part_of(c + u) + r) * DV + d);
-          x[u] = v[0];
-          y[u] = v[32];
-        }
-#pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-          if (c + u > c1) continue;
-          const float w = __shfl_sync(0xffffffffu, f, c + u - base);
-          all += __shfl_sync(0xffffffffu, st.y, c + u - base) * w;
-          a = make_float4(a.x + x[u].x * w, a.y + x[u].y * w, a.z + x[u].z * w, a.w + x[u].w * w);
-          b = make_float4(b.x + y[u].x * w, b.y + y[u].y * w, b.z + y[u].z * w, b.w + y[u].w * w);
-        }
+      for (int u = 0; u < kAhead; ++u) {
+        if (c + u > c1) continue;
+        const float w = __shfl_sync(0xffffffffu, f, (c + u - c0) & 31);
+        all += __shfl_sync(0xffffffffu, st.y, (c + u - c0) & 31) * w;
+        a = make_float4(a.x + x[u].x * w, a.y + x[u].y * w, a.z + x[u].z * w, a.w + x[u].w * w);
+        b = make_float4(b.x + y[u].x * w, b.y + y[u].y * w, b.z + y[u].z * w, b.w + y[u].w * w);
       }
     }
     const float inv = all == 0.0f ? 0.0f : 1.0f / all;
