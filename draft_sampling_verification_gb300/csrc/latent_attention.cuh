@@ -369,7 +369,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1) __cluster_dims__(2, 1, 1)
             else if (node0 > -32)
               w &= (uint32_t)(mask << -node0) | ((1u << -node0) - 1u);
           }
-          if (!__all_sync(0xffffffffu, w == ~0u)) {
+          if (__builtin_expect(!__all_sync(0xffffffffu, w == ~0u), 0)) {
 #pragma unroll
             for (int j = 0; j < 32; ++j)
               if (!((w >> j) & 1u)) v[j] = -INFINITY;
@@ -385,7 +385,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1) __cluster_dims__(2, 1, 1)
           if (item_row < live) top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * scale;
         }
         bool waited = i == 0;  // for the products before, of which the weights' place is free
-        if (any_of_256(bad || top > ref + kSlack)) {
+        if (__builtin_expect(any_of_256(bad || top > ref + kSlack), 0)) {
           if (!waited) wait_values(tile_no - 1u);
           waited = true;
           put(top);
@@ -440,7 +440,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1) __cluster_dims__(2, 1, 1)
                          "r"(w16[4 * j + 3])
                          : "memory");
         }
-        if (nodes_here) {
+        if (__builtin_expect(nodes_here, 0)) {
           // Rows from the first node on, which some rows see and others do not, and what lies
           // behind the end: infinities and NaN are cleared, as 0 times them would reach rows that
           // do not see them.  CTA 1 learns from CTA 0 that its values are there.
@@ -764,11 +764,16 @@ __global__ void __launch_bounds__(kLatentThreads, 1) __cluster_dims__(2, 1, 1)
                 pair_mma(on, s_col(g), a + c * (L::kChunkBytes / 16) + k * 2, b + c * step + k * 2,
                          kScores, c + k > 0 || x > 0);
             };
-            if (here >= L::kGroup) {  // without a branch between its products
+            uint64_t ac = a, bc = b;
+            bool add = x > 0;
+#pragma unroll 1
+            for (int c = min(here, L::kGroup); c > 0; --c) {
 #pragma unroll
-              for (int c = 0; c < L::kGroup; ++c) chunk(c);
-            } else {
-              for (int c = 0; c < here; ++c) chunk(c);
+              for (int k = 0; k < 4; ++k)
+                pair_mma(on, s_col(g), ac + k * 2, bc + k * 2, kScores, add || k > 0);
+              add = true;
+              ac += L::kChunkBytes / 16;
+              bc += step;
             }
             pair_commit(on, &sh.k_empty[slot]);
             // the other warp needs as long to see it as the rest takes
@@ -791,7 +796,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1) __cluster_dims__(2, 1, 1)
         step[k] = ((16 * k >> shift) * v_run + (16 * k & (rows - 1)) * 128) / 16;
       while (ok && cur.advance(p, kKeys)) {
         for (int i = 0; i < cur.count && ok; ++i, ++g) {
-#pragma unroll
+#pragma unroll 1
           for (int s = 0; s < 2; ++s) {
             ok = ok && wait_all(&sh.v_full[slot], phase) &&
                  wait_all(&sh.p_full[s][g & 1u], (g >> 1) & 1u) &&
@@ -801,11 +806,11 @@ __global__ void __launch_bounds__(kLatentThreads, 1) __cluster_dims__(2, 1, 1)
             tc_after_sync();
             const uint64_t a = p_desc + s * (8192 / 16);
             const uint64_t b = v_desc + slot * (L::kVBytes / 16);
-#pragma unroll
+#pragma unroll 1
             for (int k = 0; k < 4; ++k)
 #pragma unroll
               for (int j = 0; j < DV / 256; ++j)
-                pair_mma(on, o_col + j * 128, a + k * 2, b + step[k] + j * (2 * v_chunk / 16),
+                pair_mma(on, o_col + j * 128, a + k * 2, b + ((16 * k >> shift) * v_run + (16 * k & (rows - 1)) * 128) / 16 + j * (2 * v_chunk / 16),
                          kValues, i > 0 || s + k > 0);
             pair_commit(on, &sh.v_empty[slot]);
             pair_commit(on, &sh.o_full[s]);
