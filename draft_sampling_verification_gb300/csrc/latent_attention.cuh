@@ -91,6 +91,22 @@ __device__ __forceinline__ bool any_of_256(bool v) {
   return r != 0u;
 }
 
+// The rest of a bounded wait of a whole warp, out of its callers' loops.
+static __device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t phase, uint32_t* failed) {
+  const uint64_t t0 = global_ns();
+  uint32_t nap = 32;
+  while (!__any_sync(0xffffffffu, *(volatile uint32_t*)failed)) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, phase))) return true;
+    if (__any_sync(0xffffffffu, global_ns() - t0 >= kWaitLimitNs)) {
+      *(volatile uint32_t*)failed = 1u;
+      break;
+    }
+    if (nap > 32u) __nanosleep(nap);
+    nap = nap < 1024u ? 2u * nap : 1024u;
+  }
+  return false;
+}
+
 // ------------------------------------------------------------ the kernel
 // A pair of CTAs takes 128 rows of an item, 64 a CTA, and goes over the keys
 // in tiles of 128 positions.  512 dims of fp32 accumulators for 128 rows
@@ -240,19 +256,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1) __cluster_dims__(2, 1, 1)
 
   // bounded waits of a whole warp, as in tree_attention_wide_kernel
   auto wait_all = [&](uint64_t* bar, uint32_t phase) -> bool {
-    if (__all_sync(0xffffffffu, mbar_try_wait(bar, phase))) return true;
-    const uint64_t t0 = global_ns();
-    uint32_t nap = 32;
-    while (!__any_sync(0xffffffffu, *(volatile uint32_t*)&sh.failed)) {
-      if (__all_sync(0xffffffffu, mbar_try_wait(bar, phase))) return true;
-      if (__any_sync(0xffffffffu, global_ns() - t0 >= kWaitLimitNs)) {
-        *(volatile uint32_t*)&sh.failed = 1u;
-        break;
-      }
-      if (nap > 32u) __nanosleep(nap);
-      nap = nap < 1024u ? 2u * nap : 1024u;
-    }
-    return false;
+    return __all_sync(0xffffffffu, mbar_try_wait(bar, phase)) || wait_long(bar, phase, &sh.failed);
   };
 
   if (warp < 8) {
