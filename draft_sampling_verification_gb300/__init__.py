@@ -529,15 +529,18 @@ _ELEMENTS = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
 def _head_args(name, t):
     """(dtype code, pointer, token stride, head stride, tokens, heads, head_dim) of a tensor
     [.., n_heads, head_dim] whose tokens are uniformly strided."""
-    if t.dtype not in _ELEMENTS:
+    code, shape, strides = _ELEMENTS.get(t.dtype), t.shape, t.stride()
+    if code is None:
         raise TypeError("%s must be float32, bfloat16 or float16, got %s" % (name, t.dtype))
-    shape, strides = t.shape, t.stride()
     if len(shape) < 3 or (strides[-1] != 1 and shape[-1] > 1) or not t.is_cuda:
         raise ValueError("%s must be a CUDA tensor [.., n_heads, head_dim], contiguous in head_dim"
                          % name)
-    n, step = _uniform(t, len(shape) - 2, "the tokens of " + name)
-    return (_ELEMENTS[t.dtype], t.data_ptr(), step, strides[-2] if shape[-2] > 1 else 0, n,
-            shape[-2], shape[-1])
+    heads, dim = shape[-2:]
+    if len(shape) == 3:
+        n, step = shape[0], strides[0]
+    else:
+        n, step = _uniform(t, len(shape) - 2, "the tokens of " + name)
+    return code, t.data_ptr(), step if n > 1 else 0, strides[-2] if heads > 1 else 0, n, heads, dim
 
 
 def _written(name, t, heads):
@@ -554,23 +557,26 @@ def _table_arg(table, rot_start):
     return _arg("table", table, torch.int64, table.shape), rot_start, 2 * table.numel()
 
 
+def _fresh(t, dtype):
+    """A new tensor for the output of t, and its _head_args: whole rows one after the other."""
+    out = torch.empty(t.shape, dtype=dtype, device=t.device)
+    heads, dim = t.shape[-2:]
+    return out, (_ELEMENTS.get(dtype), out.data_ptr(), heads * dim, dim, None, heads, dim)
+
+
+_NONE = (0, None, 0, 0, 0, 0, 0)
+
+
 def dspark_qk_rotate(q, k, positions, table, q_weight, k_weight, eps, rot_start, interleaved,
                      magnitude, q_out, k_out, stream=None):
     """q, k [.., n_heads, head_dim] (either may be None, with its output) of one type, with the
     same tokens and head_dim; positions int32 of n_tokens; table int64 [rot_dim / 2] of
     rope_table, on the device, or None (norms alone); weights float32 [head_dim] or None; q_out,
     k_out like q, k in shape, of one type: the sources' or, for float32 sources, a 16-bit one."""
-    none = (0, None, 0, 0, 0, 0, 0)
-    a, b = (none if t is None else _head_args(n, t) for n, t in (("q", q), ("k", k)))
-    some = a if q is not None else b
-    if some is none:
-        raise ValueError("q or k is needed")
-    if q is not None and k is not None and (a[0] != b[0] or a[4] != b[4] or a[6] != b[6]):
-        raise ValueError("q and k must have the same type, tokens and head_dim")
     outs = []
-    for name, t, o, x in (("q_out", q, q_out, a), ("k_out", k, k_out, b)):
+    for name, t, o in (("q_out", q, q_out), ("k_out", k, k_out)):
         if t is None:
-            outs.append(none)
+            outs.append(_NONE)
             continue
         outs.append(_head_args(name, o))
         if o.shape != t.shape:
@@ -578,14 +584,26 @@ def dspark_qk_rotate(q, k, positions, table, q_weight, k_weight, eps, rot_start,
         _written(name, o, outs[-1])
     if q is not None and k is not None and outs[0][0] != outs[1][0]:
         raise TypeError("q_out and k_out must have the same type")
-    code = outs[0][0] if q is not None else outs[1][0]
+    _qk_rotate(q, k, positions, table, q_weight, k_weight, eps, rot_start, interleaved, magnitude,
+               *outs, stream)
+
+
+def _qk_rotate(q, k, positions, table, q_weight, k_weight, eps, rot_start, interleaved, magnitude,
+               q_out, k_out, stream):
+    """The call, with the outputs as _head_args."""
+    a, b = (_NONE if t is None else _head_args(n, t) for n, t in (("q", q), ("k", k)))
+    some, code = (a, q_out[0]) if q is not None else (b, k_out[0])
+    if some is _NONE:
+        raise ValueError("q or k is needed")
+    if q is not None and k is not None and (a[0] != b[0] or a[4] != b[4] or a[6] != b[6]):
+        raise ValueError("q and k must have the same type, tokens and head_dim")
     n, dim = some[4], some[6]
     tp, start, rot = _table_arg(table, rot_start)
     _call("dspark_qk_rotate", a[1], b[1], some[0], a[2], a[3], b[2], b[3], n, a[5], b[5], dim,
           _arg("q_weight", q_weight, torch.float32, (dim,)),
           _arg("k_weight", k_weight, torch.float32, (dim,)), eps,
-          _positions(positions, n), tp, start, rot, int(interleaved), magnitude, outs[0][1],
-          outs[0][2], outs[0][3], outs[1][1], outs[1][2], outs[1][3], code, _stream(stream))
+          _positions(positions, n), tp, start, rot, interleaved, magnitude, q_out[1], q_out[2],
+          q_out[3], k_out[1], k_out[2], k_out[3], code, _stream(stream))
 
 
 def _positions(positions, n):
@@ -600,6 +618,19 @@ def dspark_rotate_write(q, k, v, positions, table, k_cache, v_cache, slots, rows
     strides, all float32 or the caches' type; positions, slots int32 of n_tokens; rows int32 of
     n_tokens (q None) or None (then n_tokens is the number of tokens of k, and of q); the caches as
     in dspark_kv_write; q_out like q, of the caches' type; the rest as in dspark_qk_rotate."""
+    o = _NONE
+    if q is not None:
+        o = _head_args("q_out", q_out)
+        if q_out.shape != q.shape:
+            raise ValueError("q_out must have q's shape")
+        _written("q_out", q_out, o)
+    _rotate_write(q, k, v, positions, table, k_cache, v_cache, slots, rows, q_weight, k_weight, eps,
+                  rot_start, interleaved, magnitude, o, stream)
+
+
+def _rotate_write(q, k, v, positions, table, k_cache, v_cache, slots, rows, q_weight, k_weight, eps,
+                  rot_start, interleaved, magnitude, q_out, stream):
+    """The call, with q_out as _head_args."""
     code, kp, vp, sb, st, sh = _cache_args(k_cache, v_cache)
     x = _head_args("k", k)
     if v.shape != k.shape or v.dtype is not k.dtype or not v.is_cuda:
@@ -607,27 +638,27 @@ def dspark_rotate_write(q, k, v, positions, table, k_cache, v_cache, slots, rows
     if v.stride() != k.stride() and any(
             i != j and size > 1 for i, j, size in zip(k.stride(), v.stride(), k.shape)):
         raise ValueError("k and v must have the same strides")
-    if k.shape[-2:] != k_cache.shape[-2:]:
+    n_blocks, page, kv_heads, dim = k_cache.shape
+    if x[5] != kv_heads or x[6] != dim:
         raise ValueError("k and v must have the caches' heads and head_dim")
     if x[0] != F32 and x[0] != code:
         raise TypeError("q, k and v must be float32 or of the caches' type")
-    n, dim = slots.numel(), x[6]
+    n = slots.numel()
     if rows is None and n != x[4]:
         raise ValueError("slots must hold one slot for each token")
-    a = o = (0, None, 0, 0, 0, 0, 0)
+    a = _NONE
     if q is not None:
-        a, o = _head_args("q", q), _head_args("q_out", q_out)
+        a = _head_args("q", q)
         if a[0] != x[0] or a[4] != n or a[6] != dim:
             raise ValueError("q and k must have the same type, tokens and head_dim")
-        if q_out.shape != q.shape or o[0] != code:
-            raise ValueError("q_out must have q's shape and the caches' type")
-        _written("q_out", q_out, o)
+        if q_out[0] != code:
+            raise ValueError("q_out must have the caches' type")
     tp, start, rot = _table_arg(table, rot_start)
     _call("dspark_rotate_write", a[1], x[1], v.data_ptr(), x[0], a[2], a[3], x[2], x[3], x[4],
-          a[5], x[5], dim, _arg("q_weight", q_weight, torch.float32, (dim,)),
+          a[5], kv_heads, dim, _arg("q_weight", q_weight, torch.float32, (dim,)),
           _arg("k_weight", k_weight, torch.float32, (dim,)), eps, _positions(positions, n), tp,
-          start, rot, int(interleaved), magnitude, o[1], o[2], o[3], kp, vp, code, sb, st, sh,
-          k_cache.shape[0], k_cache.shape[1], _arg("slots", slots, torch.int32, slots.shape),
+          start, rot, interleaved, magnitude, q_out[1], q_out[2], q_out[3], kp, vp, code, sb, st,
+          sh, n_blocks, page, _arg("slots", slots, torch.int32, slots.shape),
           _arg("rows", rows, torch.int32, slots.shape), n, _stream(stream))
 
 
@@ -716,10 +747,12 @@ def _latent_attention(q, cache, block_table, ctx_len, n_nodes, latent_dim, tree_
     n_blocks, page, row = cache.shape
     if row != width:
         raise ValueError("q and the cache's rows must have the same width")
+    # a dimension of one element may have any stride
+    req, node, head = (st if n > 1 else width for st, n in zip(strides, q.shape[:3]))
     table, ld, wide = _table_args(block_table, B)
-    _call("dspark_latent_attention", q.data_ptr(), code, strides[0], strides[1], strides[2], B,
-          nodes, heads, latent_dim, width - latent_dim, cp, sb, st, n_blocks, page, table, ld,
-          wide, _arg("ctx_len", ctx_len, i32, (B,)), _arg("n_nodes", n_nodes, i32, (B,)),
+    _call("dspark_latent_attention", q.data_ptr(), code, req, node, head, B, nodes, heads,
+          latent_dim, width - latent_dim, cp, sb, st, n_blocks, page, table, ld, wide,
+          _arg("ctx_len", ctx_len, i32, (B,)), _arg("n_nodes", n_nodes, i32, (B,)),
           _arg("tree_mask", tree_mask, torch.int64, (B, nodes)), scale, out, lse, req_status,
           workspace, _stream(stream))
 
@@ -1037,7 +1070,10 @@ def qk_rotate(q, k, positions, table, q_weight=None, k_weight=None, eps=1e-6, ro
             return qk_rotate(q, k, positions, table, q_weight, k_weight, eps, rot_start,
                              interleaved, magnitude, out)
     if out is None:
-        out = tuple(None if t is None else _empty(t.shape, t.dtype, t.device) for t in (q, k))
+        (a, x), (b, y) = ((None, _NONE) if t is None else _fresh(t, t.dtype) for t in (q, k))
+        _qk_rotate(q, k, positions, table, q_weight, k_weight, eps, rot_start, interleaved,
+                   magnitude, x, y, stream)
+        return a, b
     dspark_qk_rotate(q, k, positions, table, q_weight, k_weight, eps, rot_start, interleaved,
                      magnitude, out[0], out[1], stream)
     return out[0], out[1]
@@ -1052,10 +1088,13 @@ def rotate_write(q, k, v, positions, table, k_cache, v_cache, slots, rows=None, 
         with torch.cuda.stream(stream):
             return rotate_write(q, k, v, positions, table, k_cache, v_cache, slots, rows, q_weight,
                                 k_weight, eps, rot_start, interleaved, magnitude, out)
-    if out is None and q is not None:
-        out = _empty(q.shape, k_cache.dtype, q.device)
-    dspark_rotate_write(q, k, v, positions, table, k_cache, v_cache, slots, rows, q_weight,
-                        k_weight, eps, rot_start, interleaved, magnitude, out, stream)
+    if out is None:
+        out, o = (None, _NONE) if q is None else _fresh(q, k_cache.dtype)
+        _rotate_write(q, k, v, positions, table, k_cache, v_cache, slots, rows, q_weight, k_weight,
+                      eps, rot_start, interleaved, magnitude, o, stream)
+    else:
+        dspark_rotate_write(q, k, v, positions, table, k_cache, v_cache, slots, rows, q_weight,
+                            k_weight, eps, rot_start, interleaved, magnitude, out, stream)
     return out, k_cache, v_cache
 
 

@@ -141,6 +141,7 @@ cudaError_t launch_latent_attention(const void* q, int dtype, int64_t q_req, int
   p.tile = attn::kLatentKeys;
   p.item_cost = attn::kLatentCost;
   p.row_tiles = 1;
+  p.min_range = attn::kLatentMinRange;
   p.part_rows = attn::latent_part_rows(nodes * heads);
   p.part_wide = 8;
   p.waits = true;

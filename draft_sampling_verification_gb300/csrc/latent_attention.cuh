@@ -129,7 +129,7 @@ static __device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t phase, uin
 // 10 and 11 of CTA 0 issue the pair's products.
 constexpr int kLatentKeys = 128;  // positions of a tile
 constexpr int kLatentThreads = 384;  // 168 registers a thread; from 416 on it is 128, and spills
-constexpr int kLatentCost = 3;
+constexpr int kLatentCost = 3, kLatentMinRange = 2;
 
 template <int DV>
 struct Latent {

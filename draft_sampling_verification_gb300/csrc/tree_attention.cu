@@ -55,6 +55,7 @@ cudaError_t launch_tree_attention(const void* q, int dtype, int64_t q_req, int64
   p.status = status;
   p.workspace = static_cast<char*>(workspace);
   p.row_tiles = 1;
+  p.min_range = attn::kMinRange;
   p.max_ctas = p.tile = p.item_cost = p.part_rows = p.part_wide = 0;
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);

@@ -32,6 +32,7 @@ struct Params {
   int max_ctas;   // ranges that the workspace has room for
   int tile;       // positions of a tile
   int item_cost;  // an item's start and end, in tiles
+  int min_range;  // of a team, in tiles
   int row_tiles;  // tiles of an item's rows: ceil(nodes * group / rows per CTA)
   int part_rows;  // rows of a partial result in the workspace
   int part_wide;  // elements of a row that lie together there, a power of two
@@ -156,7 +157,8 @@ __device__ __forceinline__ uint32_t without_special(uint32_t w) {
 // 89, 100 (head_dim 64: 98, 69, 74, 84); kOne, 64 of 300 to 8,000 tokens, 219
 // at 0, 210 at 1, 204 at 2, 206 at 4.  The streaming and kOne values are not
 // their best.
-// A range is at least kMinRange long: the join of more parts costs more than they save.
+// A range is at least kMinRange long: the join of more parts costs more than they save.  (Latent
+// attention has its own.)
 constexpr int kMinRange = 3;
 constexpr int kStreamCost = 5, kPairCost = 2, kBothCost = 8, kOneCost = 1;
 
@@ -257,9 +259,9 @@ struct Cut {
     return more + (int)(per >= INT32_MAX ? (x - head) / per : divide(x - head, (int)per));
   }
 };
-__device__ __forceinline__ Cut cut(int64_t total, int teams) {
+__device__ __forceinline__ Cut cut(int64_t total, int teams, int min_range) {
   Cut c;
-  c.teams = (int)max(1ll, min((long long)teams, (long long)total / kMinRange));
+  c.teams = (int)max(1ll, min((long long)teams, (long long)total / min_range));
   c.per = divide(total, c.teams);
   c.more = (int)(total - c.per * c.teams);
   return c;
@@ -355,7 +357,7 @@ __device__ __forceinline__ void find_range(const Params& p, const Workspace& ws,
                                            bool writes) {
   int64_t before, upto;
   const int64_t total = axis_part<kBlock>(p, scan, &before, &upto);
-  const Cut c = cut(total, ctas * kStreams / p.row_tiles);
+  const Cut c = cut(total, ctas * kStreams / p.row_tiles, p.min_range);
 #pragma unroll
   for (int x = 0; x < kStreams; ++x) {
     const int team = cta / p.row_tiles * kStreams + x;

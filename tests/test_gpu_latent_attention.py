@@ -264,6 +264,33 @@ def test_single_blocks_requests_and_broadcast_queries():
     c.check(c.run())
 
 
+@pytest.mark.parametrize("poison", [math.nan, math.inf, 3e38])
+def test_queries_of_no_node(poison):
+    """What stands in the queries behind a request's nodes reaches nothing."""
+    c = Case([300, 4000, 0], [3, 1, 0], 5, heads=40, seed=8)
+    want = c.run()
+    for b in range(3):
+        c.q[b, int(c.nodes[b]):] = poison
+    got = c.run()
+    assert all(torch.equal(x, y) for x, y in zip(want, got))
+    assert (got[0][2] == 0).all() and torch.isneginf(got[1][1, 1:]).all()
+
+
+def test_sizes_of_one_and_none():
+    c = Case([33, 80], [1, 1], 1, heads=1)
+    want = c.run()
+    a = c.device()
+    odd = torch.zeros(2, 577 * 8, dtype=c.q.dtype, device="cuda")
+    odd[:, :576] = c.q[:, 0, 0]
+    # one node and one head: their strides are no multiples of anything
+    a[0] = odd.as_strided((2, 1, 1, 576), (577 * 8, 3, 5, 1))
+    got = c.call(*a)
+    assert all(torch.equal(x, y) for x, y in zip(want, got))
+    a = [c.q[:0], c.cache, a[2][:0], a[3][:0], a[4][:0], None]
+    out, lse, status = c.call(*a)
+    assert out.shape == (0, 1, 1, 512) and lse.shape == (0, 1, 1) and status.shape == (0,)
+
+
 @pytest.mark.parametrize("scale", [0.31, -0.05, 0.0, 1e-39])
 def test_scales(scale):
     c = Case([90, 11], [3, 3], 3, spread=0.3)
