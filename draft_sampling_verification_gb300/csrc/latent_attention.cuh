@@ -113,22 +113,42 @@ static __device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t phase, uin
 // would fill the tensor memory of one SM; with products of the pair
 // (cta_group::2, 128 rows) a CTA's 64 rows take its 128 lanes twice: half of
 // a product's columns in lanes 0-63, the other half in lanes 64-127, so that
-// 64 columns hold the scores of 128 positions and 256 the accumulators.
+// 64 columns hold the scores of 128 positions and 256 the accumulators, at
+// the full rate (32 cycles a product of 128 columns, 64 of 256).
 //
 // S = Q K^T: each CTA brings its 64 rows of Q and 64 of the tile's rows of
 // the cache, in groups of three chunks of 64 elements (24 KB) that are freed
 // one by one.  O += P V: each CTA brings its rows' weights (through shared
 // memory) and its half of the values' dims for all 128 positions, in pieces
-// of 64 positions.  The scores of the next tile are computed before the
-// values of this one, while the softmax of this one runs.
+// of 64 positions; a row's values are its keys' first elements, but half of
+// them belong to the other CTA, so they are copied again (from L2).  The
+// scores of the next tile are computed before the values of this one, while
+// the softmax of this one runs; its weights are handed over by halves of the
+// positions, as the products free their place by halves.
 //
 // Warps 0-7: softmax; a thread has a row's scores of 32 positions, so four
 // threads share a row: the threads vote whether any score passes its row's
 // reference by more than 8, and only then exchange maxima and rescale.  Also
 // results.  Warp 8: tensor copies of keys; warp 9: of queries and values.  Warps
 // 10 and 11 of CTA 0 issue the pair's products.
+//
+// A tile's 52 products take 2,192 cycles, its softmax 1,600; it takes about
+// 3,000 in the loop: the issuing warps' waits (200 cycles each), the softmax
+// between a tile's scores and its values, and the copies' latency behind a
+// ring of one tile.  Two requests of 120,000 tokens and 192 rows 107 us (256
+// rows' products, 1.3 PFLOP/s), 64 of 4,000 and 96 rows 74 us (4.2 TB/s), of
+// which 7 us pass before the first keys, 5 behind the last product and 5 to 10
+// in the join.  Slower or the same: cluster-scoped barrier operations (524 us
+// where 217 were left), half the values through the load path by four more
+// warps (112 -> 122 us), four chunks of Q in tensor memory and a longer ring
+// instead (112 -> 113), unrolled product loops (107 -> 112: they fall out of the
+// scheduler's instruction cache), the prefetch two tiles ahead (106 -> 112).
 constexpr int kLatentKeys = 128;  // positions of a tile
 constexpr int kLatentThreads = 384;  // 168 registers a thread; from 416 on it is 128, and spills
+// An item's cost in tiles, at 3, 4, 5, 6: 256 requests of mixed lengths and 128 rows 157, 157, 156,
+// 158 us, 64 of 96 rows 57, 55, 55, 55, two long ones 107, 110, 114, 114 (at 2 all are 1 to 3 %
+// slower than at 3).  The least of a range: one request of 717 tokens at 1, 2, 3, 4 takes 16.2,
+// 16.3, 17.9, 18.6 us.
 constexpr int kLatentCost = 3, kLatentMinRange = 2;
 
 template <int DV>
@@ -171,8 +191,11 @@ struct LatentMaps {
   CUtensorMap values;  // the same, a CTA's values of `rows` rows
   CUtensorMap q;       // {elements, rows of a request, requests}, a chunk of 64 rows
   int rows;            // of a block that are copied together: 8, 16, 32 or 64
-  int k_rows;          // 64 or 8; 0: keys are copied chunk by chunk
-  int q_copies;        // Q has a map
+  // 64 or 8; 0: keys are copied chunk by chunk.  64 requests of 4,000 tokens, 96 rows, in blocks of
+  // 8, 16, 32, 64 tokens: by chunks 114, 82, 75, 75 us, by eight rows 78, 77, 77, 77, by 64 rows 74.
+  int k_rows;
+  // Q has a map (else the softmax warps copy it, 74 -> 81 us)
+  int q_copies;
 };
 
 template <typename T, int DV>
@@ -780,8 +803,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1) __cluster_dims__(2, 1, 1)
               bc += step;
             }
             pair_commit(on, &sh.k_empty[slot]);
-            // the other warp needs as long to see it as the rest takes
-            if (x == 0) mbar_arrive(&sh.s_turn[g & 1u]);
+            if (x == groups - 1) mbar_arrive(&sh.s_turn[g & 1u]);
             if (++slot == L::kKSlots) slot = 0, phase ^= 1u;
           }
           if (!ok) break;
@@ -818,6 +840,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1) __cluster_dims__(2, 1, 1)
                          kValues, i > 0 || s + k > 0);
             pair_commit(on, &sh.v_empty[slot]);
             pair_commit(on, &sh.o_full[s]);
+            // the other warp needs as long to see it as the rest takes
             if (s == 0) mbar_arrive(&sh.v_turn[g & 1u]);
             if (++slot == L::kVSlots) slot = 0, phase ^= 1u;
           }
