@@ -4,8 +4,6 @@
 // are in latent_attention.cuh.
 #define DSPARK_TU 16  // this file's number in the checked build's site codes
 
-#include <tuple>
-
 #include "latent_attention.cuh"
 
 namespace dspark {
@@ -46,13 +44,17 @@ bool make_maps(LatentMaps* m, const LatentParams& p) {
   // keys in one copy a group, or in eight of eight rows where those are fewer than by chunks
   m->k_rows = m->rows == 64 ? 64 : m->rows <= 16 ? 8 : 0;
   const cuuint32_t run = m->rows, k_run = m->k_rows ? m->k_rows : 8;
-  bool ok = encode_map<T, 3>(&m->tail, p.k, {width, page, blocks}, {p.token_stride, p.block_stride},
-                             {64, run, 1});
-  for (auto [map, box_rows, chunks] : {std::tuple{&m->keys, k_run, (int)L::kGroup},
-                                       std::tuple{&m->values, run, (int)L::kVParts}})
-    ok = ok && encode_map<T, 4>(map, p.k, {64, page, width / 64, blocks},
-                                {p.token_stride, 64, p.block_stride},
-                                {64, box_rows, (cuuint32_t)chunks, 1});
+  // a map takes the host half a microsecond: those that no copy uses are the values' once more
+  auto whole = [&](CUtensorMap* map, cuuint32_t box_rows, cuuint32_t chunks) {
+    return encode_map<T, 4>(map, p.k, {64, page, width / 64, blocks},
+                            {p.token_stride, 64, p.block_stride}, {64, box_rows, chunks, 1});
+  };
+  bool ok = whole(&m->values, run, L::kVParts);
+  m->tail = m->keys = m->q = m->values;
+  if (m->k_rows) ok = ok && whole(&m->keys, k_run, L::kGroup);
+  if (!m->k_rows || p.width % (64 * L::kGroup))
+    ok = ok && encode_map<T, 3>(&m->tail, p.k, {width, page, blocks},
+                                {p.token_stride, p.block_stride}, {64, run, 1});
   // Q by tensor copies where a request's rows are uniformly strided (and not broadcast); a negative
   // scale goes into its sign, which a copy cannot change
   const int64_t row = p.heads > 1 ? p.q_head : p.nodes > 1 ? p.q_node : p.width;
@@ -61,8 +63,6 @@ bool make_maps(LatentMaps* m, const LatentParams& p) {
                 row > 0 && request > 0 && row < (1ll << 38) && request < (1ll << 38);
   if (m->q_copies)
     ok = ok && encode_map<T, 3>(&m->q, p.q, {width, rows, B}, {row, request}, {64, 64, 1});
-  else
-    m->q = m->tail;  // not used
   return ok;
 }
 

@@ -327,6 +327,7 @@ __global__ void __launch_bounds__(kLatentThreads) latent_write_kernel(const Late
     sn[i] = __shfl_sync(0xffffffffu, turn.y, (4 * lane + i) & 31);
   }
   float f = 1.0f;
+  const bool whole = reinterpret_cast<uintptr_t>(p.weight) % 16 == 0;  // the weights' fours
   if (p.weight) {
     float sum = 0.0f;
 #pragma unroll
@@ -342,8 +343,11 @@ __global__ void __launch_bounds__(kLatentThreads) latent_write_kernel(const Late
     const int d = (i * 32 + lane) * 4;
     if (d >= p.latent) continue;
     float4 v = In::widen(x[i]);
-    if (p.weight)
-      v = scale4(v, f, make_float4(p.weight[d], p.weight[d + 1], p.weight[d + 2], p.weight[d + 3]));
+    if (p.weight) {
+      const float* w = p.weight + d;
+      v = scale4(v, f, whole ? *reinterpret_cast<const float4*>(w)
+                             : make_float4(w[0], w[1], w[2], w[3]));
+    }
     *reinterpret_cast<typename Out::Load*>(to + d) = Out::round(v);
   }
   if (turning) {
