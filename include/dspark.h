@@ -724,7 +724,8 @@ int dspark_logits_process(const void* logits, int32_t dtype, int64_t ld, int32_t
  * "NTK-by-parts"): frequencies of many turns stay, those of few are divided.
  * inv_freq: host, may be NULL.  rot_dim a multiple of 8 in [8,
  * DSPARK_MAX_HEAD]; base > 0, factor > 0 and, for PARTS, original_len > 0
- * and high > low, all finite, as every f_i (DSPARK_ERR_ARG otherwise).
+ * and high > low, all finite; every f_i, and f_i / factor where a factor is
+ * used, in [0, 1.3e10) (DSPARK_ERR_ARG otherwise).
  */
 int dspark_rope_table(int32_t rot_dim, double base, int32_t scaling, double factor,
                       double original_len, double low, double high, const double* inv_freq,
