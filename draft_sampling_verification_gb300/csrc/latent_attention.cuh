@@ -135,7 +135,7 @@ static __device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t phase, uin
 // A tile's 52 products take 2,192 cycles, its softmax 1,600; it takes about
 // 3,000 in the loop: the issuing warps' waits (200 cycles each), the softmax
 // between a tile's scores and its values, and the copies' latency behind a
-// ring of one tile.  Two requests of 120,000 tokens and 192 rows 107 us (256
+// ring of one tile.  Two requests of 120,000 tokens and 192 rows 104 us (256
 // rows' products, 1.3 PFLOP/s), 64 of 4,000 and 96 rows 74 us (4.2 TB/s), of
 // which 7 us pass before the first keys, 5 behind the last product and 5 to 10
 // in the join.  Slower or the same: cluster-scoped barrier operations (524 us
