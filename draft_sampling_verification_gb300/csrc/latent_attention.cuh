@@ -781,26 +781,19 @@ __global__ void __launch_bounds__(kLatentThreads, 1) __cluster_dims__(2, 1, 1)
             if (!ok) break;
             tc_after_sync();
             const bool whole = x < whole_groups;
-            const uint64_t a = q_desc + x * (L::kKBytes / 16);
-            const uint64_t b = (whole ? k_whole : k_desc) + slot * (L::kKBytes / 16);
+            uint64_t a = q_desc + x * (L::kKBytes / 16);
+            uint64_t b = (whole ? k_whole : k_desc) + slot * (L::kKBytes / 16);
             const uint32_t step = (whole ? k_chunk : L::kChunkBytes) / 16;
             const int here = chunks - x * L::kGroup;
-            auto chunk = [&](int c) {  // zeros lie behind a row's end
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                pair_mma(on, s_col(g), a + c * (L::kChunkBytes / 16) + k * 2, b + c * step + k * 2,
-                         kScores, c + k > 0 || x > 0);
-            };
-            uint64_t ac = a, bc = b;
             bool add = x > 0;
 #pragma unroll 1
-            for (int c = min(here, L::kGroup); c > 0; --c) {
+            for (int c = min(here, L::kGroup); c > 0; --c) {  // zeros lie behind a row's end
 #pragma unroll
               for (int k = 0; k < 4; ++k)
-                pair_mma(on, s_col(g), ac + k * 2, bc + k * 2, kScores, add || k > 0);
+                pair_mma(on, s_col(g), a + k * 2, b + k * 2, kScores, add || k > 0);
               add = true;
-              ac += L::kChunkBytes / 16;
-              bc += step;
+              a += L::kChunkBytes / 16;
+              b += step;
             }
             pair_commit(on, &sh.k_empty[slot]);
             if (x == groups - 1) mbar_arrive(&sh.s_turn[g & 1u]);
@@ -816,10 +809,6 @@ __global__ void __launch_bounds__(kLatentThreads, 1) __cluster_dims__(2, 1, 1)
       const uint64_t p_desc = operand_desc(p_at, 16, 1024);
       // a piece of values, 16 positions after 16: within a run, or in the next ones
       const uint64_t v_desc = operand_desc(v_at, v_chunk, rows == 8 ? v_run : 1024u);
-      uint32_t step[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        step[k] = ((16 * k >> shift) * v_run + (16 * k & (rows - 1)) * 128) / 16;
       while (ok && cur.advance(p, kKeys)) {
         for (int i = 0; i < cur.count && ok; ++i, ++g) {
 #pragma unroll 1
@@ -833,11 +822,13 @@ __global__ void __launch_bounds__(kLatentThreads, 1) __cluster_dims__(2, 1, 1)
             const uint64_t a = p_desc + s * (8192 / 16);
             const uint64_t b = v_desc + slot * (L::kVBytes / 16);
 #pragma unroll 1
-            for (int k = 0; k < 4; ++k)
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t step = (16 * k >> shift) * v_run + (16 * k & (rows - 1)) * 128;
 #pragma unroll
               for (int j = 0; j < DV / 256; ++j)
-                pair_mma(on, o_col + j * 128, a + k * 2, b + ((16 * k >> shift) * v_run + (16 * k & (rows - 1)) * 128) / 16 + j * (2 * v_chunk / 16),
+                pair_mma(on, o_col + j * 128, a + k * 2, b + step / 16 + j * (2 * v_chunk / 16),
                          kValues, i > 0 || s + k > 0);
+            }
             pair_commit(on, &sh.v_empty[slot]);
             pair_commit(on, &sh.o_full[s]);
             // the other warp needs as long to see it as the rest takes
@@ -915,8 +906,8 @@ __global__ void __launch_bounds__(kLatentThreads, 1) __cluster_dims__(2, 1, 1)
 // ------------------------------------------------------- the joining kernel
 // The item that is first cut between pairs x and x + 1, if there is one, is
 // joined from the pairs' partial rows, in the pairs' order: a warp takes 256
-// dims of a row, four parts in flight together.  CTA (x, 0) also gives the requests that pair x lost their
-// status.
+// dims of a row, four parts in flight together.  CTA (x, 0) also gives the
+// requests that pair x lost their status.
 constexpr int kLatentJoinThreads = 128;
 
 template <typename T, int DV>
