@@ -115,3 +115,14 @@ def test_latent_attention(lib):
     for a in ((1, 0, 16, 512), (1, 65, 16, 512), (1, 1, 0, 512), (1, 1, 129, 512), (1, 1, 16, 500),
               (-1, 1, 16, 512), (1, 1, 16, 576)):
         assert size(*a) == 0, a
+
+
+def test_latent_write_refuses_a_cache_whose_rows_overlap(lib):
+    # as in test_latent_write; n = 0: nothing is launched where the call is good
+    call = caller(lib.dspark_latent_write, (P, 576, P, 576, 0, 3, 512, 64, None, 1e-6, P, P, 0, 1.0,
+                                            P, 1, 9216, 576, 5, 16, P, None, 0, None))
+    for kw in (dict(a17=568), dict(a17=0), dict(a16=568), dict(a16=0)):
+        assert call(**kw) == SIZE, kw
+    # one row, one block; blocks that lie between one another's rows
+    for kw in (dict(a17=0, a19=1), dict(a16=0, a18=1), dict(a16=576, a17=2880)):
+        assert call(**kw) == 0, kw
