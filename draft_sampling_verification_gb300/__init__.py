@@ -523,6 +523,14 @@ def dspark_rope_table(rot_dim, base, scaling, factor, original_len, low, high, i
           float(original_len), float(low), float(high), _host(inv_freq), _host(table))
 
 
+def _here(*tensors):
+    """Refuses tensors of another device than the current one, which the calls launch on."""
+    device = torch._C._cuda_getDevice()
+    for t in tensors:
+        if t is not None and t.get_device() != device:
+            raise ValueError("tensors must be on the current CUDA device")
+
+
 _ELEMENTS = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
 
 
@@ -597,6 +605,7 @@ def _qk_rotate(q, k, positions, table, q_weight, k_weight, eps, rot_start, inter
         raise ValueError("q or k is needed")
     if q is not None and k is not None and (a[0] != b[0] or a[4] != b[4] or a[6] != b[6]):
         raise ValueError("q and k must have the same type, tokens and head_dim")
+    _here(q, k, positions, table)
     n, dim = some[4], some[6]
     tp, start, rot = _table_arg(table, rot_start)
     _call("dspark_qk_rotate", a[1], b[1], some[0], a[2], a[3], b[2], b[3], n, a[5], b[5], dim,
@@ -638,6 +647,7 @@ def _rotate_write(q, k, v, positions, table, k_cache, v_cache, slots, rows, q_we
     if v.stride() != k.stride() and any(
             i != j and size > 1 for i, j, size in zip(k.stride(), v.stride(), k.shape)):
         raise ValueError("k and v must have the same strides")
+    _here(q, k, v, k_cache, positions, table, slots)
     n_blocks, page, kv_heads, dim = k_cache.shape
     if x[5] != kv_heads or x[6] != dim:
         raise ValueError("k and v must have the caches' heads and head_dim")
@@ -700,6 +710,7 @@ def dspark_latent_write(c, k_rope, positions, table, cache, slots, rows, weight,
             raise ValueError("c and k_rope must have the same tokens and type")
         if table is None or 2 * table.numel() != rope:
             raise ValueError("table must hold one entry for each pair of k_rope")
+    _here(c, k_rope, cache, positions, table, slots)
     if c.dtype is not torch.float32 and c.dtype is not cache.dtype:
         raise TypeError("c must be float32 or of the cache's type")
     if cache.shape[2] != latent + rope:
@@ -743,6 +754,7 @@ def _latent_attention(q, cache, block_table, ctx_len, n_nodes, latent_dim, tree_
     if q.dim() != 4 or q.dtype is not cache.dtype or strides[3] != 1 or not q.is_cuda:
         raise ValueError("q must be a CUDA tensor [B, nodes, n_heads, latent_dim + rope_dim] of "
                          "the cache's type, contiguous in its last dimension")
+    _here(q, cache, block_table, ctx_len)
     B, nodes, heads, width = q.shape
     n_blocks, page, row = cache.shape
     if row != width:

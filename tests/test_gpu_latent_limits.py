@@ -121,3 +121,20 @@ def test_queries_far_apart():
         got = c.call(*a)
         torch.cuda.synchronize()
         assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
+def test_tensors_of_another_device_are_refused(monkeypatch):
+    """The calls launch on the current device; stood in for by another device's number."""
+    q, k, table, at = rand(0, 4, 2, 64).to(BF16), rand(1, 4, 1, 64).to(BF16), ds.rope_table(64), \
+        i32([0, 1, 2, 3])
+    kc, vc = (torch.zeros(1, 8, 1, 64, device="cuda", dtype=BF16) for _ in range(2))
+    cache, c = torch.zeros(1, 8, 64, device="cuda", dtype=BF16), rand(2, 4, 64).to(BF16)
+    one = i32([1])
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1)
+    for call in (lambda: ds.qk_rotate(q, k, at, table),
+                 lambda: ds.qk_rotate(q, k, at, table, out=(q, k)),
+                 lambda: ds.rotate_write(q, k, k, at, table, kc, vc, at),
+                 lambda: ds.latent_write(c, None, at, None, cache, at),
+                 lambda: ds.latent_attention(q[:1, None, :, :], cache, one[None], one, one, 64, 0.1)):
+        with pytest.raises(ValueError, match="current CUDA device"):
+            call()
