@@ -205,8 +205,7 @@ __device__ __forceinline__ void rotate_heads(const RotateParams& p, const Src* f
 // Bound by HBM: every element is read once and written once, the turns of a token computed once for
 // all its heads.  Few registers, so that four or five CTAs of an SM hide one another's starts: 16,384
 // tokens of 48 rows of 128, fp32 to bf16, take 98 us (6.2 TB/s; with five CTAs 100, and with all of
-// a token's rows in one loop, 106 registers and two CTAs 141); 384 tokens in bf16 6.6 us (with four
-// CTAs 8.8).
+// a token's rows in one loop, 106 registers and two CTAs 141); 384 tokens in bf16 5.9 us.
 template <typename Src, typename Dst, bool kInterleaved>
 __global__ void __launch_bounds__(kRotThreads, sizeof(Src) == 4 ? 4 : 5)
     rotate_kernel(const RotateParams p) {
@@ -267,7 +266,7 @@ __global__ void __launch_bounds__(kRotThreads, sizeof(Src) == 4 ? 4 : 5)
 
 // -------------------------------------------------- rows of a latent cache
 constexpr int kLatentThreads = 256;
-constexpr int kMaxLatent = 512, kMaxLatentRope = 64;
+constexpr int kMaxLatent = 512;
 
 struct LatentWriteParams {
   const void* c;
@@ -442,9 +441,12 @@ cudaError_t launch_rotate(const void* q, const void* k, const void* v, int src_d
   p.src_rows = src_rows;
   const int64_t tiles = ((int64_t)n_tokens + kRotTokens - 1) / kRotTokens;
   const int groups = kRotLanes >> p.lane_bits;
-  // few tokens: a token's rows go to several CTAs
+  // Few tokens: a token's rows go to several CTAs, until there are two an SM; more of them compute
+  // the turns too often.  32 + 8 + 8 heads of 128, bf16, from 1, 152, 304, 456, 608 CTAs on: 1 token
+  // 7.5, 3.4, 3.4, 3.4, 3.4 us; 384 tokens 7.5, 6.0, 6.0, 6.3, 6.8; 768: 8.9 (152), 7.0, 6.7, 9.0;
+  // 2,400: 13.9, 13.8, 13.9, 14.9.
   const int most = (p.rows + groups - 1) / groups;
-  const int64_t wanted = (608 + tiles - 1) / tiles;
+  const int64_t wanted = (2 * 152 + tiles - 1) / tiles;
   const int splits = wanted < most ? (int)wanted : most;
   p.per = (p.rows + splits - 1) / splits;
   const dim3 grid((unsigned)tiles, (unsigned)((p.rows + p.per - 1) / p.per));
