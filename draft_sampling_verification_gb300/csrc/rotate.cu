@@ -181,6 +181,9 @@ __device__ __forceinline__ void rotate_heads(const RotateParams& p, const Src* f
     }
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
+      // no row of the token is left (for all lanes).  32 heads of 64 in f16, 384 tokens 5.2 us without
+      // it, 4.6 with it; 16,384 tokens in fp32 98.9 and 101.2.
+      if (sizeof(Src) == 2 && u > 0 && first + u * groups >= h1) break;
       const int h = first + u * groups + group;
       float4 a = In::widen(x[u][0]), b = In::widen(x[u][1]);
       if constexpr (kTurned) {
@@ -203,11 +206,13 @@ __device__ __forceinline__ void rotate_heads(const RotateParams& p, const Src* f
 }
 
 // Bound by HBM: every element is read once and written once, the turns of a token computed once for
-// all its heads.  Few registers, so that four or five CTAs of an SM hide one another's starts: 16,384
+// all its heads.  Few registers, so that four CTAs of an SM hide one another's starts: 16,384
 // tokens of 48 rows of 128, fp32 to bf16, take 98 us (6.2 TB/s; with five CTAs 100, and with all of
-// a token's rows in one loop, 106 registers and two CTAs 141); 384 tokens in bf16 5.9 us.
+// a token's rows in one loop, 106 registers and two CTAs 141), in bf16 87 us (with three, four, five,
+// six CTAs 98, 87, 85, 86; 2,400 tokens 17.7, 13.6, 15.2, 16.9).  Two rows in flight: one alone takes
+// 100 us in bf16, four 95.
 template <typename Src, typename Dst, bool kInterleaved>
-__global__ void __launch_bounds__(kRotThreads, sizeof(Src) == 4 ? 4 : 5)
+__global__ void __launch_bounds__(kRotThreads, 4)
     rotate_kernel(const RotateParams p) {
   __shared__ float2 turns[kRotTokens][kMaxRot / 2];
   const int sub = threadIdx.x / kRotLanes, t = threadIdx.x % kRotLanes;
@@ -442,13 +447,15 @@ cudaError_t launch_rotate(const void* q, const void* k, const void* v, int src_d
   const int64_t tiles = ((int64_t)n_tokens + kRotTokens - 1) / kRotTokens;
   const int groups = kRotLanes >> p.lane_bits;
   // Few tokens: a token's rows go to several CTAs, until there are two an SM; more of them compute
-  // the turns too often.  32 + 8 + 8 heads of 128, bf16, from 1, 152, 304, 456, 608 CTAs on: 1 token
-  // 7.5, 3.4, 3.4, 3.4, 3.4 us; 384 tokens 7.5, 6.0, 6.0, 6.3, 6.8; 768: 8.9 (152), 7.0, 6.7, 9.0;
-  // 2,400: 13.9, 13.8, 13.9, 14.9.
+  // the turns too often.  32 + 8 + 8 heads of 128, bf16, until 1, 152, 304, 456, 608 CTAs: 1 token
+  // 6.4, 2.5, 2.5, 2.5, 2.5 us; 384 tokens 7.0, 5.4, 5.0, 5.0, 4.8; 768: 8.1, 8.1, 6.4, 6.2, 7.5;
+  // 2,400: 12.7, 12.7, 12.6, 12.7, 14.1.
   const int most = (p.rows + groups - 1) / groups;
   const int64_t wanted = (2 * 152 + tiles - 1) / tiles;
   const int splits = wanted < most ? (int)wanted : most;
   p.per = (p.rows + splits - 1) / splits;
+  // whole groups: 28 + 4 + 4 heads of 64, 384 tokens 4.6 -> 3.8 us
+  if (splits > 1) p.per = (p.per + groups - 1) / groups * groups;
   const dim3 grid((unsigned)tiles, (unsigned)((p.rows + p.per - 1) / p.per));
   return by_types<LaunchRotate>(src_dtype, dst_dtype, interleaved, p, grid, stream);
 }
