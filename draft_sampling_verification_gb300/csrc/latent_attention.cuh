@@ -438,7 +438,11 @@ __global__ void __launch_bounds__(kLatentThreads, 1) __cluster_dims__(2, 1, 1)
             }
             tmem_wait_store();
           }
+          // The next product takes all lanes, and its first half waits for half of these warps only:
+          // it is ordered behind the others' stores by this barrier.
+          tc_before_sync();
           any_of_256(false);  // all have read before the weights take the place
+          tc_after_sync();
         }
         uint32_t w16[16];
         if (!idle) {
