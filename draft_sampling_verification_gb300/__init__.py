@@ -524,7 +524,8 @@ def dspark_rope_table(rot_dim, base, scaling, factor, original_len, low, high, i
 
 
 def _here(*tensors):
-    """Refuses tensors of another device than the current one, which the calls launch on."""
+    """Refuses tensors of another device than the current one, which the calls launch on.  Given
+    every tensor of a call, outputs and workspace among them: the kernels get bare pointers."""
     device = torch._C._cuda_getDevice()
     for t in tensors:
         if t is not None and t.get_device() != device:
@@ -582,6 +583,7 @@ def dspark_qk_rotate(q, k, positions, table, q_weight, k_weight, eps, rot_start,
     rope_table, on the device, or None (norms alone); weights float32 [head_dim] or None; q_out,
     k_out like q, k in shape, of one type: the sources' or, for float32 sources, a 16-bit one."""
     outs = []
+    _here(q_out, k_out)
     for name, t, o in (("q_out", q, q_out), ("k_out", k, k_out)):
         if t is None:
             outs.append(_NONE)
@@ -605,7 +607,7 @@ def _qk_rotate(q, k, positions, table, q_weight, k_weight, eps, rot_start, inter
         raise ValueError("q or k is needed")
     if q is not None and k is not None and (a[0] != b[0] or a[4] != b[4] or a[6] != b[6]):
         raise ValueError("q and k must have the same type, tokens and head_dim")
-    _here(q, k, positions, table)
+    _here(q, k, positions, table, q_weight, k_weight)
     n, dim = some[4], some[6]
     tp, start, rot = _table_arg(table, rot_start)
     _call("dspark_qk_rotate", a[1], b[1], some[0], a[2], a[3], b[2], b[3], n, a[5], b[5], dim,
@@ -629,6 +631,7 @@ def dspark_rotate_write(q, k, v, positions, table, k_cache, v_cache, slots, rows
     in dspark_kv_write; q_out like q, of the caches' type; the rest as in dspark_qk_rotate."""
     o = _NONE
     if q is not None:
+        _here(q_out)
         o = _head_args("q_out", q_out)
         if q_out.shape != q.shape:
             raise ValueError("q_out must have q's shape")
@@ -647,7 +650,7 @@ def _rotate_write(q, k, v, positions, table, k_cache, v_cache, slots, rows, q_we
     if v.stride() != k.stride() and any(
             i != j and size > 1 for i, j, size in zip(k.stride(), v.stride(), k.shape)):
         raise ValueError("k and v must have the same strides")
-    _here(q, k, v, k_cache, positions, table, slots)
+    _here(q, k, v, k_cache, v_cache, positions, table, slots, rows, q_weight, k_weight)
     n_blocks, page, kv_heads, dim = k_cache.shape
     if x[5] != kv_heads or x[6] != dim:
         raise ValueError("k and v must have the caches' heads and head_dim")
@@ -710,7 +713,7 @@ def dspark_latent_write(c, k_rope, positions, table, cache, slots, rows, weight,
             raise ValueError("c and k_rope must have the same tokens and type")
         if table is None or 2 * table.numel() != rope:
             raise ValueError("table must hold one entry for each pair of k_rope")
-    _here(c, k_rope, cache, positions, table, slots)
+    _here(c, k_rope, cache, positions, table, slots, rows, weight)
     if c.dtype is not torch.float32 and c.dtype is not cache.dtype:
         raise TypeError("c must be float32 or of the cache's type")
     if cache.shape[2] != latent + rope:
@@ -740,6 +743,7 @@ def dspark_latent_attention(q, cache, block_table, ctx_len, n_nodes, latent_dim,
     need = dspark_latent_attention_workspace_bytes(B, nodes, heads, latent_dim)
     if workspace.numel() * workspace.element_size() < need:
         raise ValueError("the workspace is too small")
+    _here(out, lse, req_status, workspace)
     _latent_attention(q, cache, block_table, ctx_len, n_nodes, latent_dim, tree_mask, scale,
                       _arg("out", out, q.dtype, (B, nodes, heads, latent_dim)),
                       _arg("lse", lse, torch.float32, (B, nodes, heads)),
@@ -754,7 +758,7 @@ def _latent_attention(q, cache, block_table, ctx_len, n_nodes, latent_dim, tree_
     if q.dim() != 4 or q.dtype is not cache.dtype or strides[3] != 1 or not q.is_cuda:
         raise ValueError("q must be a CUDA tensor [B, nodes, n_heads, latent_dim + rope_dim] of "
                          "the cache's type, contiguous in its last dimension")
-    _here(q, cache, block_table, ctx_len)
+    _here(q, cache, block_table, ctx_len, n_nodes, tree_mask)
     B, nodes, heads, width = q.shape
     n_blocks, page, row = cache.shape
     if row != width:
