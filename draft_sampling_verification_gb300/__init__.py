@@ -555,7 +555,14 @@ def _head_args(name, t):
 def _written(name, t, heads):
     """Refuses an output whose elements share a place, by the arguments of _head_args."""
     _, _, token, head, n, n_heads, dim = heads
-    if (n_heads > 1 and head < dim) or (n > 1 and token < dim):
+    (near, few), (far, many) = sorted(((head, n_heads), (token, n)))
+    shared = few > 0 < many and ((few > 1 and near < dim) or (many > 1 and far < dim))
+    if not shared and few > 1 < many:
+        # i steps of the farther dimension, as many as steps of the nearer one can lead back from
+        for i in range(1, min(many, ((few - 1) * near + dim - 1) // far + 1)):
+            j = i * far // near
+            shared = shared or any(k < few and abs(i * far - k * near) < dim for k in (j, j + 1))
+    if shared:
         raise ValueError("the tokens and heads of %s must not overlap" % name)
 
 

@@ -185,6 +185,46 @@ int check_topk(int32_t top_k, int32_t V) {
 
 int launch_result(cudaError_t e) { return e == cudaSuccess ? 0 : (int)e; }
 
+// `count` places, `stride` >= 0 elements apart
+struct Dim {
+  int64_t count, stride;
+};
+
+// Whether two different places of a layout share an element, `width` elements lying at each: whether
+// steps along its dimensions that are not all 0 lead less than `width` from where they start.  From
+// the last dimension to the first, only steps that the dimensions before it can make good: with
+// dimensions in the order of their strides, none where each lies within one step of the next.
+bool meets(const Dim* dims, int n, __int128 at, int64_t width, bool moved) {
+  if (n == 0) return moved && at > -(__int128)width && at < width;
+  const __int128 stride = dims[n - 1].stride, most = dims[n - 1].count - 1;
+  __int128 reach = width - 1;
+  for (int i = 0; i < n - 1; ++i) reach += (__int128)(dims[i].count - 1) * dims[i].stride;
+  // at + k stride in [-reach, reach]
+  const __int128 lo = -reach - at, hi = reach - at;
+  __int128 first = lo / stride + (lo % stride > 0 ? 1 : 0);
+  __int128 last = hi / stride - (hi % stride < 0 ? 1 : 0);
+  first = first < -most ? -most : first;
+  last = last > most ? most : last;
+  for (__int128 k = first; k <= last; ++k)
+    if (meets(dims, n - 1, at + k * stride, width, moved || k != 0)) return true;
+  return false;
+}
+template <int N>
+bool shares_places(const Dim (&all)[N], int64_t width) {
+  Dim dims[N];
+  int n = 0;
+  for (const Dim& d : all)
+    if (d.count < 1) return false;
+  for (const Dim& d : all) {
+    if (d.count == 1) continue;
+    if (d.stride < width) return true;
+    int i = n++;
+    for (; i > 0 && dims[i - 1].stride > d.stride; --i) dims[i] = dims[i - 1];
+    dims[i] = d;
+  }
+  return meets(dims, n, 0, width, false);
+}
+
 }  // namespace
 
 extern "C" {
@@ -925,6 +965,11 @@ int dspark_qk_rotate(const void* q, const void* k, int32_t src_dtype, int64_t q_
   if (n_kv_heads && k == k_out && (src_dtype != out_dtype || k_token_stride != ko_token_stride ||
                                    k_head_stride != ko_head_stride))
     return DSPARK_ERR_ARG;
+  if ((n_heads && shares_places<2>({{n_tokens, qo_token_stride}, {n_heads, qo_head_stride}},
+                                   head_dim)) ||
+      (n_kv_heads && shares_places<2>({{n_tokens, ko_token_stride}, {n_kv_heads, ko_head_stride}},
+                                      head_dim)))
+    return DSPARK_ERR_SIZE;
   return launch_result(dspark::launch_rotate(
       q, k, nullptr, src_dtype, q_token_stride, q_head_stride, k_token_stride, k_head_stride,
       n_tokens, n_tokens, n_heads, n_kv_heads, head_dim, n_heads ? q_weight : nullptr,
@@ -973,6 +1018,8 @@ int dspark_rotate_write(const void* q, const void* k, const void* v, int32_t src
   if (n_heads && q == q_out && (src_dtype != cache_dtype || q_token_stride != qo_token_stride ||
                                 q_head_stride != qo_head_stride))
     return DSPARK_ERR_ARG;
+  if (n_heads && shares_places<2>({{n_tokens, qo_token_stride}, {n_heads, qo_head_stride}}, head_dim))
+    return DSPARK_ERR_SIZE;
   return launch_result(dspark::launch_rotate(
       q, k, v, src_dtype, q_token_stride, q_head_stride, kv_token_stride, kv_head_stride, n_src,
       n_tokens, n_heads, n_kv_heads, head_dim, n_heads ? q_weight : nullptr, k_weight, eps,

@@ -750,7 +750,8 @@ int dspark_rope_table(int32_t rot_dim, double base, int32_t scaling, double fact
  * d, queries and keys with strides of their own, so both may be views of one
  * projection's output; outputs the same.  An output may be its source itself
  * (of the same dtype and strides, DSPARK_ERR_ARG otherwise) and must not
- * overlap a source else.  n_heads or n_kv_heads may be 0 (then q, k and what
+ * overlap a source else.  Rows of one output that share elements are refused
+ * (DSPARK_ERR_SIZE).  n_heads or n_kv_heads may be 0 (then q, k and what
  * belongs to them are not looked at).  src_dtype DSPARK_F32, _BF16 or _F16;
  * out_dtype the same, or a 16-bit type for fp32 sources (DSPARK_ERR_DTYPE).
  * Weights fp32 [head_dim]; eps >= 0; head_dim a multiple of 8 in [8,
