@@ -1051,8 +1051,7 @@ int dspark_latent_write(const void* c, int64_t c_token_stride, const void* r,
   if (n_src < 0 || n_tokens < 0 || c_token_stride < 0 || (rope_dim && r_token_stride < 0))
     return DSPARK_ERR_SIZE;
   // rows that overlap would hold either one's elements
-  if ((page_size > 1 && token_stride < latent_dim + rope_dim) ||
-      (n_blocks > 1 && block_stride < latent_dim + rope_dim))
+  if (shares_places<2>({{n_blocks, block_stride}, {page_size, token_stride}}, latent_dim + rope_dim))
     return DSPARK_ERR_SIZE;
   if (!(eps >= 0.0f && eps <= FLT_MAX) || !(magnitude >= -FLT_MAX && magnitude <= FLT_MAX))
     return DSPARK_ERR_ARG;

@@ -811,9 +811,8 @@ int dspark_rotate_write(const void* q, const void* k, const void* v, int32_t src
  * dspark_qk_rotate at positions[i].  A token with a negative position, a slot
  * outside the cache or a source outside [0, n_src) is skipped.
  * latent_dim a multiple of 64 in [64, DSPARK_MAX_LATENT]; rope_dim a multiple
- * of 8 in [0, DSPARK_MAX_LATENT_ROPE] (0: r and table not looked at);
- * token_stride (of more than one row) and block_stride (of more than one
- * block) at least latent_dim + rope_dim.
+ * of 8 in [0, DSPARK_MAX_LATENT_ROPE] (0: r and table not looked at).  A cache
+ * two of whose rows share elements is refused (DSPARK_ERR_SIZE).
  * src_dtype the cache's or DSPARK_F32.  Alignments as above.
  */
 int dspark_latent_write(const void* c, int64_t c_token_stride, const void* r,
