@@ -1002,6 +1002,9 @@ int dspark_rotate_write(const void* q, const void* k, const void* v, int32_t src
       (n_heads && (q_token_stride < 0 || q_head_stride < 0 || qo_token_stride < 0 ||
                    qo_head_stride < 0)))
     return DSPARK_ERR_SIZE;
+  if (shares_places<3>({{n_blocks, block_stride}, {page_size, token_stride}, {n_kv_heads, head_stride}},
+                       head_dim))
+    return DSPARK_ERR_SIZE;
   if (rows && n_heads) return DSPARK_ERR_ARG;
   if (n_tokens == 0 || (n_src == 0 && n_heads == 0)) return 0;
   if (!k || !v || !k_cache || !v_cache || !slots || !positions || (rot_dim && !table) ||

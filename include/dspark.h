@@ -781,8 +781,8 @@ int dspark_qk_rotate(const void* q, const void* k, int32_t src_dtype, int64_t q_
  * Queries: of token i, rotated to q_out of the caches' dtype; n_heads 0: none
  * (q, q_out not looked at), and always so with rows (DSPARK_ERR_ARG
  * otherwise).  k and v have the same strides.  src_dtype the caches' dtype or
- * DSPARK_F32.  Sizes, alignments and the caches' layout as above;
- * n_blocks*page_size < 2^31.
+ * DSPARK_F32.  Sizes, alignments and the caches' layout as above, no two rows
+ * of a cache sharing elements (DSPARK_ERR_SIZE); n_blocks*page_size < 2^31.
  */
 int dspark_rotate_write(const void* q, const void* k, const void* v, int32_t src_dtype,
                         int64_t q_token_stride, int64_t q_head_stride, int64_t kv_token_stride,

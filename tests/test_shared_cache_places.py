@@ -1,5 +1,7 @@
-"""The latent write refuses a cache two of whose rows share elements: the
-library's rule against every place of many layouts -- no GPU needed."""
+"""The latent write and the write of rotated keys refuse a cache two of whose
+rows share elements: the library's rule against every place of many layouts --
+no GPU needed."""
+import ctypes
 import random
 
 import pytest
@@ -51,3 +53,35 @@ def test_layouts_of_the_largest_sizes(latent_write):
     assert latent_write(a16=big, a17=big, **kw) == SIZE
     assert latent_write(a16=2 ** 62, a17=2 ** 61, **kw) == SIZE
     assert latent_write(a16=1024 * 2 ** 50, a17=2 ** 50, **kw) == 0
+
+
+@pytest.fixture(scope="module")
+def rotate_write(lib):  # noqa: F811
+    # as in test_latent_abi, with no tokens
+    return caller(lib.dspark_rotate_write, (
+        P, P, P, 0, 512, 64, 128, 64, 3, 8, 2, 64, None, None, 1e-6, P, P, 0, 64, 0, 1.0,
+        ctypes.c_void_p(32), 512, 64, P, P, 1, 2048, 128, 64, 5, 16, P, None, 0, None))
+
+
+@pytest.mark.parametrize("block,token,head", [
+    (2048, 128, 64), (2048, 64, 1024), (64, 640, 320), (128, 640, 64), (2048, 128, 0), (0, 128, 64),
+    (1984, 128, 64), (128, 128, 64), (2048, 64, 64), (2048, 120, 64), (2048, 64, 960)])
+def test_caches_of_heads(rotate_write, block, token, head):
+    want = shared(64, [(5, block), (16, token), (2, head)])
+    assert want == ((block, token, head) not in ((2048, 128, 64), (2048, 64, 1024), (64, 640, 320),
+                                                 (128, 640, 64)))
+    assert rotate_write(a27=block, a28=token, a29=head) == (SIZE if want else 0)
+
+
+def test_many_caches_of_heads(rotate_write):
+    rng = random.Random(2)
+    seen = [0, 0]
+    for _ in range(4000):
+        count = [rng.randint(1, 4) for _ in range(3)]
+        stride = [8 * rng.randint(0, 1 << rng.randint(2, 5)) for _ in range(3)]
+        want = shared(16, list(zip(count, stride)))
+        got = rotate_write(a11=16, a18=16, a30=count[0], a31=count[1], a10=count[2], a27=stride[0],
+                           a28=stride[1], a29=stride[2])
+        assert got == (SIZE if want else 0), (count, stride)
+        seen[want] += 1
+    assert min(seen) > 500
