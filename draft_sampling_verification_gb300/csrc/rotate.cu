@@ -444,14 +444,18 @@ cudaError_t launch_rotate(const void* q, const void* k, const void* v, int src_d
   p.page = page;
   p.slots = slots;
   p.src_rows = src_rows;
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
   const int64_t tiles = ((int64_t)n_tokens + kRotTokens - 1) / kRotTokens;
   const int groups = kRotLanes >> p.lane_bits;
   // Few tokens: a token's rows go to several CTAs, until there are two an SM; more of them compute
-  // the turns too often.  32 + 8 + 8 heads of 128, bf16, until 1, 152, 304, 456, 608 CTAs: 1 token
-  // 6.4, 2.5, 2.5, 2.5, 2.5 us; 384 tokens 7.0, 5.4, 5.0, 5.0, 4.8; 768: 8.1, 8.1, 6.4, 6.2, 7.5;
-  // 2,400: 12.7, 12.7, 12.6, 12.7, 14.1.
+  // the turns too often.  32 + 8 + 8 heads of 128, bf16, on 152 SMs until 1, 152, 304, 456, 608 CTAs:
+  // 1 token 6.4, 2.5, 2.5, 2.5, 2.5 us; 384 tokens 7.0, 5.4, 5.0, 5.0, 4.8; 768: 8.1, 8.1, 6.4, 6.2,
+  // 7.5; 2,400: 12.7, 12.7, 12.6, 12.7, 14.1.
   const int most = (p.rows + groups - 1) / groups;
-  const int64_t wanted = (2 * 152 + tiles - 1) / tiles;
+  const int64_t wanted = (2 * (int64_t)sms + tiles - 1) / tiles;
   const int splits = wanted < most ? (int)wanted : most;
   p.per = (p.rows + splits - 1) / splits;
   // whole groups: 28 + 4 + 4 heads of 64, 384 tokens 4.6 -> 3.8 us
