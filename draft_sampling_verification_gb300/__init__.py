@@ -1071,7 +1071,8 @@ _SCALINGS = {None: ROPE_PLAIN, "linear": ROPE_LINEAR, "parts": ROPE_PARTS}
 def rope_table(rot_dim, base=10000.0, scaling=None, factor=1.0, original_len=1.0, low=1.0,
                high=32.0, inv_freq=None, device=None):
     """The table of a rotation of rot_dim elements, int64 [rot_dim / 2] on the device (the current
-    CUDA device when None), made once and kept.  scaling: None, "linear" or "parts"; inv_freq:
+    CUDA device when None), made once and kept.  scaling: None, "linear" or "parts" (linear in the
+    turns over original_len; models whose ramp is linear in the pair's index give inv_freq); inv_freq:
     radians a position, a sequence or a tensor, in place of base's."""
     if scaling not in _SCALINGS:
         raise ValueError("scaling must be None, 'linear' or 'parts', got %r" % (scaling,))

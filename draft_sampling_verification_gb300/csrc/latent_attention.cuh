@@ -138,13 +138,17 @@ static __device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t phase, uin
 // ring of one tile.  Two requests of 120,000 tokens and 192 rows 104 us (256
 // rows' products, 1.3 PFLOP/s), 64 of 4,000 and 96 rows 74 us (4.2 TB/s), of
 // which 7 us pass before the first keys, 5 behind the last product and 5 to 10
-// in the join.  Slower or the same: cluster-scoped barrier operations (524 us
+// in the join.  A request's tiles of rows are counted from the batch's nodes:
+// those without a node of the request's cost as much as full ones (16 requests
+// of 2,500 to 8,100 tokens, 32 heads, 24 nodes 109 us; with one node each 105,
+// and 29 where the batch has one).  Slower or the same: cluster-scoped barrier operations (524 us
 // where 217 were left), half the values through the load path by four more
 // warps (112 -> 122 us), four chunks of Q in tensor memory and a longer ring
 // instead (112 -> 113), unrolled product loops (107 -> 112: they fall out of the
 // scheduler's instruction cache), the prefetch two tiles ahead (106 -> 112).
 constexpr int kLatentKeys = 128;  // positions of a tile
-constexpr int kLatentThreads = 384;  // 168 registers a thread; from 416 on it is 128, and spills
+// 168 registers a thread, 16 to 24 bytes of it spilled; from 416 threads on 128 and 146 to 314.
+constexpr int kLatentThreads = 384;
 // An item's cost in tiles, at 3, 4, 5, 6: 256 requests of mixed lengths and 128 rows 157, 157, 156,
 // 158 us, 64 of 96 rows 57, 55, 55, 55, two long ones 107, 110, 114, 114 (at 2 all are 1 to 3 %
 // slower than at 3).  The least of a range: one request of 717 tokens at 1, 2, 3, 4 takes 16.2,
@@ -759,10 +763,13 @@ __global__ void __launch_bounds__(kLatentThreads, 1) __cluster_dims__(2, 1, 1)
     // ------------------------------------------------------------- products
     // A warp for the scores and one for the values, so that one's waits, 200 cycles each where the
     // tensor cores hold some 100 cycles of products ahead, pass during the other's products.  They
-    // take turns: tile g's scores behind tile g - 2's values, which have read the weights that
-    // were its scores' place, and tile g's values behind tile g + 1's scores (of the same item).
-    // Products of both side by side would end together, and the softmax would wait for both.  A
-    // warp goes through its loop together; one lane issues.
+    // take turns: tile g's scores behind the first half of tile g - 2's values, and tile g's values
+    // behind tile g + 1's scores (of the same item).  Products of both side by side would end
+    // together, and the softmax would wait for both.  The turn also says that the columns of tile
+    // g - 2's scores are free for tile g's: the values waited for the first half's weights, and these
+    // come behind the vote that every softmax thread of a CTA joins once its scores are loaded.
+    // Without that vote the threads of the second half could still be loading.  A warp goes through
+    // its loop together; one lane issues.
     constexpr uint32_t kFormat = H::kExponent == 0x7F80u ? 1u : 0u;  // bf16 or f16
     // fp32 accumulators, both operands of T, 128 rows; for P V the second has its dims outermost
     constexpr uint32_t kCommon = (1u << 4) | (kFormat << 7) | (kFormat << 10) | (8u << 24);

@@ -722,6 +722,10 @@ int dspark_logits_process(const void* logits, int32_t dtype, int64_t ld, int32_t
  * r = original_len * f_i / (2 pi) and keep = clamp((r - low) / (high - low),
  * 0, 1), f_i * (keep + (1 - keep) / factor) (Peng et al., "YaRN", 2023,
  * "NTK-by-parts"): frequencies of many turns stay, those of few are divided.
+ * This ramp is linear in the turns.  A model whose ramp is linear in the pair's
+ * index, between the two (rounded) indices of `low` and `high` turns, as in
+ * many checkpoints of that method, latent-attention ones among them, has other
+ * frequencies: it gives its own as inv_freq, with DSPARK_ROPE_PLAIN.
  * inv_freq: host, may be NULL.  rot_dim a multiple of 8 in [8,
  * DSPARK_MAX_HEAD]; base > 0, factor > 0 and, for PARTS, original_len > 0
  * and high > low, all finite; every f_i, and f_i / factor where a factor is
