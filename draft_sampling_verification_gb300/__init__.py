@@ -590,11 +590,11 @@ def dspark_qk_rotate(q, k, positions, table, q_weight, k_weight, eps, rot_start,
     rope_table, on the device, or None (norms alone); weights float32 [head_dim] or None; q_out,
     k_out like q, k in shape, of one type: the sources' or, for float32 sources, a 16-bit one."""
     outs = []
-    _here(q_out, k_out)
     for name, t, o in (("q_out", q, q_out), ("k_out", k, k_out)):
         if t is None:
             outs.append(_NONE)
             continue
+        _here(o)
         outs.append(_head_args(name, o))
         if o.shape != t.shape:
             raise ValueError("%s must have its source's shape" % name)
@@ -614,7 +614,8 @@ def _qk_rotate(q, k, positions, table, q_weight, k_weight, eps, rot_start, inter
         raise ValueError("q or k is needed")
     if q is not None and k is not None and (a[0] != b[0] or a[4] != b[4] or a[6] != b[6]):
         raise ValueError("q and k must have the same type, tokens and head_dim")
-    _here(q, k, positions, table, q_weight, k_weight)
+    _here(q, k, positions, table, q_weight if q is not None else None,
+          k_weight if k is not None else None)
     n, dim = some[4], some[6]
     tp, start, rot = _table_arg(table, rot_start)
     _call("dspark_qk_rotate", a[1], b[1], some[0], a[2], a[3], b[2], b[3], n, a[5], b[5], dim,
@@ -657,7 +658,8 @@ def _rotate_write(q, k, v, positions, table, k_cache, v_cache, slots, rows, q_we
     if v.stride() != k.stride() and any(
             i != j and size > 1 for i, j, size in zip(k.stride(), v.stride(), k.shape)):
         raise ValueError("k and v must have the same strides")
-    _here(q, k, v, k_cache, v_cache, positions, table, slots, rows, q_weight, k_weight)
+    _here(q, k, v, k_cache, v_cache, positions, table, slots, rows, k_weight,
+          q_weight if q is not None else None)
     n_blocks, page, kv_heads, dim = k_cache.shape
     if x[5] != kv_heads or x[6] != dim:
         raise ValueError("k and v must have the caches' heads and head_dim")

@@ -99,3 +99,14 @@ def test_given_outputs(called, argument):
         with pytest.raises(ValueError, match="current CUDA device"):
             ds.rotate_write(**args, out=out["q_out"])
     assert called == []
+
+
+def test_what_is_not_looked_at(called):
+    """Without keys or queries, what belongs to them may lie anywhere."""
+    args = {k: on(Current, *shape, dtype=dtype) for k, (shape, dtype) in HEADS.items()}
+    weight, out = on(Another, 64, dtype=F32), on(Another, 4, 1, 64)
+    ds.qk_rotate(**{**args, "k": None, "k_weight": weight}, out=(args["q"], out))
+    ds.qk_rotate(**{**args, "q": None, "q_weight": weight}, out=(out, args["k"]))
+    paged = {k: on(Current, *shape, dtype=dtype) for k, (shape, dtype) in PAGED.items()}
+    ds.rotate_write(**{**args, **paged, "q": None, "q_weight": weight})
+    assert called == ["dspark_qk_rotate"] * 2 + ["dspark_rotate_write"]
